@@ -10,6 +10,10 @@ Entry points (same names as the C ABI in include/moe_w4.h):
     route_topk, permute, expert_ffn_w4a16, combine, layer_forward,
     layer_workspace_size, permute_workspace_size, expert_ffn_workspace_size,
     get_device_error, status_str, version
+and, for 16-bit experts and training (expert16.py):
+    grouped_mm, grouped_mm_dx, grouped_mm_dw, grouped_mm_workspace_size,
+    swiglu, swiglu_backward, block_norm, block_norm_backward,
+    block_norm_backward_workspace_size
 """
 from __future__ import annotations
 
@@ -58,6 +62,7 @@ def lib() -> ctypes.CDLL:
                                "`python -m bit_quantized_expert_moe_gb300.build` (no CPU fallback exists)")
         L = ctypes.CDLL(LIB_PATH)
         V, I32, SZ, P = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.POINTER(moe_w4_layer)
+        F = ctypes.c_float
         sig = {
             "moe_route_topk": (I32, [V, I32, I32, I32, V, V, V]),
             "moe_permute": (I32, [V, I32, I32, I32, V, I32, V, V, V, V, V, V, SZ, V]),
@@ -67,6 +72,15 @@ def lib() -> ctypes.CDLL:
             "moe_combine": (I32, [V, V, V, I32, I32, I32, V, V]),
             "moe_layer_forward": (I32, [P, V, V, I32, I32, V, V, V, SZ, V]),
             "moe_layer_workspace_size": (SZ, [P, I32, I32]),
+            "moe_grouped_mm_workspace_size": (SZ, [I32] * 4),
+            "moe_grouped_mm": (I32, [I32, V, V, V, I32, I32, I32, I32, V, V, SZ, V]),
+            "moe_grouped_mm_dx": (I32, [I32, V, V, V, I32, I32, I32, I32, V, V, SZ, V]),
+            "moe_grouped_mm_dw": (I32, [I32, V, V, V, I32, I32, I32, I32, V, V, SZ, V]),
+            "moe_swiglu": (I32, [I32, V, V, V, I32, I32, V, V]),
+            "moe_swiglu_backward": (I32, [I32, V, V, V, V, I32, I32, V, V, V]),
+            "moe_block_norm": (I32, [I32] * 5 + [F, F] + [V] * 8),
+            "moe_block_norm_backward_workspace_size": (SZ, [I32] * 3),
+            "moe_block_norm_backward": (I32, [I32] * 5 + [F, F] + [V] * 13 + [SZ, V]),
             "moe_get_device_error": (I32, [V, V]),
             "moe_profile_stages": (I32, [V, I32, V]),
             "moe_kernel_launches": (ctypes.c_uint64, []),
@@ -295,3 +309,7 @@ class StageProfiler:
 def get_device_error(ws: torch.Tensor, stream=None) -> int:
     """Reads and clears the workspace error word (synchronises the stream)."""
     return lib().moe_get_device_error(_ptr(ws), _stream(stream))
+
+
+from .expert16 import (block_norm, block_norm_backward, block_norm_backward_workspace_size, grouped_mm,  # noqa: E402
+                       grouped_mm_dw, grouped_mm_dx, grouped_mm_workspace_size, swiglu, swiglu_backward)

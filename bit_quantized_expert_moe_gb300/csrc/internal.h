@@ -123,6 +123,37 @@ int tc_max_tiles(int R, int E);
 cudaError_t launch_tc_gateup(int E, int d, int f, int R, const TcIn& in, cudaStream_t s);
 cudaError_t launch_tc_down(int E, int d, int f, int R, const TcIn& in, cudaStream_t s);
 
+// ------------------------------------------- 16-bit expert operators
+struct GroupedShape {
+    moe_dtype_t dtype;       // bf16 or fp16
+    int R, E, N, K;
+    const int32_t* offsets;  // [E+1]
+    uint32_t* err;
+};
+// y = x W_e^T, dx = dy W_e, dW_e = dy_e^T x_e over the segments of `offsets`.
+cudaError_t launch_grouped_mm(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s);
+cudaError_t launch_grouped_mm_dx(const GroupedShape& g, const void* dy, const void* w, void* dx, cudaStream_t s);
+cudaError_t launch_grouped_mm_dw(const GroupedShape& g, const void* dy, const void* x, void* dw, cudaStream_t s);
+
+cudaError_t launch_swiglu(moe_dtype_t dt, const void* gu, const float* row_w, const int32_t* row_map, int R, int F,
+                          void* h, cudaStream_t s);
+cudaError_t launch_swiglu_backward(moe_dtype_t dt, const void* dh, const void* gu, const float* row_w,
+                                   const int32_t* row_map, int R, int F, void* dgu, float* drow_w, cudaStream_t s);
+
+struct NormShape {
+    moe_dtype_t dtype, param_dtype;
+    int T, D, G;
+    float alpha, eps;
+    const void *gamma_post, *gate, *gamma_pre;  // any may be null
+};
+struct NormGrads {
+    const void *x_out, *y, *dx_out, *dh;
+    void *dx, *dy, *dgamma_post, *dgate, *dgamma_pre;
+};
+size_t block_norm_partial_floats(int T, int D);  // scratch of the backward pass
+cudaError_t launch_block_norm(const NormShape& n, const void* x, const void* y, void* x_out, void* h, cudaStream_t s);
+cudaError_t launch_block_norm_backward(const NormShape& n, const NormGrads& g, float* part, cudaStream_t s);
+
 // 3D tensor map over 32-bit words: dims {d0, d1, d2} (d0 contiguous), byte
 // strides s1 (dim 1) and s2 (dim 2), box {b0, b1, b2}, 128-byte swizzle.
 bool make_tensor_map_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,

@@ -240,10 +240,102 @@ moe_status_t moe_layer_forward(const moe_w4_layer* L, const void* x_bf16, const 
                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
 size_t moe_layer_workspace_size(const moe_w4_layer* L, int32_t T, int32_t k);
 
+/* ======================================================================
+ * 16-bit expert operators: what stands around the int4 layer in training and
+ * in models with 16-bit experts.  They use the permutation of moe_permute
+ * (`offsets`, `sorted`) and follow the conventions above.
+ * Widths (N, K, F, D) are multiples of 8 (MOE_ERR_UNSUPPORTED otherwise), at
+ * most 32768, and 16384 for D.
+ * ====================================================================== */
+
+/* Element type of a call's tensors. */
+typedef enum {
+    MOE_DT_BF16 = 0,
+    MOE_DT_F16 = 1,
+    MOE_DT_F32 = 2   /* gated activation and block norms only */
+} moe_dtype_t;
+
+/*
+ * Products grouped by expert, bf16 or fp16, fp32 accumulation, one rounding.
+ * Segment e is rows offsets[e] .. offsets[e+1]-1 of the R permuted rows:
+ *   moe_grouped_mm     y[r][n]     = sum_k x[r][k] * w[e][n][k]
+ *   moe_grouped_mm_dx  dx[r][k]    = sum_n dy[r][n] * w[e][n][k]
+ *   moe_grouped_mm_dw  dw[e][n][k] = sum over r in segment e of dy[r][n] * x[r][k]
+ *                                    (zeros for an expert without rows)
+ *   x, dx  device [R][K]    y, dy  device [R][N]    w, dw  device [E][N][K]
+ *   offsets  device int32 [E+1], offsets[0] = 0, offsets[E] = R, non-decreasing.
+ * A segment that is not inside [0, R] counts as empty and is reported as
+ * MOE_ERR_DEVICE_RANGE by moe_get_device_error; rows that no segment holds
+ * are not written.  1 <= E <= 1024.  R = 0: nothing to do, and zeros in dw.
+ * Workspace: >= moe_grouped_mm_workspace_size(R, E, N, K) bytes, the same for
+ * the three products.
+ */
+size_t moe_grouped_mm_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K);
+moe_status_t moe_grouped_mm(moe_dtype_t dtype, const void* x, const void* w, const int32_t* offsets,
+                            int32_t R, int32_t E, int32_t N, int32_t K, void* y,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+moe_status_t moe_grouped_mm_dx(moe_dtype_t dtype, const void* dy, const void* w, const int32_t* offsets,
+                               int32_t R, int32_t E, int32_t N, int32_t K, void* dx,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+moe_status_t moe_grouped_mm_dw(moe_dtype_t dtype, const void* dy, const void* x, const int32_t* offsets,
+                               int32_t R, int32_t E, int32_t N, int32_t K, void* dw,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Gated activation between the two products, with the row's routing weight:
+ *   h[r][f] = w_r * SiLU(gu[r][f]) * gu[r][F + f],   w_r = row_w[row_map[r]]
+ * and its gradients: dgu [R][2F] and drow_w[row_map[r]] = sum_f dh * SiLU * up.
+ * With row_map = `sorted` of moe_permute, row_w and drow_w are in the order of
+ * topk_w.  With the weight here, a combine with weights 1 finishes the layer.
+ *   gu, dgu  device [R][2F] (gate, then up)   h, dh  device [R][F]
+ *   row_w    device fp32 [R], NULL for weights 1
+ *   row_map  device int32 [R], a permutation of 0..R-1; NULL for the identity.
+ *            An entry outside [0, R) gives weight 0 and no drow_w.
+ *   drow_w   device fp32 [R] (out), NULL to skip; needs row_w
+ * h may not overlap gu; dgu may be gu.
+ */
+moe_status_t moe_swiglu(moe_dtype_t dtype, const void* gu, const float* row_w, const int32_t* row_map,
+                        int32_t R, int32_t F, void* h, cudaStream_t stream);
+moe_status_t moe_swiglu_backward(moe_dtype_t dtype, const void* dh, const void* gu, const float* row_w,
+                                 const int32_t* row_map, int32_t R, int32_t F, void* dgu, float* drow_w,
+                                 cudaStream_t stream);
+
+/*
+ * The norms before and after a block, with its gate and residual scale, in
+ * one pass over the rows of the stream x and the block's output y:
+ *   n     = y / rms(y) * gamma_post     (gamma_post NULL: n = y)
+ *   x_out = x + alpha * gate * n        (gate NULL: 1)
+ *   h     = x_out / rms(x_out) * gamma_pre   (gamma_pre and h NULL: not wanted)
+ *   rms(v) = sqrt(mean v^2 + eps)
+ * With y and x_out NULL it is the first norm alone: h from x.
+ *   x, y, x_out, h  device [T][D] in `dtype`; x_out may be x
+ *   gamma_post, gamma_pre  device [D];  gate  device [G][D], row t / (T / G)
+ *     for token t (G divides T; G = 1: one gate per channel), all three in
+ *     `param_dtype`: `dtype` or MOE_DT_F32
+ * Statistics in fp32; h is taken from x_out before its rounding.
+ *
+ * moe_block_norm_backward: the gradients at the stored x_out, from dx_out (of
+ * x_out; NULL: zero) and dh (of h; with gamma_pre):
+ *   dx, dy  device [T][D];  dgamma_post, dgate, dgamma_pre as their parameters,
+ *   each NULL to skip.  dx may be dx_out.  The order of every sum is fixed.
+ * Workspace: >= moe_block_norm_backward_workspace_size(T, D, G) bytes.
+ */
+moe_status_t moe_block_norm(moe_dtype_t dtype, moe_dtype_t param_dtype, int32_t T, int32_t D, int32_t G,
+                            float alpha, float eps, const void* gamma_post, const void* gate,
+                            const void* gamma_pre, const void* x, const void* y, void* x_out, void* h,
+                            cudaStream_t stream);
+size_t moe_block_norm_backward_workspace_size(int32_t T, int32_t D, int32_t G);
+moe_status_t moe_block_norm_backward(moe_dtype_t dtype, moe_dtype_t param_dtype, int32_t T, int32_t D, int32_t G,
+                                     float alpha, float eps, const void* gamma_post, const void* gate,
+                                     const void* gamma_pre, const void* x_out, const void* y,
+                                     const void* dx_out, const void* dh, void* dx, void* dy,
+                                     void* dgamma_post, void* dgate, void* dgamma_pre,
+                                     void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /*
  * Reads and clears the device error word kept at the start of a workspace
- * used by moe_permute, moe_expert_ffn_w4a16 or moe_layer_forward.  Waits for
- * `stream` to finish.  When it reports an error it clears the whole 256-byte
+ * used by moe_permute, moe_expert_ffn_w4a16, moe_layer_forward or the grouped
+ * products.  Waits for `stream` to finish.  When it reports an error it clears the whole 256-byte
  * header, which also holds the grid-barrier counter of the one-kernel decode
  * layer (a call that gave up can leave that counter inconsistent).  Returns MOE_OK, MOE_ERR_TIMEOUT, MOE_ERR_DEVICE_RANGE
  * or MOE_ERR_F16_RANGE, in that order of precedence (or MOE_ERR_CUDA if the
