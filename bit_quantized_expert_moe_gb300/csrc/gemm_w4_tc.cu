@@ -694,6 +694,23 @@ bool make_tensor_map_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d
     return make_tensor_map_u32(m, ptr, 3, dims, strides, box);
 }
 
+bool make_tensor_map_16(CUtensorMap* m, bool bf16, const void* ptr, int rank, const uint64_t* dims,
+                        const uint64_t* strides, const uint32_t* box) {
+    EncodeFn enc = get_encode();
+    if (!enc || rank < 1 || rank > 5) return false;
+    cuuint64_t gd[5], gs[4];
+    cuuint32_t bx[5], estr[5];
+    for (int i = 0; i < rank; ++i) {
+        gd[i] = dims[i];
+        bx[i] = box[i];
+        estr[i] = 1;
+        if (i + 1 < rank) gs[i] = strides[i];
+    }
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+               const_cast<void*>(ptr), gd, gs, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int tc_max_tiles(int R, int E) { return ceil_div(R, TILE_ROWS) + std::min(R, E); }
 
 bool tc_supported(int E, int d, int f) {

@@ -1,12 +1,41 @@
-// Products of 16-bit expert weights with ragged row segments.
+// Products of 16-bit expert weights with ragged row segments, on the
+// 5th-generation tensor cores (tcgen05, TMEM accumulators, TMA).
 //
 // Segment e is rows offsets[e] .. offsets[e+1]-1.
-//   y[r][n]     = sum_k x[r][k] W[e][n][k]
-//   dx[r][k]    = sum_n dy[r][n] W[e][n][k]
-//   dW[e][n][k] = sum_{r in e} dy[r][n] x[r][k]
-// One block computes 64 x 64 outputs of one segment, 16 of the summed index
-// at a time from shared memory, in fp32.
+//   Y    y[r][n]     = sum_k x[r][k] W[e][n][k]
+//   DX   dx[r][k]    = sum_n dy[r][n] W[e][n][k]
+//   DW   dW[e][n][k] = sum_{r in e} dy[r][n] x[r][k]
+//
+// The three are one kernel: D[m][c] = sum_l A[m][l] B[c][l] in tiles of 256 x
+// (at most) 256, by CTA pairs (2-SM clusters, cta_group::2): each CTA holds its
+// 128 rows of A and half of B, so an SM receives 32 KB for 64 l instead of the
+// 48 KB that one CTA alone would need for the same 2 x 128 x 256 products.
+//         m            c           l                 A            B
+//   Y     weight row n row r       k                 W   K-major  x   K-major
+//   DX    weight col k row r       n                 W   MN-major dy  K-major
+//   DW    n            k           row r of segment  dy  MN-major x   MN-major
+// MN-major operands are read by the tensor core from the rows as TMA brings
+// them (descriptor with the transpose bit): nothing is transposed in memory.
+// The weights are M in Y and DX, so that a tile of few rows costs an MMA of
+// few columns (a multiple of 16) and not an M of 128 that is mostly padding:
+// with 16 rows an expert the weights' bytes are all that counts.
+// Widths that are no multiple of a tile: TMA fills zeros out of bounds.  Rows
+// behind a segment belong to the next expert: in Y and DX they are columns of
+// D that are not stored; in DW they would be summed, so the rows up to the next
+// multiple of 16 are set to zero in shared memory and no MMA reads further.
+//
+// Warp roles (384 threads a CTA): 0 TMA producer, 1 TMEM owner and (even CTA)
+// MMA issuer, 2 (DW) relay, 4-11 epilogue (warp w: TMEM lanes 32 (w % 4) .. + 31,
+// every second block of 32 columns).  Two accumulators: the epilogue of a tile
+// runs beside the MMAs of the next.
+// Barriers: Y, DX: both CTAs' copies complete on the even CTA's full[s].  DW: on
+// each CTA's own full[s], where the relay warp waits, clears the rows behind the
+// segment and arrives on the even CTA's ready[s].  empty[s] and accfull[b] are
+// signalled to both CTAs by the MMAs' completion, accempty[b] of the even CTA
+// counts both epilogues' warps.  Every wait is bounded in time: one that gives up
+// sets the error word and every role leaves its loop.
 #include "internal.h"
+#include "tc_ptx.cuh"
 #include "vec8.cuh"
 
 namespace moe {
@@ -14,66 +43,410 @@ namespace {
 
 enum class Product { Y, DX, DW };
 
-template <class T, Product PR>
-__global__ void __launch_bounds__(256) grouped_kernel(const void* __restrict__ a, const void* __restrict__ b,
-                                                      void* __restrict__ out, GroupedShape g) {
-    __shared__ float sa[16][65], sb[16][65];
-    const int e = blockIdx.z;
-    const int i = g.offsets[e], j = g.offsets[e + 1];
-    const bool bad = i < 0 || j < i || j > g.R;
-    if (bad && threadIdx.x == 0) set_error(g.err, ERRBIT_RANGE);
-    const int r0 = bad ? 0 : i, cnt = bad ? 0 : j - i;
-    const int M = PR == Product::DW ? g.N : cnt;                               // output rows
-    const int C = PR == Product::Y ? g.N : g.K;                                // output columns
-    const int L = PR == Product::Y ? g.K : PR == Product::DX ? g.N : cnt;      // summed index
-    const size_t we = (size_t)e * g.N * g.K;
-    const int c0 = blockIdx.x * 64, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    for (int m0 = blockIdx.y * 64; m0 < M; m0 += gridDim.y * 64) {
-        float acc[4][4] = {};
-        for (int l0 = 0; l0 < L; l0 += 16) {
-            for (int t = threadIdx.x; t < 64 * 16; t += 256) {
-                const int l = PR == Product::DW ? t / 64 : t % 16, m = PR == Product::DW ? t % 64 : t / 16;
-                float v = 0.f;
-                if (m0 + m < M && l0 + l < L)
-                    v = PR == Product::DW ? load1<T>(a, (size_t)(r0 + l0 + l) * g.N + m0 + m)
-                                          : load1<T>(a, (size_t)(r0 + m0 + m) * L + l0 + l);
-                sa[l][m] = v;
-            }
-            for (int t = threadIdx.x; t < 64 * 16; t += 256) {
-                const int l = PR == Product::Y ? t % 16 : t / 64, c = PR == Product::Y ? t / 16 : t % 64;
-                float v = 0.f;
-                if (c0 + c < C && l0 + l < L)
-                    v = PR == Product::Y    ? load1<T>(b, we + (size_t)(c0 + c) * g.K + l0 + l)
-                        : PR == Product::DX ? load1<T>(b, we + (size_t)(l0 + l) * g.K + c0 + c)
-                                            : load1<T>(b, (size_t)(r0 + l0 + l) * g.K + c0 + c);
-                sb[l][c] = v;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int l = 0; l < 16; ++l)
-#pragma unroll
-                for (int p = 0; p < 4; ++p)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[p][q] = fmaf(sa[l][ty + 16 * p], sb[l][tx + 16 * q], acc[p][q]);
-            __syncthreads();
-        }
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int m = m0 + ty + 16 * p, c = c0 + tx + 16 * q;
-                if (m < M && c < C)
-                    store1<T>(out, PR == Product::DW ? we + (size_t)m * g.K + c : (size_t)(r0 + m) * C + c, acc[p][q]);
-            }
+constexpr int BM = 128;             // A rows of a CTA (256 a pair)
+constexpr int BN = 256;             // most columns of a tile
+constexpr int BL = 64;              // l of a stage: one 128-byte swizzle row
+constexpr int A_BYTES = BM * BL * 2;
+constexpr int B_BYTES = BN / 2 * BL * 2;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int ATOM64 = 64 * BL * 2;  // MN-major: 64 l rows of 64 elements
+constexpr int STAGES = 6;
+constexpr int THREADS = 384;
+constexpr int EP_WARP0 = 4, EP_WARPS = 8;
+constexpr uint32_t TMEM_COLS = 512;  // two accumulators of 256 columns
+constexpr int NBAR = 3 * STAGES + 4;
+constexpr size_t BAR_BYTES = 256;
+constexpr size_t SMEM_LIMIT = 232448;
+static_assert(8 * NBAR + 8 <= BAR_BYTES, "barrier area too small");
+
+size_t smem_bytes(int E) { return 1024 + (size_t)STAGES * STAGE_BYTES + BAR_BYTES + 4 * ((size_t)E + 1); }
+
+struct GroupedParams {
+    int R, E, N, K;
+    const int32_t* offsets;
+    void* out;
+    uint32_t type;  // 0 fp16, 1 bf16
+    uint32_t* err;
+};
+
+// Rows of segment e; false if it is not inside [0, R].
+__device__ __forceinline__ bool segment(const GroupedParams& p, int e, int& r0, int& cnt) {
+    const int i = __ldg(p.offsets + e), j = __ldg(p.offsets + e + 1);
+    const bool ok = i >= 0 && i <= j && j <= p.R;
+    r0 = ok ? i : 0;
+    cnt = ok ? j - i : 0;
+    return ok;
+}
+
+// One tile of the output.
+struct Item {
+    int e;
+    int m0;        // first of the pair's 256 A rows
+    int c0, ncols; // first column and how many (Y, DX: rows r; DW: k)
+    int l0, nl;    // the summed index: first (DW: row) and how many
+};
+
+template <Product PR>
+struct Work {
+    int mb;     // blocks of 256 A rows
+    int cb;     // DW: blocks of 256 columns
+    int items;
+    const int* tile_pre;  // row tiles before each expert, [E + 1]; the last < 0: bad offsets
+
+    __device__ Work(const GroupedParams& p, const int* pre) : tile_pre(pre) {
+        mb = ceil_div(PR == Product::DX ? p.K : p.N, 2 * BM);
+        cb = ceil_div(p.K, BN);
+        items = pre[p.E] < 0 ? 0 : PR == Product::DW ? p.E * mb * cb : pre[p.E] * mb;
     }
+    __device__ Item item(const GroupedParams& p, int i) const {
+        Item t;
+        if (PR == Product::DW) {
+            const int per = mb * cb;
+            t.e = i / per;
+            i -= t.e * per;
+            t.m0 = i / cb * 2 * BM;
+            t.c0 = i % cb * BN;
+            t.ncols = min(BN, p.K - t.c0);
+            segment(p, t.e, t.l0, t.nl);
+        } else {
+            const int tile = i / mb;
+            t.m0 = (i - tile * mb) * 2 * BM;
+            // the expert whose row tiles include `tile`
+            int lo = 0, hi = p.E - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (tile_pre[mid + 1] <= tile) lo = mid + 1;
+                else hi = mid;
+            }
+            t.e = lo;
+            int r0, cnt;
+            segment(p, t.e, r0, cnt);
+            // the segment's units of 16 rows are spread evenly over its tiles
+            const int nt = tile_pre[lo + 1] - tile_pre[lo], k = tile - tile_pre[lo];
+            const long long units = (cnt + 15) >> 4;
+            const int u0 = (int)(units * k / nt), u1 = (int)(units * (k + 1) / nt);
+            t.c0 = r0 + 16 * u0;
+            t.ncols = min(16 * (u1 - u0), cnt - 16 * u0);
+            t.l0 = 0;
+            t.nl = PR == Product::DX ? p.N : p.K;
+        }
+        return t;
+    }
+};
+
+__device__ __forceinline__ int mma_cols(const Item& t) { return (t.ncols + 15) & ~15; }
+
+// Boxes of B rows (Y, DX): a CTA's half of a tile is 8 .. 128 rows.
+constexpr int BOX_S = 16, BOX_M = 64, BOX_L = 128;
+
+template <Product PR>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    grouped_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ CUtensorMap map_b_m, const __grid_constant__ CUtensorMap map_b_s,
+                      const GroupedParams p) {
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    unsigned char* gbase = smem_raw + (base - raw);
+    const uint32_t bars = base + STAGES * STAGE_BYTES;
+    const uint32_t bar_full = bars, bar_empty = bars + 8 * STAGES, bar_ready = bars + 16 * STAGES;
+    const uint32_t bar_accfull = bars + 24 * STAGES, bar_accempty = bar_accfull + 16;
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + STAGES * STAGE_BYTES + 8 * NBAR);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* tile_pre = reinterpret_cast<int*>(gbase + STAGES * STAGE_BYTES + BAR_BYTES);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            tc::mbar_init(bar_full + 8 * s, 1);
+            tc::mbar_init(bar_empty + 8 * s, 1);
+            tc::mbar_init(bar_ready + 8 * s, 2);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(bar_accfull + 8 * b, 1);
+            tc::mbar_init(bar_accempty + 8 * b, 2 * EP_WARPS);
+        }
+        *abort_flag = 0;
+        tc::fence_mbar_init();
+        tc::tma_prefetch_desc(&map_a);
+        tc::tma_prefetch_desc(&map_b);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc_pair(smem_u32((const void*)tmem_slot), TMEM_COLS);
+        tc::tmem_relinquish_pair();
+    }
+    if (warp == 2) {
+        // row tiles before each expert; with a segment out of place there is
+        // nothing to do (overlapping ones could add up to any number of tiles)
+        int sum = 0;
+        bool all_ok = true;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            int r0 = 0, cnt = 0;
+            bool ok = true;
+            if (e < p.E) ok = segment(p, e, r0, cnt);
+            all_ok = all_ok && __all_sync(0xffffffffu, ok);
+            const int nt = ceil_div(cnt, BN);
+            int inc = nt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (e < p.E) tile_pre[e] = sum + inc - nt;
+            sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) {
+            tile_pre[p.E] = all_ok ? sum : -1;
+            if (!all_ok && blockIdx.x == 0) set_error(p.err, ERRBIT_RANGE);
+        }
+    }
+    // both CTAs' barriers are initialised and the tensor memory allocated
+    // before either CTA signals the other
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const Work<PR> work(p, tile_pre);
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const uint32_t full_lead = tc::mapa_shared(bar_full, 0);
+            int g = 0;  // stages issued so far
+            bool ok = true;
+            for (int i = pair; ok && i < work.items; i += npairs) {
+                const Item t = work.item(p, i);
+                const int half = mma_cols(t) >> 1;
+                const int box = half <= BOX_S ? BOX_S : half <= BOX_M ? BOX_M : BOX_L;
+                const CUtensorMap* mb = half <= BOX_S ? &map_b_s : half <= BOX_M ? &map_b_m : &map_b;
+                const uint32_t bytes = PR == Product::DW ? STAGE_BYTES : 2 * (A_BYTES + (uint32_t)box * BL * 2);
+                const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
+                for (int l = 0; l < t.nl; l += BL, ++g) {
+                    const int s = g % STAGES;
+                    if (!tc::mbar_wait(bar_empty + 8 * s, ((uint32_t)(g / STAGES) & 1u) ^ 1u, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
+                    const uint32_t fl = full_lead + 8 * s, f = bar_full + 8 * s;
+                    if (PR == Product::DW) {
+                        tc::mbar_arrive_expect_tx(f, bytes);
+                        tc::tma_load_2d(sa, &map_a, f, m, t.l0 + l);
+                        tc::tma_load_2d(sa + ATOM64, &map_a, f, m + 64, t.l0 + l);
+                        tc::tma_load_2d(sb, &map_b, f, c, t.l0 + l);
+                        tc::tma_load_2d(sb + ATOM64, &map_b, f, c + 64, t.l0 + l);
+                    } else {
+                        if (rank == 0) tc::mbar_arrive_expect_tx(f, bytes);
+                        if (PR == Product::Y) {
+                            tc::tma_load_3d_pair(sa, &map_a, fl, l, m, t.e);
+                        } else {
+                            tc::tma_load_3d_pair(sa, &map_a, fl, m, l, t.e);
+                            tc::tma_load_3d_pair(sa + ATOM64, &map_a, fl, m + 64, l, t.e);
+                        }
+                        tc::tma_load_2d_pair(sb, mb, fl, l, c);
+                    }
+                }
+            }
+            // the MMAs have read every stage, so every copy has landed
+            for (int k = max(0, g - STAGES); ok && k < g; ++k)
+                ok = tc::mbar_wait(bar_empty + 8 * (k % STAGES), (uint32_t)(k / STAGES) & 1u, abort_flag, p.err);
+        }
+    } else if (warp == 1) {
+        // -------------------------------------- MMA issuer (even CTA of the pair)
+        if (lane == 0 && rank == 0) {
+            int g = 0, ic = 0;
+            bool ok = true;
+            for (int i = pair; ok && i < work.items; i += npairs) {
+                const Item t = work.item(p, i);
+                if (t.nl == 0) continue;
+                const uint32_t idesc = tc::idesc_16_f32(2 * BM, mma_cols(t), p.type, PR != Product::Y, PR == Product::DW);
+                const int b = ic & 1;
+                // both CTAs' epilogues have read the accumulator
+                if (!tc::mbar_wait_cluster(bar_accempty + 8 * b, ((uint32_t)(ic >> 1) & 1u) ^ 1u, abort_flag, p.err)) break;
+                tc::tc_fence_after();
+                const uint32_t d = tmem_base + 256u * b;
+                for (int l = 0; l < t.nl; l += BL, ++g) {
+                    const int s = g % STAGES;
+                    const uint32_t in = (PR == Product::DW ? bar_ready : bar_full) + 8 * s;
+                    if (!tc::mbar_wait_cluster(in, (uint32_t)(g / STAGES) & 1u, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::tc_fence_after();
+                    const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
+                    const int steps = min(BL, t.nl - l + 15) >> 4;
+                    for (int k = 0; k < steps; ++k) {
+                        const uint64_t da = PR == Product::Y ? tc::sw128_kmajor_desc(sa + 32 * k)
+                                                             : tc::sw128_mnmajor_desc(sa + 2048 * k, ATOM64);
+                        const uint64_t db = PR == Product::DW ? tc::sw128_mnmajor_desc(sb + 2048 * k, ATOM64)
+                                                              : tc::sw128_kmajor_desc(sb + 32 * k);
+                        tc::mma_f16_pair(d, da, db, idesc, l + k > 0);
+                    }
+                    tc::mma_commit_pair(bar_empty + 8 * s);
+                }
+                if (!ok) break;
+                tc::mma_commit_pair(bar_accfull + 8 * b);
+                ++ic;
+            }
+        }
+    } else if (warp == 2 && PR == Product::DW) {
+        // ------------------------------------------------------------- relay
+        const uint32_t ready_lead = tc::mapa_shared(bar_ready, 0);
+        int g = 0;
+        bool ok = true;
+        for (int i = pair; ok && i < work.items; i += npairs) {
+            const Item t = work.item(p, i);
+            for (int l = 0; l < t.nl; l += BL, ++g) {
+                const int s = g % STAGES;
+                ok = tc::mbar_wait(bar_full + 8 * s, (uint32_t)(g / STAGES) & 1u, abort_flag, p.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const int left = t.nl - l, end = min(BL, (left + 15) & ~15);
+                if (left < end) {
+                    // rows left .. end-1 of the four blocks of 64 rows x 128 B
+                    unsigned char* st = gbase + s * STAGE_BYTES;
+                    const int words = (end - left) * 8;
+                    for (int w = lane; w < 4 * words; w += 32)
+                        *reinterpret_cast<uint4*>(st + (w / words) * ATOM64 + left * 128 + (w % words) * 16) = make_uint4(0, 0, 0, 0);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster_release(ready_lead + 8 * s);
+                } else {
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(ready_lead + 8 * s);
+                }
+            }
+        }
+    } else if (warp >= EP_WARP0) {
+        // ---------------------------------------------------------- epilogue
+        const int q = warp & 3, eh = (warp - EP_WARP0) >> 2;
+        const uint32_t accempty_lead = tc::mapa_shared(bar_accempty, 0);
+        const uint32_t t_lane = (uint32_t)(32 * q) << 16;
+        const int M = PR == Product::DX ? p.K : p.N;
+        uint16_t* const out = static_cast<uint16_t*>(p.out);
+        int ic = 0;
+        for (int i = pair; i < work.items; i += npairs) {
+            const Item t = work.item(p, i);
+            const int m = t.m0 + (int)rank * BM + 32 * q + lane;  // this thread's A row
+            const int b = ic & 1;
+            if (t.nl > 0) {
+                const bool ok = tc::mbar_wait(bar_accfull + 8 * b, (uint32_t)(ic >> 1) & 1u, abort_flag, p.err);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::tc_fence_after();
+            }
+            const int blocks = ceil_div(t.ncols, 32);
+            for (int cb = eh; cb < blocks; cb += 2) {
+                uint32_t v[32];
+                if (t.nl > 0) {
+                    tc::tmem_ld_32x32b_x32(tmem_base + 256u * b + 32u * cb + t_lane, v);
+                    tc::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0;
+                }
+                if (PR == Product::DW) {
+                    uint16_t* o = out + ((size_t)t.e * p.N + m) * p.K + t.c0 + 32 * cb;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float f[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[8 * j + k]);
+                        if (m < M && 32 * cb + 8 * j < t.ncols) {
+                            if (p.type) store8<Bf16>(o, j, f);
+                            else store8<F16>(o, j, f);
+                        }
+                    }
+                } else {
+                    uint16_t* o = out + (size_t)(t.c0 + 32 * cb) * M + m;
+                    const int n = min(32, t.ncols - 32 * cb);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float f = __uint_as_float(v[j]);
+                        if (m < M && j < n) o[(size_t)j * M] = p.type ? float_to_bf16_bits(f) : float_to_f16_bits(f);
+                    }
+                }
+            }
+            if (t.nl > 0) {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(accempty_lead + 8 * b);
+                ++ic;
+            }
+        }
+    }
+
+    // A wait that gave up: copies and MMAs that were issued finish well inside
+    // this time.  Otherwise nothing is in flight here.
+    __syncwarp();
+    if (*abort_flag) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {}
+    }
+    // neither CTA frees its tensor memory or exits while the other may still
+    // signal its barriers or use its memory
+    __syncwarp();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+bool map_2d(CUtensorMap* m, bool bf16, const void* ptr, int cols, int rows, int box_cols, int box_rows) {
+    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)cols * 2};
+    const uint32_t box[2] = {(uint32_t)box_cols, (uint32_t)box_rows};
+    return make_tensor_map_16(m, bf16, ptr, 2, dims, strides, box);
+}
+bool map_w(CUtensorMap* m, bool bf16, const void* ptr, const GroupedShape& g, int box_rows) {
+    const uint64_t dims[3] = {(uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.E};
+    const uint64_t strides[2] = {(uint64_t)g.K * 2, (uint64_t)g.N * g.K * 2};
+    const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
+    return make_tensor_map_16(m, bf16, ptr, 3, dims, strides, box);
 }
 
 template <Product PR>
 cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
-    const int M = PR == Product::DW ? g.N : g.R, C = PR == Product::Y ? g.N : g.K;
-    const dim3 grid(ceil_div(C, 64), std::min(ceil_div(M, 64), PR == Product::DW ? 65535 : 16), g.E);
-    if (g.dtype == MOE_DT_BF16) grouped_kernel<Bf16, PR><<<grid, 256, 0, s>>>(a, b, out, g);
-    else grouped_kernel<F16, PR><<<grid, 256, 0, s>>>(a, b, out, g);
+    const bool bf = g.dtype == MOE_DT_BF16;
+    CUtensorMap ma, mb, mb_m, mb_s;
+    bool ok;
+    int max_items;
+    if (PR == Product::DW) {
+        ok = map_2d(&ma, bf, a, g.N, g.R, 64, 64) && map_2d(&mb, bf, b, g.K, g.R, 64, 64);
+        mb_m = mb_s = mb;
+        max_items = g.E * ceil_div(g.N, 2 * BM) * ceil_div(g.K, BN);
+    } else {
+        const int L = PR == Product::Y ? g.K : g.N, M = PR == Product::Y ? g.N : g.K;
+        ok = map_w(&ma, bf, a, g, PR == Product::Y ? BM : 64) && map_2d(&mb, bf, b, L, g.R, 64, BOX_L) &&
+             map_2d(&mb_m, bf, b, L, g.R, 64, BOX_M) && map_2d(&mb_s, bf, b, L, g.R, 64, BOX_S);
+        max_items = (g.R / BN + std::min(g.R, g.E)) * ceil_div(M, 2 * BM);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    static int max_pairs = 0;  // CTA pairs that the GPU holds at once
+    if (max_pairs == 0) {
+        cudaError_t e = cudaFuncSetAttribute(grouped_tc_kernel<PR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)SMEM_LIMIT);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = smem_bytes(1024);
+        int nc = 0;
+        if (cudaOccupancyMaxActiveClusters(&nc, grouped_tc_kernel<PR>, &cfg) != cudaSuccess || nc < 1) {
+            (void)cudaGetLastError();
+            nc = num_sms() / 2;
+        }
+        max_pairs = std::max(1, nc);
+    }
+    const GroupedParams p{g.R, g.E, g.N, g.K, g.offsets, out, bf ? 1u : 0u, g.err};
+    const int grid = 2 * std::max(1, std::min(max_pairs, max_items));
+    grouped_tc_kernel<PR><<<grid, THREADS, smem_bytes(g.E), s>>>(ma, mb, mb_m, mb_s, p);
     note_launch();
     return cudaGetLastError();
 }
@@ -81,12 +454,13 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
 }  // namespace
 
 cudaError_t launch_grouped_mm(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s) {
-    return launch<Product::Y>(g, x, w, y, s);
+    return launch<Product::Y>(g, w, x, y, s);
 }
 cudaError_t launch_grouped_mm_dx(const GroupedShape& g, const void* dy, const void* w, void* dx, cudaStream_t s) {
-    return launch<Product::DX>(g, dy, w, dx, s);
+    return launch<Product::DX>(g, w, dy, dx, s);
 }
 cudaError_t launch_grouped_mm_dw(const GroupedShape& g, const void* dy, const void* x, void* dw, cudaStream_t s) {
+    if (g.R == 0) return cudaMemsetAsync(dw, 0, (size_t)g.E * g.N * g.K * 2, s);
     return launch<Product::DW>(g, dy, x, dw, s);
 }
 

@@ -165,6 +165,9 @@ bool make_tensor_map_u32(CUtensorMap* m, const void* ptr, int rank, const uint64
 // The same over 16-bit elements, without swizzle.
 bool make_tensor_map_u16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
                          const uint32_t* box);
+// The same over bf16 or fp16 elements, 128-byte swizzle, zeros out of bounds.
+bool make_tensor_map_16(CUtensorMap* m, bool bf16, const void* ptr, int rank, const uint64_t* dims,
+                        const uint64_t* strides, const uint32_t* box);
 
 // ----------------------------------------------------------- device info
 int num_sms();

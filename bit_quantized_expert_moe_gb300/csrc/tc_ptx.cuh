@@ -122,6 +122,10 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 // that copies have completed into, not ordinary writes another CTA would
 // read.  A release at cluster scope costs the arriving thread about 1300
 // cycles, which on every stage doubled the pair's stage time.
+// (mbar_arrive_cluster_release is the form for such writes.)
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cl_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cl_bar) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cl_bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(cl_bar) : "memory");
 }
@@ -188,6 +192,24 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5}], [%2];"
         :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+// The same loads by a CTA of a pair into its own shared memory, completing the
+// bytes on an mbarrier of either CTA of the pair (cl_bar: its shared::cluster
+// address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t cl_bar, int32_t x,
+                                                 int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];"
+        :: "r"(dst), "l"(map), "r"(cl_bar), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t cl_bar, int32_t x,
+                                                 int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        :: "r"(dst), "l"(map), "r"(cl_bar), "r"(x), "r"(y), "r"(z) : "memory");
 }
 
 // 4D tiled load of box at (x, y, z, w) into shared memory, completing the
@@ -264,6 +286,16 @@ __device__ __forceinline__ void mma_f16_tmem_a_pair(uint32_t d_tmem, uint32_t a_
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Both operands from shared memory, each CTA holding its own 128 rows of A and
+// its half of B at the same offsets.
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 // Arrive on `bar` (same offset) in both CTAs of the pair once all previously
 // issued MMAs of this thread complete.
@@ -355,6 +387,28 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
     d |= (uint64_t)1 << 46;                        // bits 46-47: descriptor version 1
     d |= (uint64_t)2 << 61;                        // bits 61-63: 128-byte swizzle
     return d;
+}
+
+// The same for an operand whose M or N index is contiguous (MN-major): rows of
+// 64 M or N elements (128 B), one row per K, 8-row atoms of 1024 B one after
+// the other along K (SBO = 1024), the next 64 M or N elements `lbo` bytes on.
+// 16 K elements are 2048 B.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(lbo >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Instruction descriptor of tcgen05.mma kind::f16 with fp32 accumulation:
+// operand type (0 fp16, 1 bf16, the same for both), and which operands are
+// MN-major (bits 15 and 16).
+__host__ __device__ constexpr uint32_t idesc_16_f32(int M, int N, uint32_t type, bool a_mn, bool b_mn) {
+    return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16)
+         | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // Instruction descriptor of tcgen05.mma kind::f16: D fp32, A and B fp16 (format

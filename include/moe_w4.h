@@ -264,9 +264,9 @@ typedef enum {
  *                                    (zeros for an expert without rows)
  *   x, dx  device [R][K]    y, dy  device [R][N]    w, dw  device [E][N][K]
  *   offsets  device int32 [E+1], offsets[0] = 0, offsets[E] = R, non-decreasing.
- * A segment that is not inside [0, R] counts as empty and is reported as
- * MOE_ERR_DEVICE_RANGE by moe_get_device_error; rows that no segment holds
- * are not written.  1 <= E <= 1024.  R = 0: nothing to do, and zeros in dw.
+ * Offsets that decrease or leave [0, R] are reported as MOE_ERR_DEVICE_RANGE by
+ * moe_get_device_error, and the output is unspecified; rows that no segment
+ * holds are not written.  1 <= E <= 1024.  R = 0: nothing to do, and zeros in dw.
  * Workspace: >= moe_grouped_mm_workspace_size(R, E, N, K) bytes, the same for
  * the three products.
  */
