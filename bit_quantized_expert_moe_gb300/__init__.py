@@ -107,7 +107,9 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle of torch.cuda.current_stream(), without making the object:
+        # 0.2 us of host time a call instead of 3 on the GPU's Arm host
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 

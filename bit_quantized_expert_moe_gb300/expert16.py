@@ -2,7 +2,9 @@
 the gated activation with the routing weight, and the norms around a block.
 
 Argument marshalling only, as in the rest of the binding: shapes and types are
-checked here, everything else by the library.  `offsets` and `row_map` are the
+checked here, everything else by the library.  The checks are spelled out in
+place: a small call takes a few microseconds on the GPU, and helper calls on
+the host would take longer than that.  `offsets` and `row_map` are the
 `offsets` and `sorted` of permute().
 """
 from __future__ import annotations
@@ -12,6 +14,7 @@ import torch
 from . import _check, _ptr, _stream, lib, workspace
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_I32, _F32 = torch.int32, torch.float32
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -21,16 +24,8 @@ def _dtype(t: torch.Tensor) -> int:
     return d
 
 
-def _same_type(first: torch.Tensor, *others: torch.Tensor | None) -> None:
-    for t in others:
-        if t is not None and (t.dtype != first.dtype or t.device != first.device):
-            raise ValueError("tensors of one type on one device expected")
-
-
-def _want(t: torch.Tensor | None, what: str, *shape: int, dtype: torch.dtype | None = None) -> None:
-    if t is not None and (tuple(t.shape) != shape or (dtype is not None and t.dtype != dtype)):
-        raise ValueError(f"{what}: shape {shape}" + (f" of {dtype}" if dtype else "") +
-                         f" expected, not {tuple(t.shape)} of {t.dtype}")
+def _refuse(what: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype):
+    raise ValueError(f"{what}: shape {tuple(shape)} of {dtype} expected, not {tuple(t.shape)} of {t.dtype}")
 
 
 # ---------------------------------------------------------------------------
@@ -38,49 +33,54 @@ def grouped_mm_workspace_size(R: int, E: int, N: int, K: int) -> int:
     return lib().moe_grouped_mm_workspace_size(R, E, N, K)
 
 
-def _grouped(fn: str, a, b, offsets, R: int, E: int, N: int, K: int, out, ws, stream):
-    _want(offsets, "offsets", E + 1, dtype=torch.int32)
+def _grouped(fn, what: str, a, b, offsets, R: int, E: int, N: int, K: int, out, ws, stream):
+    if offsets.shape != (E + 1,) or offsets.dtype is not _I32:
+        _refuse("offsets", offsets, (E + 1,), _I32)
     if ws is None:
         ws = workspace(grouped_mm_workspace_size(R, E, N, K), offsets.device)
-    _check(getattr(lib(), fn)(_dtype(a), _ptr(a), _ptr(b), _ptr(offsets), R, E, N, K, _ptr(out), _ptr(ws), ws.numel(),
-                              _stream(stream)), fn)
+    st = fn(_dtype(a), _ptr(a), _ptr(b), _ptr(offsets), R, E, N, K, _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
+    if st:
+        _check(st, what)
     return out
 
 
 def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: torch.Tensor | None = None,
                ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y[r] = w[e] x[r] for the rows r of every expert e: x [R, K], w [E, N, K]."""
-    (R, K), (E, N, _) = x.shape, w.shape
-    _want(w, "w", E, N, K)
+    (R, K), (E, N, Kw), dt = x.shape, w.shape, x.dtype
+    if Kw != K or w.dtype is not dt:
+        _refuse("w", w, (E, N, K), dt)
     if y is None:
-        y = torch.empty((R, N), dtype=x.dtype, device=x.device)
-    _want(y, "y", R, N)
-    _same_type(x, w, y)
-    return _grouped("moe_grouped_mm", x, w, offsets, R, E, N, K, y, ws, stream)
+        y = torch.empty((R, N), dtype=dt, device=x.device)
+    elif y.shape != (R, N) or y.dtype is not dt:
+        _refuse("y", y, (R, N), dt)
+    return _grouped(lib().moe_grouped_mm, "moe_grouped_mm", x, w, offsets, R, E, N, K, y, ws, stream)
 
 
 def grouped_mm_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dx: torch.Tensor | None = None,
                   ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of grouped_mm in x: dx[r] = dy[r] w[e]."""
-    (R, N), (E, _, K) = dy.shape, w.shape
-    _want(w, "w", E, N, K)
+    (R, N), (E, Nw, K), dt = dy.shape, w.shape, dy.dtype
+    if Nw != N or w.dtype is not dt:
+        _refuse("w", w, (E, N, K), dt)
     if dx is None:
-        dx = torch.empty((R, K), dtype=dy.dtype, device=dy.device)
-    _want(dx, "dx", R, K)
-    _same_type(dy, w, dx)
-    return _grouped("moe_grouped_mm_dx", dy, w, offsets, R, E, N, K, dx, ws, stream)
+        dx = torch.empty((R, K), dtype=dt, device=dy.device)
+    elif dx.shape != (R, K) or dx.dtype is not dt:
+        _refuse("dx", dx, (R, K), dt)
+    return _grouped(lib().moe_grouped_mm_dx, "moe_grouped_mm_dx", dy, w, offsets, R, E, N, K, dx, ws, stream)
 
 
 def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, dw: torch.Tensor | None = None,
                   ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of grouped_mm in w: dw[e] = sum of dy[r]^T x[r] over the expert's rows."""
-    (R, N), K, E = dy.shape, x.shape[1], offsets.numel() - 1
-    _want(x, "x", R, K)
+    (R, N), (Rx, K), E, dt = dy.shape, x.shape, offsets.numel() - 1, dy.dtype
+    if Rx != R or x.dtype is not dt:
+        _refuse("x", x, (R, K), dt)
     if dw is None:
-        dw = torch.empty((E, N, K), dtype=dy.dtype, device=dy.device)
-    _want(dw, "dw", E, N, K)
-    _same_type(dy, x, dw)
-    return _grouped("moe_grouped_mm_dw", dy, x, offsets, R, E, N, K, dw, ws, stream)
+        dw = torch.empty((E, N, K), dtype=dt, device=dy.device)
+    elif dw.shape != (E, N, K) or dw.dtype is not dt:
+        _refuse("dw", dw, (E, N, K), dt)
+    return _grouped(lib().moe_grouped_mm_dw, "moe_grouped_mm_dw", dy, x, offsets, R, E, N, K, dw, ws, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -88,8 +88,10 @@ def _check_swiglu(gu, row_w, row_map) -> tuple[int, int]:
     R, F2 = gu.shape
     if F2 % 2:
         raise ValueError("gu holds the gate and the up half of every row")
-    _want(row_w, "row_w", R, dtype=torch.float32)
-    _want(row_map, "row_map", R, dtype=torch.int32)
+    if row_w is not None and (row_w.shape != (R,) or row_w.dtype is not _F32):
+        _refuse("row_w", row_w, (R,), _F32)
+    if row_map is not None and (row_map.shape != (R,) or row_map.dtype is not _I32):
+        _refuse("row_map", row_map, (R,), _I32)
     return R, F2 // 2
 
 
@@ -97,11 +99,14 @@ def swiglu(gu: torch.Tensor, row_w: torch.Tensor | None = None, row_map: torch.T
            h: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """h[r] = row_w[row_map[r]] SiLU(gate) up for gu [R, 2F], gate then up."""
     R, F = _check_swiglu(gu, row_w, row_map)
+    dt = gu.dtype
     if h is None:
-        h = torch.empty((R, F), dtype=gu.dtype, device=gu.device)
-    _want(h, "h", R, F, dtype=gu.dtype)
-    _check(lib().moe_swiglu(_dtype(gu), _ptr(gu), _ptr(row_w), _ptr(row_map), R, F, _ptr(h), _stream(stream)),
-           "moe_swiglu")
+        h = torch.empty((R, F), dtype=dt, device=gu.device)
+    elif h.shape != (R, F) or h.dtype is not dt:
+        _refuse("h", h, (R, F), dt)
+    st = lib().moe_swiglu(_dtype(gu), _ptr(gu), _ptr(row_w), _ptr(row_map), R, F, _ptr(h), _stream(stream))
+    if st:
+        _check(st, "moe_swiglu")
     return h
 
 
@@ -110,15 +115,22 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, row_w: torch.Tensor | No
                     drow_w: torch.Tensor | None = None, stream=None):
     """Gradients of swiglu: (dgu [R, 2F], drow_w [R] fp32, or None without row_w)."""
     R, F = _check_swiglu(gu, row_w, row_map)
-    _want(dh, "dh", R, F, dtype=gu.dtype)
+    dt = gu.dtype
+    if dh.shape != (R, F) or dh.dtype is not dt:
+        _refuse("dh", dh, (R, F), dt)
     if dgu is None:
         dgu = torch.empty_like(gu)
-    if drow_w is None and row_w is not None:
+    elif dgu.shape != gu.shape or dgu.dtype is not dt:
+        _refuse("dgu", dgu, gu.shape, dt)
+    if drow_w is not None:
+        if drow_w.shape != (R,) or drow_w.dtype is not _F32:
+            _refuse("drow_w", drow_w, (R,), _F32)
+    elif row_w is not None:
         drow_w = torch.empty_like(row_w)
-    _want(dgu, "dgu", R, 2 * F, dtype=gu.dtype)
-    _want(drow_w, "drow_w", R, dtype=torch.float32)
-    _check(lib().moe_swiglu_backward(_dtype(gu), _ptr(dh), _ptr(gu), _ptr(row_w), _ptr(row_map), R, F, _ptr(dgu),
-                                     _ptr(drow_w), _stream(stream)), "moe_swiglu_backward")
+    st = lib().moe_swiglu_backward(_dtype(gu), _ptr(dh), _ptr(gu), _ptr(row_w), _ptr(row_map), R, F, _ptr(dgu),
+                                   _ptr(drow_w), _stream(stream))
+    if st:
+        _check(st, "moe_swiglu_backward")
     return dgu, drow_w
 
 
@@ -128,18 +140,19 @@ def _norm_params(x, gamma_post, gate, gamma_pre) -> tuple[int, int, int, int]:
     T, D = x.shape
     G, given = 1, None
     if gate is not None:
+        given = gate.dtype
         G = gate.shape[0] if gate.dim() == 2 else 0
-        given = gate
-    if G < 1 or T % G:
-        raise ValueError("gate: [G, D] with G a divisor of the rows expected")
-    _want(gate, "gate", G, D)
-    _want(gamma_post, "gamma_post", D)
-    _want(gamma_pre, "gamma_pre", D)
-    for t in (gamma_post, gamma_pre):
+        if G < 1 or T % G or gate.shape[1] != D:
+            raise ValueError(f"gate: [G, {D}] with G a divisor of {T} rows expected, not {tuple(gate.shape)}")
+    for what, t in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
         if t is not None:
-            given = t if given is None else given
-            _same_type(given, t)
-    return T, D, G, _dtype(given if given is not None else x)
+            given = given or t.dtype
+            if t.shape != (D,) or t.dtype is not given:
+                _refuse(what, t, (D,), given)
+    pt = _DTYPES.get(given or x.dtype)
+    if pt is None:
+        raise ValueError(f"bfloat16, float16 or float32 parameters expected, not {given}")
+    return T, D, G, pt
 
 
 def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, gamma_post: torch.Tensor | None = None,
@@ -150,14 +163,23 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, gamma_post: torch
     Returns (x_out, h): x_out is None without y, h is None without gamma_pre.
     gamma_post None: y enters unnormalised; gate [G, D] None: 1; x_out may be x."""
     T, D, G, pt = _norm_params(x, gamma_post, gate, gamma_pre)
-    if x_out is None and y is not None:
+    shape, dt = x.shape, x.dtype
+    if y is not None and (y.shape != shape or y.dtype is not dt):
+        _refuse("y", y, shape, dt)
+    if x_out is not None:
+        if x_out.shape != shape or x_out.dtype is not dt:
+            _refuse("x_out", x_out, shape, dt)
+    elif y is not None:
         x_out = torch.empty_like(x)
-    if h is None and gamma_pre is not None:
+    if h is not None:
+        if h.shape != shape or h.dtype is not dt:
+            _refuse("h", h, shape, dt)
+    elif gamma_pre is not None:
         h = torch.empty_like(x)
-    for t, what in ((y, "y"), (x_out, "x_out"), (h, "h")):
-        _want(t, what, T, D, dtype=x.dtype)
-    _check(lib().moe_block_norm(_dtype(x), pt, T, D, G, alpha, eps, _ptr(gamma_post), _ptr(gate), _ptr(gamma_pre),
-                                _ptr(x), _ptr(y), _ptr(x_out), _ptr(h), _stream(stream)), "moe_block_norm")
+    st = lib().moe_block_norm(_dtype(x), pt, T, D, G, alpha, eps, _ptr(gamma_post), _ptr(gate), _ptr(gamma_pre),
+                              _ptr(x), _ptr(y), _ptr(x_out), _ptr(h), _stream(stream))
+    if st:
+        _check(st, "moe_block_norm")
     return x_out, h
 
 
@@ -172,15 +194,22 @@ def block_norm_backward(x_out: torch.Tensor, y: torch.Tensor | None = None, dx_o
     """Gradients of block_norm at the stored x_out (x, where there is no y):
     (dx, dy, dgamma_post, dgate, dgamma_pre), None for what was not there."""
     T, D, G, pt = _norm_params(x_out, gamma_post, gate, gamma_pre)
-    for t, what in ((y, "y"), (dx_out, "dx_out"), (dh, "dh")):
-        _want(t, what, T, D, dtype=x_out.dtype)
-    dx = torch.empty_like(x_out)
-    dy = torch.empty_like(y) if y is not None else None
-    dpost, dgate, dpre = (torch.empty_like(t) if t is not None else None for t in (gamma_post, gate, gamma_pre))
+    shape, dt = x_out.shape, x_out.dtype
+    for what, t in (("y", y), ("dx_out", dx_out), ("dh", dh)):
+        if t is not None and (t.shape != shape or t.dtype is not dt):
+            _refuse(what, t, shape, dt)
+    like = torch.empty_like
+    dx = like(x_out)
+    dy = like(y) if y is not None else None
+    dpost = like(gamma_post) if gamma_post is not None else None
+    dgate = like(gate) if gate is not None else None
+    dpre = like(gamma_pre) if gamma_pre is not None else None
     if ws is None:
         ws = workspace(block_norm_backward_workspace_size(T, D, G), x_out.device)
-    _check(lib().moe_block_norm_backward(
+    st = lib().moe_block_norm_backward(
         _dtype(x_out), pt, T, D, G, alpha, eps, _ptr(gamma_post), _ptr(gate), _ptr(gamma_pre), _ptr(x_out), _ptr(y),
         _ptr(dx_out), _ptr(dh), _ptr(dx), _ptr(dy), _ptr(dpost), _ptr(dgate), _ptr(dpre), _ptr(ws), ws.numel(),
-        _stream(stream)), "moe_block_norm_backward")
+        _stream(stream))
+    if st:
+        _check(st, "moe_block_norm_backward")
     return dx, dy, dpost, dgate, dpre
