@@ -125,7 +125,7 @@ moe_status_t moe_block_norm(moe_dtype_t dtype, moe_dtype_t param_dtype, int32_t 
 
 size_t moe_block_norm_backward_workspace_size(int32_t T, int32_t D, int32_t G) {
     if (T < 0 || D < 1 || G < 1 || T % G) return 0;
-    return WS_HEADER + block_norm_partial_floats(T, D) * sizeof(float);
+    return WS_HEADER + block_norm_partial_floats(T, D, G) * sizeof(float);
 }
 
 moe_status_t moe_block_norm_backward(moe_dtype_t dtype, moe_dtype_t param_dtype, int32_t T, int32_t D, int32_t G,

@@ -1,0 +1,335 @@
+// Gradients of the block norms (block_norm.cu), given dx' and dh, with the
+// statistics taken again from y and x':
+//   D  = dx' + r2 v - x' r2^3 mean(v x'),   v = dh gamma_pre;   dx = D
+//   q  = alpha gate gamma_post D;  dy = r1 q - y r1^3 mean(q y)
+//   dgamma_pre = sum dh x' r2,  dgate = sum alpha D n,  dgamma_post = sum alpha gate D y r1
+// x' is the stored one, the value that every later reader sees.  Each tensor is
+// read and written once: bound by memory.
+#include "block_norm.cuh"
+
+namespace moe {
+namespace norm {
+namespace {
+
+// A row group takes p.rows consecutive rows, the loads of the next SLOTS - 1
+// under way while it computes one (SLOTS = 1: none).  One reduction a row:
+// sum(q y) is taken apart into sums that do not wait for D, with
+// w = alpha gate gamma_post y:
+//   sum(q y) = sum(w dx') + r2 sum(w v) - r2^3 mean(v x') sum(w x').
+// The parameters' gradients add up in registers.  While the gate row stays the
+// same, gate and gamma_post are factors of one sum z = sum D y r1:
+// dgate = alpha gamma_post z, dgamma_post = sum over gate rows of alpha gate z.
+// A gate row that lies wholly inside the group's rows is written at once; its
+// first and last one may be shared with the neighbours and go to gate_part.
+// ALL: y, gamma_post, gamma_pre, dx' and dh are there and the rows share one gate.
+template <class T, int VPT, int SLOTS, bool ALL>
+__global__ void __launch_bounds__(512, 1) block_norm_backward_kernel(const Args p) {
+    extern __shared__ __align__(16) float smem[];
+    // the kernel that adds the blocks' sums up may take its place already
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int grp = threadIdx.x / p.threads;
+    RowGroup rg(p.threads, grp, smem + grp * RowGroup::SUM_FLOATS);
+    const int chunks = p.D / 8, n = VPT * p.threads;
+    const ParamTable table(smem + p.groups * RowGroup::SUM_FLOATS, n);
+    float* const space = smem + p.groups * RowGroup::SUM_FLOATS + 16 * n;
+    // places in a slot: x', dh, dx', y
+    ThreadRing<T, 4 * VPT, SLOTS> ring(space);
+    const float inv_d = 1.f / (float)p.D;
+    const int vb = blockIdx.x * p.groups + grp;
+    const int r_begin = min(p.T, vb * p.rows), r_end = min(p.T, r_begin + p.rows);
+    const int g_first = r_begin / p.S, g_last = (r_end - 1) / p.S;
+    const bool one_gate = p.S == p.T, row_gate = !ALL && p.gate && !one_gate;
+    constexpr size_t CH = 8 * T::BYTES;
+    const bool has_y = ALL || p.y, has_post = ALL || p.gamma_post, has_dh = ALL || p.dh, has_dx = ALL || p.dx_out;
+    const size_t row_bytes = (size_t)chunks * CH, next = CH * p.threads;
+    size_t off = row_bytes * r_begin + CH * rg.tid, foff = off;
+    int fr = r_begin;  // the next row to fetch, at foff
+    bool in[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) in[i] = i * p.threads + rg.tid < chunks;
+    auto fetch = [&]() {
+        if (fr < r_end) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (in[i]) {
+                    if (has_dh) {
+                        ring.fetch(i, at(p.x, foff + i * next));
+                        ring.fetch(VPT + i, at(p.dh, foff + i * next));
+                    }
+                    if (has_dx) ring.fetch(2 * VPT + i, at(p.dx_out, foff + i * next));
+                    if (has_y) ring.fetch(3 * VPT + i, at(p.y, foff + i * next));
+                }
+        }
+        ++fr;
+        foff += row_bytes;
+        ring.commit();
+    };
+    if (SLOTS > 1)
+#pragma unroll
+        for (int k = 0; k < SLOTS - 1; ++k) fetch();
+    table.fill(p);
+    for (int i = threadIdx.x; i < p.groups * RowGroup::SUM_FLOATS; i += blockDim.x) smem[i] = 0.f;
+    __syncthreads();
+    V8 a_post[VPT], a_pre[VPT], z[VPT];
+    V8 ka[VPT == 1 ? 1 : VPT], kb[VPT == 1 ? 1 : VPT];  // the parameters of this row: kept for VPT = 1
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) a_post[i] = a_pre[i] = z[i] = ka[i] = kb[i] = v8(0.f);
+    // A of row r's gate and B into ka, kb
+    auto params = [&](int i, int c, size_t grow) {
+        ka[i] = table.get(0, c);
+        if (row_gate) ka[i] = mul(ka[i], load8(p.ptype, p.gate, grow + c));
+        if (has_dh) kb[i] = table.get(1, c);
+    };
+    bool fresh = true;  // the row is the first of its gate here
+    for (int r = r_begin; r < r_end; ++r, off += row_bytes) {
+        const int g = ALL ? 0 : r / p.S;
+        const size_t grow = (size_t)g * chunks;
+        if (SLOTS > 1) {
+            fetch();
+            ring.wait();
+        }
+        typename T::Raw rx[VPT], rdh[VPT], rdx[VPT], ry[VPT];
+        float2 s[6];
+#pragma unroll
+        for (int k = 0; k < 6; ++k) s[k] = f2(0.f);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = i * p.threads + rg.tid;
+            rx[i] = rdh[i] = rdx[i] = ry[i] = typename T::Raw{};
+            if (in[i]) {
+                if (has_dh) {
+                    rx[i] = SLOTS > 1 ? ring.get(i) : raw_at<T>(p.x, off + i * next);
+                    rdh[i] = SLOTS > 1 ? ring.get(VPT + i) : raw_at<T>(p.dh, off + i * next);
+                }
+                if (has_dx) rdx[i] = SLOTS > 1 ? ring.get(2 * VPT + i) : raw_at<T>(p.dx_out, off + i * next);
+                if (has_y) ry[i] = SLOTS > 1 ? ring.get(3 * VPT + i) : raw_at<T>(p.y, off + i * next);
+                if (VPT > 1 || fresh) params(i, c, grow);
+                const V8 x = unpack8<T>(rx[i]), v = mul(unpack8<T>(rdh[i]), kb[i]), y = unpack8<T>(ry[i]);
+                dot(s[0], x, x);
+                dot(s[1], v, x);
+                if (has_post) {
+                    const V8 w = mul(ka[i], y);
+                    dot(s[2], y, y);
+                    dot(s[3], w, unpack8<T>(rdx[i]));
+                    dot(s[4], w, v);
+                    dot(s[5], w, x);
+                }
+            }
+        }
+        fresh = false;
+        ring.next();
+        float t[6];
+#pragma unroll
+        for (int k = 0; k < 6; ++k) t[k] = s[k].x + s[k].y;
+        rg.sum6(t);
+        const float r2 = has_dh ? rsqrtf(t[0] * inv_d + p.eps) : 0.f;
+        const float c2 = r2 * r2 * r2 * (t[1] * inv_d);
+        const float r1 = has_post ? rsqrtf(t[2] * inv_d + p.eps) : 1.f;
+        const float c1 = has_post ? r1 * r1 * r1 * ((t[3] + r2 * t[4] - c2 * t[5]) * inv_d) : 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = i * p.threads + rg.tid;
+            if (in[i]) {
+                if (VPT > 1) params(i, c, grow);
+                const V8 x = unpack8<T>(rx[i]), dh = mul(unpack8<T>(rdh[i]), r2);
+                a_pre[i] = fma(dh, x, a_pre[i]);
+                const V8 d = fma(x, -c2, fma(dh, kb[i], unpack8<T>(rdx[i])));
+                store_at<T>(p.dx, off + i * next, d);
+                if (has_y) {
+                    const V8 y = unpack8<T>(ry[i]), dr = mul(d, r1);
+                    z[i] = fma(dr, y, z[i]);
+                    store_at<T>(p.dy, off + i * next, fma(y, -c1, mul(dr, ka[i])));
+                }
+            }
+        }
+        // the gate row ends here
+        if (has_y && (r + 1 == r_end || (!ALL && r + 1 == (g + 1) * p.S))) {
+            fresh = true;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = i * p.threads + rg.tid;
+                if (c < chunks) {
+                    const V8 az = mul(z[i], p.alpha);
+                    a_post[i] = p.gate ? fma(load8(p.ptype, p.gate, grow + c), az, a_post[i]) : fma(az, 1.f, a_post[i]);
+                    const V8 w = p.gamma_post ? mul(load8(p.ptype, p.gamma_post, c), az) : az;
+                    z[i] = one_gate ? w : v8(0.f);
+                    if (p.dgate && !one_gate) {
+                        float* gp = p.gate_part + (size_t)vb * 2 * p.D;
+                        if (g == g_first) store8<F32>(gp, c, w);
+                        else if (g == g_last) store8<F32>(gp + p.D, c, w);
+                        else store8(p.ptype, p.dgate, grow + c, w);
+                    }
+                }
+            }
+        }
+    }
+
+    // the block's groups add theirs up in order and write one partial sum; the
+    // ring's space is free
+    cp_async_wait<0>();
+    for (int k = 1; k < p.groups; ++k) {
+        __syncthreads();
+        if (grp == k)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = i * p.threads + rg.tid;
+                store8<F32>(space, c, a_post[i]);
+                store8<F32>(space, n + c, a_pre[i]);
+                store8<F32>(space, 2 * n + c, z[i]);
+            }
+        __syncthreads();
+        if (grp == 0)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = i * p.threads + rg.tid;
+                a_post[i] = fma(load8<F32>(space, c), 1.f, a_post[i]);
+                a_pre[i] = fma(load8<F32>(space, n + c), 1.f, a_pre[i]);
+                z[i] = fma(load8<F32>(space, 2 * n + c), 1.f, z[i]);
+            }
+    }
+    if (grp == 0) {
+        float* const part = p.part + (size_t)blockIdx.x * 3 * p.D;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = i * p.threads + rg.tid;
+            if (c < chunks) {
+                if (p.dgamma_post) store8<F32>(part, c, a_post[i]);
+                if (p.dgamma_pre) store8<F32>(part + p.D, c, a_pre[i]);
+                if (p.dgate && one_gate) store8<F32>(part + 2 * p.D, c, z[i]);
+            }
+        }
+    }
+}
+
+// Sums the partial sums in their order.  `what`: 0 gamma_post, 1 gamma_pre,
+// 2 + g gate row g.  32 columns a block, 8 threads a column.
+__device__ __forceinline__ void reduce_one(const Args& p, int what, float (&red)[8][33]) {
+    const int col = blockIdx.x * 32 + threadIdx.x;
+    int b0 = 0, b1 = p.blocks - 1;
+    const float* src = p.part + (size_t)what * p.D + col;
+    size_t stride = (size_t)3 * p.D;
+    void* out = what == 0 ? p.dgamma_post : what == 1 ? p.dgamma_pre : p.dgate;
+    size_t at = col;
+    const int g = what - 2;
+    const bool shared_gate = what >= 2 && p.S != p.T;
+    if (shared_gate) {
+        const long long first = (long long)g * p.S;
+        b0 = (int)(first / p.rows);
+        b1 = (int)((first + p.S - 1) / p.rows);
+        const int r_end = min(p.T, (b0 + 1) * p.rows);
+        // wholly inside one row group, and neither its first nor its last gate row
+        if (b0 == b1 && b0 * p.rows / p.S != g && (r_end - 1) / p.S != g) return;
+        src = p.gate_part + col;
+        stride = (size_t)2 * p.D;
+        at += (size_t)g * p.D;
+    }
+    if (!out) return;
+    float s = 0.f;
+    if (col < p.D) {
+#pragma unroll 4
+        for (int b = b0 + threadIdx.y; b <= b1; b += 8) {
+            const float* q = src + b * stride;
+            // the gate row is the row group's first, or its last
+            if (shared_gate && b * p.rows / p.S != g) q += p.D;
+            s += *q;
+        }
+    }
+    red[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && col < p.D) {
+        for (int i = 1; i < 8; ++i) s += red[i][threadIdx.x];
+        store1(p.ptype, out, at, s);
+    }
+    __syncthreads();
+}
+
+// Launched as a programmatic dependent: it starts while the gradients' kernel
+// ends and waits for its results here.
+__global__ void __launch_bounds__(256) block_norm_reduce_kernel(const Args p, int gates) {
+    __shared__ float red[8][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int what = blockIdx.y; what < 2 + gates; what += gridDim.y) reduce_one(p, what, red);
+}
+
+// How the backward pass splits the rows: one block an SM with as many row
+// groups as 512 threads hold (15 named barriers), fewer where the rows are few.
+struct BackwardPlan {
+    int vpt, threads, groups, rows, blocks;
+};
+BackwardPlan backward_plan(int T, int D) {
+    BackwardPlan b;
+    b.vpt = chunks_per_thread(D);
+    b.threads = group_threads(D, b.vpt);
+    b.groups = std::max(1, std::min({512 / b.threads, 15, ceil_div(T, num_sms())}));
+    b.rows = std::max(1, ceil_div(T, num_sms() * b.groups));
+    b.blocks = ceil_div(ceil_div(T, b.rows), b.groups);
+    return b;
+}
+
+template <class T>
+cudaError_t run_backward(const Args& p, const BackwardPlan& b, cudaStream_t s) {
+    const int threads = b.groups * b.threads;
+    const size_t slot = (size_t)4 * b.vpt * 8 * T::BYTES * threads;
+    const size_t other = b.groups * RowGroup::SUM_FLOATS * sizeof(float) + ParamTable::bytes(b.vpt * b.threads);
+    const int slots = b.rows > 1 && b.vpt < 4 ? ring_slots(slot, other) : 1;
+    const size_t merge = b.groups > 1 ? (size_t)3 * b.vpt * b.threads * 8 * sizeof(float) : 0;
+    const size_t smem = other + std::max(slots > 1 ? slots * slot : 0, merge);
+    const bool all = p.y && p.gamma_post && p.dh && p.dx_out && p.S == p.T;
+    return with_shape(b.vpt, slots, [&](auto v, auto n) {
+        constexpr int V = decltype(v)::value, N = decltype(n)::value;
+        return all ? launch_smem(block_norm_backward_kernel<T, V, N, true>, b.blocks, threads, smem, s, p)
+                   : launch_smem(block_norm_backward_kernel<T, V, N, false>, b.blocks, threads, smem, s, p);
+    });
+}
+
+cudaError_t run_reduce(const Args& p, int gates, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ceil_div(p.D, 32), std::min(2 + gates, 1024));
+    cfg.blockDim = dim3(32, 8);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, block_norm_reduce_kernel, p, gates);
+}
+
+}  // namespace
+}  // namespace norm
+
+size_t block_norm_partial_floats(int T, int D, int G) {
+    const norm::BackwardPlan b = norm::backward_plan(T, D);
+    return (size_t)b.blocks * D * (3 + (G > 1 ? 2 * b.groups : 0));
+}
+
+cudaError_t launch_block_norm_backward(const NormShape& n, const NormGrads& g, float* part, cudaStream_t s) {
+    const norm::BackwardPlan b = norm::backward_plan(n.T, n.D);
+    norm::Args a = norm::common_args(n);
+    a.x = g.x_out;
+    a.y = g.y;
+    a.dx_out = g.dx_out;
+    a.dh = g.dh;
+    a.dx = g.dx;
+    a.dy = g.dy;
+    a.dgamma_post = g.dgamma_post;
+    a.dgate = g.dgate;
+    a.dgamma_pre = g.dgamma_pre;
+    a.threads = b.threads;
+    a.groups = b.groups;
+    a.rows = b.rows;
+    a.blocks = b.blocks;
+    a.part = part;
+    a.gate_part = part + (size_t)b.blocks * 3 * n.D;
+    cudaError_t e = n.dtype == MOE_DT_BF16  ? norm::run_backward<Bf16>(a, b, s)
+                    : n.dtype == MOE_DT_F16 ? norm::run_backward<F16>(a, b, s)
+                                            : norm::run_backward<F32>(a, b, s);
+    if (e != cudaSuccess) return e;
+    note_launch();
+    if (!g.dgamma_post && !g.dgate && !g.dgamma_pre) return e;
+    e = norm::run_reduce(a, g.dgate ? n.G : 0, s);
+    note_launch();
+    return e;
+}
+
+}  // namespace moe

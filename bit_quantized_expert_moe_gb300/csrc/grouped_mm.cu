@@ -353,9 +353,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     uint16_t* o = out + ((size_t)t.e * p.N + m) * p.K + t.c0 + 32 * cb;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        float f[8];
+                        V8 f;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[8 * j + k]);
+                        for (int k = 0; k < 4; ++k)
+                            f.p[k] = make_float2(__uint_as_float(v[8 * j + 2 * k]), __uint_as_float(v[8 * j + 2 * k + 1]));
                         if (m < M && 32 * cb + 8 * j < t.ncols) {
                             if (p.type) store8<Bf16>(o, j, f);
                             else store8<F16>(o, j, f);

@@ -150,7 +150,7 @@ struct NormGrads {
     const void *x_out, *y, *dx_out, *dh;
     void *dx, *dy, *dgamma_post, *dgate, *dgamma_pre;
 };
-size_t block_norm_partial_floats(int T, int D);  // scratch of the backward pass
+size_t block_norm_partial_floats(int T, int D, int G);  // scratch of the backward pass
 cudaError_t launch_block_norm(const NormShape& n, const void* x, const void* y, void* x_out, void* h, cudaStream_t s);
 cudaError_t launch_block_norm_backward(const NormShape& n, const NormGrads& g, float* part, cudaStream_t s);
 
@@ -171,6 +171,17 @@ bool make_tensor_map_16(CUtensorMap* m, bool bf16, const void* ptr, int rank, co
 
 // ----------------------------------------------------------- device info
 int num_sms();
+// Launches a kernel that may need more dynamic shared memory than the default
+// 48 KB.
+template <class K, class... A>
+cudaError_t launch_smem(K kernel, int blocks, int threads, size_t smem, cudaStream_t s, const A&... args) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<blocks, threads, smem, s>>>(args...);
+    return cudaGetLastError();
+}
 // Counts one kernel launch of this library (reported by moe_kernel_launches).
 void note_launch(int n = 1);
 
