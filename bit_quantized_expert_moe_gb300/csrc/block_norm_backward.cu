@@ -11,6 +11,8 @@ namespace moe {
 namespace norm {
 namespace {
 
+constexpr int BLOCK_THREADS = 512;  // most threads of a block: 128 registers each
+
 // A row group takes p.rows consecutive rows, the loads of the next SLOTS - 1
 // under way while it computes one (SLOTS = 1: none).  One reduction a row:
 // sum(q y) is taken apart into sums that do not wait for D, with
@@ -23,7 +25,7 @@ namespace {
 // first and last one may be shared with the neighbours and go to gate_part.
 // ALL: y, gamma_post, gamma_pre, dx' and dh are there and the rows share one gate.
 template <class T, int VPT, int SLOTS, bool ALL>
-__global__ void __launch_bounds__(512, 1) block_norm_backward_kernel(const Args p) {
+__global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(const Args p) {
     extern __shared__ __align__(16) float smem[];
     // the kernel that adds the blocks' sums up may take its place already
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -149,8 +151,8 @@ __global__ void __launch_bounds__(512, 1) block_norm_backward_kernel(const Args 
             for (int i = 0; i < VPT; ++i) {
                 const int c = i * p.threads + rg.tid;
                 if (c < chunks) {
-                    const V8 az = mul(z[i], p.alpha);
-                    a_post[i] = p.gate ? fma(load8(p.ptype, p.gate, grow + c), az, a_post[i]) : fma(az, 1.f, a_post[i]);
+                    const V8 az = mul(z[i], p.alpha), post = p.gate ? mul(load8(p.ptype, p.gate, grow + c), az) : az;
+                    a_post[i] = ALL ? post : fma(post, 1.f, a_post[i]);
                     const V8 w = p.gamma_post ? mul(load8(p.ptype, p.gamma_post, c), az) : az;
                     z[i] = one_gate ? w : v8(0.f);
                     if (p.dgate && !one_gate) {
@@ -201,58 +203,62 @@ __global__ void __launch_bounds__(512, 1) block_norm_backward_kernel(const Args 
     }
 }
 
-// Sums the partial sums in their order.  `what`: 0 gamma_post, 1 gamma_pre,
-// 2 + g gate row g.  32 columns a block, 8 threads a column.
-__device__ __forceinline__ void reduce_one(const Args& p, int what, float (&red)[8][33]) {
-    const int col = blockIdx.x * 32 + threadIdx.x;
-    int b0 = 0, b1 = p.blocks - 1;
-    const float* src = p.part + (size_t)what * p.D + col;
-    size_t stride = (size_t)3 * p.D;
-    void* out = what == 0 ? p.dgamma_post : what == 1 ? p.dgamma_pre : p.dgate;
-    size_t at = col;
-    const int g = what - 2;
-    const bool shared_gate = what >= 2 && p.S != p.T;
-    if (shared_gate) {
-        const long long first = (long long)g * p.S;
-        b0 = (int)(first / p.rows);
-        b1 = (int)((first + p.S - 1) / p.rows);
-        const int r_end = min(p.T, (b0 + 1) * p.rows);
-        // wholly inside one row group, and neither its first nor its last gate row
-        if (b0 == b1 && b0 * p.rows / p.S != g && (r_end - 1) / p.S != g) return;
-        src = p.gate_part + col;
-        stride = (size_t)2 * p.D;
-        at += (size_t)g * p.D;
-    }
-    if (!out) return;
-    float s = 0.f;
-    if (col < p.D) {
-#pragma unroll 4
-        for (int b = b0 + threadIdx.y; b <= b1; b += 8) {
-            const float* q = src + b * stride;
-            // the gate row is the row group's first, or its last
-            if (shared_gate && b * p.rows / p.S != g) q += p.D;
-            s += *q;
-        }
-    }
-    red[threadIdx.y][threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.y == 0 && col < p.D) {
-        for (int i = 1; i < 8; ++i) s += red[i][threadIdx.x];
-        store1(p.ptype, out, at, s);
-    }
-    __syncthreads();
-}
-
-// Launched as a programmatic dependent: it starts while the gradients' kernel
-// ends and waits for its results here.
-__global__ void __launch_bounds__(256) block_norm_reduce_kernel(const Args p, int gates) {
-    __shared__ float red[8][33];
+// Sums partial sums in their order, 32 columns a block.  gamma_post and
+// gamma_pre (and the one gate row that all rows share): 32 threads a column,
+// so that a thread's few loads are all under way at once.  A gate row of
+// several: the row groups that share it are few, 8 threads a column and four
+// gate rows a block.  Launched as a programmatic dependent: it starts beside
+// the gradients' kernel and waits for its results here.
+__global__ void __launch_bounds__(1024) block_norm_reduce_kernel(const Args p, int sums, int gates) {
+    __shared__ float red[32][33];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int what = blockIdx.y; what < 2 + gates; what += gridDim.y) reduce_one(p, what, red);
+    const int tx = threadIdx.x, ty = threadIdx.y, col = blockIdx.x * 32 + tx;
+    if ((int)blockIdx.y < sums) {
+        const int what = blockIdx.y;
+        void* out = what == 0 ? p.dgamma_post : what == 1 ? p.dgamma_pre : p.dgate;
+        if (!out) return;
+        float s = 0.f;
+        if (col < p.D) {
+            const float* src = p.part + (size_t)what * p.D + col;
+#pragma unroll 8
+            for (int b = ty; b < p.blocks; b += 32) s += src[(size_t)b * 3 * p.D];
+        }
+        red[ty][tx] = s;
+        __syncthreads();
+        float t[1] = {red[tx][ty]};  // warp ty: column ty
+        warp_sum(t);
+        if (tx == 0 && blockIdx.x * 32 + ty < p.D) store1(p.ptype, out, blockIdx.x * 32 + ty, t[0]);
+        return;
+    }
+    for (int g0 = 4 * ((int)blockIdx.y - sums); g0 < gates; g0 += 4 * ((int)gridDim.y - sums)) {
+        const int g = g0 + (ty >> 3);
+        const long long first = (long long)g * p.S;
+        const int b0 = (int)(first / p.rows), b1 = (int)((first + p.S - 1) / p.rows);
+        const int r_end = min(p.T, (b0 + 1) * p.rows);
+        // rows wholly inside one row group were written there, unless they are its first or last gate row
+        const bool todo = g < gates && col < p.D && !(b0 == b1 && b0 * p.rows / p.S != g && (r_end - 1) / p.S != g);
+        float s = 0.f;
+        if (todo)
+#pragma unroll 4
+            for (int b = b0 + (ty & 7); b <= b1; b += 8)
+                // the gate row is the row group's first, or its last
+                s += p.gate_part[((size_t)b * 2 + (b * p.rows / p.S != g)) * p.D + col];
+        red[ty][tx] = s;
+        __syncthreads();
+        if (todo && (ty & 7) == 0) {
+            for (int i = 1; i < 8; ++i) s += red[ty + i][tx];
+            store1(p.ptype, p.dgate, (size_t)g * p.D + col, s);
+        }
+        __syncthreads();
+    }
 }
 
 // How the backward pass splits the rows: one block an SM with as many row
-// groups as 512 threads hold (15 named barriers), fewer where the rows are few.
+// groups as its threads hold (15 named barriers), fewer where the rows are few.
+// 4096 x 2048: 26 us with two groups of 256 threads; 40 with three at 80
+// registers, which spill; two chunks a thread and four groups of 128 take the
+// same there and 22 instead of 14 us at 1155 x 1288, whose row groups would have
+// half the threads.
 struct BackwardPlan {
     int vpt, threads, groups, rows, blocks;
 };
@@ -260,21 +266,20 @@ BackwardPlan backward_plan(int T, int D) {
     BackwardPlan b;
     b.vpt = chunks_per_thread(D);
     b.threads = group_threads(D, b.vpt);
-    b.groups = std::max(1, std::min({512 / b.threads, 15, ceil_div(T, num_sms())}));
+    b.groups = std::max(1, std::min({BLOCK_THREADS / b.threads, 15, ceil_div(T, num_sms())}));
     b.rows = std::max(1, ceil_div(T, num_sms() * b.groups));
     b.blocks = ceil_div(ceil_div(T, b.rows), b.groups);
     return b;
 }
 
 template <class T>
-cudaError_t run_backward(const Args& p, const BackwardPlan& b, cudaStream_t s) {
+cudaError_t run_backward(const Args& p, const BackwardPlan& b, bool all, cudaStream_t s) {
     const int threads = b.groups * b.threads;
     const size_t slot = (size_t)4 * b.vpt * 8 * T::BYTES * threads;
     const size_t other = b.groups * RowGroup::SUM_FLOATS * sizeof(float) + ParamTable::bytes(b.vpt * b.threads);
     const int slots = b.rows > 1 && b.vpt < 4 ? ring_slots(slot, other) : 1;
     const size_t merge = b.groups > 1 ? (size_t)3 * b.vpt * b.threads * 8 * sizeof(float) : 0;
     const size_t smem = other + std::max(slots > 1 ? slots * slot : 0, merge);
-    const bool all = p.y && p.gamma_post && p.dh && p.dx_out && p.S == p.T;
     return with_shape(b.vpt, slots, [&](auto v, auto n) {
         constexpr int V = decltype(v)::value, N = decltype(n)::value;
         return all ? launch_smem(block_norm_backward_kernel<T, V, N, true>, b.blocks, threads, smem, s, p)
@@ -282,17 +287,19 @@ cudaError_t run_backward(const Args& p, const BackwardPlan& b, cudaStream_t s) {
     });
 }
 
-cudaError_t run_reduce(const Args& p, int gates, cudaStream_t s) {
+cudaError_t run_reduce(const Args& p, cudaStream_t s) {
+    const bool one_gate = p.S == p.T;
+    const int sums = p.dgate && one_gate ? 3 : 2, gates = p.dgate && !one_gate ? p.T / p.S : 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ceil_div(p.D, 32), std::min(2 + gates, 1024));
-    cfg.blockDim = dim3(32, 8);
+    cfg.gridDim = dim3(ceil_div(p.D, 32), sums + std::min(ceil_div(gates, 4), 1024));
+    cfg.blockDim = dim3(32, 32);
     cfg.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, block_norm_reduce_kernel, p, gates);
+    return cudaLaunchKernelEx(&cfg, block_norm_reduce_kernel, p, sums, gates);
 }
 
 }  // namespace
@@ -304,6 +311,7 @@ size_t block_norm_partial_floats(int T, int D, int G) {
 }
 
 cudaError_t launch_block_norm_backward(const NormShape& n, const NormGrads& g, float* part, cudaStream_t s) {
+    const bool all = g.y && n.gamma_post && g.dh && g.dx_out && n.G == 1;
     const norm::BackwardPlan b = norm::backward_plan(n.T, n.D);
     norm::Args a = norm::common_args(n);
     a.x = g.x_out;
@@ -321,13 +329,13 @@ cudaError_t launch_block_norm_backward(const NormShape& n, const NormGrads& g, f
     a.blocks = b.blocks;
     a.part = part;
     a.gate_part = part + (size_t)b.blocks * 3 * n.D;
-    cudaError_t e = n.dtype == MOE_DT_BF16  ? norm::run_backward<Bf16>(a, b, s)
-                    : n.dtype == MOE_DT_F16 ? norm::run_backward<F16>(a, b, s)
-                                            : norm::run_backward<F32>(a, b, s);
+    cudaError_t e = n.dtype == MOE_DT_BF16  ? norm::run_backward<Bf16>(a, b, all, s)
+                    : n.dtype == MOE_DT_F16 ? norm::run_backward<F16>(a, b, all, s)
+                                            : norm::run_backward<F32>(a, b, all, s);
     if (e != cudaSuccess) return e;
     note_launch();
     if (!g.dgamma_post && !g.dgate && !g.dgamma_pre) return e;
-    e = norm::run_reduce(a, g.dgate ? n.G : 0, s);
+    e = norm::run_reduce(a, s);
     note_launch();
     return e;
 }
