@@ -86,31 +86,33 @@ struct Item {
     int l0, nl;    // the summed index: first (DW: row) and how many
 };
 
-template <Product PR>
+// NP pairs of a cluster take neighbouring blocks of 256 A rows and the same columns.
+template <Product PR, int NP>
 struct Work {
-    int mb;     // blocks of 256 A rows
+    int mb;     // blocks of NP x 256 A rows
     int cb;     // DW: blocks of 256 columns
     int items;
     const int* tile_pre;  // row tiles before each expert, [E + 1]; the last < 0: bad offsets
 
     __device__ Work(const GroupedParams& p, const int* pre) : tile_pre(pre) {
-        mb = ceil_div(PR == Product::DX ? p.K : p.N, 2 * BM);
+        mb = ceil_div(PR == Product::DX ? p.K : p.N, NP * 2 * BM);
         cb = ceil_div(p.K, BN);
         items = pre[p.E] < 0 ? 0 : PR == Product::DW ? p.E * mb * cb : pre[p.E] * mb;
     }
-    __device__ Item item(const GroupedParams& p, int i) const {
+    // Item i, for pair `q` of the cluster.
+    __device__ Item item(const GroupedParams& p, int i, int q) const {
         Item t;
         if (PR == Product::DW) {
             const int per = mb * cb;
             t.e = i / per;
             i -= t.e * per;
-            t.m0 = i / cb * 2 * BM;
+            t.m0 = (i / cb * NP + q) * 2 * BM;
             t.c0 = i % cb * BN;
             t.ncols = min(BN, p.K - t.c0);
             segment(p, t.e, t.l0, t.nl);
         } else {
             const int tile = i / mb;
-            t.m0 = (i - tile * mb) * 2 * BM;
+            t.m0 = ((i - tile * mb) * NP + q) * 2 * BM;
             // the expert whose row tiles include `tile`
             int lo = 0, hi = p.E - 1;
             while (lo < hi) {
@@ -136,14 +138,16 @@ struct Work {
 
 __device__ __forceinline__ int mma_cols(const Item& t) { return (t.ncols + 15) & ~15; }
 
-// Boxes of B rows (Y, DX): a CTA's half of a tile is 8 .. 128 rows.
-constexpr int BOX_S = 16, BOX_M = 64, BOX_L = 128;
+// Boxes of B rows (Y, DX): a CTA's half of a tile is 8 .. 128 rows.  Map i has
+// boxes of (i + 1) 16 / NP rows; the NP CTAs with the same half bring a box each.
+constexpr int BOXES = 8;
+struct Maps {
+    CUtensorMap a, b[BOXES];
+};
 
-template <Product PR>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    grouped_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ CUtensorMap map_b_m, const __grid_constant__ CUtensorMap map_b_s,
-                      const GroupedParams p) {
+template <Product PR, int NP>
+__global__ void __launch_bounds__(THREADS, 1)
+    grouped_tc_kernel(const __grid_constant__ Maps maps, const GroupedParams p) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -156,13 +160,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int* tile_pre = reinterpret_cast<int*>(gbase + STAGES * STAGE_BYTES + BAR_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = tc::cluster_ctarank();
-    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const uint32_t crank = tc::cluster_ctarank();          // in the cluster of NP pairs
+    const uint32_t rank = crank & 1, lead = crank & ~1u;   // in the pair; the pair's even CTA
+    const int q_pair = (int)(crank >> 1);
+    const int cluster = blockIdx.x / (2 * NP), clusters = gridDim.x / (2 * NP);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             tc::mbar_init(bar_full + 8 * s, 1);
-            tc::mbar_init(bar_empty + 8 * s, 1);
+            tc::mbar_init(bar_empty + 8 * s, NP);
             tc::mbar_init(bar_ready + 8 * s, 2);
         }
         for (int b = 0; b < 2; ++b) {
@@ -171,8 +177,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         *abort_flag = 0;
         tc::fence_mbar_init();
-        tc::tma_prefetch_desc(&map_a);
-        tc::tma_prefetch_desc(&map_b);
+        tc::tma_prefetch_desc(&maps.a);
     }
     if (warp == 1) {
         tc::tmem_alloc_pair(smem_u32((const void*)tmem_slot), TMEM_COLS);
@@ -211,24 +216,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc::cluster_sync();
     tc::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const Work<PR> work(p, tile_pre);
+    const Work<PR, NP> work(p, tile_pre);
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
-            const uint32_t full_lead = tc::mapa_shared(bar_full, 0);
+            const uint32_t full_lead = tc::mapa_shared(bar_full, lead);
+            const uint16_t same_half = (uint16_t)(NP == 1 ? 1u << crank : 5u << rank);  // CTAs with this half of B
             int g = 0;  // stages issued so far
             bool ok = true;
-            for (int i = pair; ok && i < work.items; i += npairs) {
-                const Item t = work.item(p, i);
+            for (int i = cluster; ok && i < work.items; i += clusters) {
+                const Item t = work.item(p, i, q_pair);
                 const int half = mma_cols(t) >> 1;
-                const int box = half <= BOX_S ? BOX_S : half <= BOX_M ? BOX_M : BOX_L;
-                const CUtensorMap* mb = half <= BOX_S ? &map_b_s : half <= BOX_M ? &map_b_m : &map_b;
-                const uint32_t bytes = PR == Product::DW ? STAGE_BYTES : 2 * (A_BYTES + (uint32_t)box * BL * 2);
+                const int bi = PR == Product::DW ? 0 : (half + 15) / 16 - 1, box = (bi + 1) * 16 / NP;
+                const CUtensorMap* mb = &maps.b[bi];
+                const uint32_t bytes = PR == Product::DW ? STAGE_BYTES : 2 * (A_BYTES + (uint32_t)(NP * box) * BL * 2);
                 const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
                 for (int l = 0; l < t.nl; l += BL, ++g) {
                     const int s = g % STAGES;
-                    if (!tc::mbar_wait(bar_empty + 8 * s, ((uint32_t)(g / STAGES) & 1u) ^ 1u, abort_flag, p.err)) {
+                    // every pair of the cluster has read the stage
+                    if (!tc::mbar_wait_cluster(bar_empty + 8 * s, ((uint32_t)(g / STAGES) & 1u) ^ 1u, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
@@ -236,71 +243,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     const uint32_t fl = full_lead + 8 * s, f = bar_full + 8 * s;
                     if (PR == Product::DW) {
                         tc::mbar_arrive_expect_tx(f, bytes);
-                        tc::tma_load_2d(sa, &map_a, f, m, t.l0 + l);
-                        tc::tma_load_2d(sa + ATOM64, &map_a, f, m + 64, t.l0 + l);
-                        tc::tma_load_2d(sb, &map_b, f, c, t.l0 + l);
-                        tc::tma_load_2d(sb + ATOM64, &map_b, f, c + 64, t.l0 + l);
+                        tc::tma_load_2d(sa, &maps.a, f, m, t.l0 + l);
+                        tc::tma_load_2d(sa + ATOM64, &maps.a, f, m + 64, t.l0 + l);
+                        if (NP == 1) {
+                            tc::tma_load_2d(sb, mb, f, c, t.l0 + l);
+                            tc::tma_load_2d(sb + ATOM64, mb, f, c + 64, t.l0 + l);
+                        } else {
+                            tc::tma_load_2d_multicast(sb + q_pair * ATOM64, mb, f, c + 64 * q_pair, t.l0 + l, same_half);
+                        }
                     } else {
                         if (rank == 0) tc::mbar_arrive_expect_tx(f, bytes);
                         if (PR == Product::Y) {
-                            tc::tma_load_3d_pair(sa, &map_a, fl, l, m, t.e);
+                            tc::tma_load_3d_pair(sa, &maps.a, fl, l, m, t.e);
                         } else {
-                            tc::tma_load_3d_pair(sa, &map_a, fl, m, l, t.e);
-                            tc::tma_load_3d_pair(sa + ATOM64, &map_a, fl, m + 64, l, t.e);
+                            tc::tma_load_3d_pair(sa, &maps.a, fl, m, l, t.e);
+                            tc::tma_load_3d_pair(sa + ATOM64, &maps.a, fl, m + 64, l, t.e);
                         }
-                        tc::tma_load_2d_pair(sb, mb, fl, l, c);
+                        if (NP == 1) tc::tma_load_2d_pair(sb, mb, fl, l, c);
+                        else tc::tma_load_2d_multicast_pair(sb + q_pair * box * BL * 2, mb, fl, l, c + q_pair * box, same_half);
                     }
                 }
             }
             // the MMAs have read every stage, so every copy has landed
             for (int k = max(0, g - STAGES); ok && k < g; ++k)
-                ok = tc::mbar_wait(bar_empty + 8 * (k % STAGES), (uint32_t)(k / STAGES) & 1u, abort_flag, p.err);
+                ok = tc::mbar_wait_cluster(bar_empty + 8 * (k % STAGES), (uint32_t)(k / STAGES) & 1u, abort_flag, p.err);
         }
     } else if (warp == 1) {
         // -------------------------------------- MMA issuer (even CTA of the pair)
-        if (lane == 0 && rank == 0) {
-            int g = 0, ic = 0;
+        // The whole warp follows the pipeline, one elected lane issues.
+        if (rank == 0) {
+            const uint16_t all = (uint16_t)((1u << (2 * NP)) - 1), own = (uint16_t)(3u << lead);
+            const uint32_t in = PR == Product::DW ? bar_ready : bar_full;
+            int s = 0, ic = 0;
+            uint32_t phase = 0;
             bool ok = true;
-            for (int i = pair; ok && i < work.items; i += npairs) {
-                const Item t = work.item(p, i);
+            for (int i = cluster; ok && i < work.items; i += clusters) {
+                const Item t = work.item(p, i, q_pair);
                 if (t.nl == 0) continue;
                 const uint32_t idesc = tc::idesc_16_f32(2 * BM, mma_cols(t), p.type, PR != Product::Y, PR == Product::DW);
                 const int b = ic & 1;
                 // both CTAs' epilogues have read the accumulator
-                if (!tc::mbar_wait_cluster(bar_accempty + 8 * b, ((uint32_t)(ic >> 1) & 1u) ^ 1u, abort_flag, p.err)) break;
+                ok = tc::mbar_wait_cluster(bar_accempty + 8 * b, ((uint32_t)(ic >> 1) & 1u) ^ 1u, abort_flag, p.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 tc::tc_fence_after();
                 const uint32_t d = tmem_base + 256u * b;
-                for (int l = 0; l < t.nl; l += BL, ++g) {
-                    const int s = g % STAGES;
-                    const uint32_t in = (PR == Product::DW ? bar_ready : bar_full) + 8 * s;
-                    if (!tc::mbar_wait_cluster(in, (uint32_t)(g / STAGES) & 1u, abort_flag, p.err)) {
-                        ok = false;
-                        break;
-                    }
+                for (int l = 0; l < t.nl; l += BL) {
+                    ok = tc::mbar_wait_cluster(in + 8 * s, phase, abort_flag, p.err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                     tc::tc_fence_after();
                     const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
-                    const int steps = min(BL, t.nl - l + 15) >> 4;
-                    for (int k = 0; k < steps; ++k) {
-                        const uint64_t da = PR == Product::Y ? tc::sw128_kmajor_desc(sa + 32 * k)
-                                                             : tc::sw128_mnmajor_desc(sa + 2048 * k, ATOM64);
-                        const uint64_t db = PR == Product::DW ? tc::sw128_mnmajor_desc(sb + 2048 * k, ATOM64)
-                                                              : tc::sw128_kmajor_desc(sb + 32 * k);
-                        tc::mma_f16_pair(d, da, db, idesc, l + k > 0);
+                    constexpr uint32_t SA = PR == Product::Y ? 32 : 2048, SB = PR == Product::DW ? 2048 : 32;
+                    const uint64_t da = PR == Product::Y ? tc::sw128_kmajor_desc(sa) : tc::sw128_mnmajor_desc(sa, ATOM64);
+                    const uint64_t db = PR == Product::DW ? tc::sw128_mnmajor_desc(sb, ATOM64) : tc::sw128_kmajor_desc(sb);
+                    const int left = t.nl - l;
+                    if (tc::elect_one()) {
+                        // 16 l further: the start address, in units of 16 bytes
+#pragma unroll
+                        for (int k = 0; k < BL / 16; ++k)
+                            if (k == 0 || 16 * k < left)
+                                tc::mma_f16_pair(d, da + k * (SA >> 4), db + k * (SB >> 4), idesc, k > 0 || l > 0);
+                        tc::mma_commit_pair_to(bar_empty + 8 * s, all);
+                        if (left <= BL) tc::mma_commit_pair_to(bar_accfull + 8 * b, own);
                     }
-                    tc::mma_commit_pair(bar_empty + 8 * s);
+                    __syncwarp();
+                    if (++s == STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
-                if (!ok) break;
-                tc::mma_commit_pair(bar_accfull + 8 * b);
                 ++ic;
             }
         }
     } else if (warp == 2 && PR == Product::DW) {
         // ------------------------------------------------------------- relay
-        const uint32_t ready_lead = tc::mapa_shared(bar_ready, 0);
+        const uint32_t ready_lead = tc::mapa_shared(bar_ready, lead);
         int g = 0;
         bool ok = true;
-        for (int i = pair; ok && i < work.items; i += npairs) {
-            const Item t = work.item(p, i);
+        for (int i = cluster; ok && i < work.items; i += clusters) {
+            const Item t = work.item(p, i, q_pair);
             for (int l = 0; l < t.nl; l += BL, ++g) {
                 const int s = g % STAGES;
                 ok = tc::mbar_wait(bar_full + 8 * s, (uint32_t)(g / STAGES) & 1u, abort_flag, p.err);
@@ -325,13 +347,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else if (warp >= EP_WARP0) {
         // ---------------------------------------------------------- epilogue
         const int q = warp & 3, eh = (warp - EP_WARP0) >> 2;
-        const uint32_t accempty_lead = tc::mapa_shared(bar_accempty, 0);
+        const uint32_t accempty_lead = tc::mapa_shared(bar_accempty, lead);
         const uint32_t t_lane = (uint32_t)(32 * q) << 16;
         const int M = PR == Product::DX ? p.K : p.N;
         uint16_t* const out = static_cast<uint16_t*>(p.out);
         int ic = 0;
-        for (int i = pair; i < work.items; i += npairs) {
-            const Item t = work.item(p, i);
+        for (int i = cluster; i < work.items; i += clusters) {
+            const Item t = work.item(p, i, q_pair);
             const int m = t.m0 + (int)rank * BM + 32 * q + lane;  // this thread's A row
             const int b = ic & 1;
             if (t.nl > 0) {
@@ -412,44 +434,55 @@ bool map_w(CUtensorMap* m, bool bf16, const void* ptr, const GroupedShape& g, in
     return make_tensor_map_16(m, bf16, ptr, 3, dims, strides, box);
 }
 
-template <Product PR>
-cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
+template <Product PR, int NP>
+cudaError_t launch_np(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
     const bool bf = g.dtype == MOE_DT_BF16;
-    CUtensorMap ma, mb, mb_m, mb_s;
+    Maps maps;
     bool ok;
     int max_items;
     if (PR == Product::DW) {
-        ok = map_2d(&ma, bf, a, g.N, g.R, 64, 64) && map_2d(&mb, bf, b, g.K, g.R, 64, 64);
-        mb_m = mb_s = mb;
-        max_items = g.E * ceil_div(g.N, 2 * BM) * ceil_div(g.K, BN);
+        ok = map_2d(&maps.a, bf, a, g.N, g.R, 64, 64) && map_2d(&maps.b[0], bf, b, g.K, g.R, 64, 64);
+        max_items = g.E * ceil_div(g.N, NP * 2 * BM) * ceil_div(g.K, BN);
     } else {
         const int L = PR == Product::Y ? g.K : g.N, M = PR == Product::Y ? g.N : g.K;
-        ok = map_w(&ma, bf, a, g, PR == Product::Y ? BM : 64) && map_2d(&mb, bf, b, L, g.R, 64, BOX_L) &&
-             map_2d(&mb_m, bf, b, L, g.R, 64, BOX_M) && map_2d(&mb_s, bf, b, L, g.R, 64, BOX_S);
-        max_items = (g.R / BN + std::min(g.R, g.E)) * ceil_div(M, 2 * BM);
+        ok = map_w(&maps.a, bf, a, g, PR == Product::Y ? BM : 64);
+        for (int i = 0; i < BOXES && ok; ++i) ok = map_2d(&maps.b[i], bf, b, L, g.R, 64, (i + 1) * 16 / NP);
+        max_items = (g.R / BN + std::min(g.R, g.E)) * ceil_div(M, NP * 2 * BM);
     }
     if (!ok) return cudaErrorInvalidValue;
-    static int max_pairs = 0;  // CTA pairs that the GPU holds at once
-    if (max_pairs == 0) {
-        cudaError_t e = cudaFuncSetAttribute(grouped_tc_kernel<PR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {2 * NP, 1, 1};
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    static int max_clusters = 0;  // that the GPU holds at once
+    if (max_clusters == 0) {
+        cudaError_t e = cudaFuncSetAttribute(grouped_tc_kernel<PR, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)SMEM_LIMIT);
         if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
-        cfg.blockDim = dim3(THREADS);
+        cfg.gridDim = dim3((unsigned)(num_sms() / (2 * NP) * (2 * NP)));
         cfg.dynamicSmemBytes = smem_bytes(1024);
         int nc = 0;
-        if (cudaOccupancyMaxActiveClusters(&nc, grouped_tc_kernel<PR>, &cfg) != cudaSuccess || nc < 1) {
+        if (cudaOccupancyMaxActiveClusters(&nc, grouped_tc_kernel<PR, NP>, &cfg) != cudaSuccess || nc < 1) {
             (void)cudaGetLastError();
-            nc = num_sms() / 2;
+            nc = num_sms() / (2 * NP);
         }
-        max_pairs = std::max(1, nc);
+        max_clusters = std::max(1, nc);
     }
     const GroupedParams p{g.R, g.E, g.N, g.K, g.offsets, out, bf ? 1u : 0u, g.err};
-    const int grid = 2 * std::max(1, std::min(max_pairs, max_items));
-    grouped_tc_kernel<PR><<<grid, THREADS, smem_bytes(g.E), s>>>(ma, mb, mb_m, mb_s, p);
-    note_launch();
-    return cudaGetLastError();
+    cfg.gridDim = dim3(2 * NP * std::max(1, std::min(max_clusters, max_items)));
+    cfg.dynamicSmemBytes = smem_bytes(g.E);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, grouped_tc_kernel<PR, NP>, maps, p);
+    if (e == cudaSuccess) note_launch();
+    return e;
+}
+
+template <Product PR>
+cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
+    return launch_np<PR, 1>(g, a, b, out, s);
 }
 
 }  // namespace

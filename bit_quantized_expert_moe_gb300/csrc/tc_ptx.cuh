@@ -169,6 +169,16 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     }
 }
 
+// True in one lane of a converged warp.  Unlike a test of the lane number it
+// tells the compiler that one thread alone is active, so the operands of the
+// tensor-core instructions go to uniform registers directly: 4 MMAs take about
+// 60 cycles to issue instead of 320.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ----------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
@@ -210,6 +220,25 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
         " [%0], [%1, {%3, %4, %5}], [%2];"
         :: "r"(dst), "l"(map), "r"(cl_bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+// Loads that land at the same offsets in every CTA of `mask` (cluster ranks).
+// The bytes count on the mbarrier at bar's offset in each of them; the _pair
+// form counts them on the barriers of those CTAs' pair members of the parity of
+// the CTA that cl_bar lies in (its even member, for an address there).
+__device__ __forceinline__ void tma_load_2d_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                                      int32_t y, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        " [%0], [%1, {%3, %4}], [%2], %5;"
+        :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "h"(mask) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_multicast_pair(uint32_t dst, const CUtensorMap* map, uint32_t cl_bar,
+                                                           int32_t x, int32_t y, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2], %5;"
+        :: "r"(dst), "l"(map), "r"(cl_bar), "r"(x), "r"(y), "h"(mask) : "memory");
 }
 
 // 4D tiled load of box at (x, y, z, w) into shared memory, completing the
@@ -304,6 +333,13 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
         "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
         :: "r"(bar) : "memory");
+}
+
+// The same with the CTAs to be signalled given by their cluster ranks.
+__device__ __forceinline__ void mma_commit_pair_to(uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        :: "r"(bar), "h"(mask) : "memory");
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, 16-bit inputs, fp32 accumulation.
