@@ -36,7 +36,6 @@
 // sets the error word and every role leaves its loop.
 #include "internal.h"
 #include "tc_ptx.cuh"
-#include "vec8.cuh"
 
 namespace moe {
 namespace {
@@ -50,16 +49,23 @@ constexpr int A_BYTES = BM * BL * 2;
 constexpr int B_BYTES = BN / 2 * BL * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int ATOM64 = 64 * BL * 2;  // MN-major: 64 l rows of 64 elements
-constexpr int STAGES = 6;
+// Ring stages; DW gives one up for the blocks that its epilogue stores.
+template <Product PR>
+constexpr int STAGES_OF = PR == Product::DW ? 5 : 6;
+constexpr int MAX_STAGES = 6;
+constexpr int OUT_BYTES = 32 * 128;  // DW: an epilogue warp's 32 rows x 64 columns
 constexpr int THREADS = 384;
 constexpr int EP_WARP0 = 4, EP_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 512;  // two accumulators of 256 columns
-constexpr int NBAR = 3 * STAGES + 4;
+constexpr int NBAR = 3 * MAX_STAGES + 4;
 constexpr size_t BAR_BYTES = 256;
 constexpr size_t SMEM_LIMIT = 232448;
 static_assert(8 * NBAR + 8 <= BAR_BYTES, "barrier area too small");
 
-size_t smem_bytes(int E) { return 1024 + (size_t)STAGES * STAGE_BYTES + BAR_BYTES + 4 * ((size_t)E + 1); }
+template <Product PR>
+constexpr int RING_BYTES = STAGES_OF<PR> * STAGE_BYTES + (PR == Product::DW ? EP_WARPS * OUT_BYTES : 0);
+template <Product PR>
+size_t smem_bytes(int E) { return 1024 + (size_t)RING_BYTES<PR> + BAR_BYTES + 4 * ((size_t)E + 1); }
 
 struct GroupedParams {
     int R, E, N, K;
@@ -86,33 +92,31 @@ struct Item {
     int l0, nl;    // the summed index: first (DW: row) and how many
 };
 
-// NP pairs of a cluster take neighbouring blocks of 256 A rows and the same columns.
-template <Product PR, int NP>
+template <Product PR>
 struct Work {
-    int mb;     // blocks of NP x 256 A rows
+    int mb;     // blocks of 256 A rows
     int cb;     // DW: blocks of 256 columns
     int items;
     const int* tile_pre;  // row tiles before each expert, [E + 1]; the last < 0: bad offsets
 
     __device__ Work(const GroupedParams& p, const int* pre) : tile_pre(pre) {
-        mb = ceil_div(PR == Product::DX ? p.K : p.N, NP * 2 * BM);
+        mb = ceil_div(PR == Product::DX ? p.K : p.N, 2 * BM);
         cb = ceil_div(p.K, BN);
         items = pre[p.E] < 0 ? 0 : PR == Product::DW ? p.E * mb * cb : pre[p.E] * mb;
     }
-    // Item i, for pair `q` of the cluster.
-    __device__ Item item(const GroupedParams& p, int i, int q) const {
+    __device__ Item item(const GroupedParams& p, int i) const {
         Item t;
         if (PR == Product::DW) {
             const int per = mb * cb;
             t.e = i / per;
             i -= t.e * per;
-            t.m0 = (i / cb * NP + q) * 2 * BM;
+            t.m0 = i / cb * 2 * BM;
             t.c0 = i % cb * BN;
             t.ncols = min(BN, p.K - t.c0);
             segment(p, t.e, t.l0, t.nl);
         } else {
             const int tile = i / mb;
-            t.m0 = ((i - tile * mb) * NP + q) * 2 * BM;
+            t.m0 = (i - tile * mb) * 2 * BM;
             // the expert whose row tiles include `tile`
             int lo = 0, hi = p.E - 1;
             while (lo < hi) {
@@ -138,37 +142,36 @@ struct Work {
 
 __device__ __forceinline__ int mma_cols(const Item& t) { return (t.ncols + 15) & ~15; }
 
-// Boxes of B rows (Y, DX): a CTA's half of a tile is 8 .. 128 rows.  Map i has
-// boxes of (i + 1) 16 / NP rows; the NP CTAs with the same half bring a box each.
+// Boxes of B rows (Y, DX): a CTA's half of a tile is 8 .. 128 rows; map i has
+// boxes of 16 (i + 1) rows.
 constexpr int BOXES = 8;
 struct Maps {
-    CUtensorMap a, b[BOXES];
+    CUtensorMap a, b[BOXES];  // DW: b[0], and b[1] the output
 };
 
-template <Product PR, int NP>
-__global__ void __launch_bounds__(THREADS, 1)
+template <Product PR>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     grouped_tc_kernel(const __grid_constant__ Maps maps, const GroupedParams p) {
+    constexpr int STAGES = STAGES_OF<PR>;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* gbase = smem_raw + (base - raw);
-    const uint32_t bars = base + STAGES * STAGE_BYTES;
+    const uint32_t bars = base + RING_BYTES<PR>;
     const uint32_t bar_full = bars, bar_empty = bars + 8 * STAGES, bar_ready = bars + 16 * STAGES;
     const uint32_t bar_accfull = bars + 24 * STAGES, bar_accempty = bar_accfull + 16;
-    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + STAGES * STAGE_BYTES + 8 * NBAR);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + RING_BYTES<PR> + 8 * NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* tile_pre = reinterpret_cast<int*>(gbase + STAGES * STAGE_BYTES + BAR_BYTES);
+    int* tile_pre = reinterpret_cast<int*>(gbase + RING_BYTES<PR> + BAR_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t crank = tc::cluster_ctarank();          // in the cluster of NP pairs
-    const uint32_t rank = crank & 1, lead = crank & ~1u;   // in the pair; the pair's even CTA
-    const int q_pair = (int)(crank >> 1);
-    const int cluster = blockIdx.x / (2 * NP), clusters = gridDim.x / (2 * NP);
+    const uint32_t rank = tc::cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             tc::mbar_init(bar_full + 8 * s, 1);
-            tc::mbar_init(bar_empty + 8 * s, NP);
+            tc::mbar_init(bar_empty + 8 * s, 1);
             tc::mbar_init(bar_ready + 8 * s, 2);
         }
         for (int b = 0; b < 2; ++b) {
@@ -216,41 +219,35 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::cluster_sync();
     tc::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const Work<PR, NP> work(p, tile_pre);
+    const Work<PR> work(p, tile_pre);
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            const uint32_t full_lead = tc::mapa_shared(bar_full, lead);
-            const uint16_t same_half = (uint16_t)(NP == 1 ? 1u << crank : 5u << rank);  // CTAs with this half of B
-            int g = 0;  // stages issued so far
-            bool ok = true;
-            for (int i = cluster; ok && i < work.items; i += clusters) {
-                const Item t = work.item(p, i, q_pair);
-                const int half = mma_cols(t) >> 1;
-                const int bi = PR == Product::DW ? 0 : (half + 15) / 16 - 1, box = (bi + 1) * 16 / NP;
-                const CUtensorMap* mb = &maps.b[bi];
-                const uint32_t bytes = PR == Product::DW ? STAGE_BYTES : 2 * (A_BYTES + (uint32_t)(NP * box) * BL * 2);
-                const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
-                for (int l = 0; l < t.nl; l += BL, ++g) {
-                    const int s = g % STAGES;
-                    // every pair of the cluster has read the stage
-                    if (!tc::mbar_wait_cluster(bar_empty + 8 * s, ((uint32_t)(g / STAGES) & 1u) ^ 1u, abort_flag, p.err)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
-                    const uint32_t fl = full_lead + 8 * s, f = bar_full + 8 * s;
+        // The whole warp follows the pipeline, one elected lane issues.
+        const uint32_t full_lead = tc::mapa_shared(bar_full, 0);
+        int s = 0, g = 0;  // stage, stages issued so far
+        uint32_t phase = 1;
+        bool ok = true;
+        for (int i = pair; ok && i < work.items; i += npairs) {
+            const Item t = work.item(p, i);
+            const int half = mma_cols(t) >> 1;
+            const int bi = PR == Product::DW ? 0 : (half + 15) / 16 - 1, box = (bi + 1) * 16;
+            const CUtensorMap* mb = &maps.b[bi];
+            const uint32_t bytes = PR == Product::DW ? STAGE_BYTES : 2 * (A_BYTES + (uint32_t)box * BL * 2);
+            const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
+            for (int l = 0; l < t.nl; l += BL, ++g) {
+                ok = tc::mbar_wait(bar_empty + 8 * s, phase, abort_flag, p.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
+                const uint32_t fl = full_lead + 8 * s, f = bar_full + 8 * s;
+                if (tc::elect_one()) {
                     if (PR == Product::DW) {
                         tc::mbar_arrive_expect_tx(f, bytes);
                         tc::tma_load_2d(sa, &maps.a, f, m, t.l0 + l);
                         tc::tma_load_2d(sa + ATOM64, &maps.a, f, m + 64, t.l0 + l);
-                        if (NP == 1) {
-                            tc::tma_load_2d(sb, mb, f, c, t.l0 + l);
-                            tc::tma_load_2d(sb + ATOM64, mb, f, c + 64, t.l0 + l);
-                        } else {
-                            tc::tma_load_2d_multicast(sb + q_pair * ATOM64, mb, f, c + 64 * q_pair, t.l0 + l, same_half);
-                        }
+                        tc::tma_load_2d(sb, mb, f, c, t.l0 + l);
+                        tc::tma_load_2d(sb + ATOM64, mb, f, c + 64, t.l0 + l);
                     } else {
                         if (rank == 0) tc::mbar_arrive_expect_tx(f, bytes);
                         if (PR == Product::Y) {
@@ -259,26 +256,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                             tc::tma_load_3d_pair(sa, &maps.a, fl, m, l, t.e);
                             tc::tma_load_3d_pair(sa + ATOM64, &maps.a, fl, m + 64, l, t.e);
                         }
-                        if (NP == 1) tc::tma_load_2d_pair(sb, mb, fl, l, c);
-                        else tc::tma_load_2d_multicast_pair(sb + q_pair * box * BL * 2, mb, fl, l, c + q_pair * box, same_half);
+                        tc::tma_load_2d_pair(sb, mb, fl, l, c);
                     }
                 }
+                __syncwarp();
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
-            // the MMAs have read every stage, so every copy has landed
-            for (int k = max(0, g - STAGES); ok && k < g; ++k)
-                ok = tc::mbar_wait_cluster(bar_empty + 8 * (k % STAGES), (uint32_t)(k / STAGES) & 1u, abort_flag, p.err);
         }
+        // the MMAs have read every stage, so every copy has landed
+        for (int k = max(0, g - STAGES); ok && k < g; ++k)
+            ok = tc::mbar_wait(bar_empty + 8 * (k % STAGES), (uint32_t)(k / STAGES) & 1u, abort_flag, p.err);
     } else if (warp == 1) {
         // -------------------------------------- MMA issuer (even CTA of the pair)
         // The whole warp follows the pipeline, one elected lane issues.
         if (rank == 0) {
-            const uint16_t all = (uint16_t)((1u << (2 * NP)) - 1), own = (uint16_t)(3u << lead);
             const uint32_t in = PR == Product::DW ? bar_ready : bar_full;
             int s = 0, ic = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int i = cluster; ok && i < work.items; i += clusters) {
-                const Item t = work.item(p, i, q_pair);
+            for (int i = pair; ok && i < work.items; i += npairs) {
+                const Item t = work.item(p, i);
                 if (t.nl == 0) continue;
                 const uint32_t idesc = tc::idesc_16_f32(2 * BM, mma_cols(t), p.type, PR != Product::Y, PR == Product::DW);
                 const int b = ic & 1;
@@ -304,8 +304,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int k = 0; k < BL / 16; ++k)
                             if (k == 0 || 16 * k < left)
                                 tc::mma_f16_pair(d, da + k * (SA >> 4), db + k * (SB >> 4), idesc, k > 0 || l > 0);
-                        tc::mma_commit_pair_to(bar_empty + 8 * s, all);
-                        if (left <= BL) tc::mma_commit_pair_to(bar_accfull + 8 * b, own);
+                        tc::mma_commit_pair(bar_empty + 8 * s);
+                        if (left <= BL) tc::mma_commit_pair(bar_accfull + 8 * b);
                     }
                     __syncwarp();
                     if (++s == STAGES) {
@@ -318,11 +318,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 2 && PR == Product::DW) {
         // ------------------------------------------------------------- relay
-        const uint32_t ready_lead = tc::mapa_shared(bar_ready, lead);
+        const uint32_t ready_lead = tc::mapa_shared(bar_ready, 0);
         int g = 0;
         bool ok = true;
-        for (int i = cluster; ok && i < work.items; i += clusters) {
-            const Item t = work.item(p, i, q_pair);
+        for (int i = pair; ok && i < work.items; i += npairs) {
+            const Item t = work.item(p, i);
             for (int l = 0; l < t.nl; l += BL, ++g) {
                 const int s = g % STAGES;
                 ok = tc::mbar_wait(bar_full + 8 * s, (uint32_t)(g / STAGES) & 1u, abort_flag, p.err);
@@ -347,13 +347,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp >= EP_WARP0) {
         // ---------------------------------------------------------- epilogue
         const int q = warp & 3, eh = (warp - EP_WARP0) >> 2;
-        const uint32_t accempty_lead = tc::mapa_shared(bar_accempty, lead);
+        const uint32_t accempty_lead = tc::mapa_shared(bar_accempty, 0);
         const uint32_t t_lane = (uint32_t)(32 * q) << 16;
         const int M = PR == Product::DX ? p.K : p.N;
         uint16_t* const out = static_cast<uint16_t*>(p.out);
         int ic = 0;
-        for (int i = cluster; i < work.items; i += clusters) {
-            const Item t = work.item(p, i, q_pair);
+        for (int i = pair; i < work.items; i += npairs) {
+            const Item t = work.item(p, i);
             const int m = t.m0 + (int)rank * BM + 32 * q + lane;  // this thread's A row
             const int b = ic & 1;
             if (t.nl > 0) {
@@ -361,30 +361,50 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::tc_fence_after();
             }
-            const int blocks = ceil_div(t.ncols, 32);
-            for (int cb = eh; cb < blocks; cb += 2) {
-                uint32_t v[32];
-                if (t.nl > 0) {
+            if (PR == Product::DW) {
+                // 64 columns at a time: rows of 128 B, 128-byte swizzle, stored by TMA
+                const int row0 = t.m0 + (int)rank * BM + 32 * q, blocks = ceil_div(t.ncols, 64);
+                const uint32_t buf = base + STAGES * STAGE_BYTES + (warp - EP_WARP0) * OUT_BYTES;
+                const uint32_t dst = buf + 128 * lane;
+                for (int cb = eh; cb < blocks; cb += 2) {
+                    uint32_t o[32];
+                    if (t.nl > 0) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t v[32];
+                            tc::tmem_ld_32x32b_x32(tmem_base + 256u * b + 64u * cb + 32u * h + t_lane, v);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float lo = __uint_as_float(v[2 * j]), hi = __uint_as_float(v[2 * j + 1]);
+                                o[16 * h + j] = p.type ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0;
+                    }
+                    tc::bulk_wait_read();  // the lane that stores: the buffer has been read
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                                     :: "r"(dst + 16 * (j ^ (lane & 7))), "r"(o[4 * j]), "r"(o[4 * j + 1]), "r"(o[4 * j + 2]),
+                                        "r"(o[4 * j + 3]) : "memory");
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (row0 < M && tc::elect_one()) {
+                        tc::tma_store_3d(&maps.b[1], buf, t.c0 + 64 * cb, row0, t.e);
+                        tc::bulk_commit();
+                    }
+                    __syncwarp();
+                }
+            } else {
+                const int blocks = ceil_div(t.ncols, 32);
+                for (int cb = eh; cb < blocks; cb += 2) {
+                    uint32_t v[32];
                     tc::tmem_ld_32x32b_x32(tmem_base + 256u * b + 32u * cb + t_lane, v);
                     tc::tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0;
-                }
-                if (PR == Product::DW) {
-                    uint16_t* o = out + ((size_t)t.e * p.N + m) * p.K + t.c0 + 32 * cb;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        V8 f;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            f.p[k] = make_float2(__uint_as_float(v[8 * j + 2 * k]), __uint_as_float(v[8 * j + 2 * k + 1]));
-                        if (m < M && 32 * cb + 8 * j < t.ncols) {
-                            if (p.type) store8<Bf16>(o, j, f);
-                            else store8<F16>(o, j, f);
-                        }
-                    }
-                } else {
                     uint16_t* o = out + (size_t)(t.c0 + 32 * cb) * M + m;
                     const int n = min(32, t.ncols - 32 * cb);
 #pragma unroll
@@ -401,6 +421,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++ic;
             }
         }
+        if (PR == Product::DW) tc::bulk_wait();
     }
 
     // A wait that gave up: copies and MMAs that were issued finish well inside
@@ -434,55 +455,44 @@ bool map_w(CUtensorMap* m, bool bf16, const void* ptr, const GroupedShape& g, in
     return make_tensor_map_16(m, bf16, ptr, 3, dims, strides, box);
 }
 
-template <Product PR, int NP>
-cudaError_t launch_np(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
+template <Product PR>
+cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
     const bool bf = g.dtype == MOE_DT_BF16;
     Maps maps;
     bool ok;
     int max_items;
     if (PR == Product::DW) {
-        ok = map_2d(&maps.a, bf, a, g.N, g.R, 64, 64) && map_2d(&maps.b[0], bf, b, g.K, g.R, 64, 64);
-        max_items = g.E * ceil_div(g.N, NP * 2 * BM) * ceil_div(g.K, BN);
+        ok = map_2d(&maps.a, bf, a, g.N, g.R, 64, 64) && map_2d(&maps.b[0], bf, b, g.K, g.R, 64, 64) &&
+             map_w(&maps.b[1], bf, out, g, 32);
+        max_items = g.E * ceil_div(g.N, 2 * BM) * ceil_div(g.K, BN);
     } else {
         const int L = PR == Product::Y ? g.K : g.N, M = PR == Product::Y ? g.N : g.K;
         ok = map_w(&maps.a, bf, a, g, PR == Product::Y ? BM : 64);
-        for (int i = 0; i < BOXES && ok; ++i) ok = map_2d(&maps.b[i], bf, b, L, g.R, 64, (i + 1) * 16 / NP);
-        max_items = (g.R / BN + std::min(g.R, g.E)) * ceil_div(M, NP * 2 * BM);
+        for (int i = 0; i < BOXES && ok; ++i) ok = map_2d(&maps.b[i], bf, b, L, g.R, 64, (i + 1) * 16);
+        max_items = (g.R / BN + std::min(g.R, g.E)) * ceil_div(M, 2 * BM);
     }
     if (!ok) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(THREADS);
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim = {2 * NP, 1, 1};
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    static int max_clusters = 0;  // that the GPU holds at once
-    if (max_clusters == 0) {
-        cudaError_t e = cudaFuncSetAttribute(grouped_tc_kernel<PR, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    static int max_pairs = 0;  // CTA pairs that the GPU holds at once
+    if (max_pairs == 0) {
+        cudaError_t e = cudaFuncSetAttribute(grouped_tc_kernel<PR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)SMEM_LIMIT);
         if (e != cudaSuccess) return e;
-        cfg.gridDim = dim3((unsigned)(num_sms() / (2 * NP) * (2 * NP)));
-        cfg.dynamicSmemBytes = smem_bytes(1024);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = smem_bytes<PR>(1024);
         int nc = 0;
-        if (cudaOccupancyMaxActiveClusters(&nc, grouped_tc_kernel<PR, NP>, &cfg) != cudaSuccess || nc < 1) {
+        if (cudaOccupancyMaxActiveClusters(&nc, grouped_tc_kernel<PR>, &cfg) != cudaSuccess || nc < 1) {
             (void)cudaGetLastError();
-            nc = num_sms() / (2 * NP);
+            nc = num_sms() / 2;
         }
-        max_clusters = std::max(1, nc);
+        max_pairs = std::max(1, nc);
     }
     const GroupedParams p{g.R, g.E, g.N, g.K, g.offsets, out, bf ? 1u : 0u, g.err};
-    cfg.gridDim = dim3(2 * NP * std::max(1, std::min(max_clusters, max_items)));
-    cfg.dynamicSmemBytes = smem_bytes(g.E);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, grouped_tc_kernel<PR, NP>, maps, p);
-    if (e == cudaSuccess) note_launch();
-    return e;
-}
-
-template <Product PR>
-cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
-    return launch_np<PR, 1>(g, a, b, out, s);
+    const int grid = 2 * std::max(1, std::min(max_pairs, max_items));
+    grouped_tc_kernel<PR><<<grid, THREADS, smem_bytes<PR>(g.E), s>>>(maps, p);
+    note_launch();
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -222,25 +222,6 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         :: "r"(dst), "l"(map), "r"(cl_bar), "r"(x), "r"(y), "r"(z) : "memory");
 }
 
-// Loads that land at the same offsets in every CTA of `mask` (cluster ranks).
-// The bytes count on the mbarrier at bar's offset in each of them; the _pair
-// form counts them on the barriers of those CTAs' pair members of the parity of
-// the CTA that cl_bar lies in (its even member, for an address there).
-__device__ __forceinline__ void tma_load_2d_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
-                                                      int32_t y, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%3, %4}], [%2], %5;"
-        :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "h"(mask) : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_multicast_pair(uint32_t dst, const CUtensorMap* map, uint32_t cl_bar,
-                                                           int32_t x, int32_t y, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2"
-        " [%0], [%1, {%3, %4}], [%2], %5;"
-        :: "r"(dst), "l"(map), "r"(cl_bar), "r"(x), "r"(y), "h"(mask) : "memory");
-}
-
 // 4D tiled load of box at (x, y, z, w) into shared memory, completing the
 // box's bytes of transaction count on mbarrier `bar`.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -250,6 +231,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%3, %4, %5, %6}], [%2];"
         :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+
+// 3D tiled store of a box from shared memory to (x, y, z); what lies out of the
+// tensor's bounds is not written.  bulk_commit closes the thread's group of
+// stores, bulk_wait_read waits until its groups have been read from shared
+// memory, bulk_wait until they are written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 :: "l"(map), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Plain bulk copy of `bytes` (a multiple of 16; both addresses 16-byte
 // aligned) from global memory into shared memory, completing that many bytes
@@ -333,13 +326,6 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
         "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
         :: "r"(bar) : "memory");
-}
-
-// The same with the CTAs to be signalled given by their cluster ranks.
-__device__ __forceinline__ void mma_commit_pair_to(uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        :: "r"(bar), "h"(mask) : "memory");
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, 16-bit inputs, fp32 accumulation.
