@@ -25,6 +25,8 @@ namespace {
 template <class T, int VPT, int SLOTS, bool ALL>
 __global__ void __launch_bounds__(SLOTS == 1 || VPT == 4 ? 512 : 1024, 1) block_norm_kernel(const Args p) {
     extern __shared__ __align__(16) float smem[];
+    grid_dependency_launch();
+    grid_dependency_wait();
     constexpr size_t CH = 8 * T::BYTES;
     const int groups = blockDim.x / p.threads, grp = threadIdx.x / p.threads;
     RowGroup rg(p.threads, grp, smem + grp * RowGroup::SUM_FLOATS);
@@ -153,8 +155,8 @@ cudaError_t run(Args p, cudaStream_t s) {
     const bool all = p.y && p.gamma_post && p.h && (!p.gate || p.S == p.T);
     return with_shape(vpt, slots, [&](auto v, auto n) {
         constexpr int V = decltype(v)::value, N = decltype(n)::value;
-        return all ? launch_smem(block_norm_kernel<T, V, N, true>, blocks, threads, smem, s, p)
-                   : launch_smem(block_norm_kernel<T, V, N, false>, blocks, threads, smem, s, p);
+        return all ? launch_overlapped(block_norm_kernel<T, V, N, true>, blocks, threads, smem, s, p)
+                   : launch_overlapped(block_norm_kernel<T, V, N, false>, blocks, threads, smem, s, p);
     });
 }
 
@@ -167,11 +169,9 @@ cudaError_t launch_block_norm(const NormShape& n, const void* x, const void* y, 
     a.y = y;
     a.x_out = x_out;
     a.h = h;
-    const cudaError_t e = n.dtype == MOE_DT_BF16  ? norm::run<Bf16>(a, s)
-                          : n.dtype == MOE_DT_F16 ? norm::run<F16>(a, s)
-                                                  : norm::run<F32>(a, s);
-    note_launch();
-    return e;
+    return n.dtype == MOE_DT_BF16  ? norm::run<Bf16>(a, s)
+           : n.dtype == MOE_DT_F16 ? norm::run<F16>(a, s)
+                                   : norm::run<F32>(a, s);
 }
 
 }  // namespace moe

@@ -28,7 +28,8 @@ template <class T, int VPT, int SLOTS, bool ALL>
 __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(const Args p) {
     extern __shared__ __align__(16) float smem[];
     // the kernel that adds the blocks' sums up may take its place already
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_dependency_launch();
+    grid_dependency_wait();
     const int grp = threadIdx.x / p.threads;
     RowGroup rg(p.threads, grp, smem + grp * RowGroup::SUM_FLOATS);
     const int chunks = p.D / 8, n = VPT * p.threads;
@@ -211,7 +212,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(c
 // the gradients' kernel and waits for its results here.
 __global__ void __launch_bounds__(1024) block_norm_reduce_kernel(const Args p, int sums, int gates) {
     __shared__ float red[32][33];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_dependency_launch();
+    grid_dependency_wait();
     const int tx = threadIdx.x, ty = threadIdx.y, col = blockIdx.x * 32 + tx;
     if ((int)blockIdx.y < sums) {
         const int what = blockIdx.y;
@@ -282,24 +284,16 @@ cudaError_t run_backward(const Args& p, const BackwardPlan& b, bool all, cudaStr
     const size_t smem = other + std::max(slots > 1 ? slots * slot : 0, merge);
     return with_shape(b.vpt, slots, [&](auto v, auto n) {
         constexpr int V = decltype(v)::value, N = decltype(n)::value;
-        return all ? launch_smem(block_norm_backward_kernel<T, V, N, true>, b.blocks, threads, smem, s, p)
-                   : launch_smem(block_norm_backward_kernel<T, V, N, false>, b.blocks, threads, smem, s, p);
+        return all ? launch_overlapped(block_norm_backward_kernel<T, V, N, true>, b.blocks, threads, smem, s, p)
+                   : launch_overlapped(block_norm_backward_kernel<T, V, N, false>, b.blocks, threads, smem, s, p);
     });
 }
 
 cudaError_t run_reduce(const Args& p, cudaStream_t s) {
     const bool one_gate = p.S == p.T;
     const int sums = p.dgate && one_gate ? 3 : 2, gates = p.dgate && !one_gate ? p.T / p.S : 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ceil_div(p.D, 32), sums + std::min(ceil_div(gates, 4), 1024));
-    cfg.blockDim = dim3(32, 32);
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, block_norm_reduce_kernel, p, sums, gates);
+    return launch_overlapped(block_norm_reduce_kernel, dim3(ceil_div(p.D, 32), sums + std::min(ceil_div(gates, 4), 1024)),
+                             dim3(32, 32), 0, s, p, sums, gates);
 }
 
 }  // namespace
@@ -329,15 +323,11 @@ cudaError_t launch_block_norm_backward(const NormShape& n, const NormGrads& g, f
     a.blocks = b.blocks;
     a.part = part;
     a.gate_part = part + (size_t)b.blocks * 3 * n.D;
-    cudaError_t e = n.dtype == MOE_DT_BF16  ? norm::run_backward<Bf16>(a, b, all, s)
+    const cudaError_t e = n.dtype == MOE_DT_BF16  ? norm::run_backward<Bf16>(a, b, all, s)
                     : n.dtype == MOE_DT_F16 ? norm::run_backward<F16>(a, b, all, s)
                                             : norm::run_backward<F32>(a, b, all, s);
-    if (e != cudaSuccess) return e;
-    note_launch();
-    if (!g.dgamma_post && !g.dgate && !g.dgamma_pre) return e;
-    e = norm::run_reduce(a, s);
-    note_launch();
-    return e;
+    if (e != cudaSuccess || (!g.dgamma_post && !g.dgate && !g.dgamma_pre)) return e;
+    return norm::run_reduce(a, s);
 }
 
 }  // namespace moe

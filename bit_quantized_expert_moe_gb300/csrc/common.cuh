@@ -175,6 +175,14 @@ __device__ __forceinline__ uint4 ldg_stream16(const void* p) {
     return r;
 }
 
+// Programmatic dependent launches.  A kernel launched by launch_overlapped may
+// start while the kernel before it in the stream still runs: it must not touch
+// global memory before grid_dependency_wait(), which returns when that kernel
+// is complete and its writes are visible.  grid_dependency_launch() allows the
+// next such kernel to start early.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // cp.async (Ampere-style LDGSTS) helpers.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");

@@ -1,0 +1,109 @@
+// y = x W_e^T for a handful of rows in all: decoding.
+//
+// The weights' bytes are all that counts, and a few tiles of 256 weight rows
+// would not occupy every SM.  A block takes 16 weight rows of one expert and up
+// to 8 of its rows; its eight warps share K and add up in shared memory.  A
+// weight goes from memory to a register once and from there into the tensor
+// cores (mma.sync m16n8k16: 16 weight rows, 8 rows of x): with so few rows the
+// tcgen05 path's staging would only add latency.  Both operands keep K in the
+// order in which a thread's 16-byte loads bring it (the same for both, so the
+// dot product is unchanged): lane 4 g + t holds elements 8 t .. 8 t + 7 of every
+// 32 for weight rows g and g + 8 and for row g of x.
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int WARPS = 8, ROWS = 16, COLS = 8, AHEAD = 8;
+
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(32 * WARPS) grouped_few_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
+                                                                 uint16_t* __restrict__ y, GroupedShape g) {
+    __shared__ int cnt[WARPS];
+    __shared__ float part[WARPS][COLS][ROWS + 1];
+    grid_dependency_launch();
+    grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.y, n0 = blockIdx.x * ROWS;
+    // the row's expert: how many segments end at or before it
+    int c = 0;
+    bool bad = false;
+    for (int i = threadIdx.x; i < g.E; i += 32 * WARPS) {
+        const int lo = __ldg(g.offsets + i), hi = __ldg(g.offsets + i + 1);
+        c += hi <= r;
+        bad |= lo < 0 || hi < lo || hi > g.R;
+    }
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) cnt[warp] = c;
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && r == 0) set_error(g.err, ERRBIT_RANGE);
+        return;
+    }
+    int e = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) e += cnt[i];
+    if (e >= g.E) return;  // behind the last segment
+    const int r0 = __ldg(g.offsets + e), r1 = __ldg(g.offsets + e + 1);
+    if (r < r0 || (r - r0) % COLS) return;  // in front of the first; another block's
+    const int rows = min(COLS, r1 - r);
+
+    const int gi = lane >> 2, t = lane & 3;
+    const int kq = (ceil_div(g.K, 32 * WARPS)) * 32, k0 = warp * kq, k1 = min(g.K, k0 + kq);
+    const size_t ld = (size_t)g.K;
+    const uint16_t* wa = w + ((size_t)e * g.N + min(n0 + gi, g.N - 1)) * ld + 8 * t;
+    const uint16_t* wb = w + ((size_t)e * g.N + min(n0 + gi + 8, g.N - 1)) * ld + 8 * t;
+    const uint16_t* xr = x + (size_t)(r + min(gi, rows - 1)) * ld + 8 * t;
+    const bool has = gi < rows;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = k0; k < k1; k += 32 * AHEAD) {
+        uint4 a[AHEAD], b[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const bool in = k + 32 * i + 8 * t < k1;
+            a[i] = in ? ldg_stream16(wa + k + 32 * i) : make_uint4(0, 0, 0, 0);
+            b[i] = in ? ldg_stream16(wb + k + 32 * i) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const bool in = has && k + 32 * i + 8 * t < k1;
+            const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(xr + k + 32 * i)) : make_uint4(0, 0, 0, 0);
+            mma16816<BF16>(acc, a[i].x, b[i].x, a[i].y, b[i].y, v.x, v.y);
+            mma16816<BF16>(acc, a[i].z, b[i].z, a[i].w, b[i].w, v.z, v.w);
+        }
+    }
+    part[warp][2 * t][gi] = acc[0];
+    part[warp][2 * t + 1][gi] = acc[1];
+    part[warp][2 * t][gi + 8] = acc[2];
+    part[warp][2 * t + 1][gi + 8] = acc[3];
+    __syncthreads();
+    const int col = threadIdx.x / ROWS, n = threadIdx.x % ROWS;
+    if (col < rows && n0 + n < g.N) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) s += part[i][col][n];
+        y[(size_t)(r + col) * g.N + n0 + n] = BF16 ? float_to_bf16_bits(s) : float_to_f16_bits(s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_few(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s) {
+    const dim3 grid(ceil_div(g.N, ROWS), g.R);
+    const auto *xp = static_cast<const uint16_t*>(x), *wp = static_cast<const uint16_t*>(w);
+    auto* yp = static_cast<uint16_t*>(y);
+    return launch_overlapped(g.dtype == MOE_DT_BF16 ? grouped_few_kernel<true> : grouped_few_kernel<false>, grid,
+                             dim3(32 * WARPS), 0, s, xp, wp, yp, g);
+}
+
+}  // namespace moe

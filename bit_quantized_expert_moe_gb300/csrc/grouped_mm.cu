@@ -53,17 +53,24 @@ constexpr int ATOM64 = 64 * BL * 2;  // MN-major: 64 l rows of 64 elements
 template <Product PR>
 constexpr int STAGES_OF = PR == Product::DW ? 5 : 6;
 constexpr int MAX_STAGES = 6;
-constexpr int OUT_BYTES = 32 * 128;  // DW: an epilogue warp's 32 rows x 64 columns
+// An epilogue warp's block on its way out: DW 32 rows of 64 columns; Y, DX 32 rows
+// r of 32 columns, 16 bytes apart so that neighbouring rows use other banks.
+template <Product PR>
+constexpr int OUT_BYTES = PR == Product::DW ? 32 * 128 : 32 * 80;
 constexpr int THREADS = 384;
 constexpr int EP_WARP0 = 4, EP_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 512;  // two accumulators of 256 columns
+// Most rows of a tile (Y, DX): 256, or less where that leaves pairs without work.
+constexpr int CAPS = 3;
+__device__ __forceinline__ constexpr int cap_of(int k) { return BN >> k; }
+
 constexpr int NBAR = 3 * MAX_STAGES + 4;
-constexpr size_t BAR_BYTES = 256;
+constexpr size_t BAR_BYTES = 512;
 constexpr size_t SMEM_LIMIT = 232448;
-static_assert(8 * NBAR + 8 <= BAR_BYTES, "barrier area too small");
+static_assert(8 * NBAR + 8 <= 192 && 192 + CAPS * THREADS / 8 <= BAR_BYTES, "barrier area too small");
 
 template <Product PR>
-constexpr int RING_BYTES = STAGES_OF<PR> * STAGE_BYTES + (PR == Product::DW ? EP_WARPS * OUT_BYTES : 0);
+constexpr int RING_BYTES = STAGES_OF<PR> * STAGE_BYTES + EP_WARPS * OUT_BYTES<PR>;
 template <Product PR>
 size_t smem_bytes(int E) { return 1024 + (size_t)RING_BYTES<PR> + BAR_BYTES + 4 * ((size_t)E + 1); }
 
@@ -162,12 +169,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t bar_accfull = bars + 24 * STAGES, bar_accempty = bar_accfull + 16;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + RING_BYTES<PR> + 8 * NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* warp_sums = reinterpret_cast<int*>(gbase + RING_BYTES<PR> + 192);
     int* tile_pre = reinterpret_cast<int*>(gbase + RING_BYTES<PR> + BAR_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
+    grid_dependency_launch();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             tc::mbar_init(bar_full + 8 * s, 1);
@@ -186,31 +195,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc::tmem_alloc_pair(smem_u32((const void*)tmem_slot), TMEM_COLS);
         tc::tmem_relinquish_pair();
     }
-    if (warp == 2) {
-        // row tiles before each expert; with a segment out of place there is
-        // nothing to do (overlapping ones could add up to any number of tiles)
-        int sum = 0;
-        bool all_ok = true;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane;
-            int r0 = 0, cnt = 0;
-            bool ok = true;
-            if (e < p.E) ok = segment(p, e, r0, cnt);
-            all_ok = all_ok && __all_sync(0xffffffffu, ok);
-            const int nt = ceil_div(cnt, BN);
-            int inc = nt;
+    // the kernels before this one in the stream are complete: from here on
+    // global memory is read and written
+    grid_dependency_wait();
+    {
+        // row tiles before each expert, three experts a thread; with a segment
+        // out of place there is nothing to do (overlapping ones could add up to
+        // any number of tiles)
+        constexpr int PER = 3;
+        static_assert(PER * THREADS >= 1024, "too few threads for the experts");
+        const int e0 = threadIdx.x * PER;
+        int cnt[PER], sum[CAPS], inc[CAPS];
+        bool bad = false;
+#pragma unroll
+        for (int c = 0; c < CAPS; ++c) sum[c] = 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            int r0 = 0;
+            cnt[k] = 0;
+            if (e0 + k < p.E) bad |= !segment(p, e0 + k, r0, cnt[k]);
+#pragma unroll
+            for (int c = 0; c < CAPS; ++c) sum[c] += ceil_div(cnt[k], cap_of(c));
+        }
+#pragma unroll
+        for (int c = 0; c < CAPS; ++c) {
+            inc[c] = sum[c];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += v;
+                const int v = __shfl_up_sync(0xffffffffu, inc[c], o);
+                if (lane >= o) inc[c] += v;
             }
-            if (e < p.E) tile_pre[e] = sum + inc - nt;
-            sum += __shfl_sync(0xffffffffu, inc, 31);
+            if (lane == 31) warp_sums[c * (THREADS / 32) + warp] = inc[c];
         }
-        if (lane == 0) {
-            tile_pre[p.E] = all_ok ? sum : -1;
-            if (!all_ok && blockIdx.x == 0) set_error(p.err, ERRBIT_RANGE);
+        bad = __syncthreads_or(bad);
+        int c = 0, before = 0;
+        for (; PR != Product::DW; ++c) {
+            int all = 0;
+            before = 0;
+            for (int w = 0; w < THREADS / 32; ++w) {
+                const int v = warp_sums[c * (THREADS / 32) + w];
+                before += w < warp ? v : 0;
+                all += v;
+            }
+            if (c + 1 == CAPS || (long long)all * ceil_div(PR == Product::DX ? p.K : p.N, 2 * BM) >= npairs) break;
         }
+        before += (c == 0 ? inc[0] - sum[0] : c == 1 ? inc[1] - sum[1] : inc[2] - sum[2]);
+        const int cap = cap_of(c);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            if (e0 + k < p.E) tile_pre[e0 + k] = before;
+            before += ceil_div(cnt[k], cap);
+            if (e0 + k == p.E - 1) tile_pre[p.E] = bad ? -1 : before;
+        }
+        if (bad && threadIdx.x == 0 && blockIdx.x == 0) set_error(p.err, ERRBIT_RANGE);
     }
     // both CTAs' barriers are initialised and the tensor memory allocated
     // before either CTA signals the other
@@ -349,6 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int q = warp & 3, eh = (warp - EP_WARP0) >> 2;
         const uint32_t accempty_lead = tc::mapa_shared(bar_accempty, 0);
         const uint32_t t_lane = (uint32_t)(32 * q) << 16;
+        const uint32_t buf = base + STAGES * STAGE_BYTES + (warp - EP_WARP0) * OUT_BYTES<PR>;
         const int M = PR == Product::DX ? p.K : p.N;
         uint16_t* const out = static_cast<uint16_t*>(p.out);
         int ic = 0;
@@ -364,7 +402,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (PR == Product::DW) {
                 // 64 columns at a time: rows of 128 B, 128-byte swizzle, stored by TMA
                 const int row0 = t.m0 + (int)rank * BM + 32 * q, blocks = ceil_div(t.ncols, 64);
-                const uint32_t buf = base + STAGES * STAGE_BYTES + (warp - EP_WARP0) * OUT_BYTES;
                 const uint32_t dst = buf + 128 * lane;
                 for (int cb = eh; cb < blocks; cb += 2) {
                     uint32_t o[32];
@@ -405,13 +442,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     uint32_t v[32];
                     tc::tmem_ld_32x32b_x32(tmem_base + 256u * b + 32u * cb + t_lane, v);
                     tc::tmem_ld_wait();
-                    uint16_t* o = out + (size_t)(t.c0 + 32 * cb) * M + m;
-                    const int n = min(32, t.ncols - 32 * cb);
+                    // D holds the output transposed: this thread's column m of 32
+                    // rows.  Through shared memory into 64 bytes of a row by 4 lanes.
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         const float f = __uint_as_float(v[j]);
-                        if (m < M && j < n) o[(size_t)j * M] = p.type ? float_to_bf16_bits(f) : float_to_f16_bits(f);
+                        asm volatile("st.shared.b16 [%0], %1;"
+                                     :: "r"(buf + 80 * j + 2 * lane), "h"(p.type ? float_to_bf16_bits(f) : float_to_f16_bits(f)) : "memory");
                     }
+                    __syncwarp();
+                    const int mc = m - lane + 8 * (lane & 3);  // this lane's 8 columns
+                    uint16_t* o = out + (size_t)(t.c0 + 32 * cb) * M + mc;
+                    const int n = mc < M ? min(32, t.ncols - 32 * cb) : 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = 8 * j + (lane >> 2);
+                        if (row < n) {
+                            uint4 w;
+                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(buf + 80 * row + 16 * (lane & 3)) : "memory");
+                            *reinterpret_cast<uint4*>(o + (size_t)row * M) = w;
+                        }
+                    }
+                    __syncwarp();
                 }
             }
             if (t.nl > 0) {
@@ -490,14 +543,16 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
     }
     const GroupedParams p{g.R, g.E, g.N, g.K, g.offsets, out, bf ? 1u : 0u, g.err};
     const int grid = 2 * std::max(1, std::min(max_pairs, max_items));
-    grouped_tc_kernel<PR><<<grid, THREADS, smem_bytes<PR>(g.E), s>>>(maps, p);
-    note_launch();
-    return cudaGetLastError();
+    return launch_overlapped(grouped_tc_kernel<PR>, dim3(grid), dim3(THREADS), smem_bytes<PR>(g.E), s, maps, p);
 }
 
 }  // namespace
 
 cudaError_t launch_grouped_mm(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s) {
+    // 8 rows of 128 experts (N 1536, K 2048): 12.6 us there, 15.1 here; 32 rows
+    // 31.9 and 37.8; 64 rows of 256 experts (N 4096, K 7168) 526 and 496, 128 rows
+    // of one expert (N and K 2048) 20.1 and 13.7
+    if (g.R <= 32) return launch_grouped_few(g, x, w, y, s);
     return launch<Product::Y>(g, w, x, y, s);
 }
 cudaError_t launch_grouped_mm_dx(const GroupedShape& g, const void* dy, const void* w, void* dx, cudaStream_t s) {

@@ -135,6 +135,9 @@ cudaError_t launch_grouped_mm(const GroupedShape& g, const void* x, const void* 
 cudaError_t launch_grouped_mm_dx(const GroupedShape& g, const void* dy, const void* w, void* dx, cudaStream_t s);
 cudaError_t launch_grouped_mm_dw(const GroupedShape& g, const void* dy, const void* x, void* dw, cudaStream_t s);
 
+// The same as launch_grouped_mm by another kernel, for few rows in all.
+cudaError_t launch_grouped_few(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s);
+
 cudaError_t launch_swiglu(moe_dtype_t dt, const void* gu, const float* row_w, const int32_t* row_map, int R, int F,
                           void* h, cudaStream_t s);
 cudaError_t launch_swiglu_backward(moe_dtype_t dt, const void* dh, const void* gu, const float* row_w,
@@ -171,18 +174,29 @@ bool make_tensor_map_16(CUtensorMap* m, bool bf16, const void* ptr, int rank, co
 
 // ----------------------------------------------------------- device info
 int num_sms();
-// Launches a kernel that may need more dynamic shared memory than the default
-// 48 KB.
-template <class K, class... A>
-cudaError_t launch_smem(K kernel, int blocks, int threads, size_t smem, cudaStream_t s, const A&... args) {
+// Counts one kernel launch of this library (reported by moe_kernel_launches).
+void note_launch(int n = 1);
+// Launches a kernel that waits for the one before it in the stream with
+// grid_dependency_wait(), and may start before that one has ended.
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<blocks, threads, smem, s>>>(args...);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e == cudaSuccess) note_launch();
+    return e;
 }
-// Counts one kernel launch of this library (reported by moe_kernel_launches).
-void note_launch(int n = 1);
 
 }  // namespace moe

@@ -53,6 +53,8 @@ template <class T>
 __global__ void __launch_bounds__(256) swiglu_kernel(const void* __restrict__ gu, const float* __restrict__ row_w,
                                                      const int32_t* __restrict__ row_map, int R, int F,
                                                      void* __restrict__ h) {
+    grid_dependency_launch();
+    grid_dependency_wait();
     const int chunks = F / 8;
     const long long total = (long long)R * chunks;
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
@@ -85,6 +87,8 @@ __global__ void __launch_bounds__(256)
                            const int32_t* __restrict__ row_map, int R, int F, void* dgu /* may be gu */,
                            float* __restrict__ drow_w, int threads) {
     extern __shared__ __align__(16) float smem[];
+    grid_dependency_launch();
+    grid_dependency_wait();
     constexpr int SLOTS = BACKWARD_SLOTS<T>;
     const int groups = blockDim.x / threads, grp = threadIdx.x / threads;
     RowGroup rg(threads, grp, smem + grp * RowGroup::SUM_FLOATS);
@@ -153,11 +157,8 @@ cudaError_t launch_swiglu(moe_dtype_t dt, const void* gu, const float* row_w, co
                           void* h, cudaStream_t s) {
     const long long work = (long long)R * (F / 8);
     const int blocks = (int)std::min<long long>((long long)num_sms() * 8, (work + 255) / 256);
-    if (dt == MOE_DT_BF16) swiglu_kernel<Bf16><<<blocks, 256, 0, s>>>(gu, row_w, row_map, R, F, h);
-    else if (dt == MOE_DT_F16) swiglu_kernel<F16><<<blocks, 256, 0, s>>>(gu, row_w, row_map, R, F, h);
-    else swiglu_kernel<F32><<<blocks, 256, 0, s>>>(gu, row_w, row_map, R, F, h);
-    note_launch();
-    return cudaGetLastError();
+    auto* kernel = dt == MOE_DT_BF16 ? swiglu_kernel<Bf16> : dt == MOE_DT_F16 ? swiglu_kernel<F16> : swiglu_kernel<F32>;
+    return launch_overlapped(kernel, blocks, 256, 0, s, gu, row_w, row_map, R, F, h);
 }
 
 namespace {
@@ -171,18 +172,16 @@ cudaError_t run_backward(const void* dh, const void* gu, const float* row_w, con
     const int threads = 32 * warps, groups = 8 / warps;
     const int blocks = std::min(num_sms() * 5, ceil_div(R, groups));
     const size_t smem = groups * RowGroup::SUM_FLOATS * sizeof(float) + (size_t)threads * groups * BackwardRing<T>::BYTES_PER_THREAD;
-    return launch_smem(swiglu_backward_kernel<T>, blocks, threads * groups, smem, s, dh, gu, row_w, row_map, R, F, dgu, drow_w,
+    return launch_overlapped(swiglu_backward_kernel<T>, blocks, threads * groups, smem, s, dh, gu, row_w, row_map, R, F, dgu, drow_w,
                        threads);
 }
 }  // namespace
 
 cudaError_t launch_swiglu_backward(moe_dtype_t dt, const void* dh, const void* gu, const float* row_w,
                                    const int32_t* row_map, int R, int F, void* dgu, float* drow_w, cudaStream_t s) {
-    const cudaError_t e = dt == MOE_DT_BF16  ? run_backward<Bf16>(dh, gu, row_w, row_map, R, F, dgu, drow_w, s)
-                          : dt == MOE_DT_F16 ? run_backward<F16>(dh, gu, row_w, row_map, R, F, dgu, drow_w, s)
-                                             : run_backward<F32>(dh, gu, row_w, row_map, R, F, dgu, drow_w, s);
-    note_launch();
-    return e;
+    return dt == MOE_DT_BF16  ? run_backward<Bf16>(dh, gu, row_w, row_map, R, F, dgu, drow_w, s)
+           : dt == MOE_DT_F16 ? run_backward<F16>(dh, gu, row_w, row_map, R, F, dgu, drow_w, s)
+                              : run_backward<F32>(dh, gu, row_w, row_map, R, F, dgu, drow_w, s);
 }
 
 }  // namespace moe
