@@ -98,11 +98,9 @@ def lib() -> ctypes.CDLL:
 def _ptr(t: torch.Tensor | None) -> int | None:
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("device tensor expected")
-    if not t.is_contiguous():
-        raise ValueError("contiguous tensor expected")
-    return t.data_ptr()
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("contiguous tensor expected" if t.is_cuda else "device tensor expected")
 
 
 def _stream(stream) -> int | None:

@@ -2,7 +2,7 @@
 //
 // The weights' bytes are all that counts, and a few tiles of 256 weight rows
 // would not occupy every SM.  A block takes 16 weight rows of one expert and up
-// to 8 of its rows; its eight warps share K and add up in shared memory.  A
+// to 8 of its rows; its four warps share K and add up in shared memory.  A
 // weight goes from memory to a register once and from there into the tensor
 // cores (mma.sync m16n8k16: 16 weight rows, 8 rows of x): with so few rows the
 // tcgen05 path's staging would only add latency.  Both operands keep K in the
@@ -14,7 +14,7 @@
 namespace moe {
 namespace {
 
-constexpr int WARPS = 8, ROWS = 16, COLS = 8, AHEAD = 8;
+constexpr int WARPS = 4, ROWS = 16, COLS = 8, AHEAD = 8;
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,

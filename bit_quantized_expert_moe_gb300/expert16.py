@@ -15,12 +15,13 @@ from . import _check, _ptr, _stream, lib, workspace
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _I32, _F32 = torch.int32, torch.float32
+_empty, _like = torch.empty, torch.empty_like
 
 
-def _dtype(t: torch.Tensor) -> int:
-    d = _DTYPES.get(t.dtype)
+def _dtype(dt: torch.dtype) -> int:
+    d = _DTYPES.get(dt)
     if d is None:
-        raise ValueError(f"bfloat16, float16 or float32 tensor expected, not {t.dtype}")
+        raise ValueError(f"bfloat16, float16 or float32 tensor expected, not {dt}")
     return d
 
 
@@ -33,12 +34,12 @@ def grouped_mm_workspace_size(R: int, E: int, N: int, K: int) -> int:
     return lib().moe_grouped_mm_workspace_size(R, E, N, K)
 
 
-def _grouped(fn, what: str, a, b, offsets, R: int, E: int, N: int, K: int, out, ws, stream):
+def _grouped(fn, what: str, dt, a, b, offsets, R: int, E: int, N: int, K: int, out, ws, stream):
     if offsets.shape != (E + 1,) or offsets.dtype is not _I32:
         _refuse("offsets", offsets, (E + 1,), _I32)
     if ws is None:
         ws = workspace(grouped_mm_workspace_size(R, E, N, K), offsets.device)
-    st = fn(_dtype(a), _ptr(a), _ptr(b), _ptr(offsets), R, E, N, K, _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
+    st = fn(_dtype(dt), _ptr(a), _ptr(b), _ptr(offsets), R, E, N, K, _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
     if st:
         _check(st, what)
     return out
@@ -51,10 +52,10 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: torch
     if Kw != K or w.dtype is not dt:
         _refuse("w", w, (E, N, K), dt)
     if y is None:
-        y = torch.empty((R, N), dtype=dt, device=x.device)
+        y = _empty((R, N), dtype=dt, device=x.device)
     elif y.shape != (R, N) or y.dtype is not dt:
         _refuse("y", y, (R, N), dt)
-    return _grouped(lib().moe_grouped_mm, "moe_grouped_mm", x, w, offsets, R, E, N, K, y, ws, stream)
+    return _grouped(lib().moe_grouped_mm, "moe_grouped_mm", dt, x, w, offsets, R, E, N, K, y, ws, stream)
 
 
 def grouped_mm_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dx: torch.Tensor | None = None,
@@ -64,10 +65,10 @@ def grouped_mm_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dx: 
     if Nw != N or w.dtype is not dt:
         _refuse("w", w, (E, N, K), dt)
     if dx is None:
-        dx = torch.empty((R, K), dtype=dt, device=dy.device)
+        dx = _empty((R, K), dtype=dt, device=dy.device)
     elif dx.shape != (R, K) or dx.dtype is not dt:
         _refuse("dx", dx, (R, K), dt)
-    return _grouped(lib().moe_grouped_mm_dx, "moe_grouped_mm_dx", dy, w, offsets, R, E, N, K, dx, ws, stream)
+    return _grouped(lib().moe_grouped_mm_dx, "moe_grouped_mm_dx", dt, dy, w, offsets, R, E, N, K, dx, ws, stream)
 
 
 def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, dw: torch.Tensor | None = None,
@@ -77,34 +78,33 @@ def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, dw: 
     if Rx != R or x.dtype is not dt:
         _refuse("x", x, (R, K), dt)
     if dw is None:
-        dw = torch.empty((E, N, K), dtype=dt, device=dy.device)
+        dw = _empty((E, N, K), dtype=dt, device=dy.device)
     elif dw.shape != (E, N, K) or dw.dtype is not dt:
         _refuse("dw", dw, (E, N, K), dt)
-    return _grouped(lib().moe_grouped_mm_dw, "moe_grouped_mm_dw", dy, x, offsets, R, E, N, K, dw, ws, stream)
+    return _grouped(lib().moe_grouped_mm_dw, "moe_grouped_mm_dw", dt, dy, x, offsets, R, E, N, K, dw, ws, stream)
 
 
 # ---------------------------------------------------------------------------
-def _check_swiglu(gu, row_w, row_map) -> tuple[int, int]:
-    R, F2 = gu.shape
-    if F2 % 2:
+def _check_row_weights(R: int, F2: int, row_w, row_map) -> None:
+    if F2 & 1:
         raise ValueError("gu holds the gate and the up half of every row")
     if row_w is not None and (row_w.shape != (R,) or row_w.dtype is not _F32):
         _refuse("row_w", row_w, (R,), _F32)
     if row_map is not None and (row_map.shape != (R,) or row_map.dtype is not _I32):
         _refuse("row_map", row_map, (R,), _I32)
-    return R, F2 // 2
 
 
 def swiglu(gu: torch.Tensor, row_w: torch.Tensor | None = None, row_map: torch.Tensor | None = None,
            h: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """h[r] = row_w[row_map[r]] SiLU(gate) up for gu [R, 2F], gate then up."""
-    R, F = _check_swiglu(gu, row_w, row_map)
-    dt = gu.dtype
+    (R, F2), dt = gu.shape, gu.dtype
+    _check_row_weights(R, F2, row_w, row_map)
+    F = F2 >> 1
     if h is None:
-        h = torch.empty((R, F), dtype=dt, device=gu.device)
+        h = _empty((R, F), dtype=dt, device=gu.device)
     elif h.shape != (R, F) or h.dtype is not dt:
         _refuse("h", h, (R, F), dt)
-    st = lib().moe_swiglu(_dtype(gu), _ptr(gu), _ptr(row_w), _ptr(row_map), R, F, _ptr(h), _stream(stream))
+    st = lib().moe_swiglu(_dtype(dt), _ptr(gu), _ptr(row_w), _ptr(row_map), R, F, _ptr(h), _stream(stream))
     if st:
         _check(st, "moe_swiglu")
     return h
@@ -114,20 +114,21 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, row_w: torch.Tensor | No
                     row_map: torch.Tensor | None = None, dgu: torch.Tensor | None = None,
                     drow_w: torch.Tensor | None = None, stream=None):
     """Gradients of swiglu: (dgu [R, 2F], drow_w [R] fp32, or None without row_w)."""
-    R, F = _check_swiglu(gu, row_w, row_map)
-    dt = gu.dtype
+    (R, F2), dt = gu.shape, gu.dtype
+    _check_row_weights(R, F2, row_w, row_map)
+    F = F2 >> 1
     if dh.shape != (R, F) or dh.dtype is not dt:
         _refuse("dh", dh, (R, F), dt)
     if dgu is None:
-        dgu = torch.empty_like(gu)
+        dgu = _like(gu)
     elif dgu.shape != gu.shape or dgu.dtype is not dt:
         _refuse("dgu", dgu, gu.shape, dt)
     if drow_w is not None:
         if drow_w.shape != (R,) or drow_w.dtype is not _F32:
             _refuse("drow_w", drow_w, (R,), _F32)
     elif row_w is not None:
-        drow_w = torch.empty_like(row_w)
-    st = lib().moe_swiglu_backward(_dtype(gu), _ptr(dh), _ptr(gu), _ptr(row_w), _ptr(row_map), R, F, _ptr(dgu),
+        drow_w = _like(row_w)
+    st = lib().moe_swiglu_backward(_dtype(dt), _ptr(dh), _ptr(gu), _ptr(row_w), _ptr(row_map), R, F, _ptr(dgu),
                                    _ptr(drow_w), _stream(stream))
     if st:
         _check(st, "moe_swiglu_backward")
@@ -135,24 +136,23 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, row_w: torch.Tensor | No
 
 
 # ---------------------------------------------------------------------------
-def _norm_params(x, gamma_post, gate, gamma_pre) -> tuple[int, int, int, int]:
-    """(rows, width, gate rows, parameter type)"""
-    T, D = x.shape
-    G, given = 1, None
+def _norm_params(T: int, D: int, dt, gamma_post, gate, gamma_pre) -> tuple[int, int]:
+    """(gate rows, parameter type); dt where there is no parameter."""
+    G, pt = 1, None
     if gate is not None:
-        given = gate.dtype
+        pt = gate.dtype
         G = gate.shape[0] if gate.dim() == 2 else 0
         if G < 1 or T % G or gate.shape[1] != D:
             raise ValueError(f"gate: [G, {D}] with G a divisor of {T} rows expected, not {tuple(gate.shape)}")
-    for what, t in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
-        if t is not None:
-            given = given or t.dtype
-            if t.shape != (D,) or t.dtype is not given:
-                _refuse(what, t, (D,), given)
-    pt = _DTYPES.get(given or x.dtype)
-    if pt is None:
-        raise ValueError(f"bfloat16, float16 or float32 parameters expected, not {given}")
-    return T, D, G, pt
+    if gamma_post is not None:
+        pt = pt or gamma_post.dtype
+        if gamma_post.shape != (D,) or gamma_post.dtype is not pt:
+            _refuse("gamma_post", gamma_post, (D,), pt)
+    if gamma_pre is not None:
+        pt = pt or gamma_pre.dtype
+        if gamma_pre.shape != (D,) or gamma_pre.dtype is not pt:
+            _refuse("gamma_pre", gamma_pre, (D,), pt)
+    return G, _dtype(pt or dt)
 
 
 def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, gamma_post: torch.Tensor | None = None,
@@ -162,21 +162,22 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, gamma_post: torch
 
     Returns (x_out, h): x_out is None without y, h is None without gamma_pre.
     gamma_post None: y enters unnormalised; gate [G, D] None: 1; x_out may be x."""
-    T, D, G, pt = _norm_params(x, gamma_post, gate, gamma_pre)
     shape, dt = x.shape, x.dtype
+    T, D = shape
+    G, pt = _norm_params(T, D, dt, gamma_post, gate, gamma_pre)
     if y is not None and (y.shape != shape or y.dtype is not dt):
         _refuse("y", y, shape, dt)
     if x_out is not None:
         if x_out.shape != shape or x_out.dtype is not dt:
             _refuse("x_out", x_out, shape, dt)
     elif y is not None:
-        x_out = torch.empty_like(x)
+        x_out = _like(x)
     if h is not None:
         if h.shape != shape or h.dtype is not dt:
             _refuse("h", h, shape, dt)
     elif gamma_pre is not None:
-        h = torch.empty_like(x)
-    st = lib().moe_block_norm(_dtype(x), pt, T, D, G, alpha, eps, _ptr(gamma_post), _ptr(gate), _ptr(gamma_pre),
+        h = _like(x)
+    st = lib().moe_block_norm(_dtype(dt), pt, T, D, G, alpha, eps, _ptr(gamma_post), _ptr(gate), _ptr(gamma_pre),
                               _ptr(x), _ptr(y), _ptr(x_out), _ptr(h), _stream(stream))
     if st:
         _check(st, "moe_block_norm")
@@ -193,21 +194,25 @@ def block_norm_backward(x_out: torch.Tensor, y: torch.Tensor | None = None, dx_o
                         eps: float = 1e-6, ws: torch.Tensor | None = None, stream=None):
     """Gradients of block_norm at the stored x_out (x, where there is no y):
     (dx, dy, dgamma_post, dgate, dgamma_pre), None for what was not there."""
-    T, D, G, pt = _norm_params(x_out, gamma_post, gate, gamma_pre)
     shape, dt = x_out.shape, x_out.dtype
-    for what, t in (("y", y), ("dx_out", dx_out), ("dh", dh)):
-        if t is not None and (t.shape != shape or t.dtype is not dt):
-            _refuse(what, t, shape, dt)
-    like = torch.empty_like
-    dx = like(x_out)
-    dy = like(y) if y is not None else None
-    dpost = like(gamma_post) if gamma_post is not None else None
-    dgate = like(gate) if gate is not None else None
-    dpre = like(gamma_pre) if gamma_pre is not None else None
+    T, D = shape
+    G, pt = _norm_params(T, D, dt, gamma_post, gate, gamma_pre)
+    if dx_out is not None and (dx_out.shape != shape or dx_out.dtype is not dt):
+        _refuse("dx_out", dx_out, shape, dt)
+    if dh is not None and (dh.shape != shape or dh.dtype is not dt):
+        _refuse("dh", dh, shape, dt)
+    dx, dy = _like(x_out), None
+    if y is not None:
+        if y.shape != shape or y.dtype is not dt:
+            _refuse("y", y, shape, dt)
+        dy = _like(y)
+    dpost = _like(gamma_post) if gamma_post is not None else None
+    dgate = _like(gate) if gate is not None else None
+    dpre = _like(gamma_pre) if gamma_pre is not None else None
     if ws is None:
         ws = workspace(block_norm_backward_workspace_size(T, D, G), x_out.device)
     st = lib().moe_block_norm_backward(
-        _dtype(x_out), pt, T, D, G, alpha, eps, _ptr(gamma_post), _ptr(gate), _ptr(gamma_pre), _ptr(x_out), _ptr(y),
+        _dtype(dt), pt, T, D, G, alpha, eps, _ptr(gamma_post), _ptr(gate), _ptr(gamma_pre), _ptr(x_out), _ptr(y),
         _ptr(dx_out), _ptr(dh), _ptr(dx), _ptr(dy), _ptr(dpost), _ptr(dgate), _ptr(dpre), _ptr(ws), ws.numel(),
         _stream(stream))
     if st:
