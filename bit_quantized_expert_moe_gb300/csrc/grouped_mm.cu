@@ -25,11 +25,11 @@
 // multiple of 16 are set to zero in shared memory and no MMA reads further.
 //
 // Warp roles (384 threads a CTA): 0 TMA producer, 1 TMEM owner and (even CTA)
-// MMA issuer, 2 (DW) relay, 4-11 epilogue (warp w: TMEM lanes 32 (w % 4) .. + 31,
+// MMA issuer, 2 and 3 (DW) relay, 4-11 epilogue (warp w: TMEM lanes 32 (w % 4) .. + 31,
 // every second block of 32 columns).  Two accumulators: the epilogue of a tile
 // runs beside the MMAs of the next.
 // Barriers: Y, DX: both CTAs' copies complete on the even CTA's full[s].  DW: on
-// each CTA's own full[s], where the relay warp waits, clears the rows behind the
+// each CTA's own full[s], where a relay warp waits, clears the rows behind the
 // segment and arrives on the even CTA's ready[s].  empty[s] and accfull[b] are
 // signalled to both CTAs by the MMAs' completion, accempty[b] of the even CTA
 // counts both epilogues' warps.  Every wait is bounded in time: one that gives up
@@ -353,31 +353,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 ++ic;
             }
         }
-    } else if (warp == 2 && PR == Product::DW) {
+    } else if (PR == Product::DW && warp < EP_WARP0) {
         // ------------------------------------------------------------- relay
+        // Each of the two warps owns every second stage of the ring: an arrival
+        // that announces cleared rows (release at cluster scope) keeps a warp
+        // for more than a thousand cycles, which one warp would add to every
+        // tile.  A warp waits for every round of its own stages and for no
+        // other's: a wait names a round by its parity alone, so it has to follow
+        // the round before it.
         const uint32_t ready_lead = tc::mapa_shared(bar_ready, 0);
-        int g = 0;
+        int s = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int i = pair; ok && i < work.items; i += npairs) {
             const Item t = work.item(p, i);
-            for (int l = 0; l < t.nl; l += BL, ++g) {
-                const int s = g % STAGES;
-                ok = tc::mbar_wait(bar_full + 8 * s, (uint32_t)(g / STAGES) & 1u, abort_flag, p.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const int left = t.nl - l, end = min(BL, (left + 15) & ~15);
-                if (left < end) {
-                    // rows left .. end-1 of the four blocks of 64 rows x 128 B
-                    unsigned char* st = gbase + s * STAGE_BYTES;
-                    const int words = (end - left) * 8;
-                    for (int w = lane; w < 4 * words; w += 32)
-                        *reinterpret_cast<uint4*>(st + (w / words) * ATOM64 + left * 128 + (w % words) * 16) = make_uint4(0, 0, 0, 0);
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster_release(ready_lead + 8 * s);
-                } else {
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(ready_lead + 8 * s);
+            for (int l = 0; l < t.nl; l += BL) {
+                if ((s & 1) == warp - 2) {
+                    ok = tc::mbar_wait(bar_full + 8 * s, phase, abort_flag, p.err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const int left = t.nl - l, end = min(BL, (left + 15) & ~15);
+                    if (left < end) {
+                        // rows left .. end-1 of the four blocks of 64 rows x 128 B
+                        unsigned char* st = gbase + s * STAGE_BYTES + (lane >> 3) * ATOM64 + (lane & 7) * 16;
+                        for (int row = left; row < end; ++row) *reinterpret_cast<uint4*>(st + row * 128) = make_uint4(0, 0, 0, 0);
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive_cluster_release(ready_lead + 8 * s);
+                    } else {
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive_cluster(ready_lead + 8 * s);
+                    }
+                }
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
                 }
             }
         }
