@@ -260,25 +260,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
-        // The whole warp follows the pipeline, one elected lane issues.
-        const uint32_t full_lead = tc::mapa_shared(bar_full, 0);
-        int s = 0, g = 0;  // stage, stages issued so far
-        uint32_t phase = 1;
-        bool ok = true;
-        for (int i = pair; ok && i < work.items; i += npairs) {
-            const Item t = work.item(p, i);
-            const int half = mma_cols(t) >> 1;
-            const int bi = PR == Product::DW ? 0 : (half + 15) / 16 - 1, box = (bi + 1) * 16;
-            const CUtensorMap* mb = &maps.b[bi];
-            const uint32_t bytes = PR == Product::DW ? STAGE_BYTES : 2 * (A_BYTES + (uint32_t)box * BL * 2);
-            const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
-            for (int l = 0; l < t.nl; l += BL, ++g) {
-                ok = tc::mbar_wait(bar_empty + 8 * s, phase, abort_flag, p.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
-                const uint32_t fl = full_lead + 8 * s, f = bar_full + 8 * s;
-                if (tc::elect_one()) {
+        if (tc::elect_one()) {
+            const uint32_t full_lead = tc::mapa_shared(bar_full, 0);
+            int s = 0, g = 0;  // stage, stages issued so far
+            uint32_t phase = 1;
+            bool ok = true;
+            for (int i = pair; ok && i < work.items; i += npairs) {
+                const Item t = work.item(p, i);
+                const int half = mma_cols(t) >> 1;
+                const int bi = PR == Product::DW ? 0 : (half + 15) / 16 - 1, box = (bi + 1) * 16;
+                const CUtensorMap* mb = &maps.b[bi];
+                const uint32_t bytes = PR == Product::DW ? STAGE_BYTES : 2 * (A_BYTES + (uint32_t)box * BL * 2);
+                const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
+                for (int l = 0; l < t.nl; l += BL, ++g) {
+                    ok = tc::mbar_wait(bar_empty + 8 * s, phase, abort_flag, p.err);
+                    if (!ok) break;
+                    const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
+                    const uint32_t fl = full_lead + 8 * s, f = bar_full + 8 * s;
                     if (PR == Product::DW) {
                         tc::mbar_arrive_expect_tx(f, bytes);
                         tc::tma_load_2d(sa, &maps.a, f, m, t.l0 + l);
@@ -295,21 +293,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         }
                         tc::tma_load_2d_pair(sb, mb, fl, l, c);
                     }
-                }
-                __syncwarp();
-                if (++s == STAGES) {
-                    s = 0;
-                    phase ^= 1u;
+                    if (++s == STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
+            // the MMAs have read every stage, so every copy has landed
+            for (int k = max(0, g - STAGES); ok && k < g; ++k)
+                ok = tc::mbar_wait(bar_empty + 8 * (k % STAGES), (uint32_t)(k / STAGES) & 1u, abort_flag, p.err);
         }
-        // the MMAs have read every stage, so every copy has landed
-        for (int k = max(0, g - STAGES); ok && k < g; ++k)
-            ok = tc::mbar_wait(bar_empty + 8 * (k % STAGES), (uint32_t)(k / STAGES) & 1u, abort_flag, p.err);
     } else if (warp == 1) {
         // -------------------------------------- MMA issuer (even CTA of the pair)
-        // The whole warp follows the pipeline, one elected lane issues.
-        if (rank == 0) {
+        if (rank == 0 && tc::elect_one()) {
             const uint32_t in = PR == Product::DW ? bar_ready : bar_full;
             int s = 0, ic = 0;
             uint32_t phase = 0;
@@ -321,13 +317,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const int b = ic & 1;
                 // both CTAs' epilogues have read the accumulator
                 ok = tc::mbar_wait_cluster(bar_accempty + 8 * b, ((uint32_t)(ic >> 1) & 1u) ^ 1u, abort_flag, p.err);
-                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc::tc_fence_after();
                 const uint32_t d = tmem_base + 256u * b;
                 for (int l = 0; l < t.nl; l += BL) {
                     ok = tc::mbar_wait_cluster(in + 8 * s, phase, abort_flag, p.err);
-                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc::tc_fence_after();
                     const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
@@ -335,16 +329,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     const uint64_t da = PR == Product::Y ? tc::sw128_kmajor_desc(sa) : tc::sw128_mnmajor_desc(sa, ATOM64);
                     const uint64_t db = PR == Product::DW ? tc::sw128_mnmajor_desc(sb, ATOM64) : tc::sw128_kmajor_desc(sb);
                     const int left = t.nl - l;
-                    if (tc::elect_one()) {
-                        // 16 l further: the start address, in units of 16 bytes
+                    // 16 l further: the start address, in units of 16 bytes
 #pragma unroll
-                        for (int k = 0; k < BL / 16; ++k)
-                            if (k == 0 || 16 * k < left)
-                                tc::mma_f16_pair(d, da + k * (SA >> 4), db + k * (SB >> 4), idesc, k > 0 || l > 0);
-                        tc::mma_commit_pair(bar_empty + 8 * s);
-                        if (left <= BL) tc::mma_commit_pair(bar_accfull + 8 * b);
-                    }
-                    __syncwarp();
+                    for (int k = 0; k < BL / 16; ++k)
+                        if (k == 0 || 16 * k < left)
+                            tc::mma_f16_pair(d, da + k * (SA >> 4), db + k * (SB >> 4), idesc, k > 0 || l > 0);
+                    tc::mma_commit_pair(bar_empty + 8 * s);
+                    if (left <= BL) tc::mma_commit_pair(bar_accfull + 8 * b);
                     if (++s == STAGES) {
                         s = 0;
                         phase ^= 1u;
