@@ -49,10 +49,7 @@ constexpr int A_BYTES = BM * BL * 2;
 constexpr int B_BYTES = BN / 2 * BL * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int ATOM64 = 64 * BL * 2;  // MN-major: 64 l rows of 64 elements
-// Ring stages; DW gives one up for the blocks that its epilogue stores.
-template <Product PR>
-constexpr int STAGES_OF = PR == Product::DW ? 5 : 6;
-constexpr int MAX_STAGES = 6;
+constexpr int STAGES = 6;
 // An epilogue warp's block on its way out: DW 32 rows of 64 columns; Y, DX 32 rows
 // r of 32 columns, 16 bytes apart so that neighbouring rows use other banks.
 template <Product PR>
@@ -64,15 +61,18 @@ constexpr uint32_t TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int CAPS = 3;
 __device__ __forceinline__ constexpr int cap_of(int k) { return BN >> k; }
 
-constexpr int NBAR = 3 * MAX_STAGES + 4;
+constexpr int NBAR = 3 * STAGES + 4;
 constexpr size_t BAR_BYTES = 512;
 constexpr size_t SMEM_LIMIT = 232448;
 static_assert(8 * NBAR + 8 <= 192 && 192 + CAPS * THREADS / 8 <= BAR_BYTES, "barrier area too small");
 
 template <Product PR>
-constexpr int RING_BYTES = STAGES_OF<PR> * STAGE_BYTES + EP_WARPS * OUT_BYTES<PR>;
+constexpr int RING_BYTES = STAGES * STAGE_BYTES + EP_WARPS * OUT_BYTES<PR>;
+// Y, DX: and the row tiles before each expert.
 template <Product PR>
-size_t smem_bytes(int E) { return 1024 + (size_t)RING_BYTES<PR> + BAR_BYTES + 4 * ((size_t)E + 1); }
+size_t smem_bytes(int E) {
+    return 1024 + (size_t)RING_BYTES<PR> + BAR_BYTES + (PR == Product::DW ? 0 : 4 * ((size_t)E + 1));
+}
 
 struct GroupedParams {
     int R, E, N, K;
@@ -104,12 +104,12 @@ struct Work {
     int mb;     // blocks of 256 A rows
     int cb;     // DW: blocks of 256 columns
     int items;
-    const int* tile_pre;  // row tiles before each expert, [E + 1]; the last < 0: bad offsets
+    const int* tile_pre;  // Y, DX: row tiles before each expert, [E + 1]
 
-    __device__ Work(const GroupedParams& p, const int* pre) : tile_pre(pre) {
+    __device__ Work(const GroupedParams& p, const int* pre, bool bad) : tile_pre(pre) {
         mb = ceil_div(PR == Product::DX ? p.K : p.N, 2 * BM);
         cb = ceil_div(p.K, BN);
-        items = pre[p.E] < 0 ? 0 : PR == Product::DW ? p.E * mb * cb : pre[p.E] * mb;
+        items = bad ? 0 : PR == Product::DW ? p.E * mb * cb : pre[p.E] * mb;
     }
     __device__ Item item(const GroupedParams& p, int i) const {
         Item t;
@@ -159,7 +159,6 @@ struct Maps {
 template <Product PR>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     grouped_tc_kernel(const __grid_constant__ Maps maps, const GroupedParams p) {
-    constexpr int STAGES = STAGES_OF<PR>;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -198,27 +197,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // the kernels before this one in the stream are complete: from here on
     // global memory is read and written
     grid_dependency_wait();
-    {
-        // row tiles before each expert, three experts a thread; with a segment
-        // out of place there is nothing to do (overlapping ones could add up to
-        // any number of tiles)
-        constexpr int PER = 3;
-        static_assert(PER * THREADS >= 1024, "too few threads for the experts");
-        const int e0 = threadIdx.x * PER;
-        int cnt[PER], sum[CAPS], inc[CAPS];
-        bool bad = false;
+    // the segments, three experts a thread; with one out of place there is
+    // nothing to do (overlapping ones could add up to any number of tiles)
+    constexpr int PER = 3;
+    static_assert(PER * THREADS >= 1024, "too few threads for the experts");
+    const int e0 = threadIdx.x * PER;
+    int cnt[PER];
+    bool bad = false;
 #pragma unroll
-        for (int c = 0; c < CAPS; ++c) sum[c] = 0;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            int r0 = 0;
-            cnt[k] = 0;
-            if (e0 + k < p.E) bad |= !segment(p, e0 + k, r0, cnt[k]);
-#pragma unroll
-            for (int c = 0; c < CAPS; ++c) sum[c] += ceil_div(cnt[k], cap_of(c));
-        }
+    for (int k = 0; k < PER; ++k) {
+        int r0 = 0;
+        cnt[k] = 0;
+        if (e0 + k < p.E) bad |= !segment(p, e0 + k, r0, cnt[k]);
+    }
+    if (PR == Product::DW) {
+        bad = __syncthreads_or(bad);
+    } else {
+        // row tiles before each expert, for the largest tiles that give every
+        // pair work
+        int sum[CAPS], inc[CAPS];
 #pragma unroll
         for (int c = 0; c < CAPS; ++c) {
+            sum[c] = 0;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) sum[c] += ceil_div(cnt[k], cap_of(c));
             inc[c] = sum[c];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -229,7 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         bad = __syncthreads_or(bad);
         int c = 0, before = 0;
-        for (; PR != Product::DW; ++c) {
+        for (;; ++c) {
             int all = 0;
             before = 0;
             for (int w = 0; w < THREADS / 32; ++w) {
@@ -245,10 +247,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int k = 0; k < PER; ++k) {
             if (e0 + k < p.E) tile_pre[e0 + k] = before;
             before += ceil_div(cnt[k], cap);
-            if (e0 + k == p.E - 1) tile_pre[p.E] = bad ? -1 : before;
+            if (e0 + k == p.E - 1) tile_pre[p.E] = before;
         }
-        if (bad && threadIdx.x == 0 && blockIdx.x == 0) set_error(p.err, ERRBIT_RANGE);
     }
+    if (bad && threadIdx.x == 0 && blockIdx.x == 0) set_error(p.err, ERRBIT_RANGE);
     // both CTAs' barriers are initialised and the tensor memory allocated
     // before either CTA signals the other
     tc::tc_fence_before();
@@ -256,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc::cluster_sync();
     tc::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const Work<PR> work(p, tile_pre);
+    const Work<PR> work(p, tile_pre, bad);
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer

@@ -2,9 +2,9 @@
 the gated activation with the routing weight, and the norms around a block.
 
 Argument marshalling only, as in the rest of the binding: shapes and types are
-checked here, everything else by the library.  The checks are spelled out in
-place: a small call takes a few microseconds on the GPU, and helper calls on
-the host would take longer than that.  `offsets` and `row_map` are the
+checked here, everything else by the library.  The checks and pointers are
+spelled out in place: a small call takes a few microseconds on the GPU, and
+helper calls on the host would take longer than that.  `offsets` and `row_map` are the
 `offsets` and `sorted` of permute().
 """
 from __future__ import annotations
@@ -15,7 +15,8 @@ from . import _check, _ptr, _stream, lib, workspace
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _I32, _F32 = torch.int32, torch.float32
-_empty, _like = torch.empty, torch.empty_like
+_empty = torch.empty
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice  # as _stream(None)
 
 
 def _dtype(dt: torch.dtype) -> int:
@@ -23,6 +24,10 @@ def _dtype(dt: torch.dtype) -> int:
     if d is None:
         raise ValueError(f"bfloat16, float16 or float32 tensor expected, not {dt}")
     return d
+
+
+def _bad(t: torch.Tensor):
+    raise ValueError("contiguous tensor expected" if t.is_cuda else "device tensor expected")
 
 
 def _refuse(what: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype):
@@ -39,7 +44,12 @@ def _grouped(fn, what: str, dt, a, b, offsets, R: int, E: int, N: int, K: int, o
         _refuse("offsets", offsets, (E + 1,), _I32)
     if ws is None:
         ws = workspace(grouped_mm_workspace_size(R, E, N, K), offsets.device)
-    st = fn(_dtype(dt), _ptr(a), _ptr(b), _ptr(offsets), R, E, N, K, _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
+    st = fn(_DTYPES.get(dt, -1), a.data_ptr() if a.is_cuda and a.is_contiguous() else _bad(a),
+            b.data_ptr() if b.is_cuda and b.is_contiguous() else _bad(b),
+            offsets.data_ptr() if offsets.is_cuda and offsets.is_contiguous() else _bad(offsets), R, E, N, K,
+            out.data_ptr() if out.is_cuda and out.is_contiguous() else _bad(out),
+            ws.data_ptr() if ws.is_cuda and ws.is_contiguous() else _bad(ws), ws.numel(),
+            _raw_stream(_device()) if stream is None else stream.cuda_stream)
     if st:
         _check(st, what)
     return out
@@ -104,7 +114,11 @@ def swiglu(gu: torch.Tensor, row_w: torch.Tensor | None = None, row_map: torch.T
         h = _empty((R, F), dtype=dt, device=gu.device)
     elif h.shape != (R, F) or h.dtype is not dt:
         _refuse("h", h, (R, F), dt)
-    st = lib().moe_swiglu(_dtype(dt), _ptr(gu), _ptr(row_w), _ptr(row_map), R, F, _ptr(h), _stream(stream))
+    st = lib().moe_swiglu(_dtype(dt), gu.data_ptr() if gu.is_cuda and gu.is_contiguous() else _bad(gu),
+                          None if row_w is None else row_w.data_ptr() if row_w.is_cuda and row_w.is_contiguous() else _bad(row_w),
+                          None if row_map is None else row_map.data_ptr() if row_map.is_cuda and row_map.is_contiguous() else _bad(row_map), R, F,
+                          h.data_ptr() if h.is_cuda and h.is_contiguous() else _bad(h),
+                          _raw_stream(_device()) if stream is None else stream.cuda_stream)
     if st:
         _check(st, "moe_swiglu")
     return h
@@ -120,14 +134,14 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, row_w: torch.Tensor | No
     if dh.shape != (R, F) or dh.dtype is not dt:
         _refuse("dh", dh, (R, F), dt)
     if dgu is None:
-        dgu = _like(gu)
+        dgu = _empty((R, F2), dtype=dt, device=gu.device)
     elif dgu.shape != gu.shape or dgu.dtype is not dt:
         _refuse("dgu", dgu, gu.shape, dt)
     if drow_w is not None:
         if drow_w.shape != (R,) or drow_w.dtype is not _F32:
             _refuse("drow_w", drow_w, (R,), _F32)
     elif row_w is not None:
-        drow_w = _like(row_w)
+        drow_w = _empty((R,), dtype=_F32, device=gu.device)
     st = lib().moe_swiglu_backward(_dtype(dt), _ptr(dh), _ptr(gu), _ptr(row_w), _ptr(row_map), R, F, _ptr(dgu),
                                    _ptr(drow_w), _stream(stream))
     if st:
@@ -171,14 +185,21 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, gamma_post: torch
         if x_out.shape != shape or x_out.dtype is not dt:
             _refuse("x_out", x_out, shape, dt)
     elif y is not None:
-        x_out = _like(x)
+        x_out = _empty(shape, dtype=dt, device=x.device)
     if h is not None:
         if h.shape != shape or h.dtype is not dt:
             _refuse("h", h, shape, dt)
     elif gamma_pre is not None:
-        h = _like(x)
-    st = lib().moe_block_norm(_dtype(dt), pt, T, D, G, alpha, eps, _ptr(gamma_post), _ptr(gate), _ptr(gamma_pre),
-                              _ptr(x), _ptr(y), _ptr(x_out), _ptr(h), _stream(stream))
+        h = _empty(shape, dtype=dt, device=x.device)
+    st = lib().moe_block_norm(_dtype(dt), pt, T, D, G, alpha, eps,
+                              None if gamma_post is None else gamma_post.data_ptr() if gamma_post.is_cuda and gamma_post.is_contiguous() else _bad(gamma_post),
+                              None if gate is None else gate.data_ptr() if gate.is_cuda and gate.is_contiguous() else _bad(gate),
+                              None if gamma_pre is None else gamma_pre.data_ptr() if gamma_pre.is_cuda and gamma_pre.is_contiguous() else _bad(gamma_pre),
+                              x.data_ptr() if x.is_cuda and x.is_contiguous() else _bad(x),
+                              None if y is None else y.data_ptr() if y.is_cuda and y.is_contiguous() else _bad(y),
+                              None if x_out is None else x_out.data_ptr() if x_out.is_cuda and x_out.is_contiguous() else _bad(x_out),
+                              None if h is None else h.data_ptr() if h.is_cuda and h.is_contiguous() else _bad(h),
+                              _raw_stream(_device()) if stream is None else stream.cuda_stream)
     if st:
         _check(st, "moe_block_norm")
     return x_out, h
@@ -201,20 +222,30 @@ def block_norm_backward(x_out: torch.Tensor, y: torch.Tensor | None = None, dx_o
         _refuse("dx_out", dx_out, shape, dt)
     if dh is not None and (dh.shape != shape or dh.dtype is not dt):
         _refuse("dh", dh, shape, dt)
-    dx, dy = _like(x_out), None
+    dev = x_out.device
+    dx, dy = _empty(shape, dtype=dt, device=dev), None
     if y is not None:
         if y.shape != shape or y.dtype is not dt:
             _refuse("y", y, shape, dt)
-        dy = _like(y)
-    dpost = _like(gamma_post) if gamma_post is not None else None
-    dgate = _like(gate) if gate is not None else None
-    dpre = _like(gamma_pre) if gamma_pre is not None else None
+        dy = _empty(shape, dtype=dt, device=dev)
+    dpost = None if gamma_post is None else _empty((D,), dtype=gamma_post.dtype, device=dev)
+    dgate = None if gate is None else _empty((G, D), dtype=gate.dtype, device=dev)
+    dpre = None if gamma_pre is None else _empty((D,), dtype=gamma_pre.dtype, device=dev)
     if ws is None:
         ws = workspace(block_norm_backward_workspace_size(T, D, G), x_out.device)
     st = lib().moe_block_norm_backward(
-        _dtype(dt), pt, T, D, G, alpha, eps, _ptr(gamma_post), _ptr(gate), _ptr(gamma_pre), _ptr(x_out), _ptr(y),
-        _ptr(dx_out), _ptr(dh), _ptr(dx), _ptr(dy), _ptr(dpost), _ptr(dgate), _ptr(dpre), _ptr(ws), ws.numel(),
-        _stream(stream))
+        _dtype(dt), pt, T, D, G, alpha, eps,
+        None if gamma_post is None else gamma_post.data_ptr() if gamma_post.is_cuda and gamma_post.is_contiguous() else _bad(gamma_post),
+        None if gate is None else gate.data_ptr() if gate.is_cuda and gate.is_contiguous() else _bad(gate),
+        None if gamma_pre is None else gamma_pre.data_ptr() if gamma_pre.is_cuda and gamma_pre.is_contiguous() else _bad(gamma_pre),
+        x_out.data_ptr() if x_out.is_cuda and x_out.is_contiguous() else _bad(x_out),
+        None if y is None else y.data_ptr() if y.is_cuda and y.is_contiguous() else _bad(y),
+        None if dx_out is None else dx_out.data_ptr() if dx_out.is_cuda and dx_out.is_contiguous() else _bad(dx_out),
+        None if dh is None else dh.data_ptr() if dh.is_cuda and dh.is_contiguous() else _bad(dh),
+        dx.data_ptr(), None if dy is None else dy.data_ptr(), None if dpost is None else dpost.data_ptr(),
+        None if dgate is None else dgate.data_ptr(), None if dpre is None else dpre.data_ptr(),
+        ws.data_ptr() if ws.is_cuda and ws.is_contiguous() else _bad(ws), ws.numel(),
+        _raw_stream(_device()) if stream is None else stream.cuda_stream)
     if st:
         _check(st, "moe_block_norm_backward")
     return dx, dy, dpost, dgate, dpre
