@@ -25,15 +25,18 @@
 // multiple of 16 are set to zero in shared memory and no MMA reads further.
 //
 // Warp roles (384 threads a CTA): 0 TMA producer, 1 TMEM owner and (even CTA)
-// MMA issuer, 2 and 3 (DW) relay, 4-11 epilogue (warp w: TMEM lanes 32 (w % 4) .. + 31,
-// every second block of 32 columns).  Two accumulators: the epilogue of a tile
-// runs beside the MMAs of the next.
-// Barriers: Y, DX: both CTAs' copies complete on the even CTA's full[s].  DW: on
-// each CTA's own full[s], where a relay warp waits, clears the rows behind the
-// segment and arrives on the even CTA's ready[s].  empty[s] and accfull[b] are
-// signalled to both CTAs by the MMAs' completion, accempty[b] of the even CTA
-// counts both epilogues' warps.  Every wait is bounded in time: one that gives up
-// sets the error word and every role leaves its loop.
+// MMA issuer, 2 (DW) ragged ends, 4-11 epilogue (warp w: TMEM lanes
+// 32 (w % 4) .. + 31, every second block of columns).  Two accumulators: the
+// epilogue of a tile runs beside the MMAs of the next.
+// Barriers: both CTAs' copies complete on the even CTA's full[s].  DW: where a
+// segment ends inside 16 rows, the copies complete on each CTA's own tail[s]
+// instead; its warp 2 clears the rows and both arrive on full[s], which counts
+// two arrivals (otherwise both by the even CTA's producer).  empty[s] and
+// accfull[b] are signalled to both CTAs by the MMAs' completion, accempty[b] of
+// the even CTA counts both epilogues' warps.  A wait names a round of its barrier
+// by the round's parity, so every waiter waits for every round of a barrier that
+// it uses, in order.  Every wait is bounded in time: one that gives up sets the
+// error word and every role leaves its loop.
 #include "internal.h"
 #include "tc_ptx.cuh"
 
@@ -147,6 +150,10 @@ struct Work {
     }
 };
 
+// DW: whether `left` rows of a segment end inside 16 rows of a stage, which an
+// MMA sums together.
+__device__ __forceinline__ bool ragged_end(int left) { return left < BL && (left & 15); }
+
 __device__ __forceinline__ int mma_cols(const Item& t) { return (t.ncols + 15) & ~15; }
 
 // Boxes of B rows (Y, DX): a CTA's half of a tile is 8 .. 128 rows; map i has
@@ -164,7 +171,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* gbase = smem_raw + (base - raw);
     const uint32_t bars = base + RING_BYTES<PR>;
-    const uint32_t bar_full = bars, bar_empty = bars + 8 * STAGES, bar_ready = bars + 16 * STAGES;
+    const uint32_t bar_full = bars, bar_empty = bars + 8 * STAGES, bar_tail = bars + 16 * STAGES;
     const uint32_t bar_accfull = bars + 24 * STAGES, bar_accempty = bar_accfull + 16;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + RING_BYTES<PR> + 8 * NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -178,9 +185,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     grid_dependency_launch();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            tc::mbar_init(bar_full + 8 * s, 1);
+            tc::mbar_init(bar_full + 8 * s, PR == Product::DW ? 2 : 1);
             tc::mbar_init(bar_empty + 8 * s, 1);
-            tc::mbar_init(bar_ready + 8 * s, 2);
+            tc::mbar_init(bar_tail + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(bar_accfull + 8 * b, 1);
@@ -272,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const int half = mma_cols(t) >> 1;
                 const int bi = PR == Product::DW ? 0 : (half + 15) / 16 - 1, box = (bi + 1) * 16;
                 const CUtensorMap* mb = &maps.b[bi];
-                const uint32_t bytes = PR == Product::DW ? STAGE_BYTES : 2 * (A_BYTES + (uint32_t)box * BL * 2);
+                const uint32_t bytes = 2 * (PR == Product::DW ? STAGE_BYTES : A_BYTES + box * BL * 2);
                 const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
                 for (int l = 0; l < t.nl; l += BL, ++g) {
                     ok = tc::mbar_wait(bar_empty + 8 * s, phase, abort_flag, p.err);
@@ -280,11 +287,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
                     const uint32_t fl = full_lead + 8 * s, f = bar_full + 8 * s;
                     if (PR == Product::DW) {
-                        tc::mbar_arrive_expect_tx(f, bytes);
-                        tc::tma_load_2d(sa, &maps.a, f, m, t.l0 + l);
-                        tc::tma_load_2d(sa + ATOM64, &maps.a, f, m + 64, t.l0 + l);
-                        tc::tma_load_2d(sb, mb, f, c, t.l0 + l);
-                        tc::tma_load_2d(sb + ATOM64, mb, f, c + 64, t.l0 + l);
+                        uint32_t to = fl;
+                        if (ragged_end(t.nl - l)) {
+                            to = tc::mapa_shared(bar_tail + 8 * s, rank);
+                            tc::mbar_arrive_expect_tx(bar_tail + 8 * s, STAGE_BYTES);
+                        } else if (rank == 0) {
+                            tc::mbar_arrive_expect_tx(f, bytes);
+                            tc::mbar_arrive(f);
+                        }
+                        tc::tma_load_2d_pair(sa, &maps.a, to, m, t.l0 + l);
+                        tc::tma_load_2d_pair(sa + ATOM64, &maps.a, to, m + 64, t.l0 + l);
+                        tc::tma_load_2d_pair(sb, mb, to, c, t.l0 + l);
+                        tc::tma_load_2d_pair(sb + ATOM64, mb, to, c + 64, t.l0 + l);
                     } else {
                         if (rank == 0) tc::mbar_arrive_expect_tx(f, bytes);
                         if (PR == Product::Y) {
@@ -308,7 +322,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else if (warp == 1) {
         // -------------------------------------- MMA issuer (even CTA of the pair)
         if (rank == 0 && tc::elect_one()) {
-            const uint32_t in = PR == Product::DW ? bar_ready : bar_full;
             int s = 0, ic = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -323,7 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 tc::tc_fence_after();
                 const uint32_t d = tmem_base + 256u * b;
                 for (int l = 0; l < t.nl; l += BL) {
-                    ok = tc::mbar_wait_cluster(in + 8 * s, phase, abort_flag, p.err);
+                    ok = tc::mbar_wait_cluster(bar_full + 8 * s, phase, abort_flag, p.err);
                     if (!ok) break;
                     tc::tc_fence_after();
                     const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
@@ -346,43 +359,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 ++ic;
             }
         }
-    } else if (PR == Product::DW && warp < EP_WARP0) {
-        // ------------------------------------------------------------- relay
-        // Each of the two warps owns every second stage of the ring: an arrival
-        // that announces cleared rows (release at cluster scope) keeps a warp
-        // for more than a thousand cycles, which one warp would add to every
-        // tile.  A warp waits for every round of its own stages and for no
-        // other's: a wait names a round by its parity alone, so it has to follow
-        // the round before it.
-        const uint32_t ready_lead = tc::mapa_shared(bar_ready, 0);
+    } else if (PR == Product::DW && warp == 2) {
+        // ------------------------- ragged ends: clears the rows behind a segment
+        const uint32_t full_lead = tc::mapa_shared(bar_full, 0);
         int s = 0;
-        uint32_t phase = 0;
+        uint32_t phases = 0;  // of the tail barriers, which are not used in every round
         bool ok = true;
         for (int i = pair; ok && i < work.items; i += npairs) {
             const Item t = work.item(p, i);
-            for (int l = 0; l < t.nl; l += BL) {
-                if ((s & 1) == warp - 2) {
-                    ok = tc::mbar_wait(bar_full + 8 * s, phase, abort_flag, p.err);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    const int left = t.nl - l, end = min(BL, (left + 15) & ~15);
-                    if (left < end) {
-                        // rows left .. end-1 of the four blocks of 64 rows x 128 B
-                        unsigned char* st = gbase + s * STAGE_BYTES + (lane >> 3) * ATOM64 + (lane & 7) * 16;
-                        for (int row = left; row < end; ++row) *reinterpret_cast<uint4*>(st + row * 128) = make_uint4(0, 0, 0, 0);
-                        tc::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive_cluster_release(ready_lead + 8 * s);
-                    } else {
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive_cluster(ready_lead + 8 * s);
-                    }
-                }
-                if (++s == STAGES) {
-                    s = 0;
-                    phase ^= 1u;
-                }
+            if (t.nl == 0) continue;
+            s = (s + (t.nl - 1) / BL) % STAGES;  // the tile's last stage
+            const int left = t.nl - (t.nl - 1) / BL * BL, end = (left + 15) & ~15;
+            if (ragged_end(left)) {
+                ok = tc::mbar_wait(bar_tail + 8 * s, (phases >> s) & 1u, abort_flag, p.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                phases ^= 1u << s;
+                // rows left .. end-1 of the four blocks of 64 rows x 128 B
+                unsigned char* st = gbase + s * STAGE_BYTES + (lane >> 3) * ATOM64 + (lane & 7) * 16;
+                for (int row = left; row < end; ++row) *reinterpret_cast<uint4*>(st + row * 128) = make_uint4(0, 0, 0, 0);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster_release(full_lead + 8 * s);
             }
+            s = (s + 1) % STAGES;
         }
     } else if (warp >= EP_WARP0) {
         // ---------------------------------------------------------- epilogue
