@@ -237,19 +237,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (lane == 31) warp_sums[c * (THREADS / 32) + warp] = inc[c];
         }
         bad = __syncthreads_or(bad);
-        int c = 0, before = 0;
-        for (;; ++c) {
-            int all = 0;
-            before = 0;
+        const int mb = ceil_div(PR == Product::DX ? p.K : p.N, 2 * BM);
+        int c = -1, before = 0;
+#pragma unroll
+        for (int k = 0; k < CAPS; ++k) {
+            int all = 0, front = inc[k] - sum[k];
+#pragma unroll
             for (int w = 0; w < THREADS / 32; ++w) {
-                const int v = warp_sums[c * (THREADS / 32) + w];
-                before += w < warp ? v : 0;
+                const int v = warp_sums[k * (THREADS / 32) + w];
+                front += w < warp ? v : 0;
                 all += v;
             }
-            if (c + 1 == CAPS || (long long)all * ceil_div(PR == Product::DX ? p.K : p.N, 2 * BM) >= npairs) break;
+            if (c < 0 && (k + 1 == CAPS || (long long)all * mb >= npairs)) {
+                c = k;
+                before = front;
+            }
         }
-        before += (c == 0 ? inc[0] - sum[0] : c == 1 ? inc[1] - sum[1] : inc[2] - sum[2]);
-        const int cap = cap_of(c);
+        const int cap = BN >> c;
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             if (e0 + k < p.E) tile_pre[e0 + k] = before;
@@ -525,7 +529,7 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
         const int L = PR == Product::Y ? g.K : g.N, M = PR == Product::Y ? g.N : g.K;
         ok = map_w(&maps.a, bf, a, g, PR == Product::Y ? BM : 64);
         for (int i = 0; i < BOXES && ok; ++i) ok = map_2d(&maps.b[i], bf, b, L, g.R, 64, (i + 1) * 16);
-        max_items = (g.R / BN + std::min(g.R, g.E)) * ceil_div(M, 2 * BM);
+        max_items = std::min<long long>(((long long)g.R / cap_of(CAPS - 1) + std::min(g.R, g.E)) * ceil_div(M, 2 * BM), 1 << 20);
     }
     if (!ok) return cudaErrorInvalidValue;
     static int max_pairs = 0;  // CTA pairs that the GPU holds at once
