@@ -311,5 +311,14 @@ def get_device_error(ws: torch.Tensor, stream=None) -> int:
     return lib().moe_get_device_error(_ptr(ws), _stream(stream))
 
 
-from .expert16 import (block_norm, block_norm_backward, block_norm_backward_workspace_size, grouped_mm,  # noqa: E402
-                       grouped_mm_dw, grouped_mm_dx, grouped_mm_workspace_size, swiglu, swiglu_backward)
+from . import expert16 as _expert16_loader  # noqa: E402
+from .expert16 import block_norm_backward_workspace_size, grouped_mm_workspace_size  # noqa: E402, F401
+
+
+def __getattr__(name: str):
+    # the compiled functions of expert16.py, at their first use: importing the
+    # package needs no built library
+    if name in _expert16_loader.NAMES:
+        fn = globals()[name] = _expert16_loader.load(name)
+        return fn
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
