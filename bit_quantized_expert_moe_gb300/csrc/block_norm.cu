@@ -155,8 +155,8 @@ cudaError_t run(Args p, cudaStream_t s) {
     const bool all = p.y && p.gamma_post && p.h && (!p.gate || p.S == p.T);
     return with_shape(vpt, slots, [&](auto v, auto n) {
         constexpr int V = decltype(v)::value, N = decltype(n)::value;
-        return all ? launch_overlapped(block_norm_kernel<T, V, N, true>, blocks, threads, smem, s, p)
-                   : launch_overlapped(block_norm_kernel<T, V, N, false>, blocks, threads, smem, s, p);
+        return all ? launch_overlapped<block_norm_kernel<T, V, N, true>>(blocks, threads, smem, s, p)
+                   : launch_overlapped<block_norm_kernel<T, V, N, false>>(blocks, threads, smem, s, p);
     });
 }
 

@@ -284,8 +284,8 @@ cudaError_t run_backward(const Args& p, const BackwardPlan& b, bool all, cudaStr
     const size_t smem = other + std::max(slots > 1 ? slots * slot : 0, merge);
     return with_shape(b.vpt, slots, [&](auto v, auto n) {
         constexpr int V = decltype(v)::value, N = decltype(n)::value;
-        return all ? launch_overlapped(block_norm_backward_kernel<T, V, N, true>, b.blocks, threads, smem, s, p)
-                   : launch_overlapped(block_norm_backward_kernel<T, V, N, false>, b.blocks, threads, smem, s, p);
+        return all ? launch_overlapped<block_norm_backward_kernel<T, V, N, true>>(b.blocks, threads, smem, s, p)
+                   : launch_overlapped<block_norm_backward_kernel<T, V, N, false>>(b.blocks, threads, smem, s, p);
     });
 }
 

@@ -60,13 +60,13 @@ constexpr int OUT_BYTES = PR == Product::DW ? 32 * 128 : 32 * 80;
 constexpr int THREADS = 384;
 constexpr int EP_WARP0 = 4, EP_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 512;  // two accumulators of 256 columns
-// Most rows of a tile (Y, DX): 256, or less where that leaves pairs without work.
+// Most columns of a tile (Y, DX: rows r): 256, or less where that leaves pairs
+// without work.
 constexpr int CAPS = 3;
 __device__ __forceinline__ constexpr int cap_of(int k) { return BN >> k; }
 
 constexpr int NBAR = 3 * STAGES + 4;
 constexpr size_t BAR_BYTES = 512;
-constexpr size_t SMEM_LIMIT = 232448;
 static_assert(8 * NBAR + 8 <= 192 && 192 + CAPS * THREADS / 8 <= BAR_BYTES, "barrier area too small");
 
 template <Product PR>
@@ -82,6 +82,7 @@ struct GroupedParams {
     const int32_t* offsets;
     void* out;
     uint32_t type;  // 0 fp16, 1 bf16
+    int dw_cols;    // DW: columns of a tile
     uint32_t* err;
 };
 
@@ -111,7 +112,7 @@ struct Work {
 
     __device__ Work(const GroupedParams& p, const int* pre, bool bad) : tile_pre(pre) {
         mb = ceil_div(PR == Product::DX ? p.K : p.N, 2 * BM);
-        cb = ceil_div(p.K, BN);
+        cb = ceil_div(p.K, p.dw_cols);
         items = bad ? 0 : PR == Product::DW ? p.E * mb * cb : pre[p.E] * mb;
     }
     __device__ Item item(const GroupedParams& p, int i) const {
@@ -121,8 +122,8 @@ struct Work {
             t.e = i / per;
             i -= t.e * per;
             t.m0 = i / cb * 2 * BM;
-            t.c0 = i % cb * BN;
-            t.ncols = min(BN, p.K - t.c0);
+            t.c0 = i % cb * p.dw_cols;
+            t.ncols = min(p.dw_cols, p.K - t.c0);
             segment(p, t.e, t.l0, t.nl);
         } else {
             const int tile = i / mb;
@@ -201,6 +202,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc::tmem_alloc_pair(smem_u32((const void*)tmem_slot), TMEM_COLS);
         tc::tmem_relinquish_pair();
     }
+    // both CTAs' barriers are initialised and the tensor memory allocated
+    // before either CTA signals the other
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
     // the kernels before this one in the stream are complete: from here on
     // global memory is read and written
     grid_dependency_wait();
@@ -262,13 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     }
     if (bad && threadIdx.x == 0 && blockIdx.x == 0) set_error(p.err, ERRBIT_RANGE);
-    // both CTAs' barriers are initialised and the tensor memory allocated
-    // before either CTA signals the other
-    tc::tc_fence_before();
     __syncthreads();
-    tc::cluster_sync();
-    tc::tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
     const Work<PR> work(p, tile_pre, bad);
 
     if (warp == 0) {
@@ -283,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const int half = mma_cols(t) >> 1;
                 const int bi = PR == Product::DW ? 0 : (half + 15) / 16 - 1, box = (bi + 1) * 16;
                 const CUtensorMap* mb = &maps.b[bi];
-                const uint32_t bytes = 2 * (PR == Product::DW ? STAGE_BYTES : A_BYTES + box * BL * 2);
+                const uint32_t bytes = 2 * (A_BYTES + (PR == Product::DW ? (half > 64 ? 2 : 1) * ATOM64 : box * BL * 2));
                 const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
                 for (int l = 0; l < t.nl; l += BL, ++g) {
                     ok = tc::mbar_wait(bar_empty + 8 * s, phase, abort_flag, p.err);
@@ -294,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         uint32_t to = fl;
                         if (ragged_end(t.nl - l)) {
                             to = tc::mapa_shared(bar_tail + 8 * s, rank);
-                            tc::mbar_arrive_expect_tx(bar_tail + 8 * s, STAGE_BYTES);
+                            tc::mbar_arrive_expect_tx(bar_tail + 8 * s, bytes >> 1);
                         } else if (rank == 0) {
                             tc::mbar_arrive_expect_tx(f, bytes);
                             tc::mbar_arrive(f);
@@ -302,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         tc::tma_load_2d_pair(sa, &maps.a, to, m, t.l0 + l);
                         tc::tma_load_2d_pair(sa + ATOM64, &maps.a, to, m + 64, t.l0 + l);
                         tc::tma_load_2d_pair(sb, mb, to, c, t.l0 + l);
-                        tc::tma_load_2d_pair(sb + ATOM64, mb, to, c + 64, t.l0 + l);
+                        if (half > 64) tc::tma_load_2d_pair(sb + ATOM64, mb, to, c + 64, t.l0 + l);
                     } else {
                         if (rank == 0) tc::mbar_arrive_expect_tx(f, bytes);
                         if (PR == Product::Y) {
@@ -520,11 +522,14 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
     const bool bf = g.dtype == MOE_DT_BF16;
     Maps maps;
     bool ok;
-    int max_items;
+    int max_items, dw_cols = BN;
     if (PR == Product::DW) {
         ok = map_2d(&maps.a, bf, a, g.N, g.R, 64, 64) && map_2d(&maps.b[0], bf, b, g.K, g.R, 64, 64) &&
              map_w(&maps.b[1], bf, out, g, 32);
-        max_items = g.E * ceil_div(g.N, 2 * BM) * ceil_div(g.K, BN);
+        // the widest tiles that give every pair work
+        const long long mb = (long long)g.E * ceil_div(g.N, 2 * BM);
+        for (int c = 1; c < CAPS && mb * ceil_div(g.K, dw_cols) < num_sms() / 2; ++c) dw_cols = cap_of(c);
+        max_items = (int)std::min<long long>(mb * ceil_div(g.K, dw_cols), 1 << 20);
     } else {
         const int L = PR == Product::Y ? g.K : g.N, M = PR == Product::Y ? g.N : g.K;
         ok = map_w(&maps.a, bf, a, g, PR == Product::Y ? BM : 64);
@@ -534,8 +539,7 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
     if (!ok) return cudaErrorInvalidValue;
     static int max_pairs = 0;  // CTA pairs that the GPU holds at once
     if (max_pairs == 0) {
-        cudaError_t e = cudaFuncSetAttribute(grouped_tc_kernel<PR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)SMEM_LIMIT);
+        const cudaError_t e = allow_smem<grouped_tc_kernel<PR>>();
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
@@ -548,9 +552,9 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
         }
         max_pairs = std::max(1, nc);
     }
-    const GroupedParams p{g.R, g.E, g.N, g.K, g.offsets, out, bf ? 1u : 0u, g.err};
+    const GroupedParams p{g.R, g.E, g.N, g.K, g.offsets, out, bf ? 1u : 0u, dw_cols, g.err};
     const int grid = 2 * std::max(1, std::min(max_pairs, max_items));
-    return launch_overlapped(grouped_tc_kernel<PR>, dim3(grid), dim3(THREADS), smem_bytes<PR>(g.E), s, maps, p);
+    return launch_overlapped<grouped_tc_kernel<PR>>(dim3(grid), dim3(THREADS), smem_bytes<PR>(g.E), s, maps, p);
 }
 
 }  // namespace

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -176,14 +177,23 @@ bool make_tensor_map_16(CUtensorMap* m, bool bf16, const void* ptr, int rank, co
 int num_sms();
 // Counts one kernel launch of this library (reported by moe_kernel_launches).
 void note_launch(int n = 1);
+// Lets a kernel without static shared memory take all of an SM's as dynamic
+// shared memory, once for each device.
+constexpr int SMEM_MOST = 232448;
+template <auto Kernel>
+cudaError_t allow_smem() {
+    static std::atomic<bool> allowed[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && allowed[dev].load(std::memory_order_relaxed))) return e;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST);
+    if (e == cudaSuccess && dev < 64) allowed[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
 // Launches a kernel that waits for the one before it in the stream with
 // grid_dependency_wait(), and may start before that one has ended.
 template <class... P, class... A>
 cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -197,6 +207,12 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e == cudaSuccess) note_launch();
     return e;
+}
+// The same for a kernel that may need more than the default 48 KB.
+template <auto Kernel, class... A>
+cudaError_t launch_overlapped(dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
+    const cudaError_t e = smem > 48 * 1024 ? allow_smem<Kernel>() : cudaSuccess;
+    return e == cudaSuccess ? launch_overlapped(Kernel, grid, block, smem, s, args...) : e;
 }
 
 }  // namespace moe

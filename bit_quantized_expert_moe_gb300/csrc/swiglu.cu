@@ -172,7 +172,7 @@ cudaError_t run_backward(const void* dh, const void* gu, const float* row_w, con
     const int threads = 32 * warps, groups = 8 / warps;
     const int blocks = std::min(num_sms() * 5, ceil_div(R, groups));
     const size_t smem = groups * RowGroup::SUM_FLOATS * sizeof(float) + (size_t)threads * groups * BackwardRing<T>::BYTES_PER_THREAD;
-    return launch_overlapped(swiglu_backward_kernel<T>, blocks, threads * groups, smem, s, dh, gu, row_w, row_map, R, F, dgu, drow_w,
+    return launch_overlapped<swiglu_backward_kernel<T>>(blocks, threads * groups, smem, s, dh, gu, row_w, row_map, R, F, dgu, drow_w,
                        threads);
 }
 }  // namespace
