@@ -234,17 +234,18 @@ __global__ void __launch_bounds__(1024) block_norm_reduce_kernel(const Args p, i
     }
     for (int g0 = 4 * ((int)blockIdx.y - sums); g0 < gates; g0 += 4 * ((int)gridDim.y - sums)) {
         const int g = g0 + (ty >> 3);
-        const long long first = (long long)g * p.S;
-        const int b0 = (int)(first / p.rows), b1 = (int)((first + p.S - 1) / p.rows);
-        const int r_end = min(p.T, (b0 + 1) * p.rows);
-        // rows wholly inside one row group were written there, unless they are its first or last gate row
-        const bool todo = g < gates && col < p.D && !(b0 == b1 && b0 * p.rows / p.S != g && (r_end - 1) / p.S != g);
+        const bool in = g < gates && col < p.D;
+        const int first = in ? g * p.S : 0, end = first + p.S;  // the gate row's rows
+        const int b0 = first / p.rows, b1 = (end - 1) / p.rows;
+        // rows wholly inside one row group, and neither its first nor its last
+        // gate row, were written there
+        const bool todo = in && !(b0 == b1 && b0 * p.rows < first && min(p.T, (b0 + 1) * p.rows) > end);
         float s = 0.f;
         if (todo)
 #pragma unroll 4
             for (int b = b0 + (ty & 7); b <= b1; b += 8)
-                // the gate row is the row group's first, or its last
-                s += p.gate_part[((size_t)b * 2 + (b * p.rows / p.S != g)) * p.D + col];
+                // the row group starts in this gate row, or in an earlier one
+                s += p.gate_part[((size_t)b * 2 + (b * p.rows < first)) * p.D + col];
         red[ty][tx] = s;
         __syncthreads();
         if (todo && (ty & 7) == 0) {
