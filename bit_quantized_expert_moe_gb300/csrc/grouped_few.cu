@@ -14,6 +14,16 @@
 namespace moe {
 namespace {
 
+// A weight load, read once: it leaves L1 alone and asks L2 for the 256 bytes
+// around it, of which the warp's other loads take the rest (16 rows of 8 of 256
+// experts, N 4096, K 7168: 154 -> 139 us; one token at N 1536, K 2048 12.3 -> 12.1).
+__device__ __forceinline__ uint4 load_weights(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
 constexpr int WARPS = 4, ROWS = 16, COLS = 8, AHEAD = 8;
 
 template <bool BF16>
@@ -71,8 +81,8 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_few_kernel(const uint16_t*
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const bool in = k + 32 * i + 8 * t < k1;
-            a[i] = in ? ldg_stream16(wa + k + 32 * i) : make_uint4(0, 0, 0, 0);
-            b[i] = in ? ldg_stream16(wb + k + 32 * i) : make_uint4(0, 0, 0, 0);
+            a[i] = in ? load_weights(wa + k + 32 * i) : make_uint4(0, 0, 0, 0);
+            b[i] = in ? load_weights(wb + k + 32 * i) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
