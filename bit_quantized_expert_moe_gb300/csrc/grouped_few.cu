@@ -1,4 +1,4 @@
-// y = x W_e^T for a handful of rows in all: decoding.
+// y = x W_e^T for a handful of rows in all, or for about one an expert: decoding.
 //
 // The weights' bytes are all that counts, and a few tiles of 256 weight rows
 // would not occupy every SM.  A block takes 16 weight rows of one expert and up

@@ -543,10 +543,11 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
 }  // namespace
 
 cudaError_t launch_grouped_mm(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s) {
-    // 8 rows of 128 experts (N 1536, K 2048): 12.6 us there, 15.1 here; 32 rows
-    // 31.9 and 37.8; 64 rows of 256 experts (N 4096, K 7168) 526 and 496, 128 rows
-    // of one expert (N and K 2048) 20.1 and 13.7
-    if (g.R <= 32) return launch_grouped_few(g, x, w, y, s);
+    // E 128, N 1536, K 2048: 8 rows 12.1 us there and 13.1 here, 32 rows 31.0 and
+    // 34.9, 128 rows 77.9 and 82.0; E 256, N 4096, K 7168: 64 rows 469 and 492.  With
+    // several rows an expert its blocks read the weights again: E 8, N 1024, K 256:
+    // 16 rows 4.0 and 4.8, 64 rows 5.8 and 4.9; E 1, N and K 2048: 64 rows 14.3 and 9.0
+    if (g.R <= 32 || (g.R <= 128 && g.R <= g.E)) return launch_grouped_few(g, x, w, y, s);
     return launch<Product::Y>(g, w, x, y, s);
 }
 cudaError_t launch_grouped_mm_dx(const GroupedShape& g, const void* dy, const void* w, void* dx, cudaStream_t s) {

@@ -13,9 +13,9 @@ namespace {
 // s(a) = 1 / (1 + e^-a) from t = e^-|a|, so that nothing overflows: 1 / (1 + t)
 // for a >= 0, t / (1 + t) below.  16-bit outputs: the hardware's exponential
 // and reciprocal (relative error below 2^-20 for |a| < 100, an eighth of the
-// half ulp of fp16 in the worst place) and s itself as a factor: beside the
-// library's exponential and division they take the backward kernel from 49 to
-// 40 us at 32768 x 768, where it is otherwise bound by the instructions.
+// half ulp of fp16 in the worst place) and s itself as a factor: the library's
+// exponential and division take the backward kernel from 45 to 50 us at 32768 x
+// 768, where it is then bound by its instructions.
 template <class T>
 struct Sigmoid {
     float s, other;  // other = 1 - s

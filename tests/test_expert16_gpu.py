@@ -89,6 +89,9 @@ GROUPED = [
     ([1000], 2048, 64),
     ([33] * 40, 64, 2048),
     ([2, 120, 0, 700, 5, 48, 130, 1], 128, 768),
+    ([1, 0, 2, 1] * 24, 520, 1096),           # about one row an expert, widths of 8
+    ([2331], 264, 200),                       # one long segment, few tiles
+    ([40, 33, 0, 50], 1048, 104),
 ]
 
 
@@ -426,6 +429,23 @@ def test_block_norm_gradient_against_differences(M):
     tol = 2 * T * D * (d * d / 6 * 100 + 64 * 2.0 ** -24 * 4 / d)
     assert abs((f(d) - f(-d)) / (2 * d) - want) <= tol
     assert abs(want) > 3 * tol
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_block_norm_where_the_block_cancels_the_stream(M, T):
+    """x' = x + alpha gate n of a hundredth of its terms' size: its mean square
+    has to come from x' itself, not from sums of squares that cancel."""
+    D, alpha, eps = 512, 0.75, 1e-6
+    y = randn(2, torch.float32, T, D)
+    post, pre, gate = (1 + randn(i, torch.float32, D, scale=0.2) for i in (3, 4, 5))
+    gate = gate[None]
+    yd = y.double()
+    n = alpha * gate.double() * yd * ((yd * yd).mean(1, keepdim=True) + eps).rsqrt() * post.double()
+    x = (-0.99 * n).float()
+    ref = norm_reference(x, y, y, y, post, gate, pre, alpha, eps)
+    xo, h = M.block_norm(x.cuda(), y.cuda(), post.cuda(), gate.cuda(), pre.cuda(), alpha, eps)
+    close(xo, *ref["x_out"], 64, "x_out")
+    close(h, *ref["h"], 64, "h")
 
 
 def test_block_norm_of_no_rows(M):
