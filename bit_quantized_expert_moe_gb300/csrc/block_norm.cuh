@@ -54,11 +54,14 @@ struct ParamTable {
     // By every thread of the block, which then has to meet.
     __device__ __forceinline__ void fill(const Args& p) const {
         for (int c = threadIdx.x; c < p.D / 8; c += blockDim.x) {
-            V8 a = v8(p.alpha);
-            if (p.gamma_post) a = mul(load8(p.ptype, p.gamma_post, c), a);
-            if (p.gate && p.S == p.T) a = mul(load8(p.ptype, p.gate, c), a);
-            put(0, c, a);
-            if (p.gamma_pre) put(1, c, load8(p.ptype, p.gamma_pre, c));
+            // all loads first: one latency, not three
+            V8 a = v8(p.alpha), g = v8(1.f), b = v8(1.f);
+            if (p.gamma_post) a = load8(p.ptype, p.gamma_post, c);
+            if (p.gate && p.S == p.T) g = load8(p.ptype, p.gate, c);
+            if (p.gamma_pre) b = load8(p.ptype, p.gamma_pre, c);
+            if (p.gamma_post) a = mul(a, p.alpha);
+            put(0, c, mul(a, g));
+            put(1, c, b);
         }
     }
     static constexpr size_t bytes(int chunks) { return (size_t)chunks * 64; }
