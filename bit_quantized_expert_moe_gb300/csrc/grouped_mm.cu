@@ -191,8 +191,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         *abort_flag = 0;
         tc::fence_mbar_init();
-        tc::tma_prefetch_desc(&maps.a);
     }
+    // the maps that the tiles may use (see launch)
+    if (warp == 2 && lane <= p.tile_cols / 32) tc::tma_prefetch_desc(lane ? &maps.b[lane - 1] : &maps.a);
     if (warp == 1) {
         tc::tmem_alloc_pair(smem_u32((const void*)tmem_slot), TMEM_COLS);
         tc::tmem_relinquish_pair();
@@ -200,7 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // both CTAs' barriers are initialised and the tensor memory allocated
     // before either CTA signals the other
     tc::tc_fence_before();
-    __syncthreads();
+    __syncwarp();
     tc::cluster_sync();
     tc::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
@@ -476,7 +477,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // signal its barriers or use its memory
     __syncwarp();
     tc::tc_fence_before();
-    __syncthreads();
     tc::cluster_sync();
     if (warp == 1) {
         tc::tc_fence_after();
@@ -514,6 +514,7 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
     if (PR == Product::DW) {
         ok = map_2d(&maps.a, bf, a, g.N, g.R, 64, 64) && map_2d(&maps.b[0], bf, b, g.K, g.R, 64, 64) &&
              map_w(&maps.b[1], bf, out, g, 32);
+        for (int i = 2; i < BOXES; ++i) maps.b[i] = maps.b[0];
     } else {
         const int L = PR == Product::Y ? g.K : g.N;
         ok = map_w(&maps.a, bf, a, g, PR == Product::Y ? BM : 64);
