@@ -53,6 +53,11 @@ constexpr int B_BYTES = BN / 2 * BL * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int ATOM64 = 64 * BL * 2;  // MN-major: 64 l rows of 64 elements
 constexpr int STAGES = 6;
+// DW: clearing the rows behind a segment takes longer than the ring is ahead
+// of the MMAs, so a tile's ragged end is loaded first and used after this many of
+// the tile's other stages (less than STAGES - 1: its stage is given back before
+// the ring needs it).  Loaded and used last, 4096 tokens took 227 us.
+constexpr int END_DEFER = 3;
 // An epilogue warp's block on its way out: DW 32 rows of 64 columns; Y, DX 32 rows
 // r of 32 columns, 16 bytes apart so that neighbouring rows use other banks.
 template <Product PR>
@@ -267,14 +272,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const CUtensorMap* mb = &maps.b[bi];
                 const uint32_t bytes = 2 * (A_BYTES + (PR == Product::DW ? (half > 64 ? 2 : 1) * ATOM64 : box * BL * 2));
                 const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
-                for (int l = 0; l < t.nl; l += BL, ++g) {
+                const int blocks = ceil_div(t.nl, BL);
+                const bool end_first = PR == Product::DW && ragged_end(t.nl - BL * (blocks - 1));
+                for (int j = 0; j < blocks; ++j, ++g) {
+                    const int l = BL * (!end_first ? j : j == 0 ? blocks - 1 : j - 1);
                     ok = tc::mbar_wait(bar_empty + 8 * s, phase, abort_flag, p.err);
                     if (!ok) break;
                     const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
                     const uint32_t fl = full_lead + 8 * s, f = bar_full + 8 * s;
                     if (PR == Product::DW) {
                         uint32_t to = fl;
-                        if (ragged_end(t.nl - l)) {
+                        if (end_first && j == 0) {
                             to = tc::mapa_shared(bar_tail + 8 * s, rank);
                             tc::mbar_arrive_expect_tx(bar_tail + 8 * s, bytes >> 1);
                         } else if (rank == 0) {
@@ -308,8 +316,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else if (warp == 1) {
         // -------------------------------------- MMA issuer (even CTA of the pair)
         if (rank == 0 && tc::elect_one()) {
-            int s = 0, ic = 0;
-            uint32_t phase = 0;
+            int s0 = 0, ic = 0;   // the tile's first stage
+            uint32_t phase0 = 0;  // and its round's parity
             bool ok = true;
             for (int i = pair; ok && i < work.items; i += npairs) {
                 const Item t = work.item(p, i);
@@ -321,7 +329,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (!ok) break;
                 tc::tc_fence_after();
                 const uint32_t d = tmem_base + 256u * b;
-                for (int l = 0; l < t.nl; l += BL) {
+                const int blocks = ceil_div(t.nl, BL), last = t.nl - BL * (blocks - 1);
+                // a ragged end is the tile's first stage in the ring and its
+                // (defer + 1)-th here
+                const int defer = PR == Product::DW && ragged_end(last) ? min(blocks - 1, END_DEFER) : 0;
+                int next = s0;
+                uint32_t next_phase = phase0;
+                auto advance = [&] {
+                    if (++next == STAGES) {
+                        next = 0;
+                        next_phase ^= 1u;
+                    }
+                };
+                if (defer) advance();
+                for (int j = 0; j < blocks; ++j) {
+                    const bool end = defer && j == defer;
+                    const int s = end ? s0 : next;
+                    const uint32_t phase = end ? phase0 : next_phase;
+                    if (!end) advance();
                     ok = tc::mbar_wait_cluster(bar_full + 8 * s, phase, abort_flag, p.err);
                     if (!ok) break;
                     tc::tc_fence_after();
@@ -329,33 +354,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     constexpr uint32_t SA = PR == Product::Y ? 32 : 2048, SB = PR == Product::DW ? 2048 : 32;
                     const uint64_t da = PR == Product::Y ? tc::sw128_kmajor_desc(sa) : tc::sw128_mnmajor_desc(sa, ATOM64);
                     const uint64_t db = PR == Product::DW ? tc::sw128_mnmajor_desc(sb, ATOM64) : tc::sw128_kmajor_desc(sb);
-                    const int left = t.nl - l;
+                    const int left = end || (!defer && j == blocks - 1) ? last : BL;
                     // 16 l further: the start address, in units of 16 bytes
 #pragma unroll
                     for (int k = 0; k < BL / 16; ++k)
                         if (k == 0 || 16 * k < left)
-                            tc::mma_f16_pair(d, da + k * (SA >> 4), db + k * (SB >> 4), idesc, k > 0 || l > 0);
+                            tc::mma_f16_pair(d, da + k * (SA >> 4), db + k * (SB >> 4), idesc, k > 0 || j > 0);
                     tc::mma_commit_pair(bar_empty + 8 * s);
-                    if (left <= BL) tc::mma_commit_pair(bar_accfull + 8 * b);
-                    if (++s == STAGES) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
+                    if (j == blocks - 1) tc::mma_commit_pair(bar_accfull + 8 * b);
                 }
+                s0 = next;
+                phase0 = next_phase;
                 ++ic;
             }
         }
     } else if (PR == Product::DW && warp == 2) {
         // ------------------------- ragged ends: clears the rows behind a segment
         const uint32_t full_lead = tc::mapa_shared(bar_full, 0);
-        int s = 0;
+        int s = 0;            // the tile's first stage
         uint32_t phases = 0;  // of the tail barriers, which are not used in every round
         bool ok = true;
         for (int i = pair; ok && i < work.items; i += npairs) {
             const Item t = work.item(p, i);
             if (t.nl == 0) continue;
-            s = (s + (t.nl - 1) / BL) % STAGES;  // the tile's last stage
-            const int left = t.nl - (t.nl - 1) / BL * BL, end = (left + 15) & ~15;
+            const int blocks = ceil_div(t.nl, BL), left = t.nl - BL * (blocks - 1), end = (left + 15) & ~15;
             if (ragged_end(left)) {
                 ok = tc::mbar_wait(bar_tail + 8 * s, (phases >> s) & 1u, abort_flag, p.err);
                 ok = __all_sync(0xffffffffu, ok);
@@ -368,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive_cluster_release(full_lead + 8 * s);
             }
-            s = (s + 1) % STAGES;
+            s = (s + blocks) % STAGES;
         }
     } else if (warp >= EP_WARP0) {
         // ---------------------------------------------------------- epilogue
