@@ -9,8 +9,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/zeros.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -115,16 +115,27 @@ struct Args {
         if (d == -1.0 && PyErr_Occurred()) throw Raised{};
         return (float)d;
     }
-    // The current stream where none is given; `of` has to be on a device.
-    cudaStream_t stream(size_t i, const Tensor& of) const {
+};
+
+// The stream of a call on `of`, which has to be on a device: the one given, else
+// the current one.  While this lives the given one is current, so that what the
+// call allocates belongs to the stream that writes it.
+struct OnStream {
+    cudaStream_t s;
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    template <size_t N>
+    OnStream(const Args<N>& a, size_t i, const Tensor& of) {
         ptr(of);
-        if (!given(i)) return c10::cuda::getCurrentCUDAStream().stream();
-        PyObject* h = PyObject_GetAttrString(v[i], "cuda_stream");
+        if (!a.given(i)) {
+            s = c10::cuda::getCurrentCUDAStream().stream();
+            return;
+        }
+        PyObject* h = PyObject_GetAttrString(a.v[i], "cuda_stream");
         if (!h) throw Raised{};
-        void* p = PyLong_AsVoidPtr(h);
+        s = static_cast<cudaStream_t>(PyLong_AsVoidPtr(h));
         Py_DECREF(h);
-        if (!p && PyErr_Occurred()) throw Raised{};
-        return static_cast<cudaStream_t>(p);
+        if (!s && PyErr_Occurred()) throw Raised{};
+        guard.reset_stream(c10::cuda::getStreamFromExternal(s, of.device().index()));
     }
 };
 
@@ -164,12 +175,14 @@ Tensor output(const Tensor& given, const char* what, const Tensor& like, Shape s
         want(what, given, shape, type);
         return given;
     }
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+    if (!like.is_cuda()) throw Refusal("device tensor expected");
+    // Straight from the CUDA allocator: 0.3 us less per output than at::empty's
+    // dispatch, of the 3.8 us that the smallest call takes.
+    return at::detail::empty_cuda(shape, type, like.device(), c10::nullopt);
 }
-// The workspace given, or a new zeroed one.
+// The workspace given, or a new one; `like` as for output().
 Tensor workspace(const Tensor& given, size_t bytes, const Tensor& like) {
-    if (given.defined()) return given;
-    return at::zeros({(int64_t)std::max<size_t>(bytes, 256)}, at::TensorOptions().dtype(at::kByte).device(like.device()));
+    return given.defined() ? given : output(given, "ws", like, {(int64_t)std::max<size_t>(bytes, 256)}, at::kByte);
 }
 PyObject* wrap(const Tensor& t) {
     if (!t.defined()) Py_RETURN_NONE;
@@ -220,8 +233,9 @@ PyObject* py_grouped_mm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject
         dims("w", w, 3);
         const int64_t R = x.size(0), K = x.size(1), E = w.size(0), N = w.size(1);
         want("w", w, {E, N, K}, x.scalar_type());
+        const OnStream on(a, 5, x);
         const Tensor y = output(a.tensor(3), "y", x, {R, N}, x.scalar_type());
-        return grouped(moe_grouped_mm, "moe_grouped_mm", x, w, off, R, E, N, K, y, a.tensor(4), a.stream(5, x));
+        return grouped(moe_grouped_mm, "moe_grouped_mm", x, w, off, R, E, N, K, y, a.tensor(4), on.s);
     });
 }
 PyObject* py_grouped_mm_dx(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
@@ -233,8 +247,9 @@ PyObject* py_grouped_mm_dx(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
         dims("w", w, 3);
         const int64_t R = dy.size(0), N = dy.size(1), E = w.size(0), K = w.size(2);
         want("w", w, {E, N, K}, dy.scalar_type());
+        const OnStream on(a, 5, dy);
         const Tensor dx = output(a.tensor(3), "dx", dy, {R, K}, dy.scalar_type());
-        return grouped(moe_grouped_mm_dx, "moe_grouped_mm_dx", dy, w, off, R, E, N, K, dx, a.tensor(4), a.stream(5, dy));
+        return grouped(moe_grouped_mm_dx, "moe_grouped_mm_dx", dy, w, off, R, E, N, K, dx, a.tensor(4), on.s);
     });
 }
 PyObject* py_grouped_mm_dw(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
@@ -246,8 +261,9 @@ PyObject* py_grouped_mm_dw(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
         dims("x", x, 2);
         const int64_t R = dy.size(0), N = dy.size(1), K = x.size(1), E = off.numel() - 1;
         want("x", x, {R, K}, dy.scalar_type());
+        const OnStream on(a, 5, dy);
         const Tensor dw = output(a.tensor(3), "dw", dy, {E, N, K}, dy.scalar_type());
-        return grouped(moe_grouped_mm_dw, "moe_grouped_mm_dw", dy, x, off, R, E, N, K, dw, a.tensor(4), a.stream(5, dy));
+        return grouped(moe_grouped_mm_dw, "moe_grouped_mm_dw", dy, x, off, R, E, N, K, dw, a.tensor(4), on.s);
     });
 }
 
@@ -267,9 +283,10 @@ PyObject* py_swiglu(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw
         const Tensor gu = a.needed_tensor(0), row_w = a.tensor(1), row_map = a.tensor(2);
         const int64_t F = gated_width(gu, row_w, row_map), R = gu.size(0);
         const moe_dtype_t dt = moe_type(gu.scalar_type());
+        const OnStream on(a, 4, gu);
         const Tensor h = output(a.tensor(3), "h", gu, {R, F}, gu.scalar_type());
         check(moe_swiglu(dt, ptr(gu), ptr_as<float>(row_w), ptr_as<int32_t>(row_map), size32(R), size32(F), ptr(h),
-                         a.stream(4, gu)), "moe_swiglu");
+                         on.s), "moe_swiglu");
         return wrap(h);
     });
 }
@@ -282,11 +299,12 @@ PyObject* py_swiglu_backward(PyObject*, PyObject* const* args, Py_ssize_t n, PyO
         const at::ScalarType t = gu.scalar_type();
         const moe_dtype_t dt = moe_type(t);
         want("dh", dh, {R, F}, t);
+        const OnStream on(a, 6, gu);
         const Tensor dgu = output(a.tensor(4), "dgu", gu, {R, 2 * F}, t);
         Tensor dw = a.tensor(5);
         if (dw.defined() || row_w.defined()) dw = output(dw, "drow_w", gu, {R}, at::kFloat);
         check(moe_swiglu_backward(dt, ptr(dh), ptr(gu), ptr_as<float>(row_w), ptr_as<int32_t>(row_map), size32(R),
-                                  size32(F), ptr(dgu), ptr_as<float>(dw), a.stream(6, gu)), "moe_swiglu_backward");
+                                  size32(F), ptr(dgu), ptr_as<float>(dw), on.s), "moe_swiglu_backward");
         return wrap_all({dgu, dw});
     });
 }
@@ -325,11 +343,12 @@ PyObject* py_block_norm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject
         const Tensor x = a.needed_tensor(0), y = a.tensor(1), post = a.tensor(2), gate = a.tensor(3), pre = a.tensor(4);
         const Norm m(x, post, gate, pre);
         m.row("y", y);
+        const OnStream on(a, 9, x);
         Tensor xo = a.tensor(7), h = a.tensor(8);
         if (xo.defined() || y.defined()) xo = output(xo, "x_out", x, {m.T, m.D}, m.type);
         if (h.defined() || pre.defined()) h = output(h, "h", x, {m.T, m.D}, m.type);
         check(moe_block_norm(m.dt, m.pt, size32(m.T), size32(m.D), size32(m.G), a.number(5, 1.0), a.number(6, 1e-6),
-                             ptr(post), ptr(gate), ptr(pre), ptr(x), ptr(y), ptr(xo), ptr(h), a.stream(9, x)), "moe_block_norm");
+                             ptr(post), ptr(gate), ptr(pre), ptr(x), ptr(y), ptr(xo), ptr(h), on.s), "moe_block_norm");
         return wrap_all({xo, h});
     });
 }
@@ -345,6 +364,7 @@ PyObject* py_block_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n,
         m.row("dx_out", dxo);
         m.row("dh", dh);
         const int32_t T = size32(m.T), D = size32(m.D), G = size32(m.G);
+        const OnStream on(a, 10, x);
         const Tensor none;
         const Tensor dx = output(none, "dx", x, {m.T, m.D}, m.type);
         const Tensor dy = y.defined() ? output(none, "dy", x, {m.T, m.D}, m.type) : none;
@@ -354,7 +374,7 @@ PyObject* py_block_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n,
         const Tensor ws = workspace(given_ws, given_ws.defined() ? 0 : moe_block_norm_backward_workspace_size(T, D, G), x);
         check(moe_block_norm_backward(m.dt, m.pt, T, D, G, a.number(7, 1.0), a.number(8, 1e-6), ptr(post), ptr(gate),
                                       ptr(pre), ptr(x), ptr(y), ptr(dxo), ptr(dh), ptr(dx), ptr(dy), ptr(dpost), ptr(dgate),
-                                      ptr(dpre), ptr(ws), (size_t)ws.numel(), a.stream(10, x)), "moe_block_norm_backward");
+                                      ptr(dpre), ptr(ws), (size_t)ws.numel(), on.s), "moe_block_norm_backward");
         return wrap_all({dx, dy, dpost, dgate, dpre});
     });
 }
@@ -370,7 +390,8 @@ PyObject* py_init(PyObject*, PyObject* check_fn) {
 PyMethodDef methods[] = {
     {"grouped_mm", FAST(py_grouped_mm),
      "grouped_mm(x, w, offsets, y=None, ws=None, stream=None) -> y\n\n"
-     "y[r] = w[e] x[r] for the rows r of every expert e: x [R, K], w [E, N, K], offsets [E + 1] of permute()."},
+     "y[r] = w[e] x[r] for the rows r of every expert e: x [R, K], w [E, N, K], offsets [E + 1] of permute().\n"
+     "Offsets out of order or range set the error word of ws, for get_device_error(ws); without ws it is lost."},
     {"grouped_mm_dx", FAST(py_grouped_mm_dx),
      "grouped_mm_dx(dy, w, offsets, dx=None, ws=None, stream=None) -> dx\n\n"
      "Gradient of grouped_mm in x: dx[r] = dy[r] w[e]."},

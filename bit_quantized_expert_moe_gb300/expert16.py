@@ -11,7 +11,10 @@ the gated activation with the routing weight, and the norms around a block.
     block_norm_backward(x_out, y=None, dx_out=None, dh=None, gamma_post=None, gate=None, gamma_pre=None, alpha=1.0,
                         eps=1e-6, ws=None, stream=None)
 
-`offsets` and `row_map` are the `offsets` and `sorted` of permute().  The
+`offsets` and `row_map` are the `offsets` and `sorted` of permute().  Offsets
+out of order or range set the error word of the `ws` that was given, which
+get_device_error(ws) reads; without one nobody learns of them.  Outputs and
+workspaces that are not given belong to the call's stream.  The
 functions are compiled (csrc/expert16_binding.cpp, argument marshalling only);
 this module loads them at their first use.
 """

@@ -481,3 +481,23 @@ def test_operators_on_a_side_stream(M):
     s.synchronize()
     assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1]) and torch.equal(sgot, sref)
     assert all(a is None or torch.equal(a, b) for a, b in zip(ggot, gref))
+
+
+def test_outputs_belong_to_the_given_stream(M):
+    """What a call allocates comes from the pool of the stream that writes it."""
+    s = torch.cuda.Stream()
+    x, w, p = randn(1, torch.bfloat16, 64, 64).cuda(), randn(2, torch.bfloat16, 2, 64, 64).cuda(), torch.ones(64, dtype=torch.bfloat16).cuda()
+    off, half, rw = torch.tensor([0, 30, 64], dtype=torch.int32).cuda(), x[:, :32].contiguous(), torch.ones(64).cuda()
+    torch.cuda.synchronize()
+    outs = [M.grouped_mm(x, w, off, stream=s), M.grouped_mm_dx(x, w, off, stream=s), M.grouped_mm_dw(x, x, off, stream=s),
+            M.swiglu(x, stream=s), *M.swiglu_backward(half, x, rw, stream=s)]
+    s.synchronize()
+    outs += [*M.block_norm(x, x, p, None, p, stream=s), *M.block_norm_backward(x, x, x, x, p, None, p, stream=s)]
+    s.synchronize()
+    pools = {}
+    for seg in torch.cuda.memory_snapshot():
+        pools[range(seg["address"], seg["address"] + seg["total_size"])] = seg["stream"]
+    for t in outs:
+        if t is not None:
+            assert [v for k, v in pools.items() if t.data_ptr() in k] == [s.cuda_stream]
+    assert torch.cuda.current_stream() != s
