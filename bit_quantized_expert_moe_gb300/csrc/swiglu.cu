@@ -10,37 +10,55 @@
 namespace moe {
 namespace {
 
-// s(a) = 1 / (1 + e^-a) from t = e^-|a|, so that nothing overflows: 1 / (1 + t)
-// for a >= 0, t / (1 + t) below.  16-bit outputs: the hardware's exponential
-// and reciprocal (relative error below 2^-20 for |a| < 100, an eighth of the
-// half ulp of fp16 in the worst place) and s itself as a factor: the library's
-// exponential and division take the backward kernel from 45 to 50 us at 32768 x
-// 768, where it is then bound by its instructions.
+// SiLU and its slope for two gates a, s(a) = 1 / (1 + e^-a) from t = e^-|a|, so
+// that nothing overflows: 1 / (1 + t) for a >= 0, t / (1 + t) below.  Each is
+// a factor by itself before the others come in: where s is 0, a (its type's
+// lowest value even) times s is 0 and stays 0.  16-bit outputs: the hardware's
+// exponential and reciprocal (relative error below 2^-20 for a > -87, an eighth
+// of the half ulp of fp16 in the worst place; s is subnormal below): the
+// library's exponential and division take the backward kernel from 45 to 50 us
+// at 32768 x 768, where it is then bound by its instructions.
 template <class T>
-struct Sigmoid {
-    float s, other;  // other = 1 - s
-    __device__ __forceinline__ explicit Sigmoid(float a) {
+struct Silu {
+    float2 as, ss;  // a s, s (1 + a (1 - s))
+    __device__ __forceinline__ static void sigmoid(float a, float& s, float& other) {
         const float t = __expf(-fabsf(a));
         const float inv = __fdividef(1.f, 1.f + t);
         s = a < 0.f ? t * inv : inv;
         other = 1.f - s;
     }
-    __device__ __forceinline__ float times(float v) const { return v * s; }
+    __device__ __forceinline__ explicit Silu(float2 a) {
+        float2 s, other;
+        sigmoid(a.x, s.x, other.x);
+        sigmoid(a.y, s.y, other.y);
+        as = f2_mul(a, s);
+        ss = f2_mul(s, ffma2(a, other, f2(1.f)));
+    }
+    __device__ __forceinline__ float2 times(float2 v) const { return f2_mul(v, as); }
+    __device__ __forceinline__ float2 times_slope(float2 v) const { return f2_mul(v, ss); }
 };
 // fp32 outputs: s = q^2 / (1 + t^2) with t = e^(-|a| / 2) and q = 1 or t; a
-// product that takes the two factors q last underflows no earlier than its
-// value does, and 1 - s does not cancel.
+// product that takes one factor q last underflows no earlier than its value
+// does, and 1 - s does not cancel.
 template <>
-struct Sigmoid<F32> {
-    float inv, q, other;
-    __device__ __forceinline__ explicit Sigmoid(float a) {
-        const float t = expf(-0.5f * fabsf(a));
-        inv = 1.f / (1.f + t * t);
-        q = a < 0.f ? t : 1.f;
+struct Silu<F32> {
+    float2 as, ss, q;  // without a factor q
+    __device__ __forceinline__ static void sigmoid(float a, float& s, float& q, float& other) {
+        const float t = expf(-0.5f * fabsf(a)), inv = 1.f / (1.f + t * t);
         const float qo = a < 0.f ? 1.f : t;
+        q = a < 0.f ? t : 1.f;
+        s = inv * q;
         other = inv * qo * qo;
     }
-    __device__ __forceinline__ float times(float v) const { return v * inv * q * q; }
+    __device__ __forceinline__ explicit Silu(float2 a) {
+        float2 s, other;
+        sigmoid(a.x, s.x, q.x, other.x);
+        sigmoid(a.y, s.y, q.y, other.y);
+        as = f2_mul(a, s);
+        ss = f2_mul(s, ffma2(a, other, f2(1.f)));
+    }
+    __device__ __forceinline__ float2 times(float2 v) const { return f2_mul(f2_mul(v, as), q); }
+    __device__ __forceinline__ float2 times_slope(float2 v) const { return f2_mul(f2_mul(v, ss), q); }
 };
 
 // Weight index of row r, -1 when the map's entry is out of range.
@@ -66,10 +84,9 @@ __global__ void __launch_bounds__(256) swiglu_kernel(const void* __restrict__ gu
         }
         const V8 a = load8<T>(gu, (size_t)r * 2 * chunks + c);
         const V8 u = load8<T>(gu, (size_t)r * 2 * chunks + chunks + c);
-        V8 v = mul(mul(a, w), u);
+        V8 v = mul(u, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v.p[j] = make_float2(Sigmoid<T>(a.p[j].x).times(v.p[j].x), Sigmoid<T>(a.p[j].y).times(v.p[j].y));
+        for (int j = 0; j < 4; ++j) v.p[j] = Silu<T>(a.p[j]).times(v.p[j]);
         store8<T>(h, (size_t)i, v);
     }
 }
@@ -126,17 +143,15 @@ __global__ void __launch_bounds__(256)
             const int c = c0 + rg.tid;
             if (c < chunks) {
                 const V8 a = unpack8<T>(ring.get(0)), u = unpack8<T>(ring.get(1)), d = unpack8<T>(ring.get(2));
-                const V8 du = mul(d, u), da = mul(d, a);
-                const V8 dua = mul(du, a), wda = mul(da, w), wdu = mul(du, w);
+                const V8 du = mul(d, u), wd = mul(d, w), wdu = mul(du, w);
                 V8 ga, gu_;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const Sigmoid<T> s(a.p[j].x), t(a.p[j].y);
-                    const float2 slope = ffma2(a.p[j], make_float2(s.other, t.other), f2(1.f));
-                    const float2 q = f2_mul(wdu.p[j], slope);
-                    sum += s.times(dua.p[j].x) + t.times(dua.p[j].y);
-                    gu_.p[j] = make_float2(s.times(wda.p[j].x), t.times(wda.p[j].y));
-                    ga.p[j] = make_float2(s.times(q.x), t.times(q.y));
+                    const Silu<T> f(a.p[j]);
+                    const float2 h = f.times(du.p[j]);
+                    sum += h.x + h.y;
+                    gu_.p[j] = f.times(wd.p[j]);
+                    ga.p[j] = f.times_slope(wdu.p[j]);
                 }
                 store8<T>(dgu, (size_t)r * 2 * chunks + c, ga);
                 store8<T>(dgu, (size_t)r * 2 * chunks + chunks + c, gu_);

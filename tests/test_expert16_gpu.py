@@ -296,6 +296,28 @@ def test_swiglu_skips_entries_outside_the_map(M):
     assert not dgu[1:3].any() and drow[1] == 7 and drow[3] == 7 and drow[0] != 7 and drow[2] != 7
 
 
+@pytest.mark.parametrize("dtype", ALL)
+def test_swiglu_of_the_lowest_gate(M, dtype):
+    """SiLU and its slope at the type's lowest values are zero, whatever the
+    other factors (nothing in between may overflow)."""
+    R, F = 3, 64
+    low = torch.finfo(dtype).min
+    gu, dh = randn(1, dtype, R, 2 * F, scale=8.0), randn(2, dtype, R, F, scale=8.0)
+    gu[:, :F:2] = low
+    gu[:, 1:F:4] = low / 2
+    row_w = torch.full((R,), 8.0)
+    h = M.swiglu(gu.cuda(), row_w.cuda())
+    dgu, drow = M.swiglu_backward(dh.cuda(), gu.cuda(), row_w.cuda())
+    h, dgu = h.cpu(), dgu.cpu()
+    rest = gu[:, :F] > low / 2
+    for t in (h, dgu[:, :F], dgu[:, F:]):
+        assert not t[~rest].any() and torch.isfinite(t.float()).all()
+    # and they add nothing to the routing weight's gradient
+    a, u, d = gu[:, :F].double(), gu[:, F:].double(), dh.double()
+    terms = torch.where(rest, d * a / (1 + torch.exp(-a)) * u, 0.0)
+    close(drow.cpu(), terms.sum(1), terms.abs().sum(1), 64 + F / 8, "drow_w")
+
+
 # ----------------------------------------------------------------- block norms
 def norm_reference(x, y, dx_out, dh, post, gate, pre, alpha, eps):
     """Forward at (x, y), backward at (x as the stored stream, y); with the
