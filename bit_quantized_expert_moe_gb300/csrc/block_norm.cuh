@@ -55,14 +55,19 @@ struct ParamTable {
     __device__ __forceinline__ void fill(const Args& p) const {
         for (int c = threadIdx.x; c < p.D / 8; c += blockDim.x) {
             // all loads first: one latency, not three
-            V8 a = v8(p.alpha), g = v8(1.f), b = v8(1.f);
-            if (p.gamma_post) a = load8(p.ptype, p.gamma_post, c);
-            if (p.gate && p.S == p.T) g = load8(p.ptype, p.gate, c);
+            V8 b = v8(1.f);
             if (p.gamma_pre) b = load8(p.ptype, p.gamma_pre, c);
-            if (p.gamma_post) a = mul(a, p.alpha);
-            put(0, c, mul(a, g));
+            fill_a(p, c, c, p.gate && p.S == p.T);
             put(1, c, b);
         }
+    }
+    // A of chunk c, with the gate's chunk g if there is one to be included.
+    __device__ __forceinline__ void fill_a(const Args& p, int c, size_t g, bool gated) const {
+        V8 a = v8(p.alpha), k = v8(1.f);
+        if (p.gamma_post) a = load8(p.ptype, p.gamma_post, c);
+        if (gated) k = load8(p.ptype, p.gate, g);
+        if (p.gamma_post) a = mul(a, p.alpha);
+        put(0, c, mul(a, k));
     }
     static constexpr size_t bytes(int chunks) { return (size_t)chunks * 64; }
 };

@@ -21,8 +21,11 @@ constexpr int BLOCK_THREADS = 512;  // most threads of a block: 128 registers ea
 // The parameters' gradients add up in registers.  While the gate row stays the
 // same, gate and gamma_post are factors of one sum z = sum D y r1:
 // dgate = alpha gamma_post z, dgamma_post = sum over gate rows of alpha gate z.
-// A gate row that lies wholly inside the group's rows is written at once; its
-// first and last one may be shared with the neighbours and go to gate_part.
+// A gate row that lies wholly inside the group's rows is written at once; one
+// that is shared with the neighbours, the group's first or last, goes to gate_part.
+// A chunk's tensors stay in registers for the second half of a row (VPT = 1) or are
+// taken a second time from where they lie (4096 x 5120 fp32 171 -> 120 us, where
+// they did not all fit; bf16 with 64 gates 161 -> 81).
 // ALL: y, gamma_post, gamma_pre, dx' and dh are there and the rows share one gate.
 template <class T, int VPT, int SLOTS, bool ALL>
 __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(const Args p) {
@@ -33,6 +36,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(c
     const int grp = threadIdx.x / p.threads;
     RowGroup rg(p.threads, grp, smem + grp * RowGroup::SUM_FLOATS);
     const int chunks = p.D / 8, n = VPT * p.threads;
+    const bool one_gate = p.S == p.T, row_gate = !ALL && p.gate && !one_gate;
     const ParamTable table(smem + p.groups * RowGroup::SUM_FLOATS, n);
     float* const space = smem + p.groups * RowGroup::SUM_FLOATS + 16 * n;
     // places in a slot: x', dh, dx', y
@@ -40,8 +44,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(c
     const float inv_d = 1.f / (float)p.D;
     const int vb = blockIdx.x * p.groups + grp;
     const int r_begin = min(p.T, vb * p.rows), r_end = min(p.T, r_begin + p.rows);
-    const int g_first = r_begin / p.S, g_last = (r_end - 1) / p.S;
-    const bool one_gate = p.S == p.T, row_gate = !ALL && p.gate && !one_gate;
+    const int g_first = r_begin / p.S;
     constexpr size_t CH = 8 * T::BYTES;
     const bool has_y = ALL || p.y, has_post = ALL || p.gamma_post, has_dh = ALL || p.dh, has_dx = ALL || p.dx_out;
     const size_t row_bytes = (size_t)chunks * CH, next = CH * p.threads;
@@ -74,14 +77,17 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(c
     for (int i = threadIdx.x; i < p.groups * RowGroup::SUM_FLOATS; i += blockDim.x) smem[i] = 0.f;
     __syncthreads();
     V8 a_post[VPT], a_pre[VPT], z[VPT];
-    V8 ka[VPT == 1 ? 1 : VPT], kb[VPT == 1 ? 1 : VPT];  // the parameters of this row: kept for VPT = 1
+    V8 ka = v8(0.f), kb = v8(0.f);  // the parameters of a chunk: kept for VPT = 1
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) a_post[i] = a_pre[i] = z[i] = ka[i] = kb[i] = v8(0.f);
-    // A of row r's gate and B into ka, kb
-    auto params = [&](int i, int c, size_t grow) {
-        ka[i] = table.get(0, c);
-        if (row_gate) ka[i] = mul(ka[i], load8(p.ptype, p.gate, grow + c));
-        if (has_dh) kb[i] = table.get(1, c);
+    for (int i = 0; i < VPT; ++i) a_post[i] = a_pre[i] = z[i] = v8(0.f);
+    // A and B into ka, kb.  VPT = 1: when a gate begins, its row at chunk grow.
+    // Else: before each use; a block is one row group then (of more than 256
+    // threads), and its table's A is filled again when a gate begins, by the thread
+    // that reads it.
+    auto params = [&](int c, size_t grow) {
+        ka = table.get(0, c);
+        if (VPT == 1 && row_gate) ka = mul(ka, load8(p.ptype, p.gate, grow + c));
+        if (has_dh) kb = table.get(1, c);
     };
     bool fresh = true;  // the row is the first of its gate here
     for (int r = r_begin; r < r_end; ++r, off += row_bytes) {
@@ -91,36 +97,44 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(c
             fetch();
             ring.wait();
         }
-        typename T::Raw rx[VPT], rdh[VPT], rdx[VPT], ry[VPT];
+        // a chunk of the row's tensors: kept (VPT = 1) or taken a second time
+        struct Chunk {
+            typename T::Raw x, dh, dx, y;
+        } kept;
+        auto load = [&](int i) {
+            Chunk k{};
+            if (has_dh) {
+                k.x = SLOTS > 1 ? ring.get(i) : raw_at<T>(p.x, off + i * next);
+                k.dh = SLOTS > 1 ? ring.get(VPT + i) : raw_at<T>(p.dh, off + i * next);
+            }
+            if (has_dx) k.dx = SLOTS > 1 ? ring.get(2 * VPT + i) : raw_at<T>(p.dx_out, off + i * next);
+            if (has_y) k.y = SLOTS > 1 ? ring.get(3 * VPT + i) : raw_at<T>(p.y, off + i * next);
+            return k;
+        };
         float2 s[6];
 #pragma unroll
         for (int k = 0; k < 6; ++k) s[k] = f2(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = i * p.threads + rg.tid;
-            rx[i] = rdh[i] = rdx[i] = ry[i] = typename T::Raw{};
             if (in[i]) {
-                if (has_dh) {
-                    rx[i] = SLOTS > 1 ? ring.get(i) : raw_at<T>(p.x, off + i * next);
-                    rdh[i] = SLOTS > 1 ? ring.get(VPT + i) : raw_at<T>(p.dh, off + i * next);
-                }
-                if (has_dx) rdx[i] = SLOTS > 1 ? ring.get(2 * VPT + i) : raw_at<T>(p.dx_out, off + i * next);
-                if (has_y) ry[i] = SLOTS > 1 ? ring.get(3 * VPT + i) : raw_at<T>(p.y, off + i * next);
-                if (VPT > 1 || fresh) params(i, c, grow);
-                const V8 x = unpack8<T>(rx[i]), v = mul(unpack8<T>(rdh[i]), kb[i]), y = unpack8<T>(ry[i]);
+                const Chunk k = load(i);
+                if (VPT == 1) kept = k;
+                if (VPT > 1 && row_gate && fresh) table.fill_a(p, c, grow + c, true);
+                if (VPT > 1 || fresh) params(c, grow);
+                const V8 x = unpack8<T>(k.x), v = mul(unpack8<T>(k.dh), kb), y = unpack8<T>(k.y);
                 dot(s[0], x, x);
                 dot(s[1], v, x);
                 if (has_post) {
-                    const V8 w = mul(ka[i], y);
+                    const V8 w = mul(ka, y);
                     dot(s[2], y, y);
-                    dot(s[3], w, unpack8<T>(rdx[i]));
+                    dot(s[3], w, unpack8<T>(k.dx));
                     dot(s[4], w, v);
                     dot(s[5], w, x);
                 }
             }
         }
         fresh = false;
-        ring.next();
         float t[6];
 #pragma unroll
         for (int k = 0; k < 6; ++k) t[k] = s[k].x + s[k].y;
@@ -133,18 +147,20 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(c
         for (int i = 0; i < VPT; ++i) {
             const int c = i * p.threads + rg.tid;
             if (in[i]) {
-                if (VPT > 1) params(i, c, grow);
-                const V8 x = unpack8<T>(rx[i]), dh = mul(unpack8<T>(rdh[i]), r2);
+                const Chunk k = VPT == 1 ? kept : load(i);
+                if (VPT > 1) params(c, grow);
+                const V8 x = unpack8<T>(k.x), dh = mul(unpack8<T>(k.dh), r2);
                 a_pre[i] = fma(dh, x, a_pre[i]);
-                const V8 d = fma(x, -c2, fma(dh, kb[i], unpack8<T>(rdx[i])));
+                const V8 d = fma(x, -c2, fma(dh, kb, unpack8<T>(k.dx)));
                 store_at<T>(p.dx, off + i * next, d);
                 if (has_y) {
-                    const V8 y = unpack8<T>(ry[i]), dr = mul(d, r1);
+                    const V8 y = unpack8<T>(k.y), dr = mul(d, r1);
                     z[i] = fma(dr, y, z[i]);
-                    store_at<T>(p.dy, off + i * next, fma(y, -c1, mul(dr, ka[i])));
+                    store_at<T>(p.dy, off + i * next, fma(y, -c1, mul(dr, ka)));
                 }
             }
         }
+        ring.next();
         // the gate row ends here
         if (has_y && (r + 1 == r_end || (!ALL && r + 1 == (g + 1) * p.S))) {
             fresh = true;
@@ -158,9 +174,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(c
                     z[i] = one_gate ? w : v8(0.f);
                     if (p.dgate && !one_gate) {
                         float* gp = p.gate_part + (size_t)vb * 2 * p.D;
-                        if (g == g_first) store8<F32>(gp, c, w);
-                        else if (g == g_last) store8<F32>(gp + p.D, c, w);
-                        else store8(p.ptype, p.dgate, grow + c, w);
+                        if (g * p.S >= r_begin && r_end - g * p.S >= p.S) store8(p.ptype, p.dgate, grow + c, w);
+                        else store8<F32>(gp + (g == g_first ? 0 : p.D), c, w);
                     }
                 }
             }
@@ -207,10 +222,11 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(c
 // Sums partial sums in their order, 32 columns a block.  gamma_post and
 // gamma_pre (and the one gate row that all rows share): 32 threads a column,
 // so that a thread's few loads are all under way at once.  A gate row of
-// several: the row groups that share it are few, 8 threads a column and four
-// gate rows a block.  Launched as a programmatic dependent: it starts beside
-// the gradients' kernel and waits for its results here.
-__global__ void __launch_bounds__(1024) block_norm_reduce_kernel(const Args p, int sums, int gates) {
+// several that row groups share: the groups are few, 8 threads a column and four
+// gate rows a block; there are at most `shared` such rows.  Launched as a
+// programmatic dependent: it starts beside the gradients' kernel and waits for
+// its results here.
+__global__ void __launch_bounds__(1024) block_norm_reduce_kernel(const Args p, int sums, int shared) {
     __shared__ float red[32][33];
     grid_dependency_launch();
     grid_dependency_wait();
@@ -232,14 +248,14 @@ __global__ void __launch_bounds__(1024) block_norm_reduce_kernel(const Args p, i
         if (tx == 0 && blockIdx.x * 32 + ty < p.D) store1(p.ptype, out, blockIdx.x * 32 + ty, t[0]);
         return;
     }
-    for (int g0 = 4 * ((int)blockIdx.y - sums); g0 < gates; g0 += 4 * ((int)gridDim.y - sums)) {
-        const int g = g0 + (ty >> 3);
-        const bool in = g < gates && col < p.D;
-        const int first = in ? g * p.S : 0, end = first + p.S;  // the gate row's rows
+    for (int j0 = 4 * ((int)blockIdx.y - sums); j0 < shared; j0 += 4 * ((int)gridDim.y - sums)) {
+        const int j = j0 + (ty >> 3);
+        // gate row j, or the one that the row groups j and j + 1 share
+        const bool by_gate = p.S >= p.rows;
+        const int g = by_gate ? j : (int)((long long)(j + 1) * p.rows / p.S);
+        const int first = g * p.S, end = first + p.S;  // the gate row's rows
         const int b0 = first / p.rows, b1 = (end - 1) / p.rows;
-        // rows wholly inside one row group, and neither its first nor its last
-        // gate row, were written there
-        const bool todo = in && !(b0 == b1 && b0 * p.rows < first && min(p.T, (b0 + 1) * p.rows) > end);
+        const bool todo = j < shared && col < p.D && b0 != b1 && (by_gate || b0 == j);
         float s = 0.f;
         if (todo)
 #pragma unroll 4
@@ -292,9 +308,14 @@ cudaError_t run_backward(const Args& p, const BackwardPlan& b, bool all, cudaStr
 
 cudaError_t run_reduce(const Args& p, cudaStream_t s) {
     const bool one_gate = p.S == p.T;
-    const int sums = p.dgate && one_gate ? 3 : 2, gates = p.dgate && !one_gate ? p.T / p.S : 0;
-    return launch_overlapped(block_norm_reduce_kernel, dim3(ceil_div(p.D, 32), sums + std::min(ceil_div(gates, 4), 1024)),
-                             dim3(32, 32), 0, s, p, sums, gates);
+    const int sums = p.dgate && one_gate ? 3 : 2;
+    // gate rows of at least a group's rows: each may be shared; smaller ones: one
+    // for two neighbouring groups, and none where every group starts with a gate
+    // row (2048 x 4096 with a gate for every row: 287 -> 47 us, when every gate row
+    // had its blocks here)
+    const int shared = !p.dgate || one_gate ? 0 : p.S >= p.rows ? p.T / p.S : p.rows % p.S ? ceil_div(p.T, p.rows) - 1 : 0;
+    return launch_overlapped(block_norm_reduce_kernel, dim3(ceil_div(p.D, 32), sums + std::min(ceil_div(shared, 4), 1024)),
+                            dim3(32, 32), 0, s, p, sums, shared);
 }
 
 }  // namespace

@@ -426,6 +426,37 @@ def test_block_norm(M, T, D, G, has_post, has_y, has_pre, has_dxo, dtype, params
     assert all(a is None or torch.equal(a, b) for a, b in zip(again, grads.values()))
 
 
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("T,D,G", [
+    (6999, 64, 2333),   # gates shorter than the rows of a row group, some shared by two
+    (7000, 64, 3500),   # and none shared
+    (7000, 64, 1000),   # longer
+    (1200, 4104, 400),
+    (1200, 4104, 24),
+    (608, 8200, 304),
+    (610, 8200, 122),
+])
+def test_block_norm_of_many_gates(M, T, D, G, dtype):
+    test_block_norm(M, T, D, G, True, True, True, True, dtype, "same")
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("D", [264, 2048, 5120, 8200])
+def test_block_norm_gradient_in_place(M, D, dtype):
+    """dx may be dx_out."""
+    T = 310
+    x, y, dxo, dh = (randn(i, dtype, T, D).cuda() for i in range(4))
+    post, gate, pre = (randn(4 + i, dtype, *s).cuda() for i, s in enumerate([(D,), (5, D), (D,)]))
+    want = M.block_norm_backward(x, y, dxo, dh, post, gate, pre)
+    ws = M.workspace(M.block_norm_backward_workspace_size(T, D, 5))
+    dx, dy = dxo.clone(), torch.empty_like(y)
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}[dtype]
+    st = M.lib().moe_block_norm_backward(code, code, T, D, 5, 1.0, 1e-6, post.data_ptr(), gate.data_ptr(), pre.data_ptr(),
+                                         x.data_ptr(), y.data_ptr(), dx.data_ptr(), dh.data_ptr(), dx.data_ptr(), dy.data_ptr(),
+                                         None, None, None, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == M.MOE_OK and torch.equal(dx, want[0]) and torch.equal(dy, want[1])
+
+
 def test_block_norm_gradient_against_differences(M):
     """Derivative of <dx_out, x_out> + <dh, h> along the signs of its gradient
     in every input, by central differences in fp32: cut-off below d^2 / 6 times a third derivative
