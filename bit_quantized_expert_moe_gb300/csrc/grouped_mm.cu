@@ -518,21 +518,45 @@ bool map_w(CUtensorMap* m, bool bf16, const void* ptr, const GroupedShape& g, in
     return make_tensor_map_16(m, bf16, ptr, 3, dims, strides, box);
 }
 
+// Tiles of `cols` columns; Y, DX: when all experts have the same rows, or the
+// most that there can be.
+template <Product PR>
+int tile_count(const GroupedShape& g, int cols, bool even) {
+    if (PR == Product::DW) return g.E * ceil_div(g.N, 2 * BM) * ceil_div(g.K, cols);
+    const int used = std::min(g.R, g.E);  // experts with rows
+    const long long tiles = even ? (long long)used * ceil_div(ceil_div(g.R, used), cols) : g.R / cols + used;
+    return (int)std::min<long long>(INT32_MAX, tiles * ceil_div(PR == Product::Y ? g.N : g.K, 2 * BM));
+}
+
+// Columns of a tile: 256, 128 or 64.  What an SM can receive bounds a pair (50
+// bytes a clock), so the least of rounds of tiles x (256 rows of A + columns)
+// is the best.  dw of 6624 rows of 2 experts, N 104, K 3616: 21.4, 20.7 and 36.2 us
+// (58 tiles of 128, 114 of 64); of 512 rows, N and K 2048: 7.4, 8.0, 10.5; y of
+// 3002 rows, N 648, K 896: 9.2, 7.6, 9.4; of 2208 of 3 experts, N 232, K 5608:
+// 36.1, 27.4, 23.0.
+template <Product PR>
+int tile_columns(const GroupedShape& g) {
+    int best = BN;
+    long long least = INT64_MAX;
+    for (int cols = BN; cols >= 64; cols >>= 1) {
+        const int all = PR == Product::DW ? g.K : ceil_div(g.R, std::min(g.R, g.E));
+        const int width = ceil_div(all, ceil_div(all, cols));
+        const long long cost = (long long)ceil_div(tile_count<PR>(g, cols, true), num_sms() / 2) * (2 * BM + width);
+        if (cost < least) {
+            least = cost;
+            best = cols;
+        }
+    }
+    return best;
+}
+
 template <Product PR>
 cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
     const bool bf = g.dtype == MOE_DT_BF16;
     Maps maps;
     bool ok;
-    // The widest tiles that can give every pair work, from the most that there
-    // can be (Y, DX: an expert's last tile of rows may be a short one): 256, 128
-    // or 64 columns.  E 8, 1238 rows, N 520, K 264: dx 11.0 us with 256, 7.6 with 64.
-    int cols = 2 * BN;
-    long long items;
-    do {
-        cols >>= 1;
-        items = PR == Product::DW ? (long long)g.E * ceil_div(g.N, 2 * BM) * ceil_div(g.K, cols)
-                                  : ((long long)g.R / cols + std::min(g.R, g.E)) * ceil_div(PR == Product::Y ? g.N : g.K, 2 * BM);
-    } while (items < num_sms() / 2 && cols > 64);
+    const int cols = tile_columns<PR>(g);
+    const int items = tile_count<PR>(g, cols, false);
     if (PR == Product::DW) {
         ok = map_2d(&maps.a, bf, a, g.N, g.R, 64, 64) && map_2d(&maps.b[0], bf, b, g.K, g.R, 64, 64) &&
              map_w(&maps.b[1], bf, out, g, 32);
@@ -559,7 +583,7 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
         max_pairs = std::max(1, nc);
     }
     const GroupedParams p{g.R, g.E, g.N, g.K, g.offsets, out, bf ? 1u : 0u, cols, g.err};
-    const int grid = 2 * (int)std::max<long long>(1, std::min<long long>(max_pairs, items));
+    const int grid = 2 * std::max(1, std::min(max_pairs, items));
     return launch_overlapped<grouped_tc_kernel<PR>>(dim3(grid), dim3(THREADS), smem_bytes<PR>(g.E), s, maps, p);
 }
 
