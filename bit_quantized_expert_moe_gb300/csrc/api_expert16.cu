@@ -40,7 +40,8 @@ moe_status_t check_grouped(moe_dtype_t dtype, const void* a, const void* b, cons
 }
 
 GroupedShape shape(moe_dtype_t dtype, const int32_t* offsets, int32_t R, int32_t E, int32_t N, int32_t K, void* ws) {
-    return GroupedShape{dtype, R, E, N, K, offsets, &static_cast<WsHeader*>(ws)->err};
+    return GroupedShape{dtype, R, E, N, K, offsets, &static_cast<WsHeader*>(ws)->err,
+                        reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + WS_HEADER)};
 }
 
 moe_status_t check_swiglu(moe_dtype_t dtype, int32_t R, int32_t F) {
@@ -66,7 +67,7 @@ extern "C" {
 
 size_t moe_grouped_mm_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K) {
     if (!grouped_sizes_ok(R, E, N, K)) return 0;
-    return WS_HEADER;
+    return WS_HEADER + grouped_split_floats(GroupedShape{MOE_DT_BF16, R, E, N, K}) * sizeof(float);
 }
 
 moe_status_t moe_grouped_mm(moe_dtype_t dtype, const void* x, const void* w, const int32_t* offsets, int32_t R, int32_t E,

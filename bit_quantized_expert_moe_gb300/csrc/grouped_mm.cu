@@ -39,6 +39,7 @@
 // error word and every role leaves its loop.
 #include "internal.h"
 #include "tc_ptx.cuh"
+#include "vec8.cuh"
 
 namespace moe {
 namespace {
@@ -83,6 +84,8 @@ struct GroupedParams {
     void* out;
     uint32_t type;  // 0 fp16, 1 bf16
     int tile_cols;  // most columns of a tile
+    int splits;     // shares of the summed index, each a tile of its own (SPLIT)
+    float* part;    // [splits][R or E][...]: the output of every share in fp32
     uint32_t* err;
 };
 
@@ -101,9 +104,10 @@ struct Item {
     int m0;        // first of the pair's 256 A rows
     int c0, ncols; // first column and how many (Y, DX: rows r; DW: k)
     int l0, nl;    // the summed index: first (DW: row) and how many
+    int split;
 };
 
-template <Product PR>
+template <Product PR, bool SPLIT>
 struct Work {
     int mb;     // blocks of 256 A rows
     int cb;     // DW: blocks of 256 columns
@@ -114,9 +118,12 @@ struct Work {
         mb = ceil_div(PR == Product::DX ? p.K : p.N, 2 * BM);
         cb = ceil_div(p.K, p.tile_cols);
         items = bad ? 0 : PR == Product::DW ? p.E * mb * cb : pre[p.E] * mb;
+        if (SPLIT) items *= p.splits;
     }
     __device__ Item item(const GroupedParams& p, int i) const {
         Item t;
+        t.split = SPLIT ? i % p.splits : 0;
+        if (SPLIT) i /= p.splits;
         if (PR == Product::DW) {
             const int per = mb * cb;
             t.e = i / per;
@@ -147,6 +154,11 @@ struct Work {
             t.l0 = 0;
             t.nl = PR == Product::DX ? p.N : p.K;
         }
+        if (SPLIT) {  // shares of whole stages; the last ones may be empty
+            const int share = ceil_div(ceil_div(t.nl, BL), p.splits) * BL, from = min(t.nl, t.split * share);
+            t.l0 += from;
+            t.nl = min(share, t.nl - from);
+        }
         return t;
     }
 };
@@ -164,7 +176,9 @@ struct Maps {
     CUtensorMap a, b[BOXES];  // DW: b[0], and b[1] the output
 };
 
-template <Product PR>
+// SPLIT: where a few tiles sum long rows, their shares go to pairs that would
+// have nothing to do, and grouped_sum_kernel adds the shares up.
+template <Product PR, bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     grouped_tc_kernel(const __grid_constant__ Maps maps, const GroupedParams p) {
     extern __shared__ unsigned char smem_raw[];
@@ -256,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     if (bad && threadIdx.x == 0 && blockIdx.x == 0) set_error(p.err, ERRBIT_RANGE);
     __syncthreads();
-    const Work<PR> work(p, tile_pre, bad);
+    const Work<PR, SPLIT> work(p, tile_pre, bad);
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -296,12 +310,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     } else {
                         if (rank == 0) tc::mbar_arrive_expect_tx(f, bytes);
                         if (PR == Product::Y) {
-                            tc::tma_load_3d_pair(sa, &maps.a, fl, l, m, t.e);
+                            tc::tma_load_3d_pair(sa, &maps.a, fl, t.l0 + l, m, t.e);
                         } else {
-                            tc::tma_load_3d_pair(sa, &maps.a, fl, m, l, t.e);
-                            tc::tma_load_3d_pair(sa + ATOM64, &maps.a, fl, m + 64, l, t.e);
+                            tc::tma_load_3d_pair(sa, &maps.a, fl, m, t.l0 + l, t.e);
+                            tc::tma_load_3d_pair(sa + ATOM64, &maps.a, fl, m + 64, t.l0 + l, t.e);
                         }
-                        tc::tma_load_2d_pair(sb, mb, fl, l, c);
+                        tc::tma_load_2d_pair(sb, mb, fl, t.l0 + l, c);
                     }
                     if (++s == STAGES) {
                         s = 0;
@@ -410,7 +424,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::tc_fence_after();
             }
-            if (PR == Product::DW) {
+            if (SPLIT) {
+                // fp32: DW 32 columns of this thread's row, Y and DX this thread's
+                // column of 32 rows
+                const int blocks = ceil_div(t.ncols, 32);
+                for (int cb = eh; cb < blocks; cb += 2) {
+                    uint32_t v[32];
+                    if (t.nl > 0) {
+                        tc::tmem_ld_32x32b_x32(tmem_base + 256u * b + 32u * cb + t_lane, v);
+                        tc::tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0;
+                    }
+                    const int n = m < M ? min(32, t.ncols - 32 * cb) : 0;
+                    if (PR == Product::DW) {
+                        float* o = p.part + (((size_t)t.split * p.E + t.e) * M + m) * p.K + t.c0 + 32 * cb;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            if (j < n) *reinterpret_cast<uint4*>(o + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    } else {
+                        float* o = p.part + ((size_t)t.split * p.R + t.c0 + 32 * cb) * M + m;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < n) o[(size_t)j * M] = __uint_as_float(v[j]);
+                    }
+                }
+            } else if (PR == Product::DW) {
                 // 64 columns at a time: rows of 128 B, 128-byte swizzle, stored by TMA
                 const int row0 = t.m0 + (int)rank * BM + 32 * q, blocks = ceil_div(t.ncols, 64);
                 const uint32_t dst = buf + 128 * lane;
@@ -485,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 ++ic;
             }
         }
-        if (PR == Product::DW) tc::bulk_wait();
+        if (PR == Product::DW && !SPLIT) tc::bulk_wait();
     }
 
     // A wait that gave up: copies and MMAs that were issued finish well inside
@@ -506,6 +546,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
 }
 
+// The shares' sums, in order, rounded to the output: `row` values for each of
+// `rows` rows, of which Y and DX write those that a segment holds.
+__global__ void __launch_bounds__(256) grouped_sum_kernel(const GroupedParams p, int rows, int row) {
+    grid_dependency_launch();
+    grid_dependency_wait();
+    const int r0 = p.offsets ? __ldg(p.offsets) : 0, r1 = p.offsets ? __ldg(p.offsets + p.E) : rows;
+    const size_t n = (size_t)rows * row / 8, step = (size_t)gridDim.x * blockDim.x;
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
+        const int r = (int)(i * 8 / row);
+        if (r < r0 || r >= r1) continue;
+        V8 s = load8<F32>(p.part, i);
+        for (int k = 1; k < p.splits; ++k) s = fma(load8<F32>(p.part, k * n + i), 1.f, s);
+        if (p.type) store8<Bf16>(p.out, i, s);
+        else store8<F16>(p.out, i, s);
+    }
+}
+
 bool map_2d(CUtensorMap* m, bool bf16, const void* ptr, int cols, int rows, int box_cols, int box_rows) {
     const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)cols * 2};
     const uint32_t box[2] = {(uint32_t)box_cols, (uint32_t)box_rows};
@@ -517,6 +574,8 @@ bool map_w(CUtensorMap* m, bool bf16, const void* ptr, const GroupedShape& g, in
     const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
     return make_tensor_map_16(m, bf16, ptr, 3, dims, strides, box);
 }
+
+int sm_pairs() { return std::max(1, num_sms() / 2); }
 
 // Tiles of `cols` columns; Y, DX: when all experts have the same rows, or the
 // most that there can be.
@@ -541,7 +600,7 @@ int tile_columns(const GroupedShape& g) {
     for (int cols = BN; cols >= 64; cols >>= 1) {
         const int all = PR == Product::DW ? g.K : ceil_div(g.R, std::min(g.R, g.E));
         const int width = ceil_div(all, ceil_div(all, cols));
-        const long long cost = (long long)ceil_div(tile_count<PR>(g, cols, true), num_sms() / 2) * (2 * BM + width);
+        const long long cost = (long long)ceil_div(tile_count<PR>(g, cols, true), sm_pairs()) * (2 * BM + width);
         if (cost < least) {
             least = cost;
             best = cols;
@@ -550,8 +609,25 @@ int tile_columns(const GroupedShape& g) {
     return best;
 }
 
+// Shares of the summed index for each tile.  A stage takes a pair 0.23 us; the
+// sum's launch takes as long as about 16 of them.  One expert, 512 rows, N 256,
+// K 7168: y 20.4 -> 9.9 us; 3851 rows, N 3064, K 96: dw 19.5 -> 12.7; two experts,
+// 300 rows, N 5608, K 232: dx 27.2 -> 10.3; 70 rows, N 88, K 2072: y 9.4 -> 7.6.
 template <Product PR>
-cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
+int tile_splits(const GroupedShape& g, int cols) {
+    const int stages = ceil_div(PR == Product::Y ? g.K : PR == Product::DX ? g.N : ceil_div(g.R, g.E), BL);
+    const int most = std::min({sm_pairs() / tile_count<PR>(g, cols, true), stages / 8, 8});
+    return most > 1 && stages - ceil_div(stages, most) >= 16 ? most : 1;
+}
+// fp32 values of the shares' outputs.
+template <Product PR>
+size_t split_floats(const GroupedShape& g) {
+    const int splits = tile_splits<PR>(g, tile_columns<PR>(g));
+    return splits == 1 ? 0 : (size_t)splits * (PR == Product::DW ? (size_t)g.E * g.N : g.R) * (PR == Product::Y ? g.N : g.K);
+}
+
+template <Product PR, bool SPLIT>
+cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, int splits, cudaStream_t s) {
     const bool bf = g.dtype == MOE_DT_BF16;
     Maps maps;
     bool ok;
@@ -569,26 +645,43 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
     if (!ok) return cudaErrorInvalidValue;
     static int max_pairs = 0;  // CTA pairs that the GPU holds at once
     if (max_pairs == 0) {
-        const cudaError_t e = allow_smem<grouped_tc_kernel<PR>>();
+        const cudaError_t e = allow_smem<grouped_tc_kernel<PR, SPLIT>>();
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
         cfg.blockDim = dim3(THREADS);
         cfg.dynamicSmemBytes = smem_bytes<PR>(1024);
         int nc = 0;
-        if (cudaOccupancyMaxActiveClusters(&nc, grouped_tc_kernel<PR>, &cfg) != cudaSuccess || nc < 1) {
+        if (cudaOccupancyMaxActiveClusters(&nc, grouped_tc_kernel<PR, SPLIT>, &cfg) != cudaSuccess || nc < 1) {
             (void)cudaGetLastError();
             nc = num_sms() / 2;
         }
         max_pairs = std::max(1, nc);
     }
-    const GroupedParams p{g.R, g.E, g.N, g.K, g.offsets, out, bf ? 1u : 0u, cols, g.err};
-    const int grid = 2 * std::max(1, std::min(max_pairs, items));
-    return launch_overlapped<grouped_tc_kernel<PR>>(dim3(grid), dim3(THREADS), smem_bytes<PR>(g.E), s, maps, p);
+    const GroupedParams p{g.R, g.E, g.N, g.K, g.offsets, out, bf ? 1u : 0u, cols, splits, g.part, g.err};
+    const int grid = 2 * (int)std::max<long long>(1, std::min<long long>(max_pairs, (long long)items * splits));
+    cudaError_t e = launch_overlapped<grouped_tc_kernel<PR, SPLIT>>(dim3(grid), dim3(THREADS), smem_bytes<PR>(g.E), s, maps, p);
+    if (SPLIT && e == cudaSuccess) {
+        GroupedParams q = p;
+        if (PR == Product::DW) q.offsets = nullptr;
+        const int rows = PR == Product::DW ? g.E * g.N : g.R, row = PR == Product::Y ? g.N : g.K;
+        const long long blocks = ((long long)rows * row / 8 + 255) / 256;
+        e = launch_overlapped(grouped_sum_kernel, (int)std::min<long long>(num_sms() * 8, blocks), 256, 0, s, q, rows, row);
+    }
+    return e;
+}
+template <Product PR>
+cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
+    const int splits = tile_splits<PR>(g, tile_columns<PR>(g));
+    return splits > 1 ? launch<PR, true>(g, a, b, out, splits, s) : launch<PR, false>(g, a, b, out, 1, s);
 }
 
 }  // namespace
 
+size_t grouped_split_floats(const GroupedShape& g) {
+    if (g.R == 0) return 0;
+    return std::max({split_floats<Product::Y>(g), split_floats<Product::DX>(g), split_floats<Product::DW>(g)});
+}
 cudaError_t launch_grouped_mm(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s) {
     // E 128, N 1536, K 2048: 8 rows 12.1 us there and 13.1 here, 32 rows 31.0 and
     // 34.9, 128 rows 77.9 and 82.0; E 256, N 4096, K 7168: 64 rows 469 and 492.  With

@@ -116,6 +116,35 @@ def test_grouped_products(M, counts, N, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES16)
+@pytest.mark.parametrize("counts,N,K", [
+    ([70], 88, 2072),              # shares of the summed index: of y,
+    ([100, 0, 37], 232, 4104),
+    ([40], 2056, 136),             # of dx,
+    ([2100], 96, 80),              # of dw
+    ([6001, 0, 1], 104, 136),      # whose second and third segment have less rows than shares
+    ([17, 4080], 40, 264),
+    ([60, 59], 2056, 2064),        # of y and dx
+])
+def test_grouped_products_of_few_tiles(M, counts, N, K, dtype):
+    """Few tiles with a long summed index are shared out and added up."""
+    R, E = sum(counts), len(counts)
+    assert M.grouped_mm_workspace_size(R, E, N, K) > 256
+    test_grouped_products(M, counts, N, K, dtype)
+
+
+def test_grouped_products_of_few_tiles_leave_other_rows(M):
+    R, N, K = 150, 64, 4096
+    x, w = randn(1, torch.bfloat16, R, K).cuda(), randn(2, torch.bfloat16, 2, N, K).cuda()
+    off = torch.tensor([10, 80, 140], dtype=torch.int32).cuda()
+    y = torch.full((R, N), 7.0, dtype=torch.bfloat16).cuda()
+    M.grouped_mm(x, w, off, y=y)
+    ref = torch.cat([x[10:80].double() @ w[0].double().T, x[80:140].double() @ w[1].double().T]).cpu()
+    terms = torch.cat([x[10:80].double().abs() @ w[0].double().abs().T, x[80:140].double().abs() @ w[1].double().abs().T]).cpu()
+    assert (y[:10] == 7).all() and (y[140:] == 7).all()
+    close(y[10:140], ref, terms, mm_steps(K), "y")
+
+
+@pytest.mark.parametrize("dtype", DTYPES16)
 def test_grouped_products_are_exact_on_small_integers_and_bilinear(M, dtype):
     """Small whole numbers: every product, sum and rounding is exact, so the
     results equal the definition's, and the gradients equal the differences of
