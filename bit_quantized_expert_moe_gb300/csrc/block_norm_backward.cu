@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(1024) block_norm_reduce_kernel(const Args p, i
 
 // How the backward pass splits the rows: one block an SM with as many row
 // groups as its threads hold (15 named barriers), fewer where the rows are few.
-// 4096 x 2048: 26 us with two groups of 256 threads; 40 with three at 80
+// 4096 x 2048: 25 us with two groups of 256 threads; 40 with three at 80
 // registers, which spill; two chunks a thread and four groups of 128 take the
 // same there and 22 instead of 14 us at 1155 x 1288, whose row groups would have
 // half the threads.

@@ -2,8 +2,8 @@
 //
 // A small call takes a few microseconds on the GPU; checking shapes, taking
 // pointers and making outputs in the interpreter takes longer than that on the
-// GPU's host (swiglu of 8 rows: 7.3 us a call there, 4.1 here; the gradients of
-// a block norm: 20 and 10).  Shapes and types are checked here, everything else
+// GPU's host (swiglu of 8 rows: 7.3 us a call there, 3.7 here; the gradients of
+// a block norm: 20 and 9).  Shapes and types are checked here, everything else
 // by the library.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
