@@ -2,7 +2,7 @@
 //
 // The weights' bytes are all that counts, and a few tiles of 256 weight rows
 // would not occupy every SM.  A block takes 16 weight rows of one expert and up
-// to 8 of its rows; its four warps share K and add up in shared memory.  A
+// to 8 of its rows; its warps (4 to 16) share K and add up in shared memory.  A
 // weight goes from memory to a register once and from there into the tensor
 // cores (mma.sync m16n8k16: 16 weight rows, 8 rows of x): with so few rows the
 // tcgen05 path's staging would only add latency.  Both operands keep K in the
@@ -24,7 +24,7 @@ __device__ __forceinline__ uint4 load_weights(const void* p) {
     return r;
 }
 
-constexpr int WARPS = 4, ROWS = 16, COLS = 8, AHEAD = 8;
+constexpr int ROWS = 16, COLS = 8, AHEAD = 8;
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -37,7 +37,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <bool BF16>
+template <bool BF16, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) grouped_few_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
                                                                  uint16_t* __restrict__ y, GroupedShape g) {
     __shared__ int cnt[WARPS];
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_few_kernel(const uint16_t*
     part[warp][2 * t + 1][gi + 8] = acc[3];
     __syncthreads();
     const int col = threadIdx.x / ROWS, n = threadIdx.x % ROWS;
-    if (col < rows && n0 + n < g.N) {
+    if (col < rows && n0 + n < g.N) {  // (the first 128 threads)
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < WARPS; ++i) s += part[i][col][n];
@@ -108,12 +108,21 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_few_kernel(const uint16_t*
 
 }  // namespace
 
+// Warps that share K: four, more where the blocks leave SMs without loads under
+// way.  us with 4, 8, 16 warps: 66 blocks, K 6592 27.0, 13.5, 7.9; 256, K 4096 14.8, 9.4,
+// 6.4; 64, K 512 2.4, 2.3, 2.9; 512, K 1024 6.2, 5.8, 7.8; 768, K 2048 11.3, 12.2, 14.0.
 cudaError_t launch_grouped_few(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s) {
     const dim3 grid(ceil_div(g.N, ROWS), g.R);
     const auto *xp = static_cast<const uint16_t*>(x), *wp = static_cast<const uint16_t*>(w);
     auto* yp = static_cast<uint16_t*>(y);
-    return launch_overlapped(g.dtype == MOE_DT_BF16 ? grouped_few_kernel<true> : grouped_few_kernel<false>, grid,
-                             dim3(32 * WARPS), 0, s, xp, wp, yp, g);
+    const bool bf = g.dtype == MOE_DT_BF16;
+    // blocks with work, at most
+    const long long blocks = (long long)grid.x * std::min(g.R, g.E + g.R / COLS);
+    const int warps = blocks > 4 * num_sms() ? 4 : blocks > 2 * num_sms() || g.K < 1024 ? 8 : 16;
+    auto* kernel = bf ? grouped_few_kernel<true, 4> : grouped_few_kernel<false, 4>;
+    if (warps == 8) kernel = bf ? grouped_few_kernel<true, 8> : grouped_few_kernel<false, 8>;
+    if (warps == 16) kernel = bf ? grouped_few_kernel<true, 16> : grouped_few_kernel<false, 16>;
+    return launch_overlapped(kernel, grid, dim3(32 * warps), 0, s, xp, wp, yp, g);
 }
 
 }  // namespace moe

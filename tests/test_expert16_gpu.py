@@ -132,6 +132,20 @@ def test_grouped_products_of_few_tiles(M, counts, N, K, dtype):
     test_grouped_products(M, counts, N, K, dtype)
 
 
+@pytest.mark.parametrize("dtype", DTYPES16)
+@pytest.mark.parametrize("counts,N,K", [
+    ([1, 0, 2], 72, 1096),
+    ([7], 264, 4104),
+    ([0, 9, 1, 1], 136, 2056),     # a second block of an expert's rows
+    ([1] * 8, 512, 4096),
+    ([3, 3], 3400, 1024),
+    ([30], 1032, 72),
+])
+def test_grouped_products_of_few_rows(M, counts, N, K, dtype):
+    """A handful of rows: K shared by 4, 8 or 16 warps."""
+    test_grouped_products(M, counts, N, K, dtype)
+
+
 def test_grouped_products_of_few_tiles_leave_other_rows(M):
     R, N, K = 150, 64, 4096
     x, w = randn(1, torch.bfloat16, R, K).cuda(), randn(2, torch.bfloat16, 2, N, K).cuda()
