@@ -132,6 +132,32 @@ def test_grouped_products_of_few_tiles(M, counts, N, K, dtype):
     test_grouped_products(M, counts, N, K, dtype)
 
 
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_grouped_products_of_few_tiles_keep_segments_apart(M, bad):
+    """Shares of one expert's sums see nothing of another's rows and weights;
+    bit for bit the same again, and in a graph; bad offsets are reported."""
+    counts, N, K = [2101, 2051], 96, 80
+    x, dy = randn(1, torch.bfloat16, sum(counts), K).cuda(), randn(2, torch.bfloat16, sum(counts), N).cuda()
+    off = offsets_of(counts).cuda()
+    ws = M.workspace(M.grouped_mm_workspace_size(sum(counts), 2, N, K))
+    assert ws.numel() > 256
+    want = M.grouped_mm_dw(dy, x, off, ws=ws)
+    assert torch.equal(M.grouped_mm_dw(dy, x, off, ws=ws), want)
+    for e, s in ((0, slice(0, counts[0])), (1, slice(counts[0], None))):
+        x2, dy2 = torch.full_like(x, bad), torch.full_like(dy, bad)
+        x2[s], dy2[s] = x[s], dy[s]
+        assert torch.equal(M.grouped_mm_dw(dy2, x2, off, ws=ws)[e], want[e])
+    out, graph = torch.empty_like(want), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.grouped_mm_dw(dy, x, off, dw=out, ws=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and M.get_device_error(ws) == M.MOE_OK
+    M.grouped_mm_dw(dy, x, torch.tensor([0, 4153, 4152], dtype=torch.int32).cuda(), ws=ws)
+    assert M.STATUS[M.get_device_error(ws)] == "MOE_ERR_DEVICE_RANGE"
+    assert torch.equal(M.grouped_mm_dw(dy, x, off, ws=ws), want)
+
+
 @pytest.mark.parametrize("dtype", DTYPES16)
 @pytest.mark.parametrize("counts,N,K", [
     ([1, 0, 2], 72, 1096),
