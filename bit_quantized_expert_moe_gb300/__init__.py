@@ -103,6 +103,14 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     raise ValueError("contiguous tensor expected" if t.is_cuda else "device tensor expected")
 
 
+def _of(what: str, t: torch.Tensor | None, *dtypes: torch.dtype) -> int | None:
+    """_ptr of a tensor of one of these types: the kernels know no other, and
+    would read the bits of another as theirs."""
+    if t is not None and t.dtype not in dtypes:
+        raise ValueError(f"{what}: {' or '.join(str(d) for d in dtypes)} expected, not {t.dtype}")
+    return _ptr(t)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         # the handle of torch.cuda.current_stream(), without making the object:
@@ -172,7 +180,8 @@ def route_topk(logits: torch.Tensor, k: int, ids: torch.Tensor | None = None, w:
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     if w is None:
         w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    _check(lib().moe_route_topk(_ptr(logits), T, E, k, _ptr(ids), _ptr(w), _stream(stream)), "moe_route_topk")
+    _check(lib().moe_route_topk(_of("logits", logits, torch.float32), T, E, k, _of("ids", ids, torch.int32),
+                                _of("w", w, torch.float32), _stream(stream)), "moe_route_topk")
     return ids, w
 
 
@@ -182,6 +191,7 @@ def permute_workspace_size(T: int, k: int, E: int) -> int:
 
 def permute(topk_ids: torch.Tensor, E: int, x: torch.Tensor | None = None, want_x_perm: bool = False,
             ws: torch.Tensor | None = None, stream=None) -> dict:
+    """The permutation and, with want_x_perm, the rows of x (bfloat16 or float16) in its order."""
     T, k = topk_ids.shape
     R = T * k
     dev = topk_ids.device
@@ -192,13 +202,15 @@ def permute(topk_ids: torch.Tensor, E: int, x: torch.Tensor | None = None, want_
         "inv": torch.empty(max(R, 1), dtype=torch.int32, device=dev),
     }
     d = 0
-    x_perm = None
+    x_perm = x_ptr = None
     if want_x_perm:
+        x_ptr = _of("x", x, torch.bfloat16, torch.float16)  # the gather moves 16-bit values as they are
         d = x.shape[1]
-        x_perm = torch.empty((max(R, 1), d), dtype=torch.bfloat16, device=dev)
+        x_perm = torch.empty((max(R, 1), d), dtype=x.dtype, device=dev)
+    ids_ptr = _of("topk_ids", topk_ids, torch.int32)
     if ws is None:
         ws = workspace(permute_workspace_size(T, k, E), dev)
-    st = lib().moe_permute(_ptr(topk_ids), T, k, E, _ptr(x) if want_x_perm else None, d,
+    st = lib().moe_permute(ids_ptr, T, k, E, x_ptr, d,
                            _ptr(out["counts"]), _ptr(out["offsets"]), _ptr(out["sorted"]), _ptr(out["inv"]),
                            _ptr(x_perm), _ptr(ws), ws.numel(), _stream(stream))
     _check(st, "moe_permute")
@@ -217,12 +229,14 @@ def expert_ffn_workspace_size(layer: Layer, R: int) -> int:
 def expert_ffn_w4a16(layer: Layer, x_perm: torch.Tensor, offsets: torch.Tensor, row_w: torch.Tensor | None = None,
                      y_perm: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
     R = x_perm.shape[0]
+    x_ptr = _of("x_perm", x_perm, torch.bfloat16)
     if y_perm is None:
         y_perm = torch.empty((R, layer.d_model), dtype=torch.bfloat16, device=x_perm.device)
     if ws is None:
         ws = workspace(expert_ffn_workspace_size(layer, R), x_perm.device)
     L = layer.c_struct()
-    st = lib().moe_expert_ffn_w4a16(ctypes.byref(L), _ptr(x_perm), _ptr(offsets), R, _ptr(row_w), _ptr(y_perm),
+    st = lib().moe_expert_ffn_w4a16(ctypes.byref(L), x_ptr, _of("offsets", offsets, torch.int32), R,
+                                    _of("row_w", row_w, torch.float32), _of("y_perm", y_perm, torch.bfloat16),
                                     _ptr(ws), ws.numel(), _stream(stream))
     _check(st, "moe_expert_ffn_w4a16")
     return y_perm
@@ -230,12 +244,14 @@ def expert_ffn_w4a16(layer: Layer, x_perm: torch.Tensor, offsets: torch.Tensor, 
 
 def combine(y_perm: torch.Tensor, inv: torch.Tensor, topk_w: torch.Tensor, out: torch.Tensor | None = None,
             stream=None):
+    """Weighted sums of the rows of y_perm (bfloat16, as the output)."""
     T, k = topk_w.shape
     d = y_perm.shape[1]
+    y_ptr = _of("y_perm", y_perm, torch.bfloat16)
     if out is None:
         out = torch.empty((T, d), dtype=torch.bfloat16, device=y_perm.device)
-    _check(lib().moe_combine(_ptr(y_perm), _ptr(inv), _ptr(topk_w), T, k, d, _ptr(out), _stream(stream)),
-           "moe_combine")
+    _check(lib().moe_combine(y_ptr, _of("inv", inv, torch.int32), _of("topk_w", topk_w, torch.float32), T, k, d,
+                             _of("out", out, torch.bfloat16), _stream(stream)), "moe_combine")
     return out
 
 
@@ -255,7 +271,8 @@ class LayerCall:
 
     def __call__(self, x: torch.Tensor, logits: torch.Tensor, out: torch.Tensor,
                  topk_ids_out: torch.Tensor | None = None, stream=None):
-        st = self._fn(ctypes.byref(self.L), _ptr(x), _ptr(logits), self.T, self.k, _ptr(out), _ptr(topk_ids_out),
+        st = self._fn(ctypes.byref(self.L), _of("x", x, torch.bfloat16), _of("logits", logits, torch.float32), self.T,
+                      self.k, _of("out", out, torch.bfloat16), _of("topk_ids_out", topk_ids_out, torch.int32),
                       _ptr(self.ws), self.ws.numel(), _stream(stream))
         _check(st, "moe_layer_forward")
         return out
