@@ -4,6 +4,8 @@
 //   da = w_r dh u s (1 + a (1 - s)),  du = w_r dh a s,  dw_r = sum_f dh a s u
 // with w_r = row_w[row_map[r]].  Each element is read and written once: bound
 // by memory.  NT threads share a row (its sum is dw_r).
+#include <type_traits>
+
 #include "internal.h"
 #include "vec8.cuh"
 
@@ -13,16 +15,20 @@ namespace {
 // SiLU and its slope for two gates a, s(a) = 1 / (1 + e^-a) from t = e^-|a|, so
 // that nothing overflows: 1 / (1 + t) for a >= 0, t / (1 + t) below.  Each is
 // a factor by itself before the others come in: where s is 0, a (its type's
-// lowest value even) times s is 0 and stays 0.  16-bit outputs: the hardware's
-// exponential and reciprocal (relative error below 2^-20 for a > -87, an eighth
-// of the half ulp of fp16 in the worst place; s is subnormal below): the
-// library's exponential and division take the backward kernel from 45 to 50 us
-// at 32768 x 768, where it is then bound by its instructions.
-template <class T>
+// lowest value even) times s is 0 and stays 0.
+// 16-bit rows: the hardware's reciprocal (2 ulp; a division takes the backward
+// kernel from 45 to 50 us at 32768 x 768).  Where nothing but 16-bit outputs is made
+// (EXACT = false) the hardware's exponential too, whose documented bound of 2 + 1.173
+// |a| ulp is 2^-18 at |a| = 24, below which fp16 results are subnormal or zero for
+// |up| < 2^11, and 2^-16.2 at |a| = 87, where s leaves the normal numbers: a 64th of
+// the half ulp of fp16, a 90th of bf16's.  The routing weight's gradient is fp32 and
+// gets the library's (2 ulp).  us with the library's and the hardware's: forward
+// 32768 x 768 30.5 and 24.7, backward 44.5 and 44.2, 40000 x 264 30.4 and 28.6.
+template <class T, bool EXACT>
 struct Silu {
     float2 as, ss;  // a s, s (1 + a (1 - s))
     __device__ __forceinline__ static void sigmoid(float a, float& s, float& other) {
-        const float t = __expf(-fabsf(a));
+        const float t = EXACT ? expf(-fabsf(a)) : __expf(-fabsf(a));
         const float inv = __fdividef(1.f, 1.f + t);
         s = a < 0.f ? t * inv : inv;
         other = 1.f - s;
@@ -40,8 +46,8 @@ struct Silu {
 // fp32 outputs: s = q^2 / (1 + t^2) with t = e^(-|a| / 2) and q = 1 or t; a
 // product that takes one factor q last underflows no earlier than its value
 // does, and 1 - s does not cancel.
-template <>
-struct Silu<F32> {
+template <bool EXACT>
+struct Silu<F32, EXACT> {
     float2 as, ss, q;  // without a factor q
     __device__ __forceinline__ static void sigmoid(float a, float& s, float& q, float& other) {
         const float t = expf(-0.5f * fabsf(a)), inv = 1.f / (1.f + t * t);
@@ -86,7 +92,7 @@ __global__ void __launch_bounds__(256) swiglu_kernel(const void* __restrict__ gu
         const V8 u = load8<T>(gu, (size_t)r * 2 * chunks + chunks + c);
         V8 v = mul(u, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v.p[j] = Silu<T>(a.p[j]).times(v.p[j]);
+        for (int j = 0; j < 4; ++j) v.p[j] = Silu<T, false>(a.p[j]).times(v.p[j]);
         store8<T>(h, (size_t)i, v);
     }
 }
@@ -98,7 +104,7 @@ constexpr int BACKWARD_SLOTS = T::BYTES == 2 ? 3 : 2;
 template <class T>
 using BackwardRing = ThreadRing<T, 3, BACKWARD_SLOTS<T>>;
 
-template <class T>
+template <class T, bool EXACT>
 __global__ void __launch_bounds__(256)
     swiglu_backward_kernel(const void* __restrict__ dh, const void* gu, const float* __restrict__ row_w,
                            const int32_t* __restrict__ row_map, int R, int F, void* dgu /* may be gu */,
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(256)
                 V8 ga, gu_;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const Silu<T> f(a.p[j]);
+                    const Silu<T, EXACT> f(a.p[j]);
                     const float2 h = f.times(du.p[j]);
                     sum += h.x + h.y;
                     gu_.p[j] = f.times(wd.p[j]);
@@ -187,8 +193,11 @@ cudaError_t run_backward(const void* dh, const void* gu, const float* row_w, con
     const int threads = 32 * warps, groups = 8 / warps;
     const int blocks = std::min(num_sms() * 5, ceil_div(R, groups));
     const size_t smem = groups * RowGroup::SUM_FLOATS * sizeof(float) + (size_t)threads * groups * BackwardRing<T>::BYTES_PER_THREAD;
-    return launch_overlapped<swiglu_backward_kernel<T>>(blocks, threads * groups, smem, s, dh, gu, row_w, row_map, R, F, dgu, drow_w,
-                       threads);
+    const auto launch = [&](auto exact) {
+        return launch_overlapped<swiglu_backward_kernel<T, decltype(exact)::value>>(
+            blocks, threads * groups, smem, s, dh, gu, row_w, row_map, R, F, dgu, drow_w, threads);
+    };
+    return drow_w || T::BYTES == 4 ? launch(std::true_type{}) : launch(std::false_type{});
 }
 }  // namespace
 
