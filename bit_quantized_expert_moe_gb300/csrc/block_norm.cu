@@ -13,6 +13,8 @@ namespace moe {
 namespace norm {
 namespace {
 
+constexpr float UNIT = 0x1p-80f;
+
 // A block's row groups take every gridDim-th set of rows, SLOTS - 1 of a
 // group's rows under way while it computes one (SLOTS = 1: a call with few
 // rows, one for a group, which takes the parameters as it needs them).
@@ -20,7 +22,11 @@ namespace {
 //   sum x'^2 = sum x^2 + 2 r1 sum x w + r1^2 sum w^2,
 // four sums that do not wait for r1.  Where x' is small beside x and r1 w the
 // terms cancel: below a quarter of sum x^2 + r1^2 sum w^2, where an error of the
-// sums could grow more than fourfold, sum x'^2 is taken from x' itself.
+// sums could grow more than fourfold, sum x'^2 is taken from x' itself; so it is
+// where a sum leaves fp32's range (|x|, |y| or |w| of 2^57 and more).  There y enters
+// r1, and x' enters r2, in units of 2^80 if their own squares overflow: a row at its
+// type's lowest value has a norm like any other.  (4096 x 2048 12.6 -> 12.9 us; as a
+// function outside the loop, whose call spills, 17.3.)
 // ALL: y, gamma_post and gamma_pre are there and the rows share one gate.
 template <class T, int VPT, int SLOTS, bool ALL>
 __global__ void __launch_bounds__(SLOTS == 1 || VPT == 4 ? 512 : 1024, 1) block_norm_kernel(const Args p) {
@@ -74,6 +80,17 @@ __global__ void __launch_bounds__(SLOTS == 1 || VPT == 4 ? 512 : 1024, 1) block_
             ring.wait();
         }
         const size_t gchunk = row_gate ? (size_t)(r / p.S) * chunks + rg.tid : 0;
+        auto load_x = [&](int i) { return unpack8<T>(SLOTS > 1 ? ring.get(i) : raw_at<T>(p.x, off + i * next)); };
+        auto load_y = [&](int i) { return unpack8<T>(SLOTS > 1 ? ring.get(VPT + i) : raw_at<T>(p.y, off + i * next)); };
+        auto weighted = [&](int i, const V8& y) {
+            const int c = i * p.threads + rg.tid;
+            V8 a;
+            if (SLOTS > 1) a = table.get(0, c);
+            else a = has_post ? mul(load8(p.ptype, p.gamma_post, c), p.alpha) : v8(p.alpha);
+            if (row_gate) a = mul(a, load8(p.ptype, p.gate, gchunk + i * p.threads));
+            if (SLOTS == 1 && ALL && p.gate) a = mul(a, load8(p.ptype, p.gate, c));
+            return mul(a, y);
+        };
         V8 x[VPT], w[VPT];
         float2 s[4];  // y^2, x^2, x w, w^2
 #pragma unroll
@@ -82,16 +99,10 @@ __global__ void __launch_bounds__(SLOTS == 1 || VPT == 4 ? 512 : 1024, 1) block_
         for (int i = 0; i < VPT; ++i) {
             x[i] = w[i] = v8(0.f);
             if (in[i]) {
-                const int c = i * p.threads + rg.tid;
-                x[i] = unpack8<T>(SLOTS > 1 ? ring.get(i) : raw_at<T>(p.x, off + i * next));
+                x[i] = load_x(i);
                 if (has_y) {
-                    const V8 y = unpack8<T>(SLOTS > 1 ? ring.get(VPT + i) : raw_at<T>(p.y, off + i * next));
-                    V8 a;
-                    if (SLOTS > 1) a = table.get(0, c);
-                    else a = has_post ? mul(load8(p.ptype, p.gamma_post, c), p.alpha) : v8(p.alpha);
-                    if (row_gate) a = mul(a, load8(p.ptype, p.gate, gchunk + i * p.threads));
-                    if (SLOTS == 1 && ALL && p.gate) a = mul(a, load8(p.ptype, p.gate, c));
-                    w[i] = mul(a, y);
+                    const V8 y = load_y(i);
+                    w[i] = weighted(i, y);
                     dot(s[0], y, y);
                     dot(s[2], x[i], w[i]);
                     dot(s[3], w[i], w[i]);
@@ -99,7 +110,6 @@ __global__ void __launch_bounds__(SLOTS == 1 || VPT == 4 ? 512 : 1024, 1) block_
                 dot(s[1], x[i], x[i]);
             }
         }
-        ring.next();
         float r1 = 1.f, r2 = 0.f;
         if (has_post || has_h) {
             float t[4];
@@ -111,14 +121,32 @@ __global__ void __launch_bounds__(SLOTS == 1 || VPT == 4 ? 512 : 1024, 1) block_
             float sum = plain + 2.f * r1 * t[2];
 #pragma unroll
             for (int i = 0; i < VPT; ++i) x[i] = fma(w[i], r1, x[i]);
-            // the same for the group's threads; written so that a NaN stays in sum
-            if (has_h && sum < 0.25f * plain) {
-                float2 q = f2(0.f);
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) dot(q, x[i], x[i]);
-                sum = rg.sum(q.x + q.y);
-            }
             r2 = rsqrtf(sum * inv_d + p.eps);
+            // the same for the group's threads, and true for a NaN
+            if (__builtin_expect(!(t[0] + plain < INFINITY && sum >= 0.25f * plain), 0)) {
+                auto squares = [&](auto value, float u) {
+                    float2 q = f2(0.f);
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i)
+                        if (in[i]) {
+                            const V8 v = mul(value(i), u);
+                            dot(q, v, v);
+                        }
+                    return rg.sum(q.x + q.y);
+                };
+                if (has_post && !(t[0] < INFINITY)) {
+                    r1 = rsqrtf(squares(load_y, UNIT) * inv_d + p.eps * UNIT * UNIT);
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i)
+                        if (in[i]) x[i] = fma(weighted(i, mul(load_y(i), UNIT)), r1, load_x(i));
+                }
+                if (has_h) {
+                    auto stream = [&](int i) { return x[i]; };
+                    sum = squares(stream, 1.f);
+                    r2 = rsqrtf(sum * inv_d + p.eps);
+                    if (!(sum < INFINITY)) r2 = rsqrtf(squares(stream, UNIT) * inv_d + p.eps * UNIT * UNIT) * UNIT;
+                }
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) x[i] = fma(w[i], r1, x[i]);
@@ -132,6 +160,7 @@ __global__ void __launch_bounds__(SLOTS == 1 || VPT == 4 ? 512 : 1024, 1) block_
                     store_at<T>(p.h, off + i * next,
                                 mul(mul(x[i], r2), SLOTS > 1 ? table.get(1, c) : load8(p.ptype, p.gamma_pre, c)));
             }
+        ring.next();
     }
     cp_async_wait<0>();
 }

@@ -312,7 +312,9 @@ moe_status_t moe_swiglu_backward(moe_dtype_t dtype, const void* dh, const void* 
  *   gamma_post, gamma_pre  device [D];  gate  device [G][D], row t / (T / G)
  *     for token t (G divides T; G = 1: one gate per channel), all three in
  *     `param_dtype`: `dtype` or MOE_DT_F32
- * Statistics in fp32; h is taken from x_out before its rounding.
+ * Statistics in fp32, for any finite x and y (squares beyond fp32 are taken in
+ * other units), with alpha * gate * gamma_post below 1e19; h is taken from x_out
+ * before its rounding.
  *
  * moe_block_norm_backward: the gradients at the stored x_out, from dx_out (of
  * x_out; NULL: zero) and dh (of h; with gamma_pre):

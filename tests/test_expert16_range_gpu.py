@@ -80,3 +80,79 @@ def test_gate_that_brings_a_large_product_back(M, dtype):
                         (drow, ref[2], (32 + F / 8) * 2.0 ** -24)):
         assert r.abs().max() < 3e38
         assert ((got.double().cpu() - r).abs() <= tol * r.abs()).all()
+
+
+# ----------------------------------------------------------------- block norms
+U = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+def within(got, ref, terms, steps, what):
+    """One rounding to the type, `steps` of 2^-24 of the terms, half a subnormal."""
+    got = got.cpu().double()
+    tol = U[BF16 if what[1] is BF16 else F32] * ref.abs() + steps * 2.0 ** -24 * terms + 2.0 ** -134
+    bad = ~((got - ref).abs() <= tol)
+    assert not bad.any(), (what, int(bad.sum()), got[bad][:4], ref[bad][:4])
+
+
+def randn(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed))
+
+
+def wide_rows(T, D, dtype):
+    """x and y of ordinary rows and, in turn, of rows whose squares, or products
+    of two tensors, are beyond fp32."""
+    x, y = randn(1, T, D), randn(2, T, D)
+    low = torch.finfo(dtype).min
+    for r in range(T):
+        kind = r % 8
+        if kind == 1:
+            y[r] = low / 4 if r % 16 == 1 else low  # one value, the type's lowest
+        elif kind == 2:
+            y[r] *= 1e30
+        elif kind == 3:
+            x[r] *= 1e30
+        elif kind == 4:
+            x[r] *= 1e25
+            y[r] *= 1e33
+        elif kind == 5:
+            x[r] *= 1e17
+            y[r] *= 1e17
+        elif kind == 6:
+            x[r] = low
+        # kinds 0 and 7 stay
+    return x.to(dtype), y.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,D", [(9, 512), (700, 512), (25, 4104), (330, 4104), (330, 8200)])
+@pytest.mark.parametrize("alpha,gates", [(0.75, 1), (1e-3, 1), (1e19, 1), (0.75, 0)])
+def test_norms_of_rows_whose_squares_leave_fp32(M, T, D, alpha, gates, dtype):
+    eps = 1e-6
+    x, y = wide_rows(T, D, dtype)
+    post, pre = 1 + 0.2 * randn(3, D), 1 + 0.2 * randn(4, D)
+    gate = 0.5 + randn(5, 1, D).abs().clamp_max(2) if gates else None
+    xd, yd = x.double(), y.double()
+    n = alpha * (gate.double() if gates else 1.0) * yd / ((yd * yd).mean(1, keepdim=True) + eps).sqrt() * post.double()
+    xo, terms = xd + n, xd.abs() + n.abs()
+    h = xo / ((xo * xo).mean(1, keepdim=True) + eps).sqrt() * pre.double()
+    limit = torch.finfo(dtype).max
+    fits = (xo.abs() <= limit).all(1)  # x at the lowest value and n of the same sign
+    assert fits.sum() > T // 2
+    got_x, got_h = M.block_norm(x.cuda(), y.cuda(), post.cuda(), gate.cuda() if gates else None, pre.cuda(), alpha, eps)
+    within(got_x[fits.cuda()], xo[fits], terms[fits], 64, ("x_out", dtype))
+    within(got_h[fits.cuda()], h[fits], (h.abs() * (1 + terms / xo.abs().clamp_min(1e-300)))[fits], 64, ("h", dtype))
+    alone = M.block_norm(x.cuda(), gamma_pre=pre.cuda(), eps=eps)[1]
+    ref = xd / ((xd * xd).mean(1, keepdim=True) + eps).sqrt() * pre.double()
+    within(alone, ref, 2 * ref.abs(), 64, ("h of x", dtype))
+
+
+def test_norms_keep_infinities_and_nans_in_their_rows(M):
+    x, y = randn(1, 40, 264), randn(2, 40, 264)
+    p = torch.ones(264).cuda()
+    want = M.block_norm(x.cuda(), y.cuda(), p, None, p)
+    x2, y2 = x.clone(), y.clone()
+    x2[3, 5], y2[7, 0], y2[9, 100] = float("inf"), float("nan"), float("-inf")
+    got = M.block_norm(x2.cuda(), y2.cuda(), p, None, p)
+    rest = [r for r in range(40) if r not in (3, 7, 9)]
+    assert torch.equal(got[0][rest], want[0][rest]) and torch.equal(got[1][rest], want[1][rest])
+    assert all(not torch.isfinite(got[1][r]).all() for r in (3, 7, 9))
