@@ -140,9 +140,11 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(c
         for (int k = 0; k < 6; ++k) t[k] = s[k].x + s[k].y;
         rg.sum6(t);
         const float r2 = has_dh ? rsqrtf(t[0] * inv_d + p.eps) : 0.f;
-        const float c2 = r2 * r2 * r2 * (t[1] * inv_d);
+        // r^3 by itself may leave fp32's range (a row of zeros and an eps of 1e-26),
+        // which 0 does not bring back: one factor r after the other
+        const float c2 = r2 * (r2 * (r2 * (t[1] * inv_d)));
         const float r1 = has_post ? rsqrtf(t[2] * inv_d + p.eps) : 1.f;
-        const float c1 = has_post ? r1 * r1 * r1 * ((t[3] + r2 * t[4] - c2 * t[5]) * inv_d) : 0.f;
+        const float c1 = has_post ? r1 * (r1 * (r1 * ((t[3] + r2 * t[4] - c2 * t[5]) * inv_d))) : 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = i * p.threads + rg.tid;

@@ -156,3 +156,47 @@ def test_norms_keep_infinities_and_nans_in_their_rows(M):
     rest = [r for r in range(40) if r not in (3, 7, 9)]
     assert torch.equal(got[0][rest], want[0][rest]) and torch.equal(got[1][rest], want[1][rest])
     assert all(not torch.isfinite(got[1][r]).all() for r in (3, 7, 9))
+
+
+def norm_gradients(x, y, dxo, dh, post, gate, pre, alpha, eps):
+    """The gradients in 64 bits and the sums of absolute terms of each."""
+    x, y, dxo, dh = (t.double() for t in (x, y, dxo, dh))
+    post, pre, a = post.double(), pre.double(), alpha * gate.double()
+    r1 = ((y * y).mean(1, keepdim=True) + eps).rsqrt()
+    r2 = ((x * x).mean(1, keepdim=True) + eps).rsqrt()
+    v, xn, yn = dh * pre, x * r2, y * r1
+    d = dxo + r2 * v - r2 * xn * (v * xn).mean(1, keepdim=True)
+    da = dxo.abs() + (r2 * v).abs() + (r2 * xn).abs() * (v * xn).abs().mean(1, keepdim=True)
+    q, qa = a * post * d, (a * post).abs() * da
+    dy = r1 * q - r1 * yn * (q * yn).mean(1, keepdim=True)
+    dya = r1 * qa + (r1 * yn).abs() * (qa * yn.abs()).mean(1, keepdim=True)
+    tp, tg, tq = a * d * yn, alpha * post * d * yn, dh * xn
+    ta, ga = (a * yn).abs() * da, (alpha * post * yn).abs() * da
+    return {"dx": (d, da), "dy": (dy, dya), "dgamma_post": (tp.sum(0), ta.sum(0)),
+            "dgate": (tg.sum(0, keepdim=True), ga.sum(0, keepdim=True)), "dgamma_pre": (tq.sum(0), tq.abs().sum(0))}
+
+
+def check_norm_gradients(M, x, y, dxo, dh, eps, alpha=0.75):
+    D = x.shape[1]
+    post, pre, gate = 1 + 0.2 * randn(13, D), 1 + 0.2 * randn(14, D), 0.5 + randn(15, 1, D).abs().clamp_max(2)
+    ref = norm_gradients(x, y, dxo, dh, post, gate, pre, alpha, eps)
+    cu = lambda t: t.cuda()
+    got = M.block_norm_backward(cu(x), cu(y), cu(dxo), cu(dh), cu(post), cu(gate), cu(pre), alpha, eps)
+    for (name, (r, terms)), g in zip(ref.items(), got):
+        rows = x.shape[0] if name.startswith("dg") else 0
+        # dgamma and dgate are fp32 whatever the rows are
+        within(g, r, terms, 64 + rows, (name, x.dtype if name in ("dx", "dy") else F32))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,D", [(7, 264), (700, 512), (330, 4104), (9, 8200)])
+@pytest.mark.parametrize("eps", [1e-6, 1e-30])
+def test_norm_gradients_of_small_rows(M, T, D, eps, dtype):
+    """1 / rms cubed is beyond fp32 where a row is zero beside a small eps."""
+    x, y = randn(1, T, D), randn(2, T, D)
+    for r in range(T):
+        x[r] *= [1.0, 0.0, 0.0, 1e-12, 1e-10][r % 5]
+        y[r] *= [1.0, 0.0, 1.0, 1e-11, 1e-12][r % 5]
+    dh, dxo = randn(3, T, D), randn(4, T, D)
+    dxo[1::2] = 0  # what comes through the norm is not hidden behind dx_out
+    check_norm_gradients(M, x.to(dtype), y.to(dtype), dxo.to(dtype), dh.to(dtype), eps)
