@@ -13,6 +13,13 @@ namespace {
 
 constexpr int BLOCK_THREADS = 512;  // most threads of a block: 128 registers each
 
+// Rows of about 2^40 (1e12) and more, whose sums or coefficients (gradients over
+// squares) would leave fp32's range, are taken a second time, in units that make them
+// of ordinary size: a sum at a time, since the six at once spill registers of the
+// ordinary rows (4096 x 5120 with 64 gates 81.6 -> 87.2 us; so 81.8).
+constexpr float LARGE_SUM = 0x1p80f;
+__device__ __forceinline__ float unit(float sum) { return !(sum < INFINITY) ? 0x1p-80f : sum < 0x1p40f ? 1.f : 0x1p-40f; }
+
 // A row group takes p.rows consecutive rows, the loads of the next SLOTS - 1
 // under way while it computes one (SLOTS = 1: none).  One reduction a row:
 // sum(q y) is taken apart into sums that do not wait for D, with
@@ -139,28 +146,73 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) block_norm_backward_kernel(c
 #pragma unroll
         for (int k = 0; k < 6; ++k) t[k] = s[k].x + s[k].y;
         rg.sum6(t);
-        const float r2 = has_dh ? rsqrtf(t[0] * inv_d + p.eps) : 0.f;
+        float r2 = has_dh ? rsqrtf(t[0] * inv_d + p.eps) : 0.f;
         // r^3 by itself may leave fp32's range (a row of zeros and an eps of 1e-26),
         // which 0 does not bring back: one factor r after the other
-        const float c2 = r2 * (r2 * (r2 * (t[1] * inv_d)));
-        const float r1 = has_post ? rsqrtf(t[2] * inv_d + p.eps) : 1.f;
-        const float c1 = has_post ? r1 * (r1 * (r1 * ((t[3] + r2 * t[4] - c2 * t[5]) * inv_d))) : 0.f;
+        float c2 = r2 * (r2 * (r2 * (t[1] * inv_d)));
+        float r1 = has_post ? rsqrtf(t[2] * inv_d + p.eps) : 1.f;
+        float c1 = has_post ? r1 * (r1 * (r1 * ((t[3] + r2 * t[4] - c2 * t[5]) * inv_d))) : 0.f;
+        // The row's outputs.  LARGE: x' in units of 1 / ux, y of 1 / uy.
+        auto finish = [&](auto large, float ux, float uy) {
+            constexpr bool LARGE = decltype(large)::value;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = i * p.threads + rg.tid;
-            if (in[i]) {
-                const Chunk k = VPT == 1 ? kept : load(i);
-                if (VPT > 1) params(c, grow);
-                const V8 x = unpack8<T>(k.x), dh = mul(unpack8<T>(k.dh), r2);
-                a_pre[i] = fma(dh, x, a_pre[i]);
-                const V8 d = fma(x, -c2, fma(dh, kb, unpack8<T>(k.dx)));
-                store_at<T>(p.dx, off + i * next, d);
-                if (has_y) {
-                    const V8 y = unpack8<T>(k.y), dr = mul(d, r1);
-                    z[i] = fma(dr, y, z[i]);
-                    store_at<T>(p.dy, off + i * next, fma(y, -c1, mul(dr, ka)));
+            for (int i = 0; i < VPT; ++i) {
+                const int c = i * p.threads + rg.tid;
+                if (in[i]) {
+                    const Chunk k = VPT == 1 ? kept : load(i);
+                    if (VPT > 1) params(c, grow);
+                    V8 x = unpack8<T>(k.x), d;
+                    const V8 dh = mul(unpack8<T>(k.dh), r2);
+                    if (LARGE) x = mul(x, ux);
+                    a_pre[i] = fma(dh, x, a_pre[i]);
+                    if (LARGE) d = fma(fma(x, -c2, mul(dh, kb)), ux, unpack8<T>(k.dx));
+                    else d = fma(x, -c2, fma(dh, kb, unpack8<T>(k.dx)));
+                    store_at<T>(p.dx, off + i * next, d);
+                    if (has_y) {
+                        V8 y = unpack8<T>(k.y);
+                        const V8 dr = mul(d, r1);
+                        if (LARGE) y = mul(y, uy);
+                        z[i] = fma(dr, y, z[i]);
+                        V8 e = fma(y, -c1, mul(dr, ka));
+                        if (LARGE) e = mul(e, uy);
+                        store_at<T>(p.dy, off + i * next, e);
+                    }
                 }
             }
+        };
+        // the same for the group's threads, and true for a NaN
+        if (__builtin_expect(!(t[0] + t[2] < LARGE_SUM), 0)) {
+            const float ux = unit(t[0]), uy = has_post ? unit(t[2]) : 1.f;
+            auto sum = [&](auto term) {
+                float2 q = f2(0.f);
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (in[i]) {
+                        const Chunk k = VPT == 1 ? kept : load(i);
+                        if (VPT > 1) params(i * p.threads + rg.tid, grow);
+                        term(q, k);
+                    }
+                return q.x + q.y;
+            };
+            auto xs = [&](const Chunk& k) { return mul(unpack8<T>(k.x), ux); };
+            auto ys = [&](const Chunk& k) { return mul(unpack8<T>(k.y), uy); };
+            auto vs = [&](const Chunk& k) { return mul(unpack8<T>(k.dh), kb); };
+            t[0] = sum([&](float2& q, const Chunk& k) { dot(q, xs(k), xs(k)); });
+            t[1] = sum([&](float2& q, const Chunk& k) { dot(q, vs(k), xs(k)); });
+            if (has_post) {
+                t[2] = sum([&](float2& q, const Chunk& k) { dot(q, ys(k), ys(k)); });
+                t[3] = sum([&](float2& q, const Chunk& k) { dot(q, mul(ka, ys(k)), unpack8<T>(k.dx)); });
+                t[4] = sum([&](float2& q, const Chunk& k) { dot(q, mul(ka, ys(k)), vs(k)); });
+                t[5] = sum([&](float2& q, const Chunk& k) { dot(q, mul(ka, ys(k)), xs(k)); });
+            }
+            rg.sum6(t);
+            r2 = has_dh ? rsqrtf(t[0] * inv_d + p.eps * ux * ux) : 0.f;
+            c2 = r2 * (r2 * (r2 * (t[1] * inv_d)));
+            r1 = has_post ? rsqrtf(t[2] * inv_d + p.eps * uy * uy) : 1.f;
+            c1 = has_post ? r1 * (r1 * (r1 * ((t[3] + ux * (r2 * t[4] - c2 * t[5])) * inv_d))) : 0.f;
+            finish(std::true_type{}, ux, uy);
+        } else {
+            finish(std::false_type{}, 1.f, 1.f);
         }
         ring.next();
         // the gate row ends here

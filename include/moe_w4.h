@@ -319,7 +319,9 @@ moe_status_t moe_swiglu_backward(moe_dtype_t dtype, const void* dh, const void* 
  * moe_block_norm_backward: the gradients at the stored x_out, from dx_out (of
  * x_out; NULL: zero) and dh (of h; with gamma_pre):
  *   dx, dy  device [T][D];  dgamma_post, dgate, dgamma_pre as their parameters,
- *   each NULL to skip.  dx may be dx_out.  The order of every sum is fixed.
+ *   each NULL to skip.  dx may be dx_out.  The order of every sum is fixed.  Any
+ *   finite x_out and y, as above; sums of dx_out or dh times a normalised row have
+ *   to be within fp32.
  * Workspace: >= moe_block_norm_backward_workspace_size(T, D, G) bytes.
  */
 moe_status_t moe_block_norm(moe_dtype_t dtype, moe_dtype_t param_dtype, int32_t T, int32_t D, int32_t G,

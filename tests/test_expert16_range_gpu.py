@@ -200,3 +200,35 @@ def test_norm_gradients_of_small_rows(M, T, D, eps, dtype):
     dh, dxo = randn(3, T, D), randn(4, T, D)
     dxo[1::2] = 0  # what comes through the norm is not hidden behind dx_out
     check_norm_gradients(M, x.to(dtype), y.to(dtype), dxo.to(dtype), dh.to(dtype), eps)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,D", [(17, 264), (700, 512), (330, 4104), (18, 8200)])
+@pytest.mark.parametrize("gates", [1, "many"])
+def test_norm_gradients_of_large_rows(M, T, D, gates, dtype):
+    """Rows whose squares, or whose gradients over squares, are beyond fp32."""
+    x, y = randn(1, T, D), randn(2, T, D)
+    scale = [1.0, 1e13, 1e15, 1e17, 1e19, 1e25, 1e33, 1e5]
+    for r in range(T):
+        x[r] *= scale[r % 8]
+        y[r] *= scale[(r + r // 8) % 8]
+    low = torch.finfo(dtype).min
+    x[3], y[5], x[7], y[7] = low, low, low, low / 2
+    dh, dxo = randn(3, T, D), randn(4, T, D)
+    dxo[1::2] = 0
+    x, y, dh, dxo = (t.to(dtype) for t in (x, y, dh, dxo))
+    if gates == 1:
+        check_norm_gradients(M, x, y, dxo, dh, 1e-6)
+        return
+    # gate by gate
+    G = {17: 17, 700: 7, 330: 110, 18: 2}[T]
+    post, pre, gate = 1 + 0.2 * randn(13, D), 1 + 0.2 * randn(14, D), 0.5 + randn(15, G, D).abs().clamp_max(2)
+    cu = lambda t: t.cuda()
+    dx, dy, _, dgate, _ = M.block_norm_backward(cu(x), cu(y), cu(dxo), cu(dh), cu(post), cu(gate), cu(pre), 0.75, 1e-6)
+    S = T // G
+    for g in (0, G // 2, G - 1):
+        s = slice(g * S, (g + 1) * S)
+        ref = norm_gradients(x[s], y[s], dxo[s], dh[s], post, gate[g:g + 1], pre, 0.75, 1e-6)
+        within(dx[s], *ref["dx"], 64, ("dx", dtype))
+        within(dy[s], *ref["dy"], 64, ("dy", dtype))
+        within(dgate[g:g + 1], *ref["dgate"], 64 + S, ("dgate", F32))
