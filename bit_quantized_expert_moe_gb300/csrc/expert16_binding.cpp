@@ -16,6 +16,8 @@
 
 #include <array>
 #include <exception>
+#include <functional>
+#include <initializer_list>
 #include <stdexcept>
 #include <string>
 
@@ -57,13 +59,20 @@ moe_dtype_t moe_type(at::ScalarType t) {
     }
 }
 
-// Device pointer of a tensor, null for one that is not there.
-void* ptr(const Tensor& t) {
-    if (!t.defined()) return nullptr;
-    if (!t.is_cuda()) throw Refusal("device tensor expected");
-    if (!t.is_contiguous()) throw Refusal("contiguous tensor expected");
-    return t.data_ptr();
+// The tensors of a call that are there: dense, and on the device of the first, on
+// which the call runs.
+void on_one_device(std::initializer_list<std::reference_wrapper<const Tensor>> ts) {
+    const Tensor& first = *ts.begin();
+    for (const Tensor& t : ts) {
+        if (!t.defined()) continue;
+        if (!t.is_cuda()) throw Refusal("device tensor expected");
+        if (!t.is_contiguous()) throw Refusal("contiguous tensor expected");
+        if (t.device() != first.device())
+            throw Refusal("tensors of one device expected, not of " + first.device().str() + " and " + t.device().str());
+    }
 }
+// Pointer of a tensor that on_one_device() has seen, null for one that is not there.
+void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 template <class T>
 T* ptr_as(const Tensor& t) { return static_cast<T*>(ptr(t)); }
 
@@ -117,17 +126,19 @@ struct Args {
     }
 };
 
-// The stream of a call on `of`, which has to be on a device: the one given, else
-// the current one.  While this lives the given one is current, so that what the
-// call allocates belongs to the stream that writes it.
+// The device of `of` and the stream of a call there: the one given, else that
+// device's current one.  While this lives both are current, so that the call launches
+// on that device and what it allocates belongs to the stream that writes it.
 struct OnStream {
     cudaStream_t s;
+    c10::cuda::OptionalCUDAGuard device;
     c10::cuda::OptionalCUDAStreamGuard guard;
     template <size_t N>
     OnStream(const Args<N>& a, size_t i, const Tensor& of) {
-        ptr(of);
+        const c10::DeviceIndex index = of.device().index();
+        if (c10::cuda::current_device() != index) device.set_index(index);
         if (!a.given(i)) {
-            s = c10::cuda::getCurrentCUDAStream().stream();
+            s = c10::cuda::getCurrentCUDAStream(index).stream();
             return;
         }
         PyObject* h = PyObject_GetAttrString(a.v[i], "cuda_stream");
@@ -135,7 +146,7 @@ struct OnStream {
         s = static_cast<cudaStream_t>(PyLong_AsVoidPtr(h));
         Py_DECREF(h);
         if (!s && PyErr_Occurred()) throw Raised{};
-        guard.reset_stream(c10::cuda::getStreamFromExternal(s, of.device().index()));
+        guard.reset_stream(c10::cuda::getStreamFromExternal(s, index));
     }
 };
 
@@ -175,7 +186,6 @@ Tensor output(const Tensor& given, const char* what, const Tensor& like, Shape s
         want(what, given, shape, type);
         return given;
     }
-    if (!like.is_cuda()) throw Refusal("device tensor expected");
     // Straight from the CUDA allocator: 0.3 us less per output than at::empty's
     // dispatch, of the 3.8 us that the smallest call takes.
     return at::detail::empty_cuda(shape, type, like.device(), c10::nullopt);
@@ -233,9 +243,11 @@ PyObject* py_grouped_mm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject
         dims("w", w, 3);
         const int64_t R = x.size(0), K = x.size(1), E = w.size(0), N = w.size(1);
         want("w", w, {E, N, K}, x.scalar_type());
+        const Tensor given = a.tensor(3), ws = a.tensor(4);
+        on_one_device({x, w, off, given, ws});
         const OnStream on(a, 5, x);
-        const Tensor y = output(a.tensor(3), "y", x, {R, N}, x.scalar_type());
-        return grouped(moe_grouped_mm, "moe_grouped_mm", x, w, off, R, E, N, K, y, a.tensor(4), on.s);
+        const Tensor y = output(given, "y", x, {R, N}, x.scalar_type());
+        return grouped(moe_grouped_mm, "moe_grouped_mm", x, w, off, R, E, N, K, y, ws, on.s);
     });
 }
 PyObject* py_grouped_mm_dx(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
@@ -247,9 +259,11 @@ PyObject* py_grouped_mm_dx(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
         dims("w", w, 3);
         const int64_t R = dy.size(0), N = dy.size(1), E = w.size(0), K = w.size(2);
         want("w", w, {E, N, K}, dy.scalar_type());
+        const Tensor given = a.tensor(3), ws = a.tensor(4);
+        on_one_device({dy, w, off, given, ws});
         const OnStream on(a, 5, dy);
-        const Tensor dx = output(a.tensor(3), "dx", dy, {R, K}, dy.scalar_type());
-        return grouped(moe_grouped_mm_dx, "moe_grouped_mm_dx", dy, w, off, R, E, N, K, dx, a.tensor(4), on.s);
+        const Tensor dx = output(given, "dx", dy, {R, K}, dy.scalar_type());
+        return grouped(moe_grouped_mm_dx, "moe_grouped_mm_dx", dy, w, off, R, E, N, K, dx, ws, on.s);
     });
 }
 PyObject* py_grouped_mm_dw(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
@@ -261,9 +275,11 @@ PyObject* py_grouped_mm_dw(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
         dims("x", x, 2);
         const int64_t R = dy.size(0), N = dy.size(1), K = x.size(1), E = off.numel() - 1;
         want("x", x, {R, K}, dy.scalar_type());
+        const Tensor given = a.tensor(3), ws = a.tensor(4);
+        on_one_device({dy, x, off, given, ws});
         const OnStream on(a, 5, dy);
-        const Tensor dw = output(a.tensor(3), "dw", dy, {E, N, K}, dy.scalar_type());
-        return grouped(moe_grouped_mm_dw, "moe_grouped_mm_dw", dy, x, off, R, E, N, K, dw, a.tensor(4), on.s);
+        const Tensor dw = output(given, "dw", dy, {E, N, K}, dy.scalar_type());
+        return grouped(moe_grouped_mm_dw, "moe_grouped_mm_dw", dy, x, off, R, E, N, K, dw, ws, on.s);
     });
 }
 
@@ -283,8 +299,10 @@ PyObject* py_swiglu(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw
         const Tensor gu = a.needed_tensor(0), row_w = a.tensor(1), row_map = a.tensor(2);
         const int64_t F = gated_width(gu, row_w, row_map), R = gu.size(0);
         const moe_dtype_t dt = moe_type(gu.scalar_type());
+        const Tensor given = a.tensor(3);
+        on_one_device({gu, row_w, row_map, given});
         const OnStream on(a, 4, gu);
-        const Tensor h = output(a.tensor(3), "h", gu, {R, F}, gu.scalar_type());
+        const Tensor h = output(given, "h", gu, {R, F}, gu.scalar_type());
         check(moe_swiglu(dt, ptr(gu), ptr_as<float>(row_w), ptr_as<int32_t>(row_map), size32(R), size32(F), ptr(h),
                          on.s), "moe_swiglu");
         return wrap(h);
@@ -299,9 +317,11 @@ PyObject* py_swiglu_backward(PyObject*, PyObject* const* args, Py_ssize_t n, PyO
         const at::ScalarType t = gu.scalar_type();
         const moe_dtype_t dt = moe_type(t);
         want("dh", dh, {R, F}, t);
-        const OnStream on(a, 6, gu);
-        const Tensor dgu = output(a.tensor(4), "dgu", gu, {R, 2 * F}, t);
+        const Tensor given = a.tensor(4);
         Tensor dw = a.tensor(5);
+        on_one_device({gu, dh, row_w, row_map, given, dw});
+        const OnStream on(a, 6, gu);
+        const Tensor dgu = output(given, "dgu", gu, {R, 2 * F}, t);
         if (dw.defined() || row_w.defined()) dw = output(dw, "drow_w", gu, {R}, at::kFloat);
         check(moe_swiglu_backward(dt, ptr(dh), ptr(gu), ptr_as<float>(row_w), ptr_as<int32_t>(row_map), size32(R),
                                   size32(F), ptr(dgu), ptr_as<float>(dw), on.s), "moe_swiglu_backward");
@@ -343,8 +363,9 @@ PyObject* py_block_norm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject
         const Tensor x = a.needed_tensor(0), y = a.tensor(1), post = a.tensor(2), gate = a.tensor(3), pre = a.tensor(4);
         const Norm m(x, post, gate, pre);
         m.row("y", y);
-        const OnStream on(a, 9, x);
         Tensor xo = a.tensor(7), h = a.tensor(8);
+        on_one_device({x, y, post, gate, pre, xo, h});
+        const OnStream on(a, 9, x);
         if (xo.defined() || y.defined()) xo = output(xo, "x_out", x, {m.T, m.D}, m.type);
         if (h.defined() || pre.defined()) h = output(h, "h", x, {m.T, m.D}, m.type);
         check(moe_block_norm(m.dt, m.pt, size32(m.T), size32(m.D), size32(m.G), a.number(5, 1.0), a.number(6, 1e-6),
@@ -364,6 +385,7 @@ PyObject* py_block_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n,
         m.row("dx_out", dxo);
         m.row("dh", dh);
         const int32_t T = size32(m.T), D = size32(m.D), G = size32(m.G);
+        on_one_device({x, y, dxo, dh, post, gate, pre, given_ws});
         const OnStream on(a, 10, x);
         const Tensor none;
         const Tensor dx = output(none, "dx", x, {m.T, m.D}, m.type);
