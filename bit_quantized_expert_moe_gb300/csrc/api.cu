@@ -5,22 +5,20 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "device_value.h"
 #include "internal.h"
 #include "moe_w4.h"
 
 namespace moe {
 
 int num_sms() {
-    static int n = 0;
-    if (n == 0) {
-        int dev = 0, v = 0;
-        if (cudaGetDevice(&dev) == cudaSuccess &&
-            cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
-            n = v;
-        else
-            return 1;
-    }
-    return n;
+    static DeviceValue sms;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    return std::max(1, sms.get(dev, [dev] {
+        int v = 0;
+        return cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? v : 0;
+    }));
 }
 
 static std::atomic<uint64_t> g_launches{0};

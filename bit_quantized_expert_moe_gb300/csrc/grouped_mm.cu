@@ -37,6 +37,7 @@
 // by the round's parity, so every waiter waits for every round of a barrier that
 // it uses, in order.  Every wait is bounded in time: one that gives up sets the
 // error word and every role leaves its loop.
+#include "device_value.h"
 #include "internal.h"
 #include "tc_ptx.cuh"
 #include "vec8.cuh"
@@ -594,13 +595,13 @@ int tile_count(const GroupedShape& g, int cols, bool even) {
 // 3002 rows, N 648, K 896: 9.2, 7.6, 9.4; of 2208 of 3 experts, N 232, K 5608:
 // 36.1, 27.4, 23.0.
 template <Product PR>
-int tile_columns(const GroupedShape& g) {
+int tile_columns(const GroupedShape& g, int pairs) {
     int best = BN;
     long long least = INT64_MAX;
     for (int cols = BN; cols >= 64; cols >>= 1) {
         const int all = PR == Product::DW ? g.K : ceil_div(g.R, std::min(g.R, g.E));
         const int width = ceil_div(all, ceil_div(all, cols));
-        const long long cost = (long long)ceil_div(tile_count<PR>(g, cols, true), sm_pairs()) * (2 * BM + width);
+        const long long cost = (long long)ceil_div(tile_count<PR>(g, cols, true), pairs) * (2 * BM + width);
         if (cost < least) {
             least = cost;
             best = cols;
@@ -614,24 +615,23 @@ int tile_columns(const GroupedShape& g) {
 // K 7168: y 20.4 -> 9.9 us; 3851 rows, N 3064, K 96: dw 19.5 -> 12.7; two experts,
 // 300 rows, N 5608, K 232: dx 27.2 -> 10.3; 70 rows, N 88, K 2072: y 9.4 -> 7.6.
 template <Product PR>
-int tile_splits(const GroupedShape& g, int cols) {
+int tile_splits(const GroupedShape& g, int cols, int pairs) {
     const int stages = ceil_div(PR == Product::Y ? g.K : PR == Product::DX ? g.N : ceil_div(g.R, g.E), BL);
-    const int most = std::min({sm_pairs() / tile_count<PR>(g, cols, true), stages / 8, 8});
+    const int most = std::min({pairs / tile_count<PR>(g, cols, true), stages / 8, 8});
     return most > 1 && stages - ceil_div(stages, most) >= 16 ? most : 1;
 }
 // fp32 values of the shares' outputs.
 template <Product PR>
-size_t split_floats(const GroupedShape& g) {
-    const int splits = tile_splits<PR>(g, tile_columns<PR>(g));
+size_t split_floats(const GroupedShape& g, int pairs) {
+    const int splits = tile_splits<PR>(g, tile_columns<PR>(g, pairs), pairs);
     return splits == 1 ? 0 : (size_t)splits * (PR == Product::DW ? (size_t)g.E * g.N : g.R) * (PR == Product::Y ? g.N : g.K);
 }
 
 template <Product PR, bool SPLIT>
-cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, int splits, cudaStream_t s) {
+cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, int cols, int splits, cudaStream_t s) {
     const bool bf = g.dtype == MOE_DT_BF16;
     Maps maps;
     bool ok;
-    const int cols = tile_columns<PR>(g);
     const int items = tile_count<PR>(g, cols, false);
     if (PR == Product::DW) {
         ok = map_2d(&maps.a, bf, a, g.N, g.R, 64, 64) && map_2d(&maps.b[0], bf, b, g.K, g.R, 64, 64) &&
@@ -643,24 +643,26 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
         for (int i = 0; i < cols / 32 && ok; ++i) ok = map_2d(&maps.b[i], bf, b, L, g.R, 64, (i + 1) * 16);
     }
     if (!ok) return cudaErrorInvalidValue;
-    static int max_pairs = 0;  // CTA pairs that the GPU holds at once
-    if (max_pairs == 0) {
-        const cudaError_t e = allow_smem<grouped_tc_kernel<PR, SPLIT>>();
-        if (e != cudaSuccess) return e;
+    static DeviceValue pairs;  // CTA pairs that the GPU holds at once
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const int max_pairs = pairs.get(dev, [] {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
         cfg.blockDim = dim3(THREADS);
         cfg.dynamicSmemBytes = smem_bytes<PR>(1024);
         int nc = 0;
-        if (cudaOccupancyMaxActiveClusters(&nc, grouped_tc_kernel<PR, SPLIT>, &cfg) != cudaSuccess || nc < 1) {
+        if (allow_smem<grouped_tc_kernel<PR, SPLIT>>() != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&nc, grouped_tc_kernel<PR, SPLIT>, &cfg) != cudaSuccess || nc < 1) {
             (void)cudaGetLastError();
-            nc = num_sms() / 2;
+            nc = sm_pairs();
         }
-        max_pairs = std::max(1, nc);
-    }
+        return nc;
+    });
     const GroupedParams p{g.R, g.E, g.N, g.K, g.offsets, out, bf ? 1u : 0u, cols, splits, g.part, g.err};
     const int grid = 2 * (int)std::max<long long>(1, std::min<long long>(max_pairs, (long long)items * splits));
-    cudaError_t e = launch_overlapped<grouped_tc_kernel<PR, SPLIT>>(dim3(grid), dim3(THREADS), smem_bytes<PR>(g.E), s, maps, p);
+    e = launch_overlapped<grouped_tc_kernel<PR, SPLIT>>(dim3(grid), dim3(THREADS), smem_bytes<PR>(g.E), s, maps, p);
     if (SPLIT && e == cudaSuccess) {
         GroupedParams q = p;
         if (PR == Product::DW) q.offsets = nullptr;
@@ -672,15 +674,16 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
 }
 template <Product PR>
 cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* out, cudaStream_t s) {
-    const int splits = tile_splits<PR>(g, tile_columns<PR>(g));
-    return splits > 1 ? launch<PR, true>(g, a, b, out, splits, s) : launch<PR, false>(g, a, b, out, 1, s);
+    const int pairs = sm_pairs(), cols = tile_columns<PR>(g, pairs), splits = tile_splits<PR>(g, cols, pairs);
+    return splits > 1 ? launch<PR, true>(g, a, b, out, cols, splits, s) : launch<PR, false>(g, a, b, out, cols, 1, s);
 }
 
 }  // namespace
 
 size_t grouped_split_floats(const GroupedShape& g) {
     if (g.R == 0) return 0;
-    return std::max({split_floats<Product::Y>(g), split_floats<Product::DX>(g), split_floats<Product::DW>(g)});
+    const int pairs = sm_pairs();
+    return std::max({split_floats<Product::Y>(g, pairs), split_floats<Product::DX>(g, pairs), split_floats<Product::DW>(g, pairs)});
 }
 cudaError_t launch_grouped_mm(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s) {
     // E 128, N 1536, K 2048: 8 rows 12.1 us there and 13.1 here, 32 rows 31.0 and

@@ -177,7 +177,7 @@ bool make_tensor_map_16(CUtensorMap* m, bool bf16, const void* ptr, int rank, co
                         const uint64_t* strides, const uint32_t* box);
 
 // ----------------------------------------------------------- device info
-int num_sms();
+int num_sms();  // of the current device
 // Counts one kernel launch of this library (reported by moe_kernel_launches).
 void note_launch(int n = 1);
 // Lets a kernel without static shared memory take all of an SM's as dynamic
