@@ -26,17 +26,19 @@ bool grouped_sizes_ok(int32_t R, int32_t E, int32_t N, int32_t K) {
 }
 bool width_supported(int32_t w, int32_t most) { return w % 8 == 0 && w <= most; }
 
+size_t with_header(size_t floats) { return WS_HEADER + floats * sizeof(float); }
+
 // The checks that the three products share; MOE_OK, or the status to return.
-// Without rows the operands may be null, and y and dx too.
-moe_status_t check_grouped(moe_dtype_t dtype, const void* a, const void* b, const int32_t* offsets, int32_t R, int32_t E,
+// Without rows the operands may be null, and y and dx too.  `floats`: what the
+// product itself needs, which may be less than the size that callers are told.
+moe_status_t check_grouped(size_t (*floats)(const GroupedShape&), moe_dtype_t dtype, const void* a, const void* b, const int32_t* offsets, int32_t R, int32_t E,
                            int32_t N, int32_t K, bool needs_out, const void* out, const void* ws, size_t ws_bytes) {
     if (!grouped_sizes_ok(R, E, N, K)) return MOE_ERR_INVALID_ARG;
     if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16) return MOE_ERR_UNSUPPORTED;
     if (!width_supported(N, MAX_WIDTH) || !width_supported(K, MAX_WIDTH)) return MOE_ERR_UNSUPPORTED;
     if (!offsets || !ws || (R > 0 && (!a || !b)) || (needs_out && !out)) return MOE_ERR_INVALID_ARG;
     if (!all_aligned({a, b, offsets, out, ws})) return MOE_ERR_MISALIGNED;
-    if (ws_bytes < moe_grouped_mm_workspace_size(R, E, N, K)) return MOE_ERR_WORKSPACE;
-    return MOE_OK;
+    return ws_bytes < with_header(floats(GroupedShape{dtype, R, E, N, K})) ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
 GroupedShape shape(moe_dtype_t dtype, const int32_t* offsets, int32_t R, int32_t E, int32_t N, int32_t K, void* ws) {
@@ -67,12 +69,12 @@ extern "C" {
 
 size_t moe_grouped_mm_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K) {
     if (!grouped_sizes_ok(R, E, N, K)) return 0;
-    return WS_HEADER + grouped_split_floats(GroupedShape{MOE_DT_BF16, R, E, N, K}) * sizeof(float);
+    return with_header(grouped_floats_bound(GroupedShape{MOE_DT_BF16, R, E, N, K}));
 }
 
 moe_status_t moe_grouped_mm(moe_dtype_t dtype, const void* x, const void* w, const int32_t* offsets, int32_t R, int32_t E,
                             int32_t N, int32_t K, void* y, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-    const moe_status_t st = check_grouped(dtype, x, w, offsets, R, E, N, K, R > 0, y, workspace, workspace_bytes);
+    const moe_status_t st = check_grouped(grouped_floats, dtype, x, w, offsets, R, E, N, K, R > 0, y, workspace, workspace_bytes);
     if (st != MOE_OK || R == 0) return st;
     return cuda_status(launch_grouped_mm(shape(dtype, offsets, R, E, N, K, workspace), x, w, y, stream));
 }
@@ -80,7 +82,7 @@ moe_status_t moe_grouped_mm(moe_dtype_t dtype, const void* x, const void* w, con
 moe_status_t moe_grouped_mm_dx(moe_dtype_t dtype, const void* dy, const void* w, const int32_t* offsets, int32_t R,
                                int32_t E, int32_t N, int32_t K, void* dx, void* workspace, size_t workspace_bytes,
                                cudaStream_t stream) {
-    const moe_status_t st = check_grouped(dtype, dy, w, offsets, R, E, N, K, R > 0, dx, workspace, workspace_bytes);
+    const moe_status_t st = check_grouped(grouped_dx_floats, dtype, dy, w, offsets, R, E, N, K, R > 0, dx, workspace, workspace_bytes);
     if (st != MOE_OK || R == 0) return st;
     return cuda_status(launch_grouped_mm_dx(shape(dtype, offsets, R, E, N, K, workspace), dy, w, dx, stream));
 }
@@ -88,7 +90,7 @@ moe_status_t moe_grouped_mm_dx(moe_dtype_t dtype, const void* dy, const void* w,
 moe_status_t moe_grouped_mm_dw(moe_dtype_t dtype, const void* dy, const void* x, const int32_t* offsets, int32_t R,
                                int32_t E, int32_t N, int32_t K, void* dw, void* workspace, size_t workspace_bytes,
                                cudaStream_t stream) {
-    const moe_status_t st = check_grouped(dtype, dy, x, offsets, R, E, N, K, true, dw, workspace, workspace_bytes);
+    const moe_status_t st = check_grouped(grouped_dw_floats, dtype, dy, x, offsets, R, E, N, K, true, dw, workspace, workspace_bytes);
     if (st != MOE_OK) return st;
     return cuda_status(launch_grouped_mm_dw(shape(dtype, offsets, R, E, N, K, workspace), dy, x, dw, stream));
 }
@@ -126,7 +128,7 @@ moe_status_t moe_block_norm(moe_dtype_t dtype, moe_dtype_t param_dtype, int32_t 
 
 size_t moe_block_norm_backward_workspace_size(int32_t T, int32_t D, int32_t G) {
     if (T < 0 || D < 1 || G < 1 || T % G) return 0;
-    return WS_HEADER + block_norm_partial_floats(T, D, G) * sizeof(float);
+    return with_header(block_norm_partial_floats(T, D, G));
 }
 
 moe_status_t moe_block_norm_backward(moe_dtype_t dtype, moe_dtype_t param_dtype, int32_t T, int32_t D, int32_t G,

@@ -614,17 +614,35 @@ int tile_columns(const GroupedShape& g, int pairs) {
 // sum's launch takes as long as about 16 of them.  One expert, 512 rows, N 256,
 // K 7168: y 20.4 -> 9.9 us; 3851 rows, N 3064, K 96: dw 19.5 -> 12.7; two experts,
 // 300 rows, N 5608, K 232: dx 27.2 -> 10.3; 70 rows, N 88, K 2072: y 9.4 -> 7.6.
+int split_count(int pairs, int tiles, int stages) {
+    const int most = std::min({pairs / tiles, stages / 8, 8});
+    return most > 1 && stages - ceil_div(stages, most) >= 16 ? most : 1;
+}
 template <Product PR>
 int tile_splits(const GroupedShape& g, int cols, int pairs) {
     const int stages = ceil_div(PR == Product::Y ? g.K : PR == Product::DX ? g.N : ceil_div(g.R, g.E), BL);
-    const int most = std::min({pairs / tile_count<PR>(g, cols, true), stages / 8, 8});
-    return most > 1 && stages - ceil_div(stages, most) >= 16 ? most : 1;
+    return split_count(pairs, tile_count<PR>(g, cols, true), stages);
 }
 // fp32 values of the shares' outputs.
 template <Product PR>
 size_t split_floats(const GroupedShape& g, int pairs) {
     const int splits = tile_splits<PR>(g, tile_columns<PR>(g, pairs), pairs);
     return splits == 1 ? 0 : (size_t)splits * (PR == Product::DW ? (size_t)g.E * g.N : g.R) * (PR == Product::Y ? g.N : g.K);
+}
+
+// No fewer than the shares of a product with R x M outputs, summed over L, take for
+// these rows or any smaller number of them (dW's never become fewer with the rows).
+// r rows fill at least min(r, E) rows of tiles, mb tiles each, and the shares with
+// all tiles are at most the pairs: up to E rows they take pairs / mb x M values,
+// beyond that what the tiles can hold.
+size_t rows_floats_bound(const GroupedShape& g, int M, int L, int pairs) {
+    const int mb = ceil_div(M, 2 * BM), stages = ceil_div(L, BL), used = std::min(g.R, g.E);
+    const size_t most = split_count(pairs, 1, stages);
+    if (most == 1) return 0;
+    const size_t few = std::min(most * used, (size_t)pairs / mb) * M;
+    const size_t splits = std::min<size_t>(most, pairs / std::max(1, std::min(pairs, g.E * mb)));
+    if (g.R <= g.E || splits < 2) return few;
+    return std::max(few, std::min(splits * g.R * M, (size_t)pairs * 2 * BM * BN));
 }
 
 template <Product PR, bool SPLIT>
@@ -680,17 +698,26 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
 
 }  // namespace
 
-size_t grouped_split_floats(const GroupedShape& g) {
+// E 128, N 1536, K 2048: 8 rows 12.1 us there and 13.1 here, 32 rows 31.0 and
+// 34.9, 128 rows 77.9 and 82.0; E 256, N 4096, K 7168: 64 rows 469 and 492.  With
+// several rows an expert its blocks read the weights again: E 8, N 1024, K 256:
+// 16 rows 4.0 and 4.8, 64 rows 5.8 and 4.9; E 1, N and K 2048: 64 rows 14.3 and 9.0
+static bool takes_few(const GroupedShape& g) { return g.R <= 32 || (g.R <= 128 && g.R <= g.E); }
+
+size_t grouped_floats(const GroupedShape& g) {
+    return g.R == 0 || takes_few(g) ? 0 : split_floats<Product::Y>(g, sm_pairs());
+}
+size_t grouped_dx_floats(const GroupedShape& g) { return g.R == 0 ? 0 : split_floats<Product::DX>(g, sm_pairs()); }
+size_t grouped_dw_floats(const GroupedShape& g) { return g.R == 0 ? 0 : split_floats<Product::DW>(g, sm_pairs()); }
+
+size_t grouped_floats_bound(const GroupedShape& g) {
     if (g.R == 0) return 0;
     const int pairs = sm_pairs();
-    return std::max({split_floats<Product::Y>(g, pairs), split_floats<Product::DX>(g, pairs), split_floats<Product::DW>(g, pairs)});
+    return std::max({rows_floats_bound(g, g.N, g.K, pairs), rows_floats_bound(g, g.K, g.N, pairs),
+                     split_floats<Product::DW>(g, pairs)});
 }
 cudaError_t launch_grouped_mm(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s) {
-    // E 128, N 1536, K 2048: 8 rows 12.1 us there and 13.1 here, 32 rows 31.0 and
-    // 34.9, 128 rows 77.9 and 82.0; E 256, N 4096, K 7168: 64 rows 469 and 492.  With
-    // several rows an expert its blocks read the weights again: E 8, N 1024, K 256:
-    // 16 rows 4.0 and 4.8, 64 rows 5.8 and 4.9; E 1, N and K 2048: 64 rows 14.3 and 9.0
-    if (g.R <= 32 || (g.R <= 128 && g.R <= g.E)) return launch_grouped_few(g, x, w, y, s);
+    if (takes_few(g)) return launch_grouped_few(g, x, w, y, s);
     return launch<Product::Y>(g, w, x, y, s);
 }
 cudaError_t launch_grouped_mm_dx(const GroupedShape& g, const void* dy, const void* w, void* dx, cudaStream_t s) {

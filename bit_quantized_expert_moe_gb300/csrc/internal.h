@@ -130,10 +130,14 @@ struct GroupedShape {
     int R, E, N, K;
     const int32_t* offsets;  // [E+1]
     uint32_t* err;
-    float* part;             // grouped_split_floats() values
+    float* part;             // values of the functions below
 };
-// What the products want to put down before their output, for the sizes alone.
-size_t grouped_split_floats(const GroupedShape& g);
+// What y, dx or dw puts down before its output, for the sizes alone; and what no
+// product exceeds for these sizes or any smaller number of rows.
+size_t grouped_floats(const GroupedShape& g);
+size_t grouped_dx_floats(const GroupedShape& g);
+size_t grouped_dw_floats(const GroupedShape& g);
+size_t grouped_floats_bound(const GroupedShape& g);
 // y = x W_e^T, dx = dy W_e, dW_e = dy_e^T x_e over the segments of `offsets`.
 cudaError_t launch_grouped_mm(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s);
 cudaError_t launch_grouped_mm_dx(const GroupedShape& g, const void* dy, const void* w, void* dx, cudaStream_t s);

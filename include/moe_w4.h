@@ -268,7 +268,8 @@ typedef enum {
  * moe_get_device_error, and the output is unspecified; rows that no segment
  * holds are not written.  1 <= E <= 1024.  R = 0: nothing to do, and zeros in dw.
  * Workspace: >= moe_grouped_mm_workspace_size(R, E, N, K) bytes, the same for
- * the three products.
+ * the three products; one for the most rows also does for fewer (the size never
+ * falls with R; it depends on the current device's SMs).
  */
 size_t moe_grouped_mm_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K);
 moe_status_t moe_grouped_mm(moe_dtype_t dtype, const void* x, const void* w, const int32_t* offsets,

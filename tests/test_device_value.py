@@ -84,3 +84,29 @@ def test_sizes_are_those_of_the_current_device(tmp_path):
 def test_values_are_kept_by_device_and_found_by_any_thread(tmp_path):
     exe = compiled(tmp_path, "values", VALUES, "-pthread")
     assert subprocess.run([exe], capture_output=True, text=True, check=True).stdout == "0\n"
+
+
+SIZES = r"""
+import ctypes, sys
+shim, lib = ctypes.CDLL(sys.argv[1]), ctypes.CDLL(sys.argv[2])
+size = lib.moe_grouped_mm_workspace_size
+size.restype = ctypes.c_size_t
+shim.stand_on(0)
+for E, N, K in ((1, 256, 7168), (2, 1024, 4096), (4, 88, 2072), (8, 1536, 2048), (256, 4096, 7168), (3, 232, 5608), (1, 96, 80)):
+    last = 0
+    for R in sorted({r + d for r in (0, 1, 8, 32, 64, 128, 300, 512, 1000, 2048, 4096, 6000, 20000, 10 ** 6) for d in (0, 1, 3)}):
+        n = size(R, E, N, K)
+        assert last <= n <= 256 + max(4 * 76 * 65536, 8 * 4 * E * N * K), (E, N, K, R, last, n)
+        last = n
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_grouped_workspace_for_many_rows_does_for_fewer(tmp_path):
+    """On a device of 152 SMs: the size never falls with the rows."""
+    try:
+        lib = build_lib()
+    except RuntimeError as e:  # pragma: no cover
+        pytest.skip(f"cannot build: {e}")
+    shim = compiled(tmp_path, "shim.so", SHIM, "-shared", "-fPIC")
+    subprocess.run([sys.executable, "-c", SIZES, shim, lib], env={**os.environ, "LD_PRELOAD": shim}, check=True)

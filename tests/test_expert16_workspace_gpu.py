@@ -1,0 +1,43 @@
+"""One workspace of the grouped products for batches of any size up to the largest."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests.util import build_lib  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def M():
+    build_lib()
+    import bit_quantized_expert_moe_gb300 as M
+    return M
+
+
+def randn(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+
+
+@pytest.mark.parametrize("E,N,K", [(2, 1024, 4096), (1, 256, 7168), (2, 2056, 2064), (4, 88, 2072)])
+def test_workspace_of_the_largest_batch_does_for_smaller_ones(M, E, N, K):
+    most = 4096
+    ws = M.workspace(M.grouped_mm_workspace_size(most, E, N, K))
+    x, dy, w = randn(1, most, K), randn(2, most, N), randn(3, E, N, K)
+    for R in (1, 20, 33, 70, 100, 300, 512, 1000, 2048, most):
+        off = torch.tensor([R * e // E for e in range(E + 1)], dtype=torch.int32).cuda()
+        xs, ds = x[:R], dy[:R]
+        for fn, a, b in ((M.grouped_mm, xs, w), (M.grouped_mm_dx, ds, w), (M.grouped_mm_dw, ds, xs)):
+            assert torch.equal(fn(a, b, off, ws=ws), fn(a, b, off)), (fn, R)
+    assert M.get_device_error(ws) == M.MOE_OK
+
+
+def test_a_product_asks_for_its_own_shares_only(M):
+    """The few-rows product has none; dx of the same rows has, and is refused without room for them."""
+    R, E, N, K = 24, 1, 4096, 256
+    x, dy, w = randn(1, R, K), randn(2, R, N), randn(3, E, N, K)
+    off, ws = torch.tensor([0, R], dtype=torch.int32).cuda(), M.workspace(256)
+    assert M.grouped_mm_workspace_size(R, E, N, K) > 256
+    assert torch.equal(M.grouped_mm(x, w, off, ws=ws), M.grouped_mm(x, w, off))
+    with pytest.raises(M.MoeError, match="WORKSPACE"):
+        M.grouped_mm_dx(dy, w, off, ws=ws)
