@@ -41,3 +41,13 @@ def test_a_product_asks_for_its_own_shares_only(M):
     assert torch.equal(M.grouped_mm(x, w, off, ws=ws), M.grouped_mm(x, w, off))
     with pytest.raises(M.MoeError, match="WORKSPACE"):
         M.grouped_mm_dx(dy, w, off, ws=ws)
+
+
+def test_an_output_that_does_not_fit_is_out_of_memory(M):
+    """As everywhere in torch, so that a caller may free memory and try again."""
+    E, N, K = 1024, 32768, 32768  # 2 TiB of gradients
+    x, dy = torch.empty(0, K, dtype=torch.bfloat16, device="cuda"), torch.empty(0, N, dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        M.grouped_mm_dw(dy, x, off)
+    assert M.grouped_mm_dw(dy[:, :64].contiguous(), x[:, :64].contiguous(), off).shape == (E, 64, 64)
