@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -60,9 +61,19 @@ moe_dtype_t moe_type(at::ScalarType t) {
 }
 
 // The tensors of a call that are there: dense, and on the device of the first, on
-// which the call runs.
+// which the call runs.  Where autograd records, it learns nothing of the call: said
+// once for each place of a program (as the warnings' filters have it).
 void on_one_device(std::initializer_list<std::reference_wrapper<const Tensor>> ts) {
     const Tensor& first = *ts.begin();
+    for (const Tensor& t : ts)
+        if (t.defined() && t.requires_grad() && at::GradMode::is_enabled()) {
+            if (PyErr_WarnEx(PyExc_UserWarning,
+                             "an operand requires gradients, but the 16-bit expert operators record no graph: their outputs "
+                             "do not require gradients; call them under torch.no_grad() and take the gradients from "
+                             "grouped_mm_dx, grouped_mm_dw, swiglu_backward and block_norm_backward", 1) < 0)
+                throw Raised{};
+            break;
+        }
     for (const Tensor& t : ts) {
         if (!t.defined()) continue;
         if (!t.is_cuda()) throw Refusal("device tensor expected");

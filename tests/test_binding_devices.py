@@ -2,6 +2,8 @@
 operands of several devices before any launch.  Tensors of two devices are stood in
 for by fake ones, which have shapes, types and devices but no memory (no GPU
 needed)."""
+import warnings
+
 import pytest
 
 from tests.util import build_lib
@@ -52,3 +54,33 @@ def test_one_operand_on_the_host_is_refused(M, fn):
             args = {n: torch.empty(s, dtype=t, device="cpu" if n == host else "cuda:0") for n, (s, t) in CALLS[fn].items()}
         with pytest.raises(ValueError, match="device tensor expected"):
             getattr(M, fn)(**args)
+
+
+def test_operands_that_require_gradients_are_not_passed_over_in_silence(M):
+    """The operators record no graph.  The calls here are refused after the warning (host tensors)."""
+    plain, grad = torch.zeros(4, 32), torch.zeros(4, 32, requires_grad=True)
+
+    def refused(*args):
+        with pytest.raises(ValueError, match="device tensor"):
+            M.block_norm(*args)
+
+    with pytest.warns(UserWarning, match="record no graph"):
+        refused(grad)
+    with pytest.warns(UserWarning, match="record no graph"):
+        refused(plain, grad)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        refused(plain, plain)
+        with torch.no_grad():
+            refused(grad)
+        with pytest.raises(UserWarning):  # an error where the program's filters make it one
+            M.block_norm(grad)
+
+
+@pytest.mark.gpu
+def test_operands_that_require_gradients_are_computed_with(M):
+    x, p = torch.randn(4, 32).cuda(), torch.ones(32).cuda()
+    want = M.block_norm(x, gamma_pre=p)[1]
+    with pytest.warns(UserWarning, match="record no graph"):
+        got = M.block_norm(x, gamma_pre=p.clone().requires_grad_())[1]
+    assert torch.equal(got, want) and not got.requires_grad
