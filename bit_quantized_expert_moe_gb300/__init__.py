@@ -336,6 +336,9 @@ def __getattr__(name: str):
     # the compiled functions of expert16.py, at their first use: importing the
     # package needs no built library
     if name in _expert16_loader.NAMES:
-        fn = globals()[name] = _expert16_loader.load(name)
+        try:
+            fn = globals()[name] = _expert16_loader.load(name)
+        except RuntimeError:
+            return _expert16_loader.unbuilt(name)
         return fn
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

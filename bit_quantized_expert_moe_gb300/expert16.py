@@ -33,9 +33,22 @@ NAMES = ("grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "swiglu", "swiglu_backw
 def load(name: str):
     """One of the compiled functions; raises if the library has not been built."""
     lib()
-    m = importlib.import_module("bit_quantized_expert_moe_gb300._expert16")
+    try:
+        m = importlib.import_module("bit_quantized_expert_moe_gb300._expert16")
+    except ImportError as e:
+        raise RuntimeError(f"the compiled binding cannot be loaded ({e}): build it with "
+                           "`python -m bit_quantized_expert_moe_gb300.build`") from e
     m._init(_check)
     return getattr(m, name)
+
+
+def unbuilt(name: str):
+    """Stands for one of the functions while there is no library: like the others
+    of the package it is there, and a call raises until the library is."""
+    def call(*args, **kwargs):
+        return load(name)(*args, **kwargs)
+    call.__name__ = call.__qualname__ = name
+    return call
 
 
 def grouped_mm_workspace_size(R: int, E: int, N: int, K: int) -> int:
