@@ -3,10 +3,12 @@
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 bit_quantized_expert_moe_gb300/libmoe_w4.so.  The Python binding of the 16-bit
 expert operators (csrc/expert16_binding.cpp) is compiled beside them with g++
-and linked against that library and torch.  Run as a module or call build().
+and linked against that library and torch; where torch or Python's headers are not
+installed the library is built without it.  Run as a module or call build().
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -45,10 +47,20 @@ def _deps() -> list[str]:
     return out
 
 
+def binding_lacks() -> str | None:
+    """What the binding needs and this machine does not have."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if not os.path.exists(os.path.join(sysconfig.get_path("include"), "Python.h")):
+        return "Python's headers"
+    return None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    made = [LIB] if binding_lacks() else [LIB, BINDING]
+    if not all(os.path.exists(p) for p in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(p) for p in made)
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -100,17 +112,21 @@ def build(verbose: bool = False, force: bool = False, extra: list[str] | None = 
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
+    lacks = binding_lacks()
     with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(_binding_object)
+        binding = None if lacks else ex.submit(_binding_object)
         objs = list(ex.map(compile_one, sources()))
-        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    # the C library is there by now, whatever becomes of the binding
+    if lacks:
+        print(f"{LIB} is built; without {lacks} the Python binding of the 16-bit expert operators is not", file=sys.stderr)
+    else:
+        _link_binding(binding.result())
     return LIB
 
 
