@@ -85,7 +85,10 @@ def _link_binding(obj: str) -> None:
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
+    # by name and not by path: it asks for the library beside itself ($ORIGIN), wherever
+    # the tree lies by then
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{os.path.dirname(LIB)}",
+           f"-l:{os.path.basename(LIB)}", f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
            "-ltorch", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

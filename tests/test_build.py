@@ -1,6 +1,9 @@
 """What build() makes and when it makes it again, with stand-ins for the compilers
 (and, for the built files, the real ones; no GPU needed)."""
 import os
+import shutil
+import subprocess
+import sys
 from types import SimpleNamespace
 
 import pytest
@@ -65,3 +68,26 @@ def test_library_is_there_when_the_binding_does_not_compile(tree, monkeypatch):
     with pytest.raises(RuntimeError, match="expert16_binding"):
         B.build()
     assert os.path.exists(B.LIB)
+
+
+MOVED = """
+import os, sys
+import bit_quantized_expert_moe_gb300 as M
+M.grouped_mm
+maps = {line.split()[-1] for line in open("/proc/self/maps") if line.rstrip().endswith(".so")}
+print(*sorted(p for p in maps if "libmoe_w4" in p or "_expert16" in p))
+"""
+
+
+@pytest.mark.skipif(not os.path.exists("/proc/self/maps"), reason="needs /proc")
+def test_a_moved_tree_loads_its_own_library(tmp_path):
+    """The binding finds the library beside itself, not where it was linked."""
+    try:
+        B.build()
+    except RuntimeError as e:  # pragma: no cover
+        pytest.skip(f"cannot build: {e}")
+    pytest.importorskip("torch")
+    here = tmp_path / os.path.basename(B.PKG)
+    shutil.copytree(B.PKG, here, ignore=shutil.ignore_patterns("_build", "csrc", "__pycache__"))
+    r = subprocess.run([sys.executable, "-c", MOVED], cwd=tmp_path, capture_output=True, text=True, check=True)
+    assert r.stdout.split() == [str(here / "_expert16.so"), str(here / "libmoe_w4.so")]
