@@ -56,9 +56,30 @@ def binding_lacks() -> str | None:
     return None
 
 
+def _torch_version() -> str:
+    """Where torch lies, its version and the CUDA and commit it was built from, without importing it."""
+    where = os.path.dirname(importlib.util.find_spec("torch").origin)
+    with open(os.path.join(where, "version.py")) as f:
+        return where + "\n" + f.read()
+
+
+def _built_against() -> str:
+    """The torch and the interpreter whose C++ and C interfaces the binding is compiled for."""
+    return f"{sysconfig.get_config_var('SOABI')}\n{_torch_version()}"
+
+
+def _binding_current() -> bool:
+    try:
+        with open(os.path.join(BUILD, "expert16.against")) as f:
+            return f.read() == _built_against()
+    except OSError:
+        return False
+
+
 def up_to_date() -> bool:
-    made = [LIB] if binding_lacks() else [LIB, BINDING]
-    if not all(os.path.exists(p) for p in made):
+    lacks = binding_lacks()
+    made = [LIB] if lacks else [LIB, BINDING]
+    if not all(os.path.exists(p) for p in made) or not (lacks or _binding_current()):
         return False
     t = min(os.path.getmtime(p) for p in made)
     return all(os.path.getmtime(p) <= t for p in _deps())
@@ -94,6 +115,8 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, "expert16.against"), "w") as f:
+        f.write(_built_against())
 
 
 def build(verbose: bool = False, force: bool = False, extra: list[str] | None = None) -> str:

@@ -4,6 +4,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from types import SimpleNamespace
 
 import pytest
@@ -40,6 +41,21 @@ def test_a_second_build_does_nothing(tree):
     n = len(tree)
     B.build()
     assert n > 2 and len(tree) == n
+
+
+def test_the_binding_is_built_again_for_another_torch(tree, monkeypatch):
+    """Its times say nothing of the torch and the interpreter it was compiled for."""
+    B.build()
+    n = len(tree)
+    monkeypatch.setattr(B, "_torch_version", lambda: "/another/torch 9.9.9", raising=False)
+    B.build()
+    assert len(tree) > n
+    n = len(tree)
+    B.build()
+    assert len(tree) == n
+    monkeypatch.setattr(B, "sysconfig", SimpleNamespace(get_path=sysconfig.get_path, get_config_var=lambda name: "cpython-999"))
+    B.build()
+    assert len(tree) > n
 
 
 @pytest.mark.parametrize("without", ["headers", "torch"])
