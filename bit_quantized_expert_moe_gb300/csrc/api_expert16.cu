@@ -1,5 +1,6 @@
 // C ABI of the 16-bit expert operators (grouped products, gated activation,
 // block norms) declared in include/moe_w4.h: argument checks and workspaces.
+#include <climits>
 #include <cmath>
 
 #include "internal.h"
@@ -11,6 +12,9 @@ namespace {
 
 constexpr int MAX_WIDTH = 32768;  // N, K, F of the expert operators
 constexpr int MAX_NORM_WIDTH = 16384;
+// Rows: the kernels step through them in 32 bits, by at most a few tens of thousands
+// beyond the last (a block norm's row groups by T / 152).
+constexpr int MAX_ROWS = INT32_MAX - (1 << 24);
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 template <size_t N>
@@ -35,7 +39,7 @@ moe_status_t check_grouped(size_t (*floats)(const GroupedShape&), moe_dtype_t dt
                            int32_t N, int32_t K, bool needs_out, const void* out, const void* ws, size_t ws_bytes) {
     if (!grouped_sizes_ok(R, E, N, K)) return MOE_ERR_INVALID_ARG;
     if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16) return MOE_ERR_UNSUPPORTED;
-    if (!width_supported(N, MAX_WIDTH) || !width_supported(K, MAX_WIDTH)) return MOE_ERR_UNSUPPORTED;
+    if (R > MAX_ROWS || !width_supported(N, MAX_WIDTH) || !width_supported(K, MAX_WIDTH)) return MOE_ERR_UNSUPPORTED;
     if (!offsets || !ws || (R > 0 && (!a || !b)) || (needs_out && !out)) return MOE_ERR_INVALID_ARG;
     if (!all_aligned({a, b, offsets, out, ws})) return MOE_ERR_MISALIGNED;
     return ws_bytes < with_header(floats(GroupedShape{dtype, R, E, N, K})) ? MOE_ERR_WORKSPACE : MOE_OK;
@@ -49,7 +53,7 @@ GroupedShape shape(moe_dtype_t dtype, const int32_t* offsets, int32_t R, int32_t
 moe_status_t check_swiglu(moe_dtype_t dtype, int32_t R, int32_t F) {
     if (R < 0 || F < 1) return MOE_ERR_INVALID_ARG;
     if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16 && dtype != MOE_DT_F32) return MOE_ERR_UNSUPPORTED;
-    return width_supported(F, MAX_WIDTH) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+    return R <= MAX_ROWS && width_supported(F, MAX_WIDTH) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 moe_status_t check_norm(const NormShape& n, const void* y) {
@@ -58,7 +62,7 @@ moe_status_t check_norm(const NormShape& n, const void* y) {
     if (!(n.eps > 0.f) || !std::isfinite(n.eps) || !std::isfinite(n.alpha)) return MOE_ERR_INVALID_ARG;
     if (n.dtype != MOE_DT_BF16 && n.dtype != MOE_DT_F16 && n.dtype != MOE_DT_F32) return MOE_ERR_UNSUPPORTED;
     if (n.param_dtype != n.dtype && n.param_dtype != MOE_DT_F32) return MOE_ERR_UNSUPPORTED;
-    if (!width_supported(n.D, MAX_NORM_WIDTH)) return MOE_ERR_UNSUPPORTED;
+    if (n.T > MAX_ROWS || !width_supported(n.D, MAX_NORM_WIDTH)) return MOE_ERR_UNSUPPORTED;
     if (n.T > 0 && !y && (n.gamma_post || n.gate)) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }

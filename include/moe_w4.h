@@ -244,8 +244,8 @@ size_t moe_layer_workspace_size(const moe_w4_layer* L, int32_t T, int32_t k);
  * 16-bit expert operators: what stands around the int4 layer in training and
  * in models with 16-bit experts.  They use the permutation of moe_permute
  * (`offsets`, `sorted`) and follow the conventions above.
- * Widths (N, K, F, D) are multiples of 8 (MOE_ERR_UNSUPPORTED otherwise), at
- * most 32768, and 16384 for D.
+ * Widths (N, K, F, D) are multiples of 8, at most 32768, and 16384 for D; rows (R,
+ * T) are at most 2^31 - 2^24 - 1 (MOE_ERR_UNSUPPORTED otherwise).
  * ====================================================================== */
 
 /* Element type of a call's tensors. */
