@@ -29,6 +29,9 @@ struct WsHeader {
 // Header word of the one-kernel decode layer (32-bit word index): the
 // grid-barrier kernel's 64-bit arrival counter, in its own 64-byte sector.
 constexpr int WS_BAR_COUNT_WORD = 16;
+// Header word of the grouped products whose sums are shared out: not 0 where the
+// call's segments are out of place and there are no shares.  Written by every such call.
+constexpr int WS_NO_SHARES_WORD = 32;
 
 // Small device-side plan written by the permutation kernels (after the header).
 struct DevPlan {

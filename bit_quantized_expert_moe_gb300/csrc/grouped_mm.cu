@@ -269,7 +269,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (e0 + k == p.E - 1) tile_pre[p.E] = before;
         }
     }
-    if (bad && threadIdx.x == 0 && blockIdx.x == 0) set_error(p.err, ERRBIT_RANGE);
+    if (threadIdx.x == 0 && blockIdx.x == 0) {
+        if (bad) set_error(p.err, ERRBIT_RANGE);
+        if (SPLIT) p.err[WS_NO_SHARES_WORD] = bad;
+    }
     __syncthreads();
     const Work<PR, SPLIT> work(p, tile_pre, bad);
 
@@ -548,17 +551,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 }
 
 // The shares' sums, in order, rounded to the output: `row` values for each of
-// `rows` rows, of which Y and DX write those that a segment holds.
+// `rows` rows, of which Y and DX write those that a segment holds.  Nothing where a
+// segment is out of place.
 __global__ void __launch_bounds__(256) grouped_sum_kernel(const GroupedParams p, int rows, int row) {
     grid_dependency_launch();
     grid_dependency_wait();
+    const uint32_t none = p.err[WS_NO_SHARES_WORD];
     const int r0 = p.offsets ? __ldg(p.offsets) : 0, r1 = p.offsets ? __ldg(p.offsets + p.E) : rows;
     const size_t n = (size_t)rows * row / 8, step = (size_t)gridDim.x * blockDim.x;
     for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
-        const int r = (int)(i * 8 / row);
-        if (r < r0 || r >= r1) continue;
+        // the shares' loads do not wait for the words above
         V8 s = load8<F32>(p.part, i);
         for (int k = 1; k < p.splits; ++k) s = fma(load8<F32>(p.part, k * n + i), 1.f, s);
+        const int r = (int)(i * 8 / row);
+        if (none || r < r0 || r >= r1) continue;
         if (p.type) store8<Bf16>(p.out, i, s);
         else store8<F16>(p.out, i, s);
     }
