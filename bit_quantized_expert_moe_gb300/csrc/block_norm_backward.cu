@@ -375,9 +375,11 @@ cudaError_t run_reduce(const Args& p, cudaStream_t s) {
 }  // namespace
 }  // namespace norm
 
+// No plan has more blocks than SMs or rows, and its row groups never become fewer
+// with the rows: so what does for many rows does for fewer, whose blocks may be more.
 size_t block_norm_partial_floats(int T, int D, int G) {
     const norm::BackwardPlan b = norm::backward_plan(T, D);
-    return (size_t)b.blocks * D * (3 + (G > 1 ? 2 * b.groups : 0));
+    return (size_t)std::min(T, num_sms()) * D * (3 + (G > 1 ? 2 * b.groups : 0));
 }
 
 cudaError_t launch_block_norm_backward(const NormShape& n, const NormGrads& g, float* part, cudaStream_t s) {

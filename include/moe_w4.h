@@ -323,7 +323,8 @@ moe_status_t moe_swiglu_backward(moe_dtype_t dtype, const void* dh, const void* 
  *   each NULL to skip.  dx may be dx_out.  The order of every sum is fixed.  Any
  *   finite x_out and y, as above; sums of dx_out or dh times a normalised row have
  *   to be within fp32.
- * Workspace: >= moe_block_norm_backward_workspace_size(T, D, G) bytes.
+ * Workspace: >= moe_block_norm_backward_workspace_size(T, D, G) bytes; one for the
+ * most rows also does for fewer (with several gates, if it was made for several).
  */
 moe_status_t moe_block_norm(moe_dtype_t dtype, moe_dtype_t param_dtype, int32_t T, int32_t D, int32_t G,
                             float alpha, float eps, const void* gamma_post, const void* gate,

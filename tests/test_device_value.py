@@ -110,3 +110,29 @@ def test_grouped_workspace_for_many_rows_does_for_fewer(tmp_path):
         pytest.skip(f"cannot build: {e}")
     shim = compiled(tmp_path, "shim.so", SHIM, "-shared", "-fPIC")
     subprocess.run([sys.executable, "-c", SIZES, shim, lib], env={**os.environ, "LD_PRELOAD": shim}, check=True)
+
+
+NORM_SIZES = r"""
+import ctypes, sys
+shim, lib = ctypes.CDLL(sys.argv[1]), ctypes.CDLL(sys.argv[2])
+size = lib.moe_block_norm_backward_workspace_size
+size.restype = ctypes.c_size_t
+shim.stand_on(0)
+for D in (64, 1288, 2048, 4104, 8192, 16384):
+    for several in (False, True):
+        last = 0
+        for T in sorted({r + d for r in (2, 150, 152, 304, 456, 700, 1000, 4096, 20000) for d in (0, 1, 2)}):
+            n = size(T, D, T if several else 1)
+            assert last <= n, (D, several, T, last, n)
+            last = n
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_norm_gradients_workspace_for_many_rows_does_for_fewer(tmp_path):
+    try:
+        lib = build_lib()
+    except RuntimeError as e:  # pragma: no cover
+        pytest.skip(f"cannot build: {e}")
+    shim = compiled(tmp_path, "shim.so", SHIM, "-shared", "-fPIC")
+    subprocess.run([sys.executable, "-c", NORM_SIZES, shim, lib], env={**os.environ, "LD_PRELOAD": shim}, check=True)

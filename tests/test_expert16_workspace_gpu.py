@@ -51,3 +51,16 @@ def test_an_output_that_does_not_fit_is_out_of_memory(M):
     with pytest.raises(torch.OutOfMemoryError):
         M.grouped_mm_dw(dy, x, off)
     assert M.grouped_mm_dw(dy[:, :64].contiguous(), x[:, :64].contiguous(), off).shape == (E, 64, 64)
+
+
+@pytest.mark.parametrize("D", [136, 2048, 4104])
+@pytest.mark.parametrize("gates", [1, 2])
+def test_norm_gradients_workspace_of_the_largest_batch_does_for_smaller_ones(M, D, gates):
+    most = 4096
+    ws = M.workspace(M.block_norm_backward_workspace_size(most, D, gates))
+    x, y, dxo, dh = (randn(i, most, D) for i in range(4))
+    post, pre, gate = randn(5, D), randn(6, D), randn(7, gates, D)
+    for T in (2, 150, 304, 306, 456, 1000, most):
+        args = (x[:T], y[:T], dxo[:T], dh[:T], post, gate, pre)
+        got, want = M.block_norm_backward(*args, ws=ws), M.block_norm_backward(*args)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), T
