@@ -24,7 +24,12 @@ __device__ __forceinline__ uint4 load_weights(const void* p) {
     return r;
 }
 
-constexpr int ROWS = 16, COLS = 8, AHEAD = 8;
+// AHEAD: pairs of weight loads under way, 32 registers of the 54 that the four-warp
+// kernel takes.  With 8 the compiler puts loads behind the first products (46
+// registers in all).  us with 2, 4, 8: 8 rows of 8 experts, N 1536, K 2048 12.6, 12.4,
+// 12.8; N 4096, K 7168 76.1, 73.5, 75.9; 32 rows of 32 36.9, 34.2, 36.6; 16 rows of 8,
+// N 1024, K 256 3.0, 2.9, 3.4.
+constexpr int ROWS = 16, COLS = 8, AHEAD = 4;
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -109,8 +114,8 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_few_kernel(const uint16_t*
 }  // namespace
 
 // Warps that share K: four, more where the blocks leave SMs without loads under
-// way.  us with 4, 8, 16 warps: 66 blocks, K 6592 27.0, 13.5, 7.9; 256, K 4096 14.8, 9.4,
-// 6.4; 64, K 512 2.4, 2.3, 2.9; 512, K 1024 6.2, 5.8, 7.8; 768, K 2048 11.3, 12.2, 14.0.
+// way.  us with 4, 8, 16 warps: 66 blocks, K 6592 28.1, 14.4, 8.7; 256, K 4096 15.6, 10.5,
+// 8.7; 64, K 512 2.5, 2.3, 2.5; 512, K 1024 6.6, 6.0, 6.9; 768, K 2048 12.5, 13.6, 13.5.
 cudaError_t launch_grouped_few(const GroupedShape& g, const void* x, const void* w, void* y, cudaStream_t s) {
     const dim3 grid(ceil_div(g.N, ROWS), g.R);
     const auto *xp = static_cast<const uint16_t*>(x), *wp = static_cast<const uint16_t*>(w);

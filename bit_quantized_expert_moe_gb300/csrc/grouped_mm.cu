@@ -704,10 +704,10 @@ cudaError_t launch(const GroupedShape& g, const void* a, const void* b, void* ou
 
 }  // namespace
 
-// E 128, N 1536, K 2048: 8 rows 12.1 us there and 13.1 here, 32 rows 31.0 and
-// 34.9, 128 rows 77.9 and 82.0; E 256, N 4096, K 7168: 64 rows 469 and 492.  With
+// E 128, N 1536, K 2048: 8 rows 12.5 us there and 12.7 here, 32 rows 34.7 and
+// 35.7, 128 rows 116 and 125; E 256, N 4096, K 7168: 64 rows 531 and 555.  With
 // several rows an expert its blocks read the weights again: E 8, N 1024, K 256:
-// 16 rows 4.0 and 4.8, 64 rows 5.8 and 4.9; E 1, N and K 2048: 64 rows 14.3 and 9.0
+// 16 rows 2.9 and 4.4, 64 rows 5.2 and 4.4; E 1, N and K 2048: 64 rows 13.2 and 9.6
 static bool takes_few(const GroupedShape& g) { return g.R <= 32 || (g.R <= 128 && g.R <= g.E); }
 
 size_t grouped_floats(const GroupedShape& g) {
