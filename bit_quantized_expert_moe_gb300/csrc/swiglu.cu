@@ -23,7 +23,7 @@ namespace {
 // |up| < 2^11, and 2^-16.2 at |a| = 87, where s leaves the normal numbers: a 64th of
 // the half ulp of fp16, a 90th of bf16's.  The routing weight's gradient is fp32 and
 // gets the library's (2 ulp).  us with the library's and the hardware's: forward
-// 32768 x 768 30.5 and 24.7, backward 44.5 and 44.2, 40000 x 264 30.4 and 28.6.
+// 32768 x 768 30.0 and 23.7, backward 43.5 and 43.4, 40000 x 264 30.0 and 27.8.
 template <class T, bool EXACT>
 struct Silu {
     float2 as, ss;  // a s, s (1 + a (1 - s))

@@ -14,7 +14,8 @@ the gated activation with the routing weight, and the norms around a block.
 `offsets` and `row_map` are the `offsets` and `sorted` of permute().  Offsets
 out of order or range set the error word of the `ws` that was given, which
 get_device_error(ws) reads; without one nobody learns of them.  Outputs and
-workspaces that are not given belong to the call's stream.  No call records an
+workspaces that are not given belong to the call's stream; operands that belong to
+another have to outlast the call there (record_stream).  No call records an
 autograd graph (operands that require gradients draw a warning where autograd
 records): the gradients are the calls above.  The functions are compiled
 (csrc/expert16_binding.cpp, argument marshalling only); this module loads them at
