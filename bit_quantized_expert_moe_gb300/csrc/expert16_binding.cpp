@@ -1,4 +1,5 @@
-// Python binding of the 16-bit expert operators: argument marshalling only.
+// Python binding of the 16-bit expert operators and of those of expert blocks in 8
+// and 16 bits: argument marshalling only.
 //
 // A small call takes a few microseconds on the GPU; checking shapes, taking
 // pointers and making outputs in the interpreter takes longer than that on the
@@ -13,6 +14,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <array>
@@ -128,6 +130,17 @@ struct Args {
     Tensor needed_tensor(size_t i) const {
         if (!given(i)) throw_type("tensor expected");
         return tensor(i);
+    }
+    int64_t integer(size_t i, int64_t otherwise) const {
+        if (!v[i]) return otherwise;
+        const long long n = PyLong_AsLongLong(v[i]);
+        if (n == -1 && PyErr_Occurred()) throw Raised{};
+        return n;
+    }
+    at::ScalarType dtype(size_t i, at::ScalarType otherwise) const {
+        if (!given(i)) return otherwise;
+        if (!THPDtype_Check(v[i])) throw_type("dtype expected");
+        return reinterpret_cast<THPDtype*>(v[i])->scalar_type;
     }
     float number(size_t i, double otherwise) const {
         if (!v[i]) return (float)otherwise;
@@ -419,6 +432,115 @@ PyObject* py_block_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n,
     });
 }
 
+// ------------------------------------------------------------------ layer norm
+// The type of gamma and beta, the rows' where there is neither.
+struct LayerNorm {
+    int64_t T, D;
+    at::ScalarType type, ptype;
+    moe_dtype_t dt, pt;
+    LayerNorm(const char* what, const Tensor& x, const Tensor& gamma, const Tensor& beta) {
+        dims(what, x, 2);
+        T = x.size(0);
+        D = x.size(1);
+        type = x.scalar_type();
+        ptype = gamma.defined() ? gamma.scalar_type() : beta.defined() ? beta.scalar_type() : type;
+        dt = moe_type(type);
+        pt = moe_type(ptype);
+        if (gamma.defined()) want("gamma", gamma, {D}, ptype);
+        if (beta.defined()) want("beta", beta, {D}, ptype);
+    }
+    void row(const char* what, const Tensor& t) const {
+        if (t.defined()) want(what, t, {T, D}, type);
+    }
+};
+
+PyObject* py_layer_norm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+    return guarded([&] {
+        static const auto names = intern<8>({"x", "y", "gamma", "beta", "eps", "x_out", "h", "stream"});
+        const Args<8> a("layer_norm", names, 1, args, n, kw);
+        const Tensor x = a.needed_tensor(0), y = a.tensor(1), gamma = a.tensor(2), beta = a.tensor(3);
+        const LayerNorm m("x", x, gamma, beta);
+        m.row("y", y);
+        Tensor xo = a.tensor(5), h = a.tensor(6);
+        on_one_device({x, y, gamma, beta, xo, h});
+        const OnStream on(a, 7, x);
+        if (xo.defined() || y.defined()) xo = output(xo, "x_out", x, {m.T, m.D}, m.type);
+        h = output(h, "h", x, {m.T, m.D}, m.type);
+        check(moe_layer_norm(m.dt, m.pt, size32(m.T), size32(m.D), a.number(4, 1e-5), ptr(gamma), ptr(beta), ptr(x), ptr(y),
+                             ptr(xo), ptr(h), on.s), "moe_layer_norm");
+        return wrap_all({xo, h});
+    });
+}
+PyObject* py_layer_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+    return guarded([&] {
+        static const auto names = intern<8>({"x_out", "dh", "dx_out", "gamma", "beta", "eps", "ws", "stream"});
+        const Args<8> a("layer_norm_backward", names, 2, args, n, kw);
+        const Tensor x = a.needed_tensor(0), dh = a.needed_tensor(1), dxo = a.tensor(2), gamma = a.tensor(3), beta = a.tensor(4);
+        const LayerNorm m("x_out", x, gamma, beta);
+        m.row("dh", dh);
+        m.row("dx_out", dxo);
+        const int32_t T = size32(m.T), D = size32(m.D);
+        const Tensor given_ws = a.tensor(6), none;
+        on_one_device({x, dh, dxo, gamma, beta, given_ws});
+        const OnStream on(a, 7, x);
+        const Tensor dx = output(none, "dx", x, {m.T, m.D}, m.type);
+        const Tensor dgamma = gamma.defined() ? output(none, "dgamma", x, {m.D}, m.ptype) : none;
+        const Tensor dbeta = beta.defined() ? output(none, "dbeta", x, {m.D}, m.ptype) : none;
+        const Tensor ws = workspace(given_ws, given_ws.defined() ? 0 : moe_layer_norm_backward_workspace_size(T, D), x);
+        check(moe_layer_norm_backward(m.dt, m.pt, T, D, a.number(5, 1e-5), ptr(gamma), ptr(x), ptr(dh), ptr(dxo), ptr(dx),
+                                      ptr(dgamma), ptr(dbeta), ptr(ws), (size_t)ws.numel(), on.s), "moe_layer_norm_backward");
+        return wrap_all({dx, dgamma, dbeta});
+    });
+}
+
+// ------------------------------------------------------------- 8-bit experts
+PyObject* py_quantize_rows(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+    return guarded([&] {
+        static const auto names = intern<6>({"x", "row_map", "k", "codes", "scales", "stream"});
+        const Args<6> a("quantize_rows", names, 1, args, n, kw);
+        const Tensor x = a.needed_tensor(0), map = a.tensor(1), codes0 = a.tensor(3), scales0 = a.tensor(4);
+        dims("x", x, 2);
+        const moe_dtype_t dt = moe_type(x.scalar_type());
+        if (map.defined()) {
+            dims("row_map", map, 1);
+            want("row_map", map, {map.size(0)}, at::kInt);
+        }
+        const int64_t T = x.size(0), D = x.size(1), R = map.defined() ? map.size(0) : T, k = a.integer(2, 1);
+        on_one_device({x, map, codes0, scales0});
+        const OnStream on(a, 5, x);
+        const Tensor codes = output(codes0, "codes", x, {R, D}, at::kChar), scales = output(scales0, "scales", x, {R}, at::kFloat);
+        check(moe_quantize_rows(dt, ptr(x), ptr_as<int32_t>(map), size32(k), size32(T), size32(R), size32(D),
+                                ptr_as<int8_t>(codes), ptr_as<float>(scales), on.s), "moe_quantize_rows");
+        return wrap_all({codes, scales});
+    });
+}
+PyObject* py_grouped_mm_i8(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+    return guarded([&] {
+        static const auto names = intern<9>({"x", "x_scale", "w", "w_scale", "offsets", "y", "dtype", "ws", "stream"});
+        const Args<9> a("grouped_mm_i8", names, 5, args, n, kw);
+        const Tensor x = a.needed_tensor(0), xs = a.needed_tensor(1), w = a.needed_tensor(2), ws_ = a.needed_tensor(3);
+        const Tensor off = a.needed_tensor(4), y0 = a.tensor(5), ws0 = a.tensor(7);
+        dims("x", x, 2);
+        dims("w", w, 3);
+        const int64_t R = x.size(0), K = x.size(1), E = w.size(0), N = w.size(1);
+        want("x", x, {R, K}, at::kChar);
+        want("w", w, {E, N, K}, at::kChar);
+        want("x_scale", xs, {R}, at::kFloat);
+        want("w_scale", ws_, {E, N}, at::kFloat);
+        want("offsets", off, {E + 1}, at::kInt);
+        const at::ScalarType type = a.dtype(6, y0.defined() ? y0.scalar_type() : at::kBFloat16);
+        const moe_dtype_t dt = moe_type(type);
+        const int32_t r = size32(R), e = size32(E), nn = size32(N), k = size32(K);
+        on_one_device({x, xs, w, ws_, off, y0, ws0});
+        const OnStream on(a, 8, x);
+        const Tensor y = output(y0, "y", x, {R, N}, type);
+        const Tensor ws = workspace(ws0, ws0.defined() ? 0 : moe_grouped_mm_i8_workspace_size(r, e, nn, k), off);
+        check(moe_grouped_mm_i8(dt, ptr_as<int8_t>(x), ptr_as<float>(xs), ptr_as<int8_t>(w), ptr_as<float>(ws_),
+                                ptr_as<int32_t>(off), r, e, nn, k, ptr(y), ptr(ws), (size_t)ws.numel(), on.s), "moe_grouped_mm_i8");
+        return wrap(y);
+    });
+}
+
 PyObject* py_init(PyObject*, PyObject* check_fn) {
     Py_INCREF(check_fn);
     Py_XDECREF(g_check);
@@ -453,6 +575,24 @@ PyMethodDef methods[] = {
      "block_norm_backward(x_out, y=None, dx_out=None, dh=None, gamma_post=None, gate=None, gamma_pre=None, alpha=1.0,\n"
      "                    eps=1e-6, ws=None, stream=None) -> (dx, dy, dgamma_post, dgate, dgamma_pre)\n\n"
      "Gradients of block_norm at the stored x_out (x, where there is no y); None for what was not there."},
+    {"layer_norm", FAST(py_layer_norm),
+     "layer_norm(x, y=None, gamma=None, beta=None, eps=1e-5, x_out=None, h=None, stream=None) -> (x_out, h)\n\n"
+     "x_out = x + y and h = (x_out - mean) / sqrt(var + eps) gamma + beta; x_out is None without y, and may be x.\n"
+     "gamma None: 1; beta None: 0."},
+    {"layer_norm_backward", FAST(py_layer_norm_backward),
+     "layer_norm_backward(x_out, dh, dx_out=None, gamma=None, beta=None, eps=1e-5, ws=None, stream=None)\n"
+     "    -> (dx, dgamma, dbeta)\n\n"
+     "Gradients of layer_norm at the stored x_out (x, where there is no y); dx is that of x and of y.  None for the\n"
+     "gradient of what was not there."},
+    {"quantize_rows", FAST(py_quantize_rows),
+     "quantize_rows(x, row_map=None, k=1, codes=None, scales=None, stream=None) -> (codes, scales)\n\n"
+     "For v = x[row_map[r] // k] (x[r] without a map): scales[r] = max|v| / 127 and codes[r] = 127 v / max|v|, rounded\n"
+     "to nearest even.  row_map is `sorted` of permute(), k its choices a token.  A row that is not finite has scale NaN."},
+    {"grouped_mm_i8", FAST(py_grouped_mm_i8),
+     "grouped_mm_i8(x, x_scale, w, w_scale, offsets, y=None, dtype=torch.bfloat16, ws=None, stream=None) -> y\n\n"
+     "y[r] = x_scale[r] w_scale[e] (w[e] x[r]) for the rows r of every expert e: int8 x [R, K] and w [E, N, K], fp32\n"
+     "scales [R] and [E, N], offsets [E + 1] of permute(); y in bfloat16 or float16.  Offsets out of order or range set\n"
+     "the error word of ws, for get_device_error(ws); without ws it is lost."},
     {"_init", py_init, METH_O, "Sets the function that raises for a status."},
     {nullptr, nullptr, 0, nullptr},
 };

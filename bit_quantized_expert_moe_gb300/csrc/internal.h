@@ -165,6 +165,42 @@ size_t block_norm_partial_floats(int T, int D, int G);  // scratch of the backwa
 cudaError_t launch_block_norm(const NormShape& n, const void* x, const void* y, void* x_out, void* h, cudaStream_t s);
 cudaError_t launch_block_norm_backward(const NormShape& n, const NormGrads& g, float* part, cudaStream_t s);
 
+// ------------------------------------ expert blocks in 8 and 16 bits
+struct LayerNormShape {
+    moe_dtype_t dtype, param_dtype;
+    int T, D;
+    float eps;
+    const void *gamma, *beta;  // either may be null
+};
+struct LayerNormGrads {
+    const void *x_out, *dh, *dx_out;
+    void *dx, *dgamma, *dbeta;
+};
+size_t layer_norm_partial_floats(int T, int D);  // scratch of the backward pass
+cudaError_t launch_layer_norm(const LayerNormShape& n, const void* x, const void* y, void* x_out, void* h, cudaStream_t s);
+cudaError_t launch_layer_norm_backward(const LayerNormShape& n, const LayerNormGrads& g, float* part, cudaStream_t s);
+
+// Rows x[row_map[r] / k] (x[r] without a map) as 8-bit codes and scales.
+cudaError_t launch_quantize_rows(moe_dtype_t dt, const void* x, const int32_t* row_map, int k, int T, int R, int D,
+                                 int8_t* codes, float* scales, cudaStream_t s);
+
+struct GroupedI8Shape {
+    moe_dtype_t out;         // bf16 or fp16
+    int R, E, N, K;
+    const int32_t* offsets;  // [E+1]
+    uint32_t* err;
+    uint16_t* x16;           // the codes of x as fp16, where the tensor-core kernel runs
+};
+struct GroupedI8Data {
+    const int8_t *x, *w;
+    const float *x_scale, *w_scale;
+    void* y;
+};
+size_t grouped_i8_halves(int R, int E, int N, int K);  // of x16, for R rows or fewer
+cudaError_t launch_grouped_i8(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s);
+// The same by another kernel, for few rows in all.
+cudaError_t launch_grouped_i8_few(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s);
+
 // 3D tensor map over 32-bit words: dims {d0, d1, d2} (d0 contiguous), byte
 // strides s1 (dim 1) and s2 (dim 2), box {b0, b1, b2}, 128-byte swizzle.
 bool make_tensor_map_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
@@ -179,6 +215,10 @@ bool make_tensor_map_u16(CUtensorMap* m, const void* ptr, int rank, const uint64
 // The same over bf16 or fp16 elements, 128-byte swizzle, zeros out of bounds.
 bool make_tensor_map_16(CUtensorMap* m, bool bf16, const void* ptr, int rank, const uint64_t* dims,
                         const uint64_t* strides, const uint32_t* box);
+
+// The same over bytes.
+bool make_tensor_map_8(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
+                       const uint32_t* box);
 
 // ----------------------------------------------------------- device info
 int num_sms();  // of the current device

@@ -160,6 +160,33 @@ struct RowGroup {
         }
         return s;
     }
+    // Two values a thread, likewise: one step of exchange, then lane l holds value l / 16.
+    __device__ __forceinline__ void sum2(float (&v)[2]) {
+        const bool h4 = lane & 16;
+        float c = (h4 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, h4 ? v[0] : v[1], 16);
+        c += __shfl_xor_sync(0xffffffffu, c, 8);
+        c += __shfl_xor_sync(0xffffffffu, c, 4);
+        c += __shfl_xor_sync(0xffffffffu, c, 2);
+        c += __shfl_xor_sync(0xffffffffu, c, 1);
+        if (warps == 1) {
+            v[0] = __shfl_sync(0xffffffffu, c, 0);
+            v[1] = __shfl_sync(0xffffffffu, c, 16);
+            return;
+        }
+        float* r = red + buf * 128;
+        buf ^= 1;
+        if ((lane & 15) == 0) r[(lane >> 4) * 16 + warp] = c;
+        sync();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            v[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 f = reinterpret_cast<const float4*>(r + 16 * k)[i];
+                v[k] += (f.x + f.y) + (f.z + f.w);
+            }
+        }
+    }
     // Four values a thread.  Halving exchange: each step sends half of the
     // values a lane still holds to the lane across, so four values take 6
     // shuffles instead of 20; lane l ends up with value l / 8.

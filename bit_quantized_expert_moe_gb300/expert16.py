@@ -1,5 +1,7 @@
 """The 16-bit expert operators: products grouped by expert with their gradients,
-the gated activation with the routing weight, and the norms around a block.
+the gated activation with the routing weight, and the norms around a block; and
+the operators of expert blocks in 8 and 16 bits: the layer norm before a block with
+its gradients, rows to 8-bit codes, and the 8-bit products grouped by expert.
 
     grouped_mm(x, w, offsets, y=None, ws=None, stream=None)
     grouped_mm_dx(dy, w, offsets, dx=None, ws=None, stream=None)
@@ -10,6 +12,10 @@ the gated activation with the routing weight, and the norms around a block.
                stream=None)
     block_norm_backward(x_out, y=None, dx_out=None, dh=None, gamma_post=None, gate=None, gamma_pre=None, alpha=1.0,
                         eps=1e-6, ws=None, stream=None)
+    layer_norm(x, y=None, gamma=None, beta=None, eps=1e-5, x_out=None, h=None, stream=None)
+    layer_norm_backward(x_out, dh, dx_out=None, gamma=None, beta=None, eps=1e-5, ws=None, stream=None)
+    quantize_rows(x, row_map=None, k=1, codes=None, scales=None, stream=None)
+    grouped_mm_i8(x, x_scale, w, w_scale, offsets, y=None, dtype=torch.bfloat16, ws=None, stream=None)
 
 `offsets` and `row_map` are the `offsets` and `sorted` of permute().  Offsets
 out of order or range set the error word of the `ws` that was given, which
@@ -28,7 +34,7 @@ import importlib
 from . import _check, lib
 
 NAMES = ("grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "swiglu", "swiglu_backward", "block_norm",
-         "block_norm_backward")
+         "block_norm_backward", "layer_norm", "layer_norm_backward", "quantize_rows", "grouped_mm_i8")
 
 
 def load(name: str):
@@ -58,3 +64,11 @@ def grouped_mm_workspace_size(R: int, E: int, N: int, K: int) -> int:
 
 def block_norm_backward_workspace_size(T: int, D: int, G: int = 1) -> int:
     return lib().moe_block_norm_backward_workspace_size(T, D, G)
+
+
+def layer_norm_backward_workspace_size(T: int, D: int) -> int:
+    return lib().moe_layer_norm_backward_workspace_size(T, D)
+
+
+def grouped_mm_i8_workspace_size(R: int, E: int, N: int, K: int) -> int:
+    return lib().moe_grouped_mm_i8_workspace_size(R, E, N, K)

@@ -252,7 +252,7 @@ size_t moe_layer_workspace_size(const moe_w4_layer* L, int32_t T, int32_t k);
 typedef enum {
     MOE_DT_BF16 = 0,
     MOE_DT_F16 = 1,
-    MOE_DT_F32 = 2   /* gated activation and block norms only */
+    MOE_DT_F32 = 2   /* gated activation, norms and quantisation only */
 } moe_dtype_t;
 
 /*
@@ -337,6 +337,73 @@ moe_status_t moe_block_norm_backward(moe_dtype_t dtype, moe_dtype_t param_dtype,
                                      const void* dx_out, const void* dh, void* dx, void* dy,
                                      void* dgamma_post, void* dgate, void* dgamma_pre,
                                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ======================================================================
+ * Expert blocks in 8 and 16 bits: the layer norm in front of a block, experts with
+ * 8-bit weights and rows, and the whole layer of 16-bit experts for a few tokens.
+ * Conventions, rows and types as above.
+ * ====================================================================== */
+
+/*
+ * Layer norm in front of a block, with the residual sum before it, in one pass:
+ *   x_out = x + y                              (y and x_out NULL: x_out = x, not written)
+ *   h     = (x_out - mean) / sqrt(var + eps) * gamma + beta,  var = mean (x_out - mean)^2
+ *   x, y, x_out, h  device [T][D] in `dtype`; x_out may be x
+ *   gamma, beta     device [D] in `param_dtype`: `dtype` or MOE_DT_F32; NULL: 1 and 0
+ * Statistics in fp32 around the mean, for any finite x + y (squares beyond fp32 are
+ * taken in other units); h is taken from x_out before its rounding.  D is a multiple
+ * of 8, at most 16384.
+ *
+ * moe_layer_norm_backward: the gradients at the stored x_out, from dh and dx_out (of
+ * x_out; NULL: zero):
+ *   dx  device [T][D], the gradient of x and of y alike; may be dx_out or dh
+ *   dgamma (needs gamma), dbeta  device [D], NULL to skip
+ * The order of every sum is fixed.  Sums of dh * gamma times a normalised row have to
+ * be within fp32.
+ * Workspace: >= moe_layer_norm_backward_workspace_size(T, D) bytes; one for the most
+ * rows also does for fewer.
+ */
+moe_status_t moe_layer_norm(moe_dtype_t dtype, moe_dtype_t param_dtype, int32_t T, int32_t D, float eps,
+                            const void* gamma, const void* beta, const void* x, const void* y,
+                            void* x_out, void* h, cudaStream_t stream);
+size_t moe_layer_norm_backward_workspace_size(int32_t T, int32_t D);
+moe_status_t moe_layer_norm_backward(moe_dtype_t dtype, moe_dtype_t param_dtype, int32_t T, int32_t D, float eps,
+                                     const void* gamma, const void* x_out, const void* dh, const void* dx_out,
+                                     void* dx, void* dgamma, void* dbeta,
+                                     void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Rows to 8-bit codes with a scale for each: for v = x[row_map[r] / k] (row_map NULL:
+ * x[r], and R = T) and a = max |v[i]|,
+ *   scales[r] = a / 127,  codes[r][i] = 127 v[i] / a rounded to nearest even, exactly
+ * (a = 0: zeros).  With row_map = `sorted` and k of moe_permute the rows come in the
+ * experts' order.
+ *   x        device [T][D] in `dtype` (bf16, fp16 or fp32), D a multiple of 16, at most 32768
+ *   row_map  device int32 [R]; an entry outside [0, T k) gives scale 0 and codes 0
+ *   codes    device int8 [R][D] (out)     scales  device fp32 [R] (out)
+ * A row that holds an infinity or a NaN gets the scale NaN and codes 0, so that all
+ * that is made of it is NaN.
+ */
+moe_status_t moe_quantize_rows(moe_dtype_t dtype, const void* x, const int32_t* row_map, int32_t k, int32_t T,
+                               int32_t R, int32_t D, int8_t* codes, float* scales, cudaStream_t stream);
+
+/*
+ * Products grouped by expert of 8-bit codes, one scale for each row and each output
+ * channel.  For the rows r of segment e (see moe_grouped_mm):
+ *   y[r][n] = x_scale[r] * w_scale[e][n] * sum_k x[r][k] * w[e][n][k]
+ *   x  device int8 [R][K]     x_scale  device fp32 [R]
+ *   w  device int8 [E][N][K]  w_scale  device fp32 [E][N]     (codes -128 .. 127)
+ *   y  device [R][N], bf16 or fp16 (`out_dtype`), rounded once
+ * K is a multiple of 16, N of 8, both at most 32768.  The sum is exact up to 2^24 and
+ * held in fp32 beyond that (in 32-bit integers for few rows).  Offsets, rows outside
+ * the segments and the error word as for moe_grouped_mm.
+ * Workspace: >= moe_grouped_mm_i8_workspace_size(R, E, N, K) bytes; one for the most
+ * rows also does for fewer.
+ */
+size_t moe_grouped_mm_i8_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K);
+moe_status_t moe_grouped_mm_i8(moe_dtype_t out_dtype, const int8_t* x, const float* x_scale, const int8_t* w,
+                               const float* w_scale, const int32_t* offsets, int32_t R, int32_t E, int32_t N,
+                               int32_t K, void* y, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Reads and clears the device error word kept at the start of a workspace
