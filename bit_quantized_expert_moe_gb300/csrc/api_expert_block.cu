@@ -1,5 +1,5 @@
 // C ABI of the operators of expert blocks in 8 and 16 bits (layer norm, quantisation of
-// rows, 8-bit grouped products) declared in include/moe_w4.h: argument checks and
+// rows, 8-bit grouped products, the 16-bit layer for a few tokens) declared in include/moe_w4.h: argument checks and
 // workspaces.
 #include <climits>
 #include <cmath>
@@ -34,6 +34,13 @@ moe_status_t check_norm(const LayerNormShape& n) {
 
 bool grouped_sizes_ok(int32_t R, int32_t E, int32_t N, int32_t K) {
     return R >= 0 && E >= 1 && E <= 1024 && N >= 1 && K >= 1;
+}
+
+bool layer_sizes_ok(int32_t T, int32_t k, int32_t E, int32_t d, int32_t f) {
+    return T >= 0 && k >= 1 && E >= 1 && E <= 1024 && k <= E && d >= 1 && f >= 1;
+}
+bool layer_supported(int32_t T, int32_t k, int32_t d, int32_t f) {
+    return expert_layer_supported(T, k) && width_supported(d, 64, MAX_WIDTH) && width_supported(f, 64, MAX_WIDTH);
 }
 
 }  // namespace
@@ -106,6 +113,26 @@ moe_status_t moe_grouped_mm_i8(moe_dtype_t out_dtype, const int8_t* x, const flo
     const GroupedI8Shape g{out_dtype, R, E, N, K, offsets, &static_cast<WsHeader*>(workspace)->err,
                            reinterpret_cast<uint16_t*>(ws + WS_HEADER)};
     return cuda_status(launch_grouped_i8(g, GroupedI8Data{x, w, x_scale, w_scale, y}, stream));
+}
+
+size_t moe_expert_layer_workspace_size(int32_t T, int32_t k, int32_t E, int32_t d_model, int32_t d_ff) {
+    if (!layer_sizes_ok(T, k, E, d_model, d_ff) || !layer_supported(T, k, d_model, d_ff)) return 0;
+    return WS_HEADER + 2 * expert_layer_halves(T, k, d_ff);
+}
+
+moe_status_t moe_expert_layer(moe_dtype_t dtype, const void* x, const float* logits, const void* w13, const void* w2,
+                              int32_t T, int32_t k, int32_t E, int32_t d_model, int32_t d_ff, void* out,
+                              int32_t* topk_ids_out, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!layer_sizes_ok(T, k, E, d_model, d_ff)) return MOE_ERR_INVALID_ARG;
+    if ((dtype != MOE_DT_BF16 && dtype != MOE_DT_F16) || !layer_supported(T, k, d_model, d_ff)) return MOE_ERR_UNSUPPORTED;
+    if (!workspace || (T > 0 && (!x || !logits || !w13 || !w2 || !out))) return MOE_ERR_INVALID_ARG;
+    if (!all_aligned({x, logits, w13, w2, out, topk_ids_out, workspace})) return MOE_ERR_MISALIGNED;
+    if (workspace_bytes < moe_expert_layer_workspace_size(T, k, E, d_model, d_ff)) return MOE_ERR_WORKSPACE;
+    if (T == 0) return MOE_OK;
+    auto* ws = static_cast<unsigned char*>(workspace);
+    return cuda_status(launch_expert_layer(ExpertLayer{dtype, x, logits, w13, w2, T, k, E, d_model, d_ff, out, topk_ids_out,
+                                                       reinterpret_cast<uint32_t*>(ws), reinterpret_cast<uint16_t*>(ws + WS_HEADER)},
+                                           stream));
 }
 
 }  // extern "C"

@@ -541,6 +541,36 @@ PyObject* py_grouped_mm_i8(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
     });
 }
 
+// ------------------------------------------------ a layer for a few tokens
+PyObject* py_expert_layer(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+    return guarded([&] {
+        static const auto names = intern<9>({"x", "logits", "w13", "w2", "k", "out", "ids", "ws", "stream"});
+        const Args<9> a("expert_layer", names, 5, args, n, kw);
+        const Tensor x = a.needed_tensor(0), logits = a.needed_tensor(1), w13 = a.needed_tensor(2), w2 = a.needed_tensor(3);
+        const Tensor out0 = a.tensor(5), ids = a.tensor(6), ws0 = a.tensor(7);
+        dims("x", x, 2);
+        dims("logits", logits, 2);
+        dims("w2", w2, 3);
+        const at::ScalarType type = x.scalar_type();
+        const moe_dtype_t dt = moe_type(type);
+        const int64_t T = x.size(0), d = x.size(1), E = logits.size(1), f = w2.size(2), k = a.integer(4, 0);
+        want("logits", logits, {T, E}, at::kFloat);
+        want("w2", w2, {E, d, f}, type);
+        want("w13", w13, {E, 2 * f, d}, type);
+        if (ids.defined()) want("ids", ids, {T, k}, at::kInt);
+        const int32_t t = size32(T), kk = size32(k), e = size32(E), dd = size32(d), ff = size32(f);
+        on_one_device({x, logits, w13, w2, out0, ids, ws0});
+        const OnStream on(a, 8, x);
+        const Tensor out = output(out0, "out", x, {T, d}, type);
+        // a new one is zeroed: the CTAs' count has to start somewhere
+        Tensor ws = ws0;
+        if (!ws.defined()) ws = workspace(ws0, moe_expert_layer_workspace_size(t, kk, e, dd, ff), x).zero_();
+        check(moe_expert_layer(dt, ptr(x), ptr_as<float>(logits), ptr(w13), ptr(w2), t, kk, e, dd, ff, ptr(out),
+                               ptr_as<int32_t>(ids), ptr(ws), (size_t)ws.numel(), on.s), "moe_expert_layer");
+        return wrap(out);
+    });
+}
+
 PyObject* py_init(PyObject*, PyObject* check_fn) {
     Py_INCREF(check_fn);
     Py_XDECREF(g_check);
@@ -593,6 +623,12 @@ PyMethodDef methods[] = {
      "y[r] = x_scale[r] w_scale[e] (w[e] x[r]) for the rows r of every expert e: int8 x [R, K] and w [E, N, K], fp32\n"
      "scales [R] and [E, N], offsets [E + 1] of permute(); y in bfloat16 or float16.  Offsets out of order or range set\n"
      "the error word of ws, for get_device_error(ws); without ws it is lost."},
+    {"expert_layer", FAST(py_expert_layer),
+     "expert_layer(x, logits, w13, w2, k, out=None, ids=None, ws=None, stream=None) -> out\n\n"
+     "The whole layer of 16-bit experts for at most 32 tokens in one kernel: the k experts of the largest logits\n"
+     "[T, E] and their softmax, SiLU(gate) up with w13 [E, 2f, d] (gate first), w2 [E, d, f], the weighted sum.\n"
+     "ids [T, k]: where the chosen experts go.  A given ws comes from workspace(), which zeroes it; one kept between\n"
+     "calls saves clearing it."},
     {"_init", py_init, METH_O, "Sets the function that raises for a status."},
     {nullptr, nullptr, 0, nullptr},
 };

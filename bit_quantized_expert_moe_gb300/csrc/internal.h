@@ -201,6 +201,22 @@ cudaError_t launch_grouped_i8(const GroupedI8Shape& g, const GroupedI8Data& d, c
 // The same by another kernel, for few rows in all.
 cudaError_t launch_grouped_i8_few(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s);
 
+// The whole layer of 16-bit experts for a few tokens.
+struct ExpertLayer {
+    moe_dtype_t dtype;       // bf16 or fp16
+    const void* x;           // [T][d]
+    const float* logits;     // [T][E]
+    const void *w13, *w2;    // [E][2f][d], [E][d][f]
+    int T, k, E, d, f;
+    void* out;               // [T][d]
+    int32_t* ids_out;        // [T][k] or null
+    uint32_t* header;        // of the workspace
+    uint16_t* h;             // expert_layer_halves() behind it
+};
+bool expert_layer_supported(int T, int k);
+size_t expert_layer_halves(int T, int k, int f);
+cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s);
+
 // 3D tensor map over 32-bit words: dims {d0, d1, d2} (d0 contiguous), byte
 // strides s1 (dim 1) and s2 (dim 2), box {b0, b1, b2}, 128-byte swizzle.
 bool make_tensor_map_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,

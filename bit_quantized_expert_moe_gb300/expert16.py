@@ -1,7 +1,8 @@
 """The 16-bit expert operators: products grouped by expert with their gradients,
 the gated activation with the routing weight, and the norms around a block; and
 the operators of expert blocks in 8 and 16 bits: the layer norm before a block with
-its gradients, rows to 8-bit codes, and the 8-bit products grouped by expert.
+its gradients, rows to 8-bit codes, the 8-bit products grouped by expert, and the
+whole layer of 16-bit experts for a few tokens.
 
     grouped_mm(x, w, offsets, y=None, ws=None, stream=None)
     grouped_mm_dx(dy, w, offsets, dx=None, ws=None, stream=None)
@@ -16,6 +17,7 @@ its gradients, rows to 8-bit codes, and the 8-bit products grouped by expert.
     layer_norm_backward(x_out, dh, dx_out=None, gamma=None, beta=None, eps=1e-5, ws=None, stream=None)
     quantize_rows(x, row_map=None, k=1, codes=None, scales=None, stream=None)
     grouped_mm_i8(x, x_scale, w, w_scale, offsets, y=None, dtype=torch.bfloat16, ws=None, stream=None)
+    expert_layer(x, logits, w13, w2, k, out=None, ids=None, ws=None, stream=None)
 
 `offsets` and `row_map` are the `offsets` and `sorted` of permute().  Offsets
 out of order or range set the error word of the `ws` that was given, which
@@ -34,7 +36,8 @@ import importlib
 from . import _check, lib
 
 NAMES = ("grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "swiglu", "swiglu_backward", "block_norm",
-         "block_norm_backward", "layer_norm", "layer_norm_backward", "quantize_rows", "grouped_mm_i8")
+         "block_norm_backward", "layer_norm", "layer_norm_backward", "quantize_rows", "grouped_mm_i8",
+         "expert_layer")
 
 
 def load(name: str):
@@ -72,3 +75,7 @@ def layer_norm_backward_workspace_size(T: int, D: int) -> int:
 
 def grouped_mm_i8_workspace_size(R: int, E: int, N: int, K: int) -> int:
     return lib().moe_grouped_mm_i8_workspace_size(R, E, N, K)
+
+
+def expert_layer_workspace_size(T: int, k: int, E: int, d: int, f: int) -> int:
+    return lib().moe_expert_layer_workspace_size(T, k, E, d, f)

@@ -406,9 +406,33 @@ moe_status_t moe_grouped_mm_i8(moe_dtype_t out_dtype, const int8_t* x, const flo
                                int32_t K, void* y, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * The whole layer of 16-bit experts for a few tokens, in one kernel: routing as
+ * moe_route_topk (logits may be -inf), then for token t with experts e_j and weights p_j
+ *   out[t] = sum_j p_j Wd[e_j] (SiLU(Wg[e_j] x[t]) * (Wu[e_j] x[t]))
+ * in bf16 or fp16 with fp32 accumulation and one rounding at the end (fp16: every
+ * SiLU * up has to be below 65504).
+ *   x       device [T][d_model]      logits  device fp32 [T][E]
+ *   w13     device [E][2 d_ff][d_model], the gate's rows first
+ *   w2      device [E][d_model][d_ff]
+ *   out     device [T][d_model] (out), may be x
+ *   topk_ids_out  device int32 [T][k] or NULL
+ * T <= 32, k <= 32, T k <= 256, k <= E <= 1024; d_model and d_ff multiples of 64, at most
+ * 32768 (MOE_ERR_UNSUPPORTED otherwise).  More tokens: moe_permute and the grouped
+ * products.  NaN logits may leave a token without some of its experts
+ * (MOE_ERR_DEVICE_RANGE by moe_get_device_error).  One CTA on every SM (cooperative
+ * launch), which meet once: calls that share a workspace must not overlap.
+ * Workspace: >= moe_expert_layer_workspace_size(...) bytes, zeroed before its first use;
+ * one for the most tokens also does for fewer.
+ */
+size_t moe_expert_layer_workspace_size(int32_t T, int32_t k, int32_t E, int32_t d_model, int32_t d_ff);
+moe_status_t moe_expert_layer(moe_dtype_t dtype, const void* x, const float* logits, const void* w13, const void* w2,
+                              int32_t T, int32_t k, int32_t E, int32_t d_model, int32_t d_ff, void* out,
+                              int32_t* topk_ids_out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Reads and clears the device error word kept at the start of a workspace
- * used by moe_permute, moe_expert_ffn_w4a16, moe_layer_forward or the grouped
- * products.  Waits for `stream` to finish.  When it reports an error it clears the whole 256-byte
+ * used by moe_permute, moe_expert_ffn_w4a16, moe_layer_forward, the grouped
+ * products or moe_expert_layer.  Waits for `stream` to finish.  When it reports an error it clears the whole 256-byte
  * header, which also holds the grid-barrier counter of the one-kernel decode
  * layer (a call that gave up can leave that counter inconsistent).  Returns MOE_OK, MOE_ERR_TIMEOUT, MOE_ERR_DEVICE_RANGE
  * or MOE_ERR_F16_RANGE, in that order of precedence (or MOE_ERR_CUDA if the

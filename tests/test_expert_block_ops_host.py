@@ -144,3 +144,55 @@ def test_python_refuses_other_types_and_shapes(M):
         M.grouped_mm_i8(i8, torch.zeros(4), w, torch.zeros(2, 8), off, dtype="bfloat16")
     with pytest.raises(TypeError):
         M.quantize_rows(x, k=1.5)
+
+
+def test_expert_layer_rejects_bad_arguments(M):
+    def call(dt=BF16, x=P, lg=P, w13=P, w2=P, T=4, k=2, E=8, d=128, f=64, out=P, ids=P, ws=P, wsb=BIG):
+        return M.lib().moe_expert_layer(dt, x, lg, w13, w2, T, k, E, d, f, out, ids, ws, wsb, None)
+
+    assert call(T=-1) == INVALID
+    assert call(k=0) == INVALID
+    assert call(k=9) == INVALID                 # more than the experts
+    assert call(E=0) == INVALID
+    assert call(E=1025) == INVALID
+    assert call(d=0) == INVALID
+    assert call(f=-64) == INVALID
+    assert call(dt=F32) == UNSUPPORTED
+    assert call(T=33) == UNSUPPORTED
+    assert call(T=2 ** 31 - 1) == UNSUPPORTED
+    assert call(T=32, k=9, E=64) == UNSUPPORTED
+    assert call(T=1, k=33, E=64) == UNSUPPORTED
+    assert call(d=96) == UNSUPPORTED
+    assert call(f=32) == UNSUPPORTED
+    assert call(d=32832) == UNSUPPORTED
+    assert call(f=32832) == UNSUPPORTED
+    for hole in ("x", "lg", "w13", "w2", "out", "ws"):
+        assert call(**{hole: None}) == INVALID, hole
+    for hole in ("x", "lg", "w13", "w2", "out", "ids", "ws"):
+        assert call(**{hole: P + 8}) == MISALIGNED, hole
+    need = M.expert_layer_workspace_size(4, 2, 8, 128, 64)
+    assert need > 256
+    assert call(wsb=need - 1) == WORKSPACE
+    assert call(T=0, x=None, lg=None, w13=None, w2=None, out=None) == OK
+    assert M.expert_layer_workspace_size(33, 2, 8, 128, 64) == 0
+    assert M.expert_layer_workspace_size(4, 2, 8, 100, 64) == 0
+    assert M.expert_layer_workspace_size(4, 0, 8, 128, 64) == 0
+
+
+def test_python_expert_layer_refuses(M):
+    torch = pytest.importorskip("torch")
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t)  # noqa: E731
+    x, lg, w13, w2 = z(4, 64), z(4, 8, t=torch.float32), z(8, 128, 64), z(8, 64, 64)
+    for call in (lambda: M.expert_layer(x, lg, w13, w2, 2),                         # host tensors
+                 lambda: M.expert_layer(x, z(4, 8), w13, w2, 2),
+                 lambda: M.expert_layer(x, z(3, 8, t=torch.float32), w13, w2, 2),
+                 lambda: M.expert_layer(x, lg, z(8, 64, 64), w2, 2),
+                 lambda: M.expert_layer(x, lg, w13, z(8, 64, 64, t=torch.float16), 2),
+                 lambda: M.expert_layer(x, lg, w13, w2, 2, ids=z(4, 3, t=torch.int32)),
+                 lambda: M.expert_layer(z(64), lg, w13, w2, 2)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        M.expert_layer(x, lg, w13, w2)
+    with pytest.raises(TypeError):
+        M.expert_layer(x, lg, w13, w2, None)
