@@ -19,9 +19,13 @@
 //            as well: no partial sums between CTAs, a fixed order, one rounding.
 // mma.sync m16n8k16 with the weight rows as M (phase 1: 8 features' gate rows and their
 // up rows, so that a thread has both) and an expert's tokens as N, 8 at a time: at a
-// few tokens an expert the tensor rate is no bound.  A chunk's 32-input units are dealt
-// out to the warps, which add up in shared memory at the end of a tile.  Both operands
-// keep K in the order in which a thread's 16-byte loads bring it, as in grouped_few.cu.
+// few tokens an expert the tensor rate is no bound.  Both operands keep K in the order
+// in which a thread's 16-byte loads bring it, as in grouped_few.cu.
+// What bounds the consumers is latency, a chunk's 0.7 us at the full rate of the stream:
+// two groups of eight warps take every second chunk, its 32-input units dealt out to
+// the warps; the tokens' values of a warp's next chunk are on their way while it has
+// one; and a warp of its own adds the warps' sums up and writes h, so that none of
+// them waits for the others at the end of a tile.
 // h is kept as two 16-bit numbers, the second one the rounding error of the first, so
 // the output is rounded once as if h were fp32; twice the (few) MMAs of phase 2.
 #include "decode_ops.cuh"
@@ -32,12 +36,25 @@ namespace moe {
 namespace {
 
 constexpr int MAX_T = 32, MAX_R = 256;
-constexpr int CW = 8;                        // consumer warps
-constexpr int CONSUMERS = 32 * CW, THREADS = CONSUMERS + 32;
-constexpr int SLOT = 32768, MAX_SLOTS = 7;
+constexpr int GROUPS = 2, GW = 8, CW = GROUPS * GW;  // consumer warps
+constexpr int CONSUMERS = 32 * CW, THREADS = CONSUMERS + 64;
+constexpr int PRODUCER = CW, FINISHER = CW + 1;      // warps
+constexpr int SLOT = 32768;
 constexpr int BLOCKS = 16;                   // most 64-input blocks of a chunk
-constexpr int UNITS = 2 * BLOCKS / CW;       // most 32-input units of a chunk for a warp
-static_assert(MAX_R <= CONSUMERS, "one thread an assignment");
+constexpr int UNITS = 2 * BLOCKS / GW;       // most 32-input units of a chunk for a warp
+constexpr int SORTERS = 256;
+static_assert(MAX_R <= SORTERS, "one thread an assignment");
+// Slots of the ring and buffers for the warps' sums (of 8 tokens each), by NT.  Both
+// are multiples of the groups, so that a slot is always one group's: a wait names a
+// round of its barrier by the round's parity, and a group that took every second round
+// of a slot would take the end of the round before for that of its own.
+constexpr int slots(int nt) { return nt <= 2 ? 6 : 4; }
+constexpr int buffers(int nt) { return nt <= 2 ? 2 : 4; }
+constexpr int SUM_FLOATS = CW * 128;         // of a buffer: [CW][32][4]
+constexpr size_t sums_bytes(int nt) {        // phase 1: the buffers; phase 2: [CW][T][17]
+    return std::max<size_t>((size_t)buffers(nt) * SUM_FLOATS, (size_t)CW * 8 * nt * 17) * sizeof(float);
+}
+constexpr int BAR_BYTES = 256;
 
 struct Tab {
     int ids[MAX_R];
@@ -57,7 +74,7 @@ struct Params {
     uint16_t *hi, *lo;   // h by sorted position, [R][f] each
     uint32_t* err;
     unsigned long long* bar_count;
-    int T, k, E, d, f, nslot;
+    int T, k, E, d, f;
     int cb1, cb2;        // 64-input blocks of a chunk of either phase
     int rows2[4];        // rows of the maps of the down projection
 };
@@ -117,33 +134,82 @@ __device__ __forceinline__ uint4 weights_at(uint32_t slot, int line, int half, i
     return dec::lds128(slot + 128u * line + ((uint32_t)((4 * half + t) ^ (line & 7)) << 4));
 }
 
+// Where a group is in phase 1's list of chunks.
+struct Place1 {
+    int x, b, q;                // tile's first feature, chunk's first block; chunks before
+    int r0, r1;                 // sums before; of tiles of one chunk: of either group
+    int i0, n, m, cnt, off;     // of the tile
+    __device__ void tile(const Tab& tab, int end, int f) {
+        const Tile1 t(x, end, f);
+        i0 = t.i0;
+        n = t.n;
+        m = t.m;
+        cnt = tab.ucnt[t.u];
+        off = tab.uoff[t.u];
+    }
+    __device__ void step(const Tab& tab, int end, int f, int nb, int cb) {
+        if (x >= end) return;
+        ++q;
+        if ((b += cb) < nb) return;
+        b = 0;
+        if (cb < nb || (q & 1)) r0 += ceil_div(cnt, 8);  // (the chunk was q - 1)
+        else r1 += ceil_div(cnt, 8);
+        x += n;
+        if (x < end) tile(tab, end, f);
+    }
+};
+
+// The buffer of sum n of a group's tile and the parity of its round: any buffer in
+// turn where all warps have a part of every tile, else one of the group's.
+template <int NBUF>
+struct SumAt {
+    int buf;
+    uint32_t parity;
+    __device__ SumAt(const Place1& c, int n, int group, bool one_chunk) {
+        constexpr int EACH = NBUF / GROUPS;
+        const int k = n + (one_chunk && group ? c.r1 : c.r0);
+        buf = one_chunk ? group * EACH + k % EACH : k % NBUF;
+        parity = (uint32_t)(one_chunk ? k / EACH : k / NBUF) & 1u;
+    }
+};
+
 // NT: most groups of 8 tokens of an expert.
 template <bool BF16, int NT>
 __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_constant__ Maps maps, const Params p) {
+    constexpr int NSLOT = slots(NT), NBUF = buffers(NT);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    const uint32_t ring = smem_u32(sm), full = ring + p.nslot * SLOT, empty = full + 8 * MAX_SLOTS;
-    Tab& tab = *reinterpret_cast<Tab*>(sm + p.nslot * SLOT + 16 * MAX_SLOTS);
-    // phase 1: [2][CW][NT][32][4]; phase 2: [CW][T][17]
-    float* sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&tab) + align_up(sizeof(Tab), 16));
+    const uint32_t ring = smem_u32(sm), full = ring + NSLOT * SLOT, empty = full + 8 * NSLOT;
+    const uint32_t sum_full = empty + 8 * NSLOT, sum_empty = sum_full + 8 * NBUF, h_ready = sum_empty + 8 * NBUF;
+    static_assert(16 * NSLOT + 16 * NBUF + 8 <= BAR_BYTES, "barrier area too small");
+    static_assert(NSLOT % GROUPS == 0 && NBUF % GROUPS == 0, "a slot and a buffer are one group's");
+    float* sums = reinterpret_cast<float*>(sm + NSLOT * SLOT + BAR_BYTES);
+    Tab& tab = *reinterpret_cast<Tab*>(sm + NSLOT * SLOT + BAR_BYTES + sums_bytes(NT));
     volatile int* abort_flag = &tab.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int R = p.T * p.k, d = p.d, f = p.f, G = gridDim.x, cta = blockIdx.x;
+    const int nb1 = d / 64, nb2 = f / 64, cb1 = p.cb1, cb2 = p.cb2;
+    const bool one_chunk = cb1 >= nb1;  // a tile of phase 1 is one group's
 
     // ------------------------------------------------ phase 0: init, routing
     if (threadIdx.x == 0) tab.abort = 0;
-    if (warp == CW && lane == 0) {
-        for (int i = 0; i < p.nslot; ++i) {
+    if (warp == PRODUCER && lane == 0) {
+        for (int i = 0; i < NSLOT; ++i) {
             tc::mbar_init(full + 8 * i, 1);
-            tc::mbar_init(empty + 8 * i, CW);
+            tc::mbar_init(empty + 8 * i, GW);
         }
+        for (int i = 0; i < NBUF; ++i) {
+            tc::mbar_init(sum_full + 8 * i, one_chunk ? GW : CW);
+            tc::mbar_init(sum_empty + 8 * i, 1);
+        }
+        tc::mbar_init(h_ready, 1);
         tc::fence_mbar_init();
         for (int i = 0; i < 4; ++i) {
             tc::tma_prefetch_desc(&maps.w13[i]);
             tc::tma_prefetch_desc(&maps.w2[i]);
         }
     }
-    if (warp == 1) {  // a hint, which returns no value: before the kernel ahead is complete
+    if (warp == FINISHER) {  // a hint, which returns no value: before the kernel ahead is complete
         const int lines = (p.T * p.E * 4 + 127) / 128;
         for (int i = lane; i < lines; i += 32)
             asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const char*>(p.logits) + 128 * (size_t)i));
@@ -154,6 +220,8 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
         for (int t = warp; t < p.T; t += CW)
             dec::route_token(p.logits + (size_t)t * p.E, p.E, p.k, &tab.ids[t * p.k], &tab.w[t * p.k]);
         dec::bar_sync(1, CONSUMERS);
+    }
+    if (threadIdx.x < SORTERS) {
         // Stable counting sort by expert, one thread an assignment.  An id out of
         // range (logits that are no numbers) has no expert.
         const int a = threadIdx.x;
@@ -170,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
         const bool first = va && before == 0;
         tab.first[a] = first;
         if (a < R && !va) set_error(p.err, ERRBIT_RANGE);
-        dec::bar_sync(1, CONSUMERS);
+        dec::bar_sync(2, SORTERS);
         int ui = 0, nu = 0;
         for (int b = 0; b < R; ++b) {
             const int fb = tab.first[b];
@@ -194,9 +262,8 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
     const int n_uniq = tab.n_uniq;
     const int x_lo = share(n_uniq * f, cta, G), x_hi = share(n_uniq * f, cta + 1, G);
     const int r_lo = share(d, cta, G), rows = share(d, cta + 1, G) - r_lo, tiles2 = ceil_div(rows, 16);
-    const int nb1 = d / 64, nb2 = f / 64;
 
-    if (warp == CW) {
+    if (warp == PRODUCER) {
         // ---------------------------------------------------------- producer
         if (tc::elect_one()) {
             int s = 0;
@@ -208,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                 return ok;
             };
             auto advance = [&] {
-                if (++s == p.nslot) {
+                if (++s == NSLOT) {
                     s = 0;
                     phase ^= 1u;
                 }
@@ -216,7 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             for (int x = x_lo; ok && x < x_hi;) {
                 const Tile1 t(x, x_hi, f);
                 const int e = tab.uexp[t.u];
-                for (int b = 0; b < nb1 && next(p.cb1 * 2 * t.n * 128); b += p.cb1, advance())
+                for (int b = 0; b < nb1 && next(cb1 * 2 * t.n * 128); b += cb1, advance())
                     asm volatile(
                         "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
                         " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];"
@@ -228,98 +295,55 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                 const int m = t.n == p.rows2[0] ? 0 : t.n == p.rows2[1] ? 1 : t.n == p.rows2[2] ? 2 : 3;
                 for (int u = 0; ok && u < n_uniq; ++u) {
                     const int e = tab.uexp[u];
-                    for (int b = 0; b < nb2 && next(p.cb2 * t.n * 128); b += p.cb2, advance())
+                    for (int b = 0; b < nb2 && next(cb2 * t.n * 128); b += cb2, advance())
                         tc::tma_load_4d(ring + s * SLOT, &maps.w2[m], full + 8 * s, 0, r_lo + t.r0, b, e);
                 }
             }
         }
         __syncwarp();
-    } else {
-        // --------------------------------------------------------- consumers
+    } else if (warp == FINISHER) {
+        // --------------------- phase 1's sums: h = SiLU(gate) up, two columns a lane
         const int g = lane >> 2, t = lane & 3;
-        int s = 0, buf = 0;
-        uint32_t phase = 0;
-        auto release = [&] {
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(empty + 8 * s);
-            if (++s == p.nslot) {
-                s = 0;
-                phase ^= 1u;
-            }
-        };
-        // ---- phase 1.  A wait that gave up skips the work but no barrier.
-        for (int x = x_lo; x < x_hi;) {
-            const Tile1 tl(x, x_hi, f);
-            const int cnt = tab.ucnt[tl.u], off = tab.uoff[tl.u], nt = ceil_div(cnt, 8);
-            const int gf = min(g, tl.n - 1);  // rows beyond the tile's: the last one again
-            const uint16_t* xr[NT];
+        Place1 c{x_lo};
+        if (c.x < x_hi) c.tile(tab, x_hi, f);
+        while (c.x < x_hi) {
+            const int group = c.q & 1, w0 = one_chunk ? group * GW : 0, w1 = one_chunk ? w0 + GW : CW;
+            for (int n = 0; 8 * n < c.cnt; ++n) {
+                const SumAt<NBUF> at(c, n, group, one_chunk);
+                const int buf = at.buf;
+                tc::mbar_wait(sum_full + 8 * buf, at.parity, abort_flag, p.err);
+                __syncwarp();
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int w = w0; w < w1; ++w) {
+                    const float4 o = *reinterpret_cast<const float4*>(sums + buf * SUM_FLOATS + (w * 32 + lane) * 4);
+                    v.x += o.x;
+                    v.y += o.y;
+                    v.z += o.z;
+                    v.w += o.w;
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(sum_empty + 8 * buf);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) xr[n] = p.x + (size_t)tab.tok[off + min(8 * n + g, cnt - 1)] * d + 8 * t;
-            float acc[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-            for (int b = 0; b < nb1; b += p.cb1) {
-                const int units = 2 * min(p.cb1, nb1 - b);
-                uint4 v[NT == 1 ? UNITS : 1];
-                if (NT == 1)  // the tokens' inputs are on their way while the weights are
-#pragma unroll
-                    for (int i = 0; i < UNITS; ++i)
-                        if (warp + CW * i < units) v[NT == 1 ? i : 0] = __ldg(reinterpret_cast<const uint4*>(xr[0] + 64 * b + 32 * (warp + CW * i)));
-                const bool ok = tc::mbar_wait(full + 8 * s, phase, abort_flag, p.err);
-                if (ok)
-#pragma unroll
-                    for (int i = 0; i < UNITS; ++i) {
-                        const int unit = warp + CW * i, kb = unit >> 1, half = unit & 1;
-                        if (unit < units) {
-                            const uint4 wg = weights_at(ring + s * SLOT, 2 * kb * tl.n + gf, half, t);
-                            const uint4 wu = weights_at(ring + s * SLOT, (2 * kb + 1) * tl.n + gf, half, t);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                if (n < nt) {
-                                    if (NT > 1) v[0] = __ldg(reinterpret_cast<const uint4*>(xr[n] + 64 * b + 32 * unit));
-                                    mma<BF16>(acc[n], wg, wu, v[NT == 1 ? i : 0]);
-                                }
-                        }
+                for (int i = 0; i < 2; ++i) {
+                    const int col = 8 * n + 2 * t + i;
+                    if (g < c.n && col < c.cnt) {
+                        const float a = i ? v.y : v.x, u = i ? v.w : v.z;
+                        const float h = a / (1.f + expf(-a)) * u;
+                        const uint16_t hi = bits16<BF16>(h);
+                        const float rest = h - value16<BF16>(hi);
+                        const size_t to = (size_t)(c.off + col) * f + c.i0 + g;
+                        p.hi[to] = hi;
+                        p.lo[to] = bits16<BF16>(isfinite(rest) ? rest : 0.f);
                     }
-                release();
-            }
-            // the warps' sums; the buffers alternate, so one barrier a tile
-            float* red = sums + buf * (CW * NT * 128);
-            buf ^= 1;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                if (n < nt)
-                    *reinterpret_cast<float4*>(red + ((warp * NT + n) * 32 + lane) * 4) =
-                        make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-            dec::bar_sync(1, CONSUMERS);
-            for (int i = threadIdx.x; i < 64 * nt; i += CONSUMERS) {
-                // feature i % 8, column i / 8: lane 4 (i % 8) + column / 2 holds them, gate
-                // at column % 2 and up two further
-                const int feat = i & 7, col = i >> 3, c8 = col & 7;
-                if (feat < tl.n && col < cnt) {
-                    float a = 0.f, u = 0.f;
-#pragma unroll
-                    for (int w = 0; w < CW; ++w) {
-                        const float* q = red + ((w * NT + (col >> 3)) * 32 + 4 * feat + (c8 >> 1)) * 4 + (c8 & 1);
-                        a += q[0];
-                        u += q[2];
-                    }
-                    const float h = a / (1.f + expf(-a)) * u;
-                    const uint16_t hi = bits16<BF16>(h);
-                    const float rest = h - value16<BF16>(hi);
-                    const size_t at = (size_t)(off + col) * f + tl.i0 + feat;
-                    p.hi[at] = hi;
-                    p.lo[at] = bits16<BF16>(isfinite(rest) ? rest : 0.f);
                 }
             }
-            x += tl.n;
+            for (int b = 0; b < nb1; b += cb1) c.step(tab, x_hi, f, nb1, cb1);
         }
-
-        // ---- every CTA's h is written before anyone reads it.  The arrival count only
+        // Every CTA's h is written before anyone reads it.  The arrival count only
         // grows, G a launch, so a CTA's own arrival tells it the count at which this
         // launch's barrier opens.
-        dec::bar_sync(1, CONSUMERS);
-        if (threadIdx.x == 0) {
+        __syncwarp();
+        if (lane == 0) {
             const uint64_t old = dec::atom_add_release_gpu(p.bar_count, 1ull);
             const uint64_t target = (old / (uint64_t)G + 1) * (uint64_t)G;
             const uint64_t t0 = globaltimer_ns();
@@ -332,83 +356,172 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                         break;
                     }
                 }
+            tc::mbar_arrive(h_ready);
         }
-        for (int i = threadIdx.x; i < CW * p.T * 17; i += CONSUMERS) sums[i] = 0.f;
-        dec::bar_sync(1, CONSUMERS);
-        // the last phase: the next kernel may be scheduled
+        __syncwarp();
         grid_dependency_launch();
+    } else {
+        // --------------------------------------------------------- consumers
+        const int g = lane >> 2, t = lane & 3, group = warp / GW, gw = warp % GW;
+        float acc[NT][4];
+        auto clear = [&] {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+        };
+        auto release = [&](int q) {
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(empty + 8 * (q % NSLOT));
+        };
+        auto wait = [&](int q) { tc::mbar_wait(full + 8 * (q % NSLOT), (uint32_t)(q / NSLOT) & 1u, abort_flag, p.err); };
+        // A wait that gave up goes on with what is in the slot: no barrier is left out,
+        // and every address stays where it was.
 
-        // ---- phase 2
-        float* mine = sums + warp * p.T * 17;
-        for (int i = 0; i < tiles2; ++i) {
-            const Tile2 tl(rows, tiles2, i);
-            const int ga = min(g, tl.n - 1), gb = min(g + 8, tl.n - 1);
-            for (int u = 0; u < n_uniq; ++u) {
-                const int cnt = tab.ucnt[u], off = tab.uoff[u], nt = ceil_div(cnt, 8);
-                size_t hr[NT];
+        // ---- phase 1
+        Place1 c{x_lo};
+        if (c.x < x_hi) c.tile(tab, x_hi, f);
+        if (group) c.step(tab, x_hi, f, nb1, cb1);
+        // Units gw, gw + GW, ... of a chunk are this warp's.  As soon as the MMAs have a
+        // unit's values, those of the warp's next chunk (or next 8 tokens) take their place.
+        uint4 v[UNITS];
+        struct From {
+            const uint16_t* x;
+            int units;
+        };
+        auto from = [&](const Place1& c, int n) {
+            return From{p.x + (size_t)tab.tok[c.off + min(8 * n + g, c.cnt - 1)] * d + 64 * c.b + 8 * t, 2 * min(cb1, nb1 - c.b)};
+        };
+        auto load = [&](int i, const From& o) {
+            if (gw + GW * i < o.units) v[i] = __ldg(reinterpret_cast<const uint4*>(o.x + 32 * (gw + GW * i)));
+        };
+        clear();
+        if (c.x < x_hi) {
+            const From o = from(c, 0);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) hr[n] = (size_t)(off + min(8 * n + g, cnt - 1)) * f + 8 * t;
-                float acc[NT][4];
+            for (int i = 0; i < UNITS; ++i) load(i, o);
+        }
+        while (c.x < x_hi) {
+            Place1 to = c;
+            to.step(tab, x_hi, f, nb1, cb1);
+            to.step(tab, x_hi, f, nb1, cb1);
+            const int units = 2 * min(cb1, nb1 - c.b), gf = min(g, c.n - 1);  // rows beyond the tile's: its last again
+            const uint32_t slot = ring + (c.q % NSLOT) * SLOT;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-                for (int b = 0; b < nb2; b += p.cb2) {
-                    const int units = 2 * min(p.cb2, nb2 - b);
-                    uint4 vh[NT == 1 ? UNITS : 1], vl[NT == 1 ? UNITS : 1];
-                    if (NT == 1)
+            for (int n = 0; n < NT; ++n)
+                if (8 * n < c.cnt) {
+                    From o{nullptr, 0};
+                    if (8 * (n + 1) < c.cnt) o = from(c, n + 1);
+                    else if (to.x < x_hi) o = from(to, 0);
+                    if (n == 0) wait(c.q);
 #pragma unroll
-                        for (int j = 0; j < UNITS; ++j)
-                            if (warp + CW * j < units) {
-                                vh[NT == 1 ? j : 0] = dec::ldg_cg16(p.hi + hr[0] + 64 * b + 32 * (warp + CW * j));
-                                vl[NT == 1 ? j : 0] = dec::ldg_cg16(p.lo + hr[0] + 64 * b + 32 * (warp + CW * j));
-                            }
-                    const bool ok = tc::mbar_wait(full + 8 * s, phase, abort_flag, p.err);
-                    if (ok)
-#pragma unroll
-                        for (int j = 0; j < UNITS; ++j) {
-                            const int unit = warp + CW * j, kb = unit >> 1, half = unit & 1;
-                            if (unit < units) {
-                                const uint4 wa = weights_at(ring + s * SLOT, kb * tl.n + ga, half, t);
-                                const uint4 wb = weights_at(ring + s * SLOT, kb * tl.n + gb, half, t);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-                                    if (n < nt) {
-                                        if (NT > 1) {
-                                            vh[0] = dec::ldg_cg16(p.hi + hr[n] + 64 * b + 32 * unit);
-                                            vl[0] = dec::ldg_cg16(p.lo + hr[n] + 64 * b + 32 * unit);
-                                        }
-                                        mma<BF16>(acc[n], wa, wb, vh[NT == 1 ? j : 0]);
-                                        mma<BF16>(acc[n], wa, wb, vl[NT == 1 ? j : 0]);
-                                    }
-                            }
-                        }
-                    release();
+                    for (int i = 0; i < UNITS; ++i) {
+                        const int unit = gw + GW * i, line = (unit >> 1) * 2 * c.n + gf;
+                        if (unit < units)
+                            mma<BF16>(acc[n], weights_at(slot, line, unit & 1, t), weights_at(slot, line + c.n, unit & 1, t), v[i]);
+                        load(i, o);
+                    }
                 }
-                // columns 2 t and 2 t + 1, rows g and g + 8, into the tokens' sums
+            release(c.q);
+            if (to.x != c.x) {  // this group's last chunk of the tile
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
+                    if (8 * n < c.cnt) {
+                        const SumAt<NBUF> at(c, n, group, one_chunk);
+                        const int buf = at.buf;
+                        tc::mbar_wait(sum_empty + 8 * buf, at.parity ^ 1u, abort_flag, p.err);
+                        *reinterpret_cast<float4*>(sums + buf * SUM_FLOATS + (warp * 32 + lane) * 4) =
+                            make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(sum_full + 8 * buf);
+                    }
+                clear();
+            }
+            c = to;
+        }
+
+        // ---- phase 2
+        tc::mbar_wait(h_ready, 0, abort_flag, p.err);
+        grid_dependency_launch();  // the last phase: the next kernel may be scheduled
+        float* mine = sums + warp * p.T * 17;
+        for (int i = lane; i < p.T * 17; i += 32) mine[i] = 0.f;
+        __syncwarp();
+        int q = c.q;  // all of phase 1
+        const int parts = ceil_div(nb2, cb2), chunks = n_uniq * parts;
+        uint4 lo[UNITS];
+        for (int i = 0; i < tiles2; ++i, q += chunks) {
+            const Tile2 tl(rows, tiles2, i);
+            const int ga = min(g, tl.n - 1), gb = min(g + 8, tl.n - 1);
+            struct FromH {
+                size_t at;
+                int units;
+            };
+            auto from_h = [&](int j, int n) {
+                const int u = j / parts, b = (j - u * parts) * cb2;
+                return FromH{(size_t)(tab.uoff[u] + min(8 * n + g, tab.ucnt[u] - 1)) * f + 64 * b + 8 * t, 2 * min(cb2, nb2 - b)};
+            };
+            auto load_h = [&](int i, const FromH& o) {
+                if (gw + GW * i < o.units) {
+                    v[i] = dec::ldg_cg16(p.hi + o.at + 32 * (gw + GW * i));
+                    lo[i] = dec::ldg_cg16(p.lo + o.at + 32 * (gw + GW * i));
+                }
+            };
+            int j = (group + q) & 1;  // chunks that are even in the whole list are group 0's
+            if (j < chunks) {
+                const FromH o = from_h(j, 0);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int col = 8 * n + 2 * t + c;
-                        if (col < cnt) {
-                            const float w = tab.pw[off + col];
-                            float* o = mine + tab.tok[off + col] * 17 + g;
-                            o[0] += w * acc[n][c];
-                            o[8] += w * acc[n][2 + c];
+                for (int i = 0; i < UNITS; ++i) load_h(i, o);
+            }
+            for (; j < chunks; j += GROUPS) {
+                const int u = j / parts, b = (j - u * parts) * cb2, cnt = tab.ucnt[u], off = tab.uoff[u];
+                const int units = 2 * min(cb2, nb2 - b);
+                const uint32_t slot = ring + ((q + j) % NSLOT) * SLOT;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    if (8 * n < cnt) {
+                        FromH o{0, 0};
+                        if (8 * (n + 1) < cnt) o = from_h(j, n + 1);
+                        else if (j + GROUPS < chunks) o = from_h(j + GROUPS, 0);
+                        if (n == 0) wait(q + j);
+#pragma unroll
+                        for (int i = 0; i < UNITS; ++i) {
+                            const int unit = gw + GW * i, line = (unit >> 1) * tl.n;
+                            if (unit < units) {
+                                const uint4 wa = weights_at(slot, line + ga, unit & 1, t), wb = weights_at(slot, line + gb, unit & 1, t);
+                                mma<BF16>(acc[n], wa, wb, v[i]);
+                                mma<BF16>(acc[n], wa, wb, lo[i]);
+                            }
+                            load_h(i, o);
                         }
                     }
-                __syncwarp();
+                release(q + j);
+                if ((j + GROUPS) / parts != u) {  // the group's last chunk of the expert
+                    // columns 2 t and 2 t + 1, rows g and g + 8, into the tokens' sums
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int col = 8 * n + 2 * t + c;
+                            if (col < cnt) {
+                                const float w = tab.pw[off + col];
+                                float* o = mine + tab.tok[off + col] * 17 + g;
+                                o[0] += w * acc[n][c];
+                                o[8] += w * acc[n][2 + c];
+                            }
+                        }
+                    clear();
+                    __syncwarp();
+                }
             }
             dec::bar_sync(1, CONSUMERS);
             for (int j = threadIdx.x; j < p.T * 16; j += CONSUMERS) {
                 const int tok = j >> 4, row = j & 15;
-                float v = 0.f;
+                float s = 0.f;
 #pragma unroll
                 for (int w = 0; w < CW; ++w) {
                     float* o = sums + (w * p.T + tok) * 17 + row;
-                    v += *o;
+                    s += *o;
                     *o = 0.f;
                 }
-                if (row < tl.n) p.out[(size_t)tok * d + r_lo + tl.r0 + row] = bits16<BF16>(v);
+                if (row < tl.n) p.out[(size_t)tok * d + r_lo + tl.r0 + row] = bits16<BF16>(s);
             }
             dec::bar_sync(1, CONSUMERS);
         }
@@ -421,20 +534,16 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
     }
 }
 
-size_t sums_bytes(int nt, int T) {
-    return std::max<size_t>((size_t)2 * CW * nt * 128, (size_t)CW * T * 17) * sizeof(float);
-}
-
 template <bool BF16, int NT>
-cudaError_t launch(const ExpertLayer& l, const Maps& maps, Params& p, cudaStream_t s) {
-    const size_t other = 1024 + 16 * MAX_SLOTS + align_up(sizeof(Tab), 16) + sums_bytes(NT, l.T);
-    p.nslot = std::min<int>(MAX_SLOTS, (int)((SMEM_MOST - other) / SLOT));
+cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
+    constexpr size_t smem = 1024 + (size_t)slots(NT) * SLOT + BAR_BYTES + sums_bytes(NT) + sizeof(Tab);
+    static_assert(smem <= SMEM_MOST, "shared memory");
     cudaError_t e = allow_smem<expert_layer_kernel<BF16, NT>>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)num_sms());
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = other + (size_t)p.nslot * SLOT;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     // cooperative: the CTAs meet, so all have to be resident; and a programmatic
     // dependent of the kernel before it
@@ -494,9 +603,9 @@ cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s) {
         ok = make_tensor_map_16(&maps.w2[i], bf, l.w2, 4, d2, s2, box);
     }
     if (!ok) return cudaErrorInvalidValue;
-    if (l.T <= 8) return bf ? launch<true, 1>(l, maps, p, s) : launch<false, 1>(l, maps, p, s);
-    if (l.T <= 16) return bf ? launch<true, 2>(l, maps, p, s) : launch<false, 2>(l, maps, p, s);
-    return bf ? launch<true, 4>(l, maps, p, s) : launch<false, 4>(l, maps, p, s);
+    if (l.T <= 8) return bf ? launch<true, 1>(maps, p, s) : launch<false, 1>(maps, p, s);
+    if (l.T <= 16) return bf ? launch<true, 2>(maps, p, s) : launch<false, 2>(maps, p, s);
+    return bf ? launch<true, 4>(maps, p, s) : launch<false, 4>(maps, p, s);
 }
 
 }  // namespace moe

@@ -104,6 +104,10 @@ CASES = [
     (27, 3, 17, 576, 320),
     (8, 32, 64, 64, 128),
     (31, 5, 200, 192, 64),
+    (32, 8, 64, 1088, 320),       # more chunks than slots, one and several groups of 8
+    (12, 4, 16, 1088, 1088),
+    (24, 6, 30, 192, 2112),
+    (14, 3, 7, 64, 192),
 ]
 
 
