@@ -6,27 +6,33 @@
 //
 // What counts is reading the weights of the experts that have a token, once:
 // 6 d f bytes an expert.  One CTA an SM (cooperative); one producer thread streams
-// the CTA's share of both matrices through a ring of 32 KB slots (TMA), eight warps
-// take them from there.  The share of the down projection does not depend on h, so
+// the CTA's share of both matrices through a ring of 24 KB slots (TMA), sixteen
+// warps take them from there.  The share of the down projection does not depend on h, so
 // the ring fills with it while the CTAs meet between the two products: the stream
 // does not stop there.
 //   Phase 0  every CTA routes all tokens and sorts the assignments by expert.
 //   Phase 1  the touched experts' features, one list of n_uniq f, are split evenly
 //            over the CTAs to a single feature (its gate and its up row): tiles of 8,
-//            4, 2 or 1 features, chunks of at most 1024 inputs.  h goes to memory.
+//            4, 2 or 1 features, chunks of at most 768 inputs.  h goes to memory.
 //   Phase 2  output features, split evenly over the CTAs; a CTA goes through all
-//            touched experts for its own, so the weighted sum over experts is its own
-//            as well: no partial sums between CTAs, a fixed order, one rounding.
+//            touched experts for its own, so the sum over experts is its own as well:
+//            no partial sums between CTAs, a fixed order, one rounding.
 // mma.sync m16n8k16 with the weight rows as M (phase 1: 8 features' gate rows and their
 // up rows, so that a thread has both) and an expert's tokens as N, 8 at a time: at a
-// few tokens an expert the tensor rate is no bound.  Both operands keep K in the order
+// few tokens an expert the tensor rate is no bound.  In phase 2 a column is a token
+// (zeros where the expert is not the token's) and h has the weight p already, so the
+// accumulators stay over all experts.  Both operands keep K in the order
 // in which a thread's 16-byte loads bring it, as in grouped_few.cu.
-// What bounds the consumers is latency, a chunk's 0.7 us at the full rate of the stream:
+// What bounds the consumers is latency, a chunk's 0.5 us at the full rate of the stream:
 // two groups of eight warps take every second chunk, its 32-input units dealt out to
-// the warps; the tokens' values of a warp's next chunk are on their way while it has
-// one; and a warp of its own adds the warps' sums up and writes h, so that none of
-// them waits for the others at the end of a tile.
-// h is kept as two 16-bit numbers, the second one the rounding error of the first, so
+// the warps.  In phase 1 a warp has the tokens' values of its next chunk on their way in
+// registers (they stay in L1 from tile to tile); in phase 2, where every chunk brings
+// another expert's, a warp of its own has rows of h copied to a ring of rows in shared
+// memory, a bulk copy each.  (x that way too: 8 tokens at 7168 x 2048 x 256 experts 804
+// against 769 us, 32 at 2048 x 768 x 128 432 against 208; h in registers too: one
+// token's phase 2 5.4 against 4.5 us.)  Another warp adds the sixteen warps' sums up and
+// writes h, so that none of them waits for the others.
+// p h is kept as two 16-bit numbers, the second one the rounding error of the first, so
 // the output is rounded once as if h were fp32; twice the (few) MMAs of phase 2.
 #include "decode_ops.cuh"
 #include "internal.h"
@@ -37,32 +43,40 @@ namespace {
 
 constexpr int MAX_T = 32, MAX_R = 256;
 constexpr int GROUPS = 2, GW = 8, CW = GROUPS * GW;  // consumer warps
-constexpr int CONSUMERS = 32 * CW, THREADS = CONSUMERS + 64;
-constexpr int PRODUCER = CW, FINISHER = CW + 1;      // warps
-constexpr int SLOT = 32768;
-constexpr int BLOCKS = 16;                   // most 64-input blocks of a chunk
-constexpr int UNITS = 2 * BLOCKS / GW;       // most 32-input units of a chunk for a warp
-constexpr int SORTERS = 256;
-static_assert(MAX_R <= SORTERS, "one thread an assignment");
-// Slots of the ring and buffers for the warps' sums (of 8 tokens each), by NT.  Both
-// are multiples of the groups, so that a slot is always one group's: a wait names a
-// round of its barrier by the round's parity, and a group that took every second round
-// of a slot would take the end of the round before for that of its own.
-constexpr int slots(int nt) { return nt <= 2 ? 6 : 4; }
-constexpr int buffers(int nt) { return nt <= 2 ? 2 : 4; }
-constexpr int SUM_FLOATS = CW * 128;         // of a buffer: [CW][32][4]
-constexpr size_t sums_bytes(int nt) {        // phase 1: the buffers; phase 2: [CW][T][17]
-    return std::max<size_t>((size_t)buffers(nt) * SUM_FLOATS, (size_t)CW * 8 * nt * 17) * sizeof(float);
-}
-constexpr int BAR_BYTES = 256;
+constexpr int CONSUMERS = 32 * CW, THREADS = CONSUMERS + 96;
+constexpr int PRODUCER = CW, ROWS_OF_H = CW + 1, FINISHER = CW + 2;  // warps
+// By NT, the most groups of 8 tokens of an expert.  Slots of the ring, chunks whose rows
+// are under way and buffers of sums are multiples of the groups, so that each is always
+// one group's: a wait names a round of its barrier by the round's parity, and a group
+// that took every second round of a slot would take the end of the round before for
+// that of its own.
+template <int NT>
+struct Plan {
+    // A slot: 8 features' 16 rows of BLOCKS1 64-input blocks, or up to 16 rows of the down
+    // projection.  One token at 2048 x 768: eight slots hold the CTA's share of that.
+    static constexpr int BLOCKS1 = NT <= 2 ? 11 : 8, BLOCKS2 = NT <= 2 ? 12 : 6;
+    static constexpr int SLOT = 16 * BLOCKS1 * 128, NSLOT = NT == 2 ? 6 : 8;
+    static constexpr int UNITS1 = (2 * BLOCKS1 + GW - 1) / GW, UNITS2 = (2 * BLOCKS2 + GW - 1) / GW;  // of 32 inputs, a warp's most
+    // A row of h, 256 bytes for 64 inputs; 64 more, so that neighbours use other banks.
+    static constexpr int PITCH = BLOCKS2 * 256 + 64, NROW = NT <= 2 ? 8 * NT : 32, NCHUNK = 8;
+    static constexpr int NBUF = 2, SUM_FLOATS = CW * 128;        // sums of 8 tokens: [CW][32][4]
+    // phase 2: [CW][8 NT][17]
+    static constexpr int SUMS = 4 * (NBUF * SUM_FLOATS > CW * 8 * NT * 17 ? NBUF * SUM_FLOATS : CW * 8 * NT * 17);
+    static constexpr int BARS = 16 * (NSLOT + NCHUNK + NBUF) + 16;
+    static constexpr int OFF_BARS = NSLOT * SLOT, OFF_ROWS = OFF_BARS + 512, OFF_SUMS = OFF_ROWS + NROW * PITCH;
+    static constexpr int OFF_TAB = OFF_SUMS + SUMS;
+    static_assert(NROW >= 8 * NT && BARS <= 512, "an expert's rows, the barriers");
+    static_assert(NSLOT % GROUPS == 0 && NCHUNK % GROUPS == 0 && SLOT % 1024 == 0 && PITCH % 128 == 64, "layout");
+};
 
 struct Tab {
     int ids[MAX_R];
     float w[MAX_R];
-    int first[MAX_R];
     int tok[MAX_R];      // by sorted position: token
     float pw[MAX_R];     // and weight
-    int uexp[MAX_R], uoff[MAX_R], ucnt[MAX_R];  // touched experts, ascending: id, first position, tokens
+    int uexp[MAX_R], uoff[MAX_R], ucnt[MAX_R];  // touched experts, ascending: id, first position, how many tokens
+    uint32_t utok[MAX_R];                       // and which, one bit a token
+    uint32_t warp_sums[CW];
     int n_uniq, abort;
 };
 
@@ -71,7 +85,7 @@ struct Params {
     const float* logits;
     uint16_t* out;
     int32_t* ids_out;
-    uint16_t *hi, *lo;   // h by sorted position, [R][f] each
+    uint16_t* h;         // p h by sorted position, [R][f / 64][2][64]: 64 values, then their rounding errors
     uint32_t* err;
     unsigned long long* bar_count;
     int T, k, E, d, f;
@@ -103,8 +117,11 @@ __device__ __forceinline__ float value16(uint16_t b) {
     return BF16 ? __uint_as_float((uint32_t)b << 16) : half_bits_to_float(b);
 }
 
-// Part c of `parts` of n things: [share(c), share(c + 1)).
-__device__ __forceinline__ int share(int n, int c, int parts) { return (int)((long long)n * c / parts); }
+// Between ordinary accesses to global memory and bulk copies of it.
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// Part c of `parts` of n things: [share(c), share(c + 1)); n parts is below 2^32.
+__device__ __forceinline__ int share(int n, int c, int parts) { return (int)((uint32_t)n * (uint32_t)c / (uint32_t)parts); }
 
 // Phase 1: the tile at feature x of the list, of those before `end`: expert u,
 // features i0 .. i0 + n - 1, box of map m (n = 8 >> m).
@@ -136,14 +153,14 @@ __device__ __forceinline__ uint4 weights_at(uint32_t slot, int line, int half, i
 
 // Where a group is in phase 1's list of chunks.
 struct Place1 {
-    int x, b, q;                // tile's first feature, chunk's first block; chunks before
-    int r0, r1;                 // sums before; of tiles of one chunk: of either group
-    int i0, n, m, cnt, off;     // of the tile
+    int x, b, q;         // tile's first feature, chunk's first block; chunks before
+    int i0, n, cnt, off; // of the tile
+    __device__ Place1(const Tab& tab, int x_, int end, int f) : x(x_), b(0), q(0), i0(0), n(0), cnt(0), off(0) { tile(tab, end, f); }
     __device__ void tile(const Tab& tab, int end, int f) {
+        if (x >= end) return;
         const Tile1 t(x, end, f);
         i0 = t.i0;
         n = t.n;
-        m = t.m;
         cnt = tab.ucnt[t.u];
         off = tab.uoff[t.u];
     }
@@ -152,44 +169,27 @@ struct Place1 {
         ++q;
         if ((b += cb) < nb) return;
         b = 0;
-        if (cb < nb || (q & 1)) r0 += ceil_div(cnt, 8);  // (the chunk was q - 1)
-        else r1 += ceil_div(cnt, 8);
         x += n;
-        if (x < end) tile(tab, end, f);
+        tile(tab, end, f);
     }
 };
 
-// The buffer of sum n of a group's tile and the parity of its round: any buffer in
-// turn where all warps have a part of every tile, else one of the group's.
-template <int NBUF>
-struct SumAt {
-    int buf;
-    uint32_t parity;
-    __device__ SumAt(const Place1& c, int n, int group, bool one_chunk) {
-        constexpr int EACH = NBUF / GROUPS;
-        const int k = n + (one_chunk && group ? c.r1 : c.r0);
-        buf = one_chunk ? group * EACH + k % EACH : k % NBUF;
-        parity = (uint32_t)(one_chunk ? k / EACH : k / NBUF) & 1u;
-    }
-};
-
-// NT: most groups of 8 tokens of an expert.
 template <bool BF16, int NT>
 __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_constant__ Maps maps, const Params p) {
-    constexpr int NSLOT = slots(NT), NBUF = buffers(NT);
+    using L = Plan<NT>;
+    constexpr int NSLOT = L::NSLOT, NCHUNK = L::NCHUNK, NROW = L::NROW, NBUF = L::NBUF;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    const uint32_t ring = smem_u32(sm), full = ring + NSLOT * SLOT, empty = full + 8 * NSLOT;
-    const uint32_t sum_full = empty + 8 * NSLOT, sum_empty = sum_full + 8 * NBUF, h_ready = sum_empty + 8 * NBUF;
-    static_assert(16 * NSLOT + 16 * NBUF + 8 <= BAR_BYTES, "barrier area too small");
-    static_assert(NSLOT % GROUPS == 0 && NBUF % GROUPS == 0, "a slot and a buffer are one group's");
-    float* sums = reinterpret_cast<float*>(sm + NSLOT * SLOT + BAR_BYTES);
-    Tab& tab = *reinterpret_cast<Tab*>(sm + NSLOT * SLOT + BAR_BYTES + sums_bytes(NT));
+    const uint32_t ring = smem_u32(sm), rows_at = ring + L::OFF_ROWS;
+    const uint32_t full = ring + L::OFF_BARS, empty = full + 8 * NSLOT;                  // slots
+    const uint32_t row_full = empty + 8 * NSLOT, row_empty = row_full + 8 * NCHUNK;      // rows of a chunk
+    const uint32_t sum_full = row_empty + 8 * NCHUNK, sum_empty = sum_full + 8 * NBUF, h_ready = sum_empty + 8 * NBUF;
+    float* sums = reinterpret_cast<float*>(sm + L::OFF_SUMS);
+    Tab& tab = *reinterpret_cast<Tab*>(sm + L::OFF_TAB);
     volatile int* abort_flag = &tab.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int R = p.T * p.k, d = p.d, f = p.f, G = gridDim.x, cta = blockIdx.x;
     const int nb1 = d / 64, nb2 = f / 64, cb1 = p.cb1, cb2 = p.cb2;
-    const bool one_chunk = cb1 >= nb1;  // a tile of phase 1 is one group's
 
     // ------------------------------------------------ phase 0: init, routing
     if (threadIdx.x == 0) tab.abort = 0;
@@ -198,8 +198,12 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             tc::mbar_init(full + 8 * i, 1);
             tc::mbar_init(empty + 8 * i, GW);
         }
+        for (int i = 0; i < NCHUNK; ++i) {
+            tc::mbar_init(row_full + 8 * i, 1);
+            tc::mbar_init(row_empty + 8 * i, GW);
+        }
         for (int i = 0; i < NBUF; ++i) {
-            tc::mbar_init(sum_full + 8 * i, one_chunk ? GW : CW);
+            tc::mbar_init(sum_full + 8 * i, CW);
             tc::mbar_init(sum_empty + 8 * i, 1);
         }
         tc::mbar_init(h_ready, 1);
@@ -209,6 +213,12 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             tc::tma_prefetch_desc(&maps.w2[i]);
         }
     }
+    // in the ring's space, which is idle: by expert, its tokens (one bit each) and their
+    // first position
+    uint32_t* tokens = reinterpret_cast<uint32_t*>(sm);
+    int* first = reinterpret_cast<int*>(sm) + p.E;
+    static_assert(8 * 1024 <= NSLOT * L::SLOT, "1024 experts");
+    for (int i = threadIdx.x; i < p.E; i += THREADS) tokens[i] = 0;
     if (warp == FINISHER) {  // a hint, which returns no value: before the kernel ahead is complete
         const int lines = (p.T * p.E * 4 + 127) / 128;
         for (int i = lane; i < lines; i += 32)
@@ -216,55 +226,76 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
     }
     // global memory is read and written from here on
     grid_dependency_wait();
-    if (warp < CW) {
-        for (int t = warp; t < p.T; t += CW)
+    __syncthreads();
+    if (warp < CW)
+        for (int t = warp; t < p.T; t += CW) {
             dec::route_token(p.logits + (size_t)t * p.E, p.E, p.k, &tab.ids[t * p.k], &tab.w[t * p.k]);
-        dec::bar_sync(1, CONSUMERS);
+            if (lane < p.k) {
+                const int e = tab.ids[t * p.k + lane];
+                // logits that are no numbers may choose no expert
+                if ((unsigned)e < (unsigned)p.E) atomicOr(&tokens[e], 1u << t);
+                else set_error(p.err, ERRBIT_RANGE);
+                if (cta == 0 && p.ids_out) p.ids_out[t * p.k + lane] = e;
+            }
+        }
+    __syncthreads();
+    // The touched experts in ascending order: places and positions before each, packed
+    // in one sum; two experts a thread.
+    uint32_t mask[2] = {0, 0}, mine = 0, before = 0;
+    if (warp < CW) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = 2 * threadIdx.x + i;
+            if (e < p.E) mask[i] = tokens[e];
+            mine += mask[i] ? 1u + ((uint32_t)__popc(mask[i]) << 16) : 0u;
+        }
+        before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        if (lane == 31) tab.warp_sums[warp] = before;
     }
-    if (threadIdx.x < SORTERS) {
-        // Stable counting sort by expert, one thread an assignment.  An id out of
-        // range (logits that are no numbers) has no expert.
-        const int a = threadIdx.x;
-        const int ea = a < R ? tab.ids[a] : INT_MAX;
-        const bool va = (unsigned)ea < (unsigned)p.E;
-        int lt = 0, before = 0, all = 0;
-        for (int b = 0; b < R; ++b) {
-            const int eb = tab.ids[b];
-            const bool vb = (unsigned)eb < (unsigned)p.E;
-            lt += vb && eb < ea;
-            all += eb == ea;
-            before += eb == ea && b < a;
+    __syncthreads();
+    if (warp < CW) {
+        const uint32_t v = lane < CW ? tab.warp_sums[lane] : 0;
+        before += __reduce_add_sync(0xffffffffu, lane < warp ? v : 0) - mine;
+        if (warp == 0) {
+            const uint32_t all = __reduce_add_sync(0xffffffffu, v);
+            if (lane == 0) tab.n_uniq = all & 0xffff;
         }
-        const bool first = va && before == 0;
-        tab.first[a] = first;
-        if (a < R && !va) set_error(p.err, ERRBIT_RANGE);
-        dec::bar_sync(2, SORTERS);
-        int ui = 0, nu = 0;
-        for (int b = 0; b < R; ++b) {
-            const int fb = tab.first[b];
-            nu += fb;
-            ui += fb && tab.ids[b] < ea;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (mask[i]) {
+                const int u = before & 0xffff, e = 2 * threadIdx.x + i, cnt = __popc(mask[i]);
+                tab.uexp[u] = e;
+                tab.uoff[u] = first[e] = before >> 16;
+                tab.ucnt[u] = cnt;
+                tab.utok[u] = mask[i];
+                before += 1u + ((uint32_t)cnt << 16);
+            }
+        dec::bar_sync(1, CONSUMERS);
+        for (int a = threadIdx.x; a < R; a += CONSUMERS) {
+            const int e = tab.ids[a], t = a / p.k;
+            if ((unsigned)e < (unsigned)p.E) {
+                const int at = first[e] + __popc(tokens[e] & ((1u << t) - 1u));
+                tab.tok[at] = t;
+                tab.pw[at] = tab.w[a];
+            }
         }
-        if (va) {
-            tab.tok[lt + before] = a / p.k;
-            tab.pw[lt + before] = tab.w[a];
-        }
-        if (first) {
-            tab.uexp[ui] = ea;
-            tab.uoff[ui] = lt;
-            tab.ucnt[ui] = all;
-        }
-        if (a == 0) tab.n_uniq = nu;
-        if (cta == 0 && p.ids_out && a < R) p.ids_out[a] = tab.ids[a];
+        tc::fence_proxy_async_smem();  // before the copies into the ring
     }
     __syncthreads();
 
     const int n_uniq = tab.n_uniq;
     const int x_lo = share(n_uniq * f, cta, G), x_hi = share(n_uniq * f, cta + 1, G);
     const int r_lo = share(d, cta, G), rows = share(d, cta + 1, G) - r_lo, tiles2 = ceil_div(rows, 16);
+    // A wait that gave up goes on with what is there: no arrival and no barrier is left
+    // out, and every address stays where it was.
 
     if (warp == PRODUCER) {
-        // ---------------------------------------------------------- producer
+        // -------------------------------------------------- weights, by TMA
         if (tc::elect_one()) {
             int s = 0;
             uint32_t phase = 1;
@@ -287,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                     asm volatile(
                         "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
                         " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];"
-                        :: "r"(ring + s * SLOT), "l"(&maps.w13[t.m]), "r"(full + 8 * s), "r"(0), "r"(t.i0), "r"(b), "r"(e) : "memory");
+                        :: "r"(ring + s * L::SLOT), "l"(&maps.w13[t.m]), "r"(full + 8 * s), "r"(0), "r"(t.i0), "r"(b), "r"(e) : "memory");
                 x += t.n;
             }
             for (int i = 0; ok && i < tiles2; ++i) {
@@ -296,26 +327,54 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                 for (int u = 0; ok && u < n_uniq; ++u) {
                     const int e = tab.uexp[u];
                     for (int b = 0; b < nb2 && next(cb2 * t.n * 128); b += cb2, advance())
-                        tc::tma_load_4d(ring + s * SLOT, &maps.w2[m], full + 8 * s, 0, r_lo + t.r0, b, e);
+                        tc::tma_load_4d(ring + s * L::SLOT, &maps.w2[m], full + 8 * s, 0, r_lo + t.r0, b, e);
                 }
             }
         }
         __syncwarp();
+    } else if (warp == ROWS_OF_H) {
+        // ------------------- the tokens' rows of h of the chunks, a lane a bulk copy
+        int q = 0, tail = 0, used = 0, at = 0, cnt_of = 0;  // cnt_of: lane i: rows of chunk i (mod NCHUNK)
+        bool ok = __all_sync(0xffffffffu, tc::mbar_wait(h_ready, 0, abort_flag, p.err));
+        fence_proxy_async_global();  // h was written by ordinary stores
+        for (int i = 0; ok && i < tiles2; ++i)
+            for (int u = 0; ok && u < n_uniq; ++u) {
+                const int cnt = tab.ucnt[u];
+                const uint16_t* src = p.h + (size_t)(tab.uoff[u] + lane) * (2 * f);
+                for (int b = 0; b < nb2; b += cb2, ++q) {
+                    while (ok && (q - tail >= NCHUNK || used + cnt > NROW)) {
+                        ok = tc::mbar_wait(row_empty + 8 * (tail % NCHUNK), (uint32_t)(tail / NCHUNK) & 1u, abort_flag, p.err);
+                        ok = __all_sync(0xffffffffu, ok);
+                        used -= __shfl_sync(0xffffffffu, cnt_of, tail % NCHUNK);
+                        ++tail;
+                    }
+                    if (!ok) break;  // nothing is copied after a wait that gave up
+                    if (lane == q % NCHUNK) cnt_of = cnt;
+                    used += cnt;
+                    const uint32_t bytes = 256 * min(cb2, nb2 - b), bar = row_full + 8 * (q % NCHUNK);
+                    if (lane == 0) tc::mbar_arrive_expect_tx(bar, cnt * bytes);
+                    __syncwarp();
+                    const int r = at + lane;
+                    if (lane < cnt) tc::bulk_load(rows_at + (r >= NROW ? r - NROW : r) * L::PITCH, src + 128 * b, bytes, bar);
+                    at += cnt;
+                    if (at >= NROW) at -= NROW;
+                }
+            }
     } else if (warp == FINISHER) {
         // --------------------- phase 1's sums: h = SiLU(gate) up, two columns a lane
         const int g = lane >> 2, t = lane & 3;
-        Place1 c{x_lo};
-        if (c.x < x_hi) c.tile(tab, x_hi, f);
-        while (c.x < x_hi) {
-            const int group = c.q & 1, w0 = one_chunk ? group * GW : 0, w1 = one_chunk ? w0 + GW : CW;
-            for (int n = 0; 8 * n < c.cnt; ++n) {
-                const SumAt<NBUF> at(c, n, group, one_chunk);
-                const int buf = at.buf;
-                tc::mbar_wait(sum_full + 8 * buf, at.parity, abort_flag, p.err);
+        int k = 0;
+        for (int x = x_lo; x < x_hi;) {
+            const Tile1 tl(x, x_hi, f);
+            const int cnt = tab.ucnt[tl.u], off = tab.uoff[tl.u];
+            for (int n = 0; 8 * n < cnt; ++n, ++k) {
+                const int buf = k % NBUF;
+                tc::mbar_wait(sum_full + 8 * buf, (uint32_t)(k / NBUF) & 1u, abort_flag, p.err);
                 __syncwarp();
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int w = w0; w < w1; ++w) {
-                    const float4 o = *reinterpret_cast<const float4*>(sums + buf * SUM_FLOATS + (w * 32 + lane) * 4);
+#pragma unroll
+                for (int w = 0; w < CW; ++w) {
+                    const float4 o = *reinterpret_cast<const float4*>(sums + buf * L::SUM_FLOATS + (w * 32 + lane) * 4);
                     v.x += o.x;
                     v.y += o.y;
                     v.z += o.z;
@@ -326,22 +385,24 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int col = 8 * n + 2 * t + i;
-                    if (g < c.n && col < c.cnt) {
+                    if (g < tl.n && col < cnt) {
                         const float a = i ? v.y : v.x, u = i ? v.w : v.z;
-                        const float h = a / (1.f + expf(-a)) * u;
+                        const float h = tab.pw[off + col] * (a / (1.f + expf(-a)) * u);
                         const uint16_t hi = bits16<BF16>(h);
                         const float rest = h - value16<BF16>(hi);
-                        const size_t to = (size_t)(c.off + col) * f + c.i0 + g;
-                        p.hi[to] = hi;
-                        p.lo[to] = bits16<BF16>(isfinite(rest) ? rest : 0.f);
+                        const int i = tl.i0 + g;
+                        uint16_t* to = p.h + ((size_t)(off + col) * nb2 + (i >> 6)) * 128 + (i & 63);
+                        to[0] = hi;
+                        to[64] = bits16<BF16>(isfinite(rest) ? rest : 0.f);
                     }
                 }
             }
-            for (int b = 0; b < nb1; b += cb1) c.step(tab, x_hi, f, nb1, cb1);
+            x += tl.n;
         }
         // Every CTA's h is written before anyone reads it.  The arrival count only
         // grows, G a launch, so a CTA's own arrival tells it the count at which this
         // launch's barrier opens.
+        fence_proxy_async_global();  // it is read by bulk copies
         __syncwarp();
         if (lane == 0) {
             const uint64_t old = dec::atom_add_release_gpu(p.bar_count, 1ull);
@@ -359,7 +420,6 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             tc::mbar_arrive(h_ready);
         }
         __syncwarp();
-        grid_dependency_launch();
     } else {
         // --------------------------------------------------------- consumers
         const int g = lane >> 2, t = lane & 3, group = warp / GW, gw = warp % GW;
@@ -368,21 +428,15 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
         };
+        auto wait = [&](int q) { tc::mbar_wait(full + 8 * (q % NSLOT), (uint32_t)(q / NSLOT) & 1u, abort_flag, p.err); };
         auto release = [&](int q) {
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(empty + 8 * (q % NSLOT));
         };
-        auto wait = [&](int q) { tc::mbar_wait(full + 8 * (q % NSLOT), (uint32_t)(q / NSLOT) & 1u, abort_flag, p.err); };
-        // A wait that gave up goes on with what is in the slot: no barrier is left out,
-        // and every address stays where it was.
-
-        // ---- phase 1
-        Place1 c{x_lo};
-        if (c.x < x_hi) c.tile(tab, x_hi, f);
-        if (group) c.step(tab, x_hi, f, nb1, cb1);
-        // Units gw, gw + GW, ... of a chunk are this warp's.  As soon as the MMAs have a
-        // unit's values, those of the warp's next chunk (or next 8 tokens) take their place.
-        uint4 v[UNITS];
+        // ---- phase 1.  Units gw, gw + GW, ... of a chunk are this warp's.  As soon as the
+        // MMAs have a unit's values, those of the warp's next chunk (or next 8 tokens)
+        // take their place.
+        uint4 v[L::UNITS1];
         struct From {
             const uint16_t* x;
             int units;
@@ -393,18 +447,39 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
         auto load = [&](int i, const From& o) {
             if (gw + GW * i < o.units) v[i] = __ldg(reinterpret_cast<const uint4*>(o.x + 32 * (gw + GW * i)));
         };
+        // every warp has a part of every sum, though it may be zero
+        int k = 0;
+        auto add_up = [&](int cnt) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (8 * n < cnt) {
+                    const int buf = k % NBUF;
+                    tc::mbar_wait(sum_empty + 8 * buf, ((uint32_t)(k / NBUF) & 1u) ^ 1u, abort_flag, p.err);
+                    *reinterpret_cast<float4*>(sums + buf * L::SUM_FLOATS + (warp * 32 + lane) * 4) =
+                        make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(sum_full + 8 * buf);
+                    ++k;
+                }
+            clear();
+        };
+        Place1 c(tab, x_lo, x_hi, f);
         clear();
+        const int first = c.x, first_cnt = c.cnt;
+        if (group) c.step(tab, x_hi, f, nb1, cb1);
+        if (c.x != first) add_up(first_cnt);  // the first tile was the other group's
         if (c.x < x_hi) {
             const From o = from(c, 0);
 #pragma unroll
-            for (int i = 0; i < UNITS; ++i) load(i, o);
+            for (int i = 0; i < L::UNITS1; ++i) load(i, o);
         }
         while (c.x < x_hi) {
-            Place1 to = c;
-            to.step(tab, x_hi, f, nb1, cb1);
+            Place1 mid = c;
+            mid.step(tab, x_hi, f, nb1, cb1);
+            Place1 to = mid;
             to.step(tab, x_hi, f, nb1, cb1);
             const int units = 2 * min(cb1, nb1 - c.b), gf = min(g, c.n - 1);  // rows beyond the tile's: its last again
-            const uint32_t slot = ring + (c.q % NSLOT) * SLOT;
+            const uint32_t slot = ring + (c.q % NSLOT) * L::SLOT;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 if (8 * n < c.cnt) {
@@ -413,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                     else if (to.x < x_hi) o = from(to, 0);
                     if (n == 0) wait(c.q);
 #pragma unroll
-                    for (int i = 0; i < UNITS; ++i) {
+                    for (int i = 0; i < L::UNITS1; ++i) {
                         const int unit = gw + GW * i, line = (unit >> 1) * 2 * c.n + gf;
                         if (unit < units)
                             mma<BF16>(acc[n], weights_at(slot, line, unit & 1, t), weights_at(slot, line + c.n, unit & 1, t), v[i]);
@@ -421,107 +496,82 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                     }
                 }
             release(c.q);
-            if (to.x != c.x) {  // this group's last chunk of the tile
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    if (8 * n < c.cnt) {
-                        const SumAt<NBUF> at(c, n, group, one_chunk);
-                        const int buf = at.buf;
-                        tc::mbar_wait(sum_empty + 8 * buf, at.parity ^ 1u, abort_flag, p.err);
-                        *reinterpret_cast<float4*>(sums + buf * SUM_FLOATS + (warp * 32 + lane) * 4) =
-                            make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(sum_full + 8 * buf);
-                    }
-                clear();
-            }
+            if (mid.x != c.x) add_up(c.cnt);
+            if (to.x != mid.x) add_up(mid.cnt);  // this one's, or a tile that was the other group's
             c = to;
         }
+        int q = c.q, q2 = 0, at = 0;  // chunks, chunks of phase 2, rows (mod NROW) before
 
         // ---- phase 2
         tc::mbar_wait(h_ready, 0, abort_flag, p.err);
         grid_dependency_launch();  // the last phase: the next kernel may be scheduled
-        float* mine = sums + warp * p.T * 17;
-        for (int i = lane; i < p.T * 17; i += 32) mine[i] = 0.f;
-        __syncwarp();
-        int q = c.q;  // all of phase 1
-        const int parts = ceil_div(nb2, cb2), chunks = n_uniq * parts;
-        uint4 lo[UNITS];
-        for (int i = 0; i < tiles2; ++i, q += chunks) {
+        // accumulators: 8 tokens each, several so that few MMAs wait for the one before
+        constexpr int SETS = NT == 1 ? 4 : 2;
+        float out[SETS][NT][4];
+        for (int i = 0; i < tiles2; ++i) {
             const Tile2 tl(rows, tiles2, i);
-            const int ga = min(g, tl.n - 1), gb = min(g + 8, tl.n - 1);
-            struct FromH {
-                size_t at;
-                int units;
-            };
-            auto from_h = [&](int j, int n) {
-                const int u = j / parts, b = (j - u * parts) * cb2;
-                return FromH{(size_t)(tab.uoff[u] + min(8 * n + g, tab.ucnt[u] - 1)) * f + 64 * b + 8 * t, 2 * min(cb2, nb2 - b)};
-            };
-            auto load_h = [&](int i, const FromH& o) {
-                if (gw + GW * i < o.units) {
-                    v[i] = dec::ldg_cg16(p.hi + o.at + 32 * (gw + GW * i));
-                    lo[i] = dec::ldg_cg16(p.lo + o.at + 32 * (gw + GW * i));
-                }
-            };
-            int j = (group + q) & 1;  // chunks that are even in the whole list are group 0's
-            if (j < chunks) {
-                const FromH o = from_h(j, 0);
+            const int ga = min(g, tl.n - 1), gb = min(g + 8, tl.n - 1);  // rows beyond the tile's: its last again
 #pragma unroll
-                for (int i = 0; i < UNITS; ++i) load_h(i, o);
-            }
-            for (; j < chunks; j += GROUPS) {
-                const int u = j / parts, b = (j - u * parts) * cb2, cnt = tab.ucnt[u], off = tab.uoff[u];
-                const int units = 2 * min(cb2, nb2 - b);
-                const uint32_t slot = ring + ((q + j) % NSLOT) * SLOT;
+            for (int s = 0; s < SETS; ++s)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    if (8 * n < cnt) {
-                        FromH o{0, 0};
-                        if (8 * (n + 1) < cnt) o = from_h(j, n + 1);
-                        else if (j + GROUPS < chunks) o = from_h(j + GROUPS, 0);
-                        if (n == 0) wait(q + j);
+                for (int n = 0; n < NT; ++n) out[s][n][0] = out[s][n][1] = out[s][n][2] = out[s][n][3] = 0.f;
+            for (int u = 0; u < n_uniq; ++u) {
+                const int cnt = tab.ucnt[u];
+                const uint32_t toks = tab.utok[u];
+                for (int b = 0; b < nb2; b += cb2, ++q, ++q2) {
+                    if ((q & 1) == group) {
+                        const int units = 2 * min(cb2, nb2 - b);
+                        const uint32_t slot = ring + (q % NSLOT) * L::SLOT;
+                        // this lane's column of every 8 tokens: its row, if it has one
+                        uint32_t has[NT], row[NT];
 #pragma unroll
-                        for (int i = 0; i < UNITS; ++i) {
+                        for (int n = 0; n < NT; ++n) {
+                            has[n] = toks >> (8 * n + g) & 1u;
+                            const int r = at + (has[n] ? __popc(toks & ((1u << (8 * n + g)) - 1u)) : 0);
+                            row[n] = rows_at + (r >= NROW ? r - NROW : r) * L::PITCH + 16 * t;
+                        }
+                        wait(q);
+                        tc::mbar_wait(row_full + 8 * (q2 % NCHUNK), (uint32_t)(q2 / NCHUNK) & 1u, abort_flag, p.err);
+#pragma unroll
+                        for (int i = 0; i < L::UNITS2; ++i) {
                             const int unit = gw + GW * i, line = (unit >> 1) * tl.n;
                             if (unit < units) {
                                 const uint4 wa = weights_at(slot, line + ga, unit & 1, t), wb = weights_at(slot, line + gb, unit & 1, t);
-                                mma<BF16>(acc[n], wa, wb, v[i]);
-                                mma<BF16>(acc[n], wa, wb, lo[i]);
+                                const uint32_t from = 256 * (unit >> 1) + 64 * (unit & 1);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    if (NT == 1 || (toks >> (8 * n) & 255u)) {
+                                        const uint4 hi = dec::lds128_if(row[n] + from, has[n]);
+                                        const uint4 lo = dec::lds128_if(row[n] + from + 128, has[n]);
+                                        mma<BF16>(out[NT == 1 ? 2 * (i & 1) : 0][n], wa, wb, hi);
+                                        mma<BF16>(out[NT == 1 ? 2 * (i & 1) + 1 : 1][n], wa, wb, lo);
+                                    }
                             }
-                            load_h(i, o);
                         }
+                        release(q);
+                        if (lane == 0) tc::mbar_arrive(row_empty + 8 * (q2 % NCHUNK));
                     }
-                release(q + j);
-                if ((j + GROUPS) / parts != u) {  // the group's last chunk of the expert
-                    // columns 2 t and 2 t + 1, rows g and g + 8, into the tokens' sums
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int col = 8 * n + 2 * t + c;
-                            if (col < cnt) {
-                                const float w = tab.pw[off + col];
-                                float* o = mine + tab.tok[off + col] * 17 + g;
-                                o[0] += w * acc[n][c];
-                                o[8] += w * acc[n][2 + c];
-                            }
-                        }
-                    clear();
-                    __syncwarp();
+                    at += cnt;
+                    if (at >= NROW) at -= NROW;
                 }
             }
+            // columns 2 t and 2 t + 1, rows g and g + 8
+            float* mine = sums + warp * (8 * NT * 17);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v = out[0][n][c] + out[1][n][c];
+                    if (SETS == 4) v += out[SETS - 2][n][c] + out[SETS - 1][n][c];
+                    mine[(8 * n + 2 * t + (c & 1)) * 17 + g + 4 * (c & 2)] = v;
+                }
             dec::bar_sync(1, CONSUMERS);
             for (int j = threadIdx.x; j < p.T * 16; j += CONSUMERS) {
-                const int tok = j >> 4, row = j & 15;
-                float s = 0.f;
+                const int tok = j >> 4, r = j & 15;
+                float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < CW; ++w) {
-                    float* o = sums + (w * p.T + tok) * 17 + row;
-                    s += *o;
-                    *o = 0.f;
-                }
-                if (row < tl.n) p.out[(size_t)tok * d + r_lo + tl.r0 + row] = bits16<BF16>(s);
+                for (int w = 0; w < CW; ++w) v += sums[(w * 8 * NT + tok) * 17 + r];
+                if (r < tl.n) p.out[(size_t)tok * d + r_lo + tl.r0 + r] = bits16<BF16>(v);
             }
             dec::bar_sync(1, CONSUMERS);
         }
@@ -536,7 +586,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
 
 template <bool BF16, int NT>
 cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
-    constexpr size_t smem = 1024 + (size_t)slots(NT) * SLOT + BAR_BYTES + sums_bytes(NT) + sizeof(Tab);
+    constexpr size_t smem = 1024 + Plan<NT>::OFF_TAB + sizeof(Tab);
     static_assert(smem <= SMEM_MOST, "shared memory");
     cudaError_t e = allow_smem<expert_layer_kernel<BF16, NT>>();
     if (e != cudaSuccess) return e;
@@ -572,8 +622,7 @@ cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s) {
     p.logits = l.logits;
     p.out = static_cast<uint16_t*>(l.out);
     p.ids_out = l.ids_out;
-    p.hi = l.h;
-    p.lo = l.h + (size_t)l.T * l.k * l.f;
+    p.h = l.h;
     p.err = l.header;
     p.bar_count = reinterpret_cast<unsigned long long*>(l.header + WS_BAR_COUNT_WORD);
     p.T = l.T;
@@ -581,9 +630,20 @@ cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s) {
     p.E = l.E;
     p.d = l.d;
     p.f = l.f;
-    // chunks of as many 64-input blocks each, at most BLOCKS
-    p.cb1 = ceil_div(l.d / 64, ceil_div(l.d / 64, BLOCKS));
-    p.cb2 = ceil_div(l.f / 64, ceil_div(l.f / 64, BLOCKS));
+    // a CTA has q or q + 1 output features, in tiles of at most two sizes each
+    const int q = l.d / num_sms();
+    int rows2 = 1;
+    for (int i = 0; i < 4; ++i) {
+        const int rows = std::max(1, q + (i & 1)), tiles = ceil_div(rows, 16);
+        p.rows2[i] = i < 2 ? rows / tiles : ceil_div(rows, tiles);
+        rows2 = std::max(rows2, p.rows2[i]);
+    }
+    // chunks of as many 64-input blocks each, as fit a slot
+    const bool few = l.T <= 16;
+    const int most1 = few ? Plan<1>::BLOCKS1 : Plan<4>::BLOCKS1;
+    const int most2 = std::min(few ? Plan<1>::BLOCKS2 : Plan<4>::BLOCKS2, 16 * most1 / rows2);
+    p.cb1 = ceil_div(l.d / 64, ceil_div(l.d / 64, most1));
+    p.cb2 = ceil_div(l.f / 64, ceil_div(l.f / 64, most2));
     Maps maps;
     bool ok = true;
     // gate_up as [expert][64-input block][gate, up][feature][64 inputs]
@@ -592,13 +652,9 @@ cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s) {
         const uint32_t box[5] = {64, 8u >> i, 2, (uint32_t)p.cb1, 1};
         ok = make_tensor_map_16(&maps.w13[i], bf, l.w13, 5, d13, s13, box);
     }
-    // down as [expert][64-input block][output feature][64 inputs]; a CTA has q or q + 1 of
-    // them, in tiles of at most two sizes
+    // down as [expert][64-input block][output feature][64 inputs]
     const uint64_t d2[4] = {64, d, f / 64, E}, s2[3] = {2 * f, 128, 2 * d * f};
-    const int q = l.d / num_sms();
     for (int i = 0; i < 4 && ok; ++i) {
-        const int rows = std::max(1, q + (i & 1)), tiles = ceil_div(rows, 16);
-        p.rows2[i] = i < 2 ? rows / tiles : ceil_div(rows, tiles);
         const uint32_t box[4] = {64, (uint32_t)p.rows2[i], (uint32_t)p.cb2, 1};
         ok = make_tensor_map_16(&maps.w2[i], bf, l.w2, 4, d2, s2, box);
     }
