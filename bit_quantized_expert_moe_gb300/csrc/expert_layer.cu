@@ -45,28 +45,29 @@ constexpr int MAX_T = 32, MAX_R = 256;
 constexpr int GROUPS = 2, GW = 8, CW = GROUPS * GW;  // consumer warps
 constexpr int CONSUMERS = 32 * CW, THREADS = CONSUMERS + 96;
 constexpr int PRODUCER = CW, ROWS_OF_H = CW + 1, FINISHER = CW + 2;  // warps
-// By NT, the most groups of 8 tokens of an expert.  Slots of the ring, chunks whose rows
-// are under way and buffers of sums are multiples of the groups, so that each is always
-// one group's: a wait names a round of its barrier by the round's parity, and a group
-// that took every second round of a slot would take the end of the round before for
-// that of its own.
+// By NT, the most groups of 8 tokens of an expert.  The ring's slots are a multiple of
+// the groups, so that each is always one group's: a wait names a round of its barrier by
+// the round's parity, and a group that took every second round of a slot would take the
+// end of the round before for that of its own.
 template <int NT>
 struct Plan {
     // A slot: 8 features' 16 rows of BLOCKS1 64-input blocks, or up to 16 rows of the down
     // projection.  One token at 2048 x 768: eight slots hold the CTA's share of that.
-    static constexpr int BLOCKS1 = NT <= 2 ? 11 : 8, BLOCKS2 = NT <= 2 ? 12 : 6;
-    static constexpr int SLOT = 16 * BLOCKS1 * 128, NSLOT = NT == 2 ? 6 : 8;
+    static constexpr int BLOCKS1 = 11, BLOCKS2 = 12;
+    static constexpr int SLOT = 16 * BLOCKS1 * 128, NSLOT = NT == 1 ? 8 : 6;
     static constexpr int UNITS1 = (2 * BLOCKS1 + GW - 1) / GW, UNITS2 = (2 * BLOCKS2 + GW - 1) / GW;  // of 32 inputs, a warp's most
     // A row of h, 256 bytes for 64 inputs; 64 more, so that neighbours use other banks.
-    static constexpr int PITCH = BLOCKS2 * 256 + 64, NROW = NT <= 2 ? 8 * NT : 32, NCHUNK = 8;
+    // The rows of an expert with tokens beyond the 16th come in two batches.
+    static constexpr int PITCH = BLOCKS2 * 256 + 64, NROW = NT == 1 ? 8 : 16, NBATCH = 8;
+    static constexpr int HALVES = NT <= 2 ? 1 : 2;
     static constexpr int NBUF = 2, SUM_FLOATS = CW * 128;        // sums of 8 tokens: [CW][32][4]
     // phase 2: [CW][8 NT][17]
     static constexpr int SUMS = 4 * (NBUF * SUM_FLOATS > CW * 8 * NT * 17 ? NBUF * SUM_FLOATS : CW * 8 * NT * 17);
-    static constexpr int BARS = 16 * (NSLOT + NCHUNK + NBUF) + 16;
+    static constexpr int BARS = 16 * (NSLOT + GROUPS * NBATCH + NBUF) + 16;
     static constexpr int OFF_BARS = NSLOT * SLOT, OFF_ROWS = OFF_BARS + 512, OFF_SUMS = OFF_ROWS + NROW * PITCH;
     static constexpr int OFF_TAB = OFF_SUMS + SUMS;
-    static_assert(NROW >= 8 * NT && BARS <= 512, "an expert's rows, the barriers");
-    static_assert(NSLOT % GROUPS == 0 && NCHUNK % GROUPS == 0 && SLOT % 1024 == 0 && PITCH % 128 == 64, "layout");
+    static_assert(NROW >= (NT < 2 ? 8 : 16) && BARS <= 512, "a batch's rows, the barriers");
+    static_assert(NSLOT % GROUPS == 0 && SLOT % 1024 == 0 && PITCH % 128 == 64, "layout");
 };
 
 struct Tab {
@@ -177,13 +178,13 @@ struct Place1 {
 template <bool BF16, int NT>
 __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_constant__ Maps maps, const Params p) {
     using L = Plan<NT>;
-    constexpr int NSLOT = L::NSLOT, NCHUNK = L::NCHUNK, NROW = L::NROW, NBUF = L::NBUF;
+    constexpr int NSLOT = L::NSLOT, NBATCH = L::NBATCH, NROW = L::NROW, NBUF = L::NBUF;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t ring = smem_u32(sm), rows_at = ring + L::OFF_ROWS;
     const uint32_t full = ring + L::OFF_BARS, empty = full + 8 * NSLOT;                  // slots
-    const uint32_t row_full = empty + 8 * NSLOT, row_empty = row_full + 8 * NCHUNK;      // rows of a chunk
-    const uint32_t sum_full = row_empty + 8 * NCHUNK, sum_empty = sum_full + 8 * NBUF, h_ready = sum_empty + 8 * NBUF;
+    const uint32_t row_full = empty + 8 * NSLOT, row_empty = row_full + 8 * GROUPS * NBATCH;      // rows of a batch
+    const uint32_t sum_full = row_empty + 8 * GROUPS * NBATCH, sum_empty = sum_full + 8 * NBUF, h_ready = sum_empty + 8 * NBUF;
     float* sums = reinterpret_cast<float*>(sm + L::OFF_SUMS);
     Tab& tab = *reinterpret_cast<Tab*>(sm + L::OFF_TAB);
     volatile int* abort_flag = &tab.abort;
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             tc::mbar_init(full + 8 * i, 1);
             tc::mbar_init(empty + 8 * i, GW);
         }
-        for (int i = 0; i < NCHUNK; ++i) {
+        for (int i = 0; i < GROUPS * NBATCH; ++i) {
             tc::mbar_init(row_full + 8 * i, 1);
             tc::mbar_init(row_empty + 8 * i, GW);
         }
@@ -334,30 +335,48 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
         __syncwarp();
     } else if (warp == ROWS_OF_H) {
         // ------------------- the tokens' rows of h of the chunks, a lane a bulk copy
-        int q = 0, tail = 0, used = 0, at = 0, cnt_of = 0;  // cnt_of: lane i: rows of chunk i (mod NCHUNK)
+        int q = 0;  // chunks before
+        for (int x = x_lo; x < x_hi;) {
+            x += Tile1(x, x_hi, f).n;
+            q += ceil_div(nb1, cb1);
+        }
+        // Batches under way, at most NBATCH: lane i has batch i (mod NBATCH), its rows, its
+        // barrier and the parity of that.  A group has NBATCH barriers of its own.
+        int head = 0, tail = 0, used = 0, at = 0, mine = 0, turn0 = 0, turn1 = 0;
         bool ok = __all_sync(0xffffffffu, tc::mbar_wait(h_ready, 0, abort_flag, p.err));
         fence_proxy_async_global();  // h was written by ordinary stores
         for (int i = 0; ok && i < tiles2; ++i)
             for (int u = 0; ok && u < n_uniq; ++u) {
-                const int cnt = tab.ucnt[u];
+                const uint32_t toks = tab.utok[u];
                 const uint16_t* src = p.h + (size_t)(tab.uoff[u] + lane) * (2 * f);
-                for (int b = 0; b < nb2; b += cb2, ++q) {
-                    while (ok && (q - tail >= NCHUNK || used + cnt > NROW)) {
-                        ok = tc::mbar_wait(row_empty + 8 * (tail % NCHUNK), (uint32_t)(tail / NCHUNK) & 1u, abort_flag, p.err);
-                        ok = __all_sync(0xffffffffu, ok);
-                        used -= __shfl_sync(0xffffffffu, cnt_of, tail % NCHUNK);
-                        ++tail;
+                for (int b = 0; ok && b < nb2; b += cb2, ++q) {
+                    const uint32_t bytes = 256 * min(cb2, nb2 - b);
+#pragma unroll
+                    for (int half = 0; half < L::HALVES; ++half) {
+                        const uint32_t few = L::HALVES == 1 ? toks : toks >> (16 * half) & 0xffffu;
+                        const int cnt = __popc(few);
+                        if (cnt == 0) continue;
+                        while (ok && (head - tail >= NBATCH || used + cnt > NROW)) {
+                            const int o = __shfl_sync(0xffffffffu, mine, tail % NBATCH);
+                            ok = __all_sync(0xffffffffu, tc::mbar_wait(row_empty + 8 * (o >> 8 & 255), (uint32_t)o >> 16, abort_flag, p.err));
+                            used -= o & 255;
+                            ++tail;
+                        }
+                        if (!ok) break;  // nothing is copied after a wait that gave up
+                        const int turn = q & 1 ? turn1++ : turn0++, slot = (q & 1) * NBATCH + turn % NBATCH;
+                        if (lane == head % NBATCH) mine = cnt | slot << 8 | (turn / NBATCH & 1) << 16;
+                        ++head;
+                        used += cnt;
+                        const uint32_t bar = row_full + 8 * slot;
+                        if (lane == 0) tc::mbar_arrive_expect_tx(bar, cnt * bytes);
+                        __syncwarp();
+                        const int r = at + lane;
+                        if (lane < cnt)
+                            tc::bulk_load(rows_at + (r >= NROW ? r - NROW : r) * L::PITCH,
+                                          src + (size_t)(half ? __popc(toks & 0xffffu) : 0) * (2 * f) + 128 * b, bytes, bar);
+                        at += cnt;
+                        if (at >= NROW) at -= NROW;
                     }
-                    if (!ok) break;  // nothing is copied after a wait that gave up
-                    if (lane == q % NCHUNK) cnt_of = cnt;
-                    used += cnt;
-                    const uint32_t bytes = 256 * min(cb2, nb2 - b), bar = row_full + 8 * (q % NCHUNK);
-                    if (lane == 0) tc::mbar_arrive_expect_tx(bar, cnt * bytes);
-                    __syncwarp();
-                    const int r = at + lane;
-                    if (lane < cnt) tc::bulk_load(rows_at + (r >= NROW ? r - NROW : r) * L::PITCH, src + 128 * b, bytes, bar);
-                    at += cnt;
-                    if (at >= NROW) at -= NROW;
                 }
             }
     } else if (warp == FINISHER) {
@@ -500,7 +519,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             if (to.x != mid.x) add_up(mid.cnt);  // this one's, or a tile that was the other group's
             c = to;
         }
-        int q = c.q, q2 = 0, at = 0;  // chunks, chunks of phase 2, rows (mod NROW) before
+        int q = c.q, turn = 0, at = 0;  // chunks, this group's batches, rows (mod NROW) before
 
         // ---- phase 2
         tc::mbar_wait(h_ready, 0, abort_flag, p.err);
@@ -516,43 +535,52 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
 #pragma unroll
                 for (int n = 0; n < NT; ++n) out[s][n][0] = out[s][n][1] = out[s][n][2] = out[s][n][3] = 0.f;
             for (int u = 0; u < n_uniq; ++u) {
-                const int cnt = tab.ucnt[u];
                 const uint32_t toks = tab.utok[u];
-                for (int b = 0; b < nb2; b += cb2, ++q, ++q2) {
-                    if ((q & 1) == group) {
-                        const int units = 2 * min(cb2, nb2 - b);
-                        const uint32_t slot = ring + (q % NSLOT) * L::SLOT;
-                        // this lane's column of every 8 tokens: its row, if it has one
-                        uint32_t has[NT], row[NT];
+                for (int b = 0; b < nb2; b += cb2, ++q) {
+                    const bool ours = (q & 1) == group;
+                    const int units = 2 * min(cb2, nb2 - b);
+                    const uint32_t slot = ring + (q % NSLOT) * L::SLOT;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            has[n] = toks >> (8 * n + g) & 1u;
-                            const int r = at + (has[n] ? __popc(toks & ((1u << (8 * n + g)) - 1u)) : 0);
-                            row[n] = rows_at + (r >= NROW ? r - NROW : r) * L::PITCH + 16 * t;
-                        }
-                        wait(q);
-                        tc::mbar_wait(row_full + 8 * (q2 % NCHUNK), (uint32_t)(q2 / NCHUNK) & 1u, abort_flag, p.err);
+                    for (int half = 0; half < L::HALVES; ++half) {
+                        constexpr int NB = NT <= 2 ? NT : 2;  // groups of 8 tokens of a batch
+                        const uint32_t few = L::HALVES == 1 ? toks : toks >> (16 * half) & 0xffffu;
+                        if (few == 0) continue;
+                        if (ours) {
+                            // this lane's column of every 8 tokens: its row, if it has one
+                            uint32_t has[NB], row[NB];
 #pragma unroll
-                        for (int i = 0; i < L::UNITS2; ++i) {
-                            const int unit = gw + GW * i, line = (unit >> 1) * tl.n;
-                            if (unit < units) {
-                                const uint4 wa = weights_at(slot, line + ga, unit & 1, t), wb = weights_at(slot, line + gb, unit & 1, t);
-                                const uint32_t from = 256 * (unit >> 1) + 64 * (unit & 1);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-                                    if (NT == 1 || (toks >> (8 * n) & 255u)) {
-                                        const uint4 hi = dec::lds128_if(row[n] + from, has[n]);
-                                        const uint4 lo = dec::lds128_if(row[n] + from + 128, has[n]);
-                                        mma<BF16>(out[NT == 1 ? 2 * (i & 1) : 0][n], wa, wb, hi);
-                                        mma<BF16>(out[NT == 1 ? 2 * (i & 1) + 1 : 1][n], wa, wb, lo);
-                                    }
+                            for (int n = 0; n < NB; ++n) {
+                                has[n] = few >> (8 * n + g) & 1u;
+                                const int r = at + (has[n] ? __popc(few & ((1u << (8 * n + g)) - 1u)) : 0);
+                                row[n] = rows_at + (r >= NROW ? r - NROW : r) * L::PITCH + 16 * t;
                             }
+                            const int batch = group * NBATCH + turn % NBATCH;
+                            if (half == 0 || !(toks & 0xffffu)) wait(q);
+                            tc::mbar_wait(row_full + 8 * batch, (uint32_t)(turn / NBATCH) & 1u, abort_flag, p.err);
+#pragma unroll
+                            for (int i = 0; i < L::UNITS2; ++i) {
+                                const int unit = gw + GW * i, line = (unit >> 1) * tl.n;
+                                if (unit < units) {
+                                    const uint4 wa = weights_at(slot, line + ga, unit & 1, t), wb = weights_at(slot, line + gb, unit & 1, t);
+                                    const uint32_t from = 256 * (unit >> 1) + 64 * (unit & 1);
+#pragma unroll
+                                    for (int n = 0; n < NB; ++n)
+                                        if (NT == 1 || (few >> (8 * n) & 255u)) {
+                                            const uint4 hi = dec::lds128_if(row[n] + from, has[n]);
+                                            const uint4 lo = dec::lds128_if(row[n] + from + 128, has[n]);
+                                            mma<BF16>(out[NT == 1 ? 2 * (i & 1) : 0][2 * half + n], wa, wb, hi);
+                                            mma<BF16>(out[NT == 1 ? 2 * (i & 1) + 1 : 1][2 * half + n], wa, wb, lo);
+                                        }
+                                }
+                            }
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive(row_empty + 8 * batch);
+                            ++turn;
                         }
-                        release(q);
-                        if (lane == 0) tc::mbar_arrive(row_empty + 8 * (q2 % NCHUNK));
+                        at += __popc(few);
+                        if (at >= NROW) at -= NROW;
                     }
-                    at += cnt;
-                    if (at >= NROW) at -= NROW;
+                    if (ours) release(q);
                 }
             }
             // columns 2 t and 2 t + 1, rows g and g + 8
@@ -639,11 +667,9 @@ cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s) {
         rows2 = std::max(rows2, p.rows2[i]);
     }
     // chunks of as many 64-input blocks each, as fit a slot
-    const bool few = l.T <= 16;
-    const int most1 = few ? Plan<1>::BLOCKS1 : Plan<4>::BLOCKS1;
-    const int most2 = std::min(few ? Plan<1>::BLOCKS2 : Plan<4>::BLOCKS2, 16 * most1 / rows2);
-    p.cb1 = ceil_div(l.d / 64, ceil_div(l.d / 64, most1));
-    p.cb2 = ceil_div(l.f / 64, ceil_div(l.f / 64, most2));
+    using L = Plan<1>;  // (the others' are the same)
+    p.cb1 = ceil_div(l.d / 64, ceil_div(l.d / 64, L::BLOCKS1));
+    p.cb2 = ceil_div(l.f / 64, ceil_div(l.f / 64, std::min(L::BLOCKS2, 16 * L::BLOCKS1 / rows2)));
     Maps maps;
     bool ok = true;
     // gate_up as [expert][64-input block][gate, up][feature][64 inputs]

@@ -33,20 +33,24 @@ constexpr int BM = 128;      // weight rows of a CTA (256 a pair)
 constexpr int BN = 192;      // most rows r of a tile
 constexpr int BL = 128;      // k of a stage: one 128-byte swizzle row of codes, two of fp16
 constexpr int W_BYTES = BM * BL;
-constexpr int X_BYTES = BN / 2 * 64 * 2;  // 64 k of a CTA's rows
-constexpr int STAGE_BYTES = W_BYTES + 2 * X_BYTES;
-constexpr int STAGES = 5;
 constexpr int OUT_BYTES = 32 * 80;  // an epilogue warp's block on its way out: 32 rows of 32 columns, 16 bytes apart
 constexpr int THREADS = 512;
 constexpr int WIDEN_WARP0 = 4, WIDEN_WARPS = 8, EP_WARP0 = 12, EP_WARPS = 4;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t A_COL = 2 * BN, A_COLS = BL / 2;  // two stages of A behind the accumulators
 static_assert(A_COL + 2 * A_COLS <= TMEM_COLS, "tensor memory");
-constexpr int NBAR = 3 * STAGES + 8;
-constexpr size_t BAR_BYTES = 320;
-static_assert(8 * NBAR + 8 <= 192 && 192 + 4 * (THREADS / 32) <= BAR_BYTES, "barrier area too small");
-constexpr int RING_BYTES = STAGES * STAGE_BYTES + EP_WARPS * OUT_BYTES;
-size_t smem_bytes(int E) { return 1024 + (size_t)RING_BYTES + BAR_BYTES + 4 * ((size_t)E + 1); }
+// Tiles of up to COLS rows r: the ring's stages are deeper where those are few and the
+// weights' stream is all that counts (two stages are being widened or multiplied: at five
+// no more than 48 KB of weights would be under way).
+template <int COLS>
+struct Ring {
+    static constexpr int X_BYTES = COLS / 2 * 64 * 2;  // 64 k of a CTA's rows
+    static constexpr int STAGE_BYTES = W_BYTES + 2 * X_BYTES, STAGES = COLS > 64 ? 5 : 8;
+    static constexpr int BYTES = STAGES * STAGE_BYTES + EP_WARPS * OUT_BYTES;
+    static constexpr int NBAR = 3 * STAGES + 8, OFF_SUMS = 8 * NBAR + 8;
+    static constexpr int BAR_BYTES = OFF_SUMS + 4 * (THREADS / 32);
+    static size_t smem(int E) { return 1024 + (size_t)BYTES + BAR_BYTES + 4 * ((size_t)E + 1); }
+};
 
 struct Params {
     int R, E, N, K;
@@ -110,20 +114,23 @@ struct Maps {
     CUtensorMap w, x[BOXES];
 };
 
+template <int COLS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     grouped_i8_tc_kernel(const __grid_constant__ Maps maps, const Params p) {
+    using L = Ring<COLS>;
+    constexpr int STAGES = L::STAGES, STAGE_BYTES = L::STAGE_BYTES, X_BYTES = L::X_BYTES;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* gbase = smem_raw + (base - raw);
-    const uint32_t bars = base + RING_BYTES;
+    const uint32_t bars = base + L::BYTES;
     const uint32_t bar_wfull = bars, bar_xfull = bars + 8 * STAGES, bar_empty = bars + 16 * STAGES;
     const uint32_t bar_afull = bars + 24 * STAGES, bar_aempty = bar_afull + 16;
     const uint32_t bar_accfull = bar_afull + 32, bar_accempty = bar_afull + 48;
-    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + RING_BYTES + 8 * NBAR);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + L::BYTES + 8 * L::NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* warp_sums = reinterpret_cast<int*>(gbase + RING_BYTES + 192);
-    int* tile_pre = reinterpret_cast<int*>(gbase + RING_BYTES + BAR_BYTES);
+    int* warp_sums = reinterpret_cast<int*>(gbase + L::BYTES + L::OFF_SUMS);
+    int* tile_pre = reinterpret_cast<int*>(gbase + L::BYTES + L::BAR_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_ctarank();
@@ -281,29 +288,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int i = pair; ok && i < work.items; i += npairs) {
             for (int j = 0; j < blocks; ++j, ++g) {
                 const int a = g & 1;
-                ok = tc::mbar_wait(bar_wfull + 8 * s, phase, abort_flag, p.err) &&
-                     tc::mbar_wait(bar_aempty + 8 * a, ((uint32_t)(g >> 1) & 1u) ^ 1u, abort_flag, p.err);
+                ok = tc::mbar_wait(bar_wfull + 8 * s, phase, abort_flag, p.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                // 64 codes of this thread's row: 16-byte piece c lies at c ^ (row % 8)
+                const uint32_t src = base + s * STAGE_BYTES + row * 128;
+                uint4 w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(w[c].x), "=r"(w[c].y), "=r"(w[c].z), "=r"(w[c].w)
+                                 : "r"(src + (((uint32_t)(4 * half + c) ^ (row & 7)) << 4)) : "memory");
+                uint32_t v[2][16];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t(&o)[16] = v[c >> 1];
+                    const int k = 8 * (c & 1);
+                    widen4(w[c].x, o[k], o[k + 1]);
+                    widen4(w[c].y, o[k + 2], o[k + 3]);
+                    widen4(w[c].z, o[k + 4], o[k + 5]);
+                    widen4(w[c].w, o[k + 6], o[k + 7]);
+                }
+                ok = tc::mbar_wait(bar_aempty + 8 * a, ((uint32_t)(g >> 1) & 1u) ^ 1u, abort_flag, p.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc::tc_fence_after();
-                // 64 codes of this thread's row: 16-byte piece c lies at c ^ (row % 8)
-                const uint32_t src = base + s * STAGE_BYTES + row * 128;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[16];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint4 w;
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                     : "r"(src + ((((uint32_t)(4 * half + 2 * h + c)) ^ (row & 7)) << 4)) : "memory");
-                        widen4(w.x, v[8 * c], v[8 * c + 1]);
-                        widen4(w.y, v[8 * c + 2], v[8 * c + 3]);
-                        widen4(w.z, v[8 * c + 4], v[8 * c + 5]);
-                        widen4(w.w, v[8 * c + 6], v[8 * c + 7]);
-                    }
-                    tc::tmem_st_32x32b_x16(t_a + A_COLS * a + 16 * h, v);
-                }
+                tc::tmem_st_32x32b_x16(t_a + A_COLS * a, v[0]);
+                tc::tmem_st_32x32b_x16(t_a + A_COLS * a + 16, v[1]);
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
@@ -417,7 +428,7 @@ int tile_columns(const GroupedI8Shape& g, int pairs) {
     for (int cols = BN; cols >= 64; cols -= 64) {
         const int all = ceil_div(g.R, std::min(g.R, g.E)), width = ceil_div(all, ceil_div(all, cols));
         const long long cost = (long long)ceil_div(tile_count(g, cols, true), pairs) * (BM + width);
-        if (cost < least) {
+        if (cost < least || (cols == 64 && all <= 64)) {
             least = cost;
             best = cols;
         }
@@ -425,12 +436,8 @@ int tile_columns(const GroupedI8Shape& g, int pairs) {
     return best;
 }
 
-cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s) {
-    const size_t n16 = (size_t)g.R * g.K / 16;
-    const int wide_blocks = (int)std::min<size_t>((n16 + 255) / 256, (size_t)num_sms() * 8);
-    cudaError_t e = launch_overlapped(widen_rows_kernel, wide_blocks, 256, 0, s, d.x, g.x16, n16);
-    if (e != cudaSuccess) return e;
-    const int cols = tile_columns(g, sm_pairs());
+template <int COLS>
+cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, int cols, cudaStream_t s) {
     Maps maps;
     const uint64_t wd[3] = {(uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.E}, ws[2] = {(uint64_t)g.K, (uint64_t)g.N * g.K};
     const uint32_t wb[3] = {BL, BM, 1};
@@ -443,16 +450,16 @@ cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStrea
     if (!ok) return cudaErrorInvalidValue;
     static DeviceValue pairs;  // CTA pairs that the GPU holds at once
     int dev = 0;
-    e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const int max_pairs = pairs.get(dev, [] {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
         cfg.blockDim = dim3(THREADS);
-        cfg.dynamicSmemBytes = smem_bytes(1024);
+        cfg.dynamicSmemBytes = Ring<COLS>::smem(1024);
         int nc = 0;
-        if (allow_smem<grouped_i8_tc_kernel>() != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&nc, grouped_i8_tc_kernel, &cfg) != cudaSuccess || nc < 1) {
+        if (allow_smem<grouped_i8_tc_kernel<COLS>>() != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&nc, grouped_i8_tc_kernel<COLS>, &cfg) != cudaSuccess || nc < 1) {
             (void)cudaGetLastError();
             nc = sm_pairs();
         }
@@ -461,7 +468,15 @@ cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStrea
     const Params p{g.R, g.E, g.N, g.K, g.offsets, d.x_scale, d.w_scale, static_cast<uint16_t*>(d.y),
                    g.out == MOE_DT_BF16, cols, g.err};
     const int grid = 2 * std::max(1, std::min(max_pairs, tile_count(g, cols, false)));
-    return launch_overlapped<grouped_i8_tc_kernel>(dim3(grid), dim3(THREADS), smem_bytes(g.E), s, maps, p);
+    return launch_overlapped<grouped_i8_tc_kernel<COLS>>(dim3(grid), dim3(THREADS), Ring<COLS>::smem(g.E), s, maps, p);
+}
+cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s) {
+    const size_t n16 = (size_t)g.R * g.K / 16;
+    const int blocks = (int)std::min<size_t>((n16 + 255) / 256, (size_t)num_sms() * 8);
+    const cudaError_t e = launch_overlapped(widen_rows_kernel, blocks, 256, 0, s, d.x, g.x16, n16);
+    if (e != cudaSuccess) return e;
+    const int cols = tile_columns(g, sm_pairs());
+    return cols > 64 ? launch_tc<BN>(g, d, cols, s) : launch_tc<64>(g, d, cols, s);
 }
 
 }  // namespace

@@ -3,11 +3,13 @@
 //
 // As for 16-bit weights (grouped_few.cu) the weights' bytes are all that counts: a
 // block takes 16 weight rows of one expert and up to 8 of its rows, its warps share K
-// and add up in shared memory.  mma.sync m16n8k32 on the codes as they are, 32-bit
-// integer sums, so the sum is exact in any order; one rounding at the end.  (int8
-// runs at 1/11 of the 16-bit rate here, which 8 rows do not reach.)  Both operands
-// keep K in the order in which a thread's 16-byte loads bring it: lane 4 g + t holds
-// elements 16 t .. 16 t + 15 of every 64 for weight rows g and g + 8 and row g of x.
+// and add up in shared memory.  Integer sums, exact in any order; one rounding at the
+// end.  Lane 4 g + t holds elements 16 t .. 16 t + 15 of every 64 for weight rows g and
+// g + 8.  Up to four rows by dp4a, a row at a time; more by mma.sync m16n8k32, which
+// runs at 1/11 of the 16-bit rate here and, at one row, costs more than the weights:
+// 8 rows of 8 experts, N 1536, K 2048 9.4 us, by dp4a 7.1; N 4096, K 7168 42.2 and 38.0.
+#include <type_traits>
+
 #include "internal.h"
 
 namespace moe {
@@ -27,44 +29,10 @@ __device__ __forceinline__ void mma16832(int (&c)[4], uint32_t a0, uint32_t a1, 
                  : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const GroupedI8Shape g, const GroupedI8Data d) {
-    __shared__ int cnt[WARPS];
-    __shared__ int part[WARPS][COLS][ROWS + 1];
-    grid_dependency_launch();
-    grid_dependency_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.y, n0 = blockIdx.x * ROWS;
-    // the row's expert: how many segments end at or before it
-    int c = 0;
-    bool bad = false;
-    for (int i = threadIdx.x; i < g.E; i += 32 * WARPS) {
-        const int lo = __ldg(g.offsets + i), hi = __ldg(g.offsets + i + 1);
-        c += hi <= r;
-        bad |= lo < 0 || hi < lo || hi > g.R;
-    }
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) cnt[warp] = c;
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0 && blockIdx.x == 0 && r == 0) set_error(g.err, ERRBIT_RANGE);
-        return;
-    }
-    int e = 0;
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) e += cnt[i];
-    if (e >= g.E) return;  // behind the last segment
-    const int r0 = __ldg(g.offsets + e), r1 = __ldg(g.offsets + e + 1);
-    if (r < r0 || (r - r0) % COLS) return;  // in front of the first; another block's
-    const int rows = min(COLS, r1 - r);
-
-    const int gi = lane >> 2, t = lane & 3;
-    const int kq = ceil_div(g.K, 64 * WARPS) * 64, k0 = warp * kq, k1 = min(g.K, k0 + kq);
-    const size_t ld = (size_t)g.K;
-    const int8_t* wa = d.w + ((size_t)e * g.N + min(n0 + gi, g.N - 1)) * ld + 16 * t;
-    const int8_t* wb = d.w + ((size_t)e * g.N + min(n0 + gi + 8, g.N - 1)) * ld + 16 * t;
-    const int8_t* xr = d.x + (size_t)(r + min(gi, rows - 1)) * ld + 16 * t;
-    const bool has = gi < rows;
-    int acc[4] = {0, 0, 0, 0};
+// This warp's part of K [k0, k1) of the products of weight rows wa and wb with RW rows.
+template <int RW>
+__device__ __forceinline__ void dots(const int8_t* wa, const int8_t* wb, const int8_t* x, size_t ld, int k0, int k1, int t,
+                                     int (&acc)[RW][2]) {
     for (int k = k0; k < k1; k += 64 * AHEAD) {
         uint4 a[AHEAD], b[AHEAD];
 #pragma unroll
@@ -74,17 +42,101 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const Groupe
             b[i] = in ? load_codes(wb + k + 64 * i) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const bool in = has && k + 64 * i + 16 * t < k1;
-            const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(xr + k + 64 * i)) : make_uint4(0, 0, 0, 0);
-            mma16832(acc, a[i].x, b[i].x, a[i].y, b[i].y, v.x, v.y);
-            mma16832(acc, a[i].z, b[i].z, a[i].w, b[i].w, v.z, v.w);
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int j = 0; j < RW; ++j) {
+                const bool in = k + 64 * i + 16 * t < k1;
+                const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(x + j * ld + k + 64 * i)) : make_uint4(0, 0, 0, 0);
+                const uint32_t c[4] = {v.x, v.y, v.z, v.w};
+                const uint32_t p[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, q[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    acc[j][0] = __dp4a((int)p[m], (int)c[m], acc[j][0]);
+                    acc[j][1] = __dp4a((int)q[m], (int)c[m], acc[j][1]);
+                }
+            }
+    }
+}
+
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const GroupedI8Shape g, const GroupedI8Data d) {
+    __shared__ int seg[3];
+    __shared__ int part[WARPS][COLS][ROWS + 1];
+    if (threadIdx.x == 0) seg[0] = -1;
+    grid_dependency_launch();
+    __syncthreads();
+    grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.y, n0 = blockIdx.x * ROWS;
+    // the row's expert and its segment
+    bool bad = false;
+    for (int i = threadIdx.x; i < g.E; i += 32 * WARPS) {
+        const int lo = __ldg(g.offsets + i), hi = __ldg(g.offsets + i + 1);
+        bad |= lo < 0 || hi < lo || hi > g.R;
+        if (lo <= r && r < hi) {
+            seg[0] = i;
+            seg[1] = lo;
+            seg[2] = hi;
         }
     }
-    part[warp][2 * t][gi] = acc[0];
-    part[warp][2 * t + 1][gi] = acc[1];
-    part[warp][2 * t][gi + 8] = acc[2];
-    part[warp][2 * t + 1][gi + 8] = acc[3];
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && r == 0) set_error(g.err, ERRBIT_RANGE);
+        return;
+    }
+    const int e = seg[0], r0 = seg[1], r1 = seg[2];
+    if (e < 0 || (r - r0) % COLS) return;  // in no segment; another block's
+    const int rows = min(COLS, r1 - r);
+
+    const int gi = lane >> 2, t = lane & 3;
+    const int kq = ceil_div(g.K, 64 * WARPS) * 64, k0 = warp * kq, k1 = min(g.K, k0 + kq);
+    const size_t ld = (size_t)g.K;
+    const int8_t* wa = d.w + ((size_t)e * g.N + min(n0 + gi, g.N - 1)) * ld + 16 * t;
+    const int8_t* wb = d.w + ((size_t)e * g.N + min(n0 + gi + 8, g.N - 1)) * ld + 16 * t;
+    const int8_t* x0 = d.x + (size_t)r * ld + 16 * t;
+    // the lanes' sums of RW rows, added up over t
+    auto few = [&](auto n) {
+        constexpr int RW = decltype(n)::value;
+        int acc[RW][2] = {};
+        dots<RW>(wa, wb, x0, ld, k0, k1, t, acc);
+#pragma unroll
+        for (int j = 0; j < RW; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                int v = acc[j][h];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                if (t == 0) part[warp][j][gi + 8 * h] = v;
+            }
+    };
+    if (rows == 1) few(std::integral_constant<int, 1>{});
+    else if (rows == 2) few(std::integral_constant<int, 2>{});
+    else if (rows == 3) few(std::integral_constant<int, 3>{});
+    else if (rows == 4) few(std::integral_constant<int, 4>{});
+    else {
+        const int8_t* xr = x0 + (size_t)min(gi, rows - 1) * ld;
+        const bool has = gi < rows;
+        int acc[4] = {0, 0, 0, 0};
+        for (int k = k0; k < k1; k += 64 * AHEAD) {
+            uint4 a[AHEAD], b[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const bool in = k + 64 * i + 16 * t < k1;
+                a[i] = in ? load_codes(wa + k + 64 * i) : make_uint4(0, 0, 0, 0);
+                b[i] = in ? load_codes(wb + k + 64 * i) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const bool in = has && k + 64 * i + 16 * t < k1;
+                const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(xr + k + 64 * i)) : make_uint4(0, 0, 0, 0);
+                mma16832(acc, a[i].x, b[i].x, a[i].y, b[i].y, v.x, v.y);
+                mma16832(acc, a[i].z, b[i].z, a[i].w, b[i].w, v.z, v.w);
+            }
+        }
+        part[warp][2 * t][gi] = acc[0];
+        part[warp][2 * t + 1][gi] = acc[1];
+        part[warp][2 * t][gi + 8] = acc[2];
+        part[warp][2 * t + 1][gi + 8] = acc[3];
+    }
     __syncthreads();
     const int col = threadIdx.x / ROWS, n = threadIdx.x % ROWS;
     if (col < rows && n0 + n < g.N) {  // (the first 128 threads)

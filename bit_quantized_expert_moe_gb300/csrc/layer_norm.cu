@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(SLOTS == 1 || VPT == 4 ? 512 : 1024, 1) layer_
         // the same for the group's threads, and true for a NaN: squares beyond fp32, in
         // other units (x' or x' - m0, whose normalised row is the same)
         if (__builtin_expect(!(t[1] < INFINITY), 0)) {
-            eps = fmaxf(eps * (UNIT * UNIT), 0x1p-126f);
+            eps = fmaxf(eps * UNIT * UNIT, 0x1p-126f);
             s = f2(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) layer_norm_backward_kernel(c
         if (fabsf(sum) < 0x1p63f) centre(sum, t);
         if (__builtin_expect(!(t[1] < INFINITY), 0)) {  // as in layer_norm.cu
             unit = UNIT;
-            eps = fmaxf(eps * (UNIT * UNIT), 0x1p-126f);
+            eps = fmaxf(eps * UNIT * UNIT, 0x1p-126f);
             s = f2(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -195,7 +195,7 @@ struct Plan {
 };
 Plan plan(int T, int D) {
     Plan b;
-    b.vpt = norm::chunks_per_thread(D);
+    b.vpt = D <= 1024 ? 1 : D <= 8192 ? 2 : 4;
     b.threads = norm::group_threads(D, b.vpt);
     b.groups = std::max(1, std::min({BLOCK_THREADS / b.threads, 15, ceil_div(T, num_sms())}));
     b.rows = std::max(1, ceil_div(T, num_sms() * b.groups));

@@ -3,10 +3,18 @@
 // for x = row (row_map[r] / k), so that the rows of a permutation go to their places
 // without a 16-bit copy in between.
 //
-// Bound by memory: a thread holds its part of the row in registers, 16 elements at a
-// time, between the maximum and the codes.  The codes are those of the formula
-// exactly: where fp32 leaves a value too close to the border between two codes, the
-// border is compared in 64 bits.
+// The rows' gather makes k rows of one: what bounds it is not the memory but the
+// instructions of an element, and packed ones keep them at about five: the maximum of
+// pairs of 16-bit patterns, products and sums of pairs in fp32, and rounding by adding
+// 1.5 2^23, whose low byte is the code.  A thread holds its part of the row in registers
+// between the maximum and the codes.
+//
+// The codes are those of the formula exactly.  With y = 1 / a, t0 = (127 x) y and the
+// residual 127 x - t0 a, which an fma has exactly, t = t0 + residual y is the quotient
+// rounded to fp32, and the quotient itself where it lies on the border n + 1/2 between
+// two codes.  Any other quotient of 16-bit numbers is at least 2^-19 t away from a border
+// (254 x and (2 n + 1) a are multiples of x's last place), 32 roundings.  fp32 rows can
+// be closer: where t is a border there, it is compared in 64 bits.
 #include "internal.h"
 #include "vec8.cuh"
 
@@ -21,17 +29,69 @@ struct QuantArgs {
     float* scales;
 };
 
-// The code of v; t: v 127 / top in fp32, off by less than 3e-5.
-__device__ __forceinline__ int code_of(float v, float t, float top) {
-    const float q = rintf(t);
-    if (__builtin_expect(fabsf(fabsf(t - q) - 0.5f) < 4e-5f, 0)) {
-        // between m and m + 1: 254 |v| against (2 m + 1) top, exact in 64 bits
-        const int m = (int)fabsf(t);
-        const double a = 254.0 * fabs((double)v), b = (2.0 * m + 1.0) * (double)top;
-        const int c = a > b || (a == b && (m & 1)) ? m + 1 : m;
-        return t < 0.f ? -c : c;
+// The largest |x| of eight elements as its pattern in T's width: ordered, and a NaN is
+// above infinity.  16 bits: of either half, to be joined at the end.
+template <class T>
+__device__ __forceinline__ uint32_t largest(uint32_t m, const typename T::Raw& r) {
+    if constexpr (T::BYTES == 2) {
+        m = __vmaxu2(__vmaxu2(m, r.x & 0x7FFF7FFFu), r.y & 0x7FFF7FFFu);
+        return __vmaxu2(__vmaxu2(m, r.z & 0x7FFF7FFFu), r.w & 0x7FFF7FFFu);
+    } else {
+        const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, u[i] & 0x7FFFFFFFu);
+        return m;
     }
-    return (int)q;
+}
+// That pattern as fp32.
+template <class T>
+__device__ __forceinline__ float value(uint32_t m) {
+    if constexpr (T::BYTES == 4) return __uint_as_float(m);
+    const uint32_t h = max(m & 0xFFFFu, m >> 16);
+    if constexpr (__is_same(T, Bf16)) return __uint_as_float(h << 16);
+    else return half_bits_to_float((uint16_t)h);
+}
+
+// The code of v where v 127 / top is next to t = m + 1/2 in fp32.
+__device__ __noinline__ int border_code(float v, float t, float top) {
+    const int m = (int)fabsf(t);
+    const double a = 254.0 * fabs((double)v), b = (2.0 * m + 1.0) * (double)top;
+    const int c = a > b || (a == b && (m & 1)) ? m + 1 : m;
+    return t < 0.f ? -c : c;
+}
+
+// Eight codes; y = 1 / top (0 for a row of zeros).
+template <class T>
+__device__ __forceinline__ uint2 codes8(const V8& v, float y, float top) {
+    constexpr float M = 12582912.f;
+    float2 t[4], s[4];
+    float off = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = f2_mul(v.p[i], f2(127.f));
+        t[i] = f2_mul(x, f2(y));
+        float2 r = ffma2(t[i], f2(-top), x);
+        if (T::BYTES == 4)  // 127 x is rounded itself
+            r = ffma2(ffma2(v.p[i], f2(127.f), make_float2(-x.x, -x.y)), f2(1.f), r);
+        t[i] = ffma2(r, f2(y), t[i]);
+        s[i] = ffma2(t[i], f2(1.f), f2(M));
+        if (T::BYTES == 4) {
+            const float2 d = ffma2(ffma2(s[i], f2(1.f), f2(-M)), f2(-1.f), t[i]);
+            off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
+        }
+    }
+    if (T::BYTES == 4 && __builtin_expect(off == 0.5f, 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (fabsf(t[i].x - rintf(t[i].x)) == 0.5f) s[i].x = __int_as_float(border_code(v.p[i].x, t[i].x, top));
+            if (fabsf(t[i].y - rintf(t[i].y)) == 0.5f) s[i].y = __int_as_float(border_code(v.p[i].y, t[i].y, top));
+        }
+    }
+    auto bytes = [](float2 a, float2 b) {
+        return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                           __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+    };
+    return make_uint2(bytes(s[0], s[1]), bytes(s[2], s[3]));
 }
 
 // THREADS threads share a row, VPT times 16 elements each; 256 / THREADS rows a block.
@@ -49,23 +109,21 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) quantize_rows_k
         src = a < 0 ? -1 : a / p.k;
     }
     const bool there = r < p.R && src >= 0 && src < p.T;
-    V8 v[VPT][2];
-    uint32_t top = 0;  // |x| as bits: ordered, and a NaN is above infinity
+    typename T::Raw v[VPT][2];
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int u = i * THREADS + tid;
-        v[i][0] = v[i][1] = v8(0.f);
+        v[i][0] = v[i][1] = typename T::Raw{};
         if (there && u < units) {
             const size_t c = (size_t)src * units * 2 + 2 * u;
-            v[i][0] = load8<T>(p.x, c);
-            v[i][1] = load8<T>(p.x, c + 1);
+            v[i][0] = load_raw<T>(p.x, c);
+            v[i][1] = load_raw<T>(p.x, c + 1);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                top = max(top, max(__float_as_uint(v[i][h].p[j].x) & 0x7FFFFFFFu, __float_as_uint(v[i][h].p[j].y) & 0x7FFFFFFFu));
     }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) top = largest<T>(largest<T>(top, v[i][0]), v[i][1]);
+    if (T::BYTES == 2) top = max(top & 0xFFFFu, top >> 16);
     top = __reduce_max_sync(0xffffffffu, top);
     if (THREADS > 32) {
         if ((tid & 31) == 0) most[grp][tid >> 5] = top;
@@ -74,25 +132,24 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) quantize_rows_k
         for (int w = 0; w < THREADS / 32; ++w) top = max(top, most[grp][w]);
     }
     if (r >= p.R) return;
-    const bool finite = top < 0x7F800000u, any = finite && top > 0;
-    const float a = __uint_as_float(top);
-    // units in which 127 / a is an ordinary number
-    const float unit = a < 0x1p-60f ? 0x1p80f : 1.f, inv = any ? 127.f / (a * unit) : 0.f;
+    const float a = value<T>(top);
+    const bool finite = a < INFINITY;  // (false for a NaN)
+    // rows whose 127 a or 1 / a is no ordinary number: in other units
+    const float unit = a < 0x1p-60f ? 0x1p80f : a > 0x1p100f ? 0x1p-20f : 1.f;
+    const float y = finite && a > 0.f ? 1.f / (a * unit) : 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int u = i * THREADS + tid;
         if (u >= units) continue;
-        uint32_t o[4] = {0, 0, 0, 0};
-        if (any)
+        uint2 o[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+        if (finite)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = v[i][h].p[j];
-                    const int lo = code_of(f.x, f.x * unit * inv, a), hi = code_of(f.y, f.y * unit * inv, a);
-                    o[2 * h + (j >> 1)] |= ((uint32_t)(lo & 255) | (uint32_t)(hi & 255) << 8) << (16 * (j & 1));
-                }
-        reinterpret_cast<uint4*>(p.codes)[(size_t)r * units + u] = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int h = 0; h < 2; ++h) {
+                V8 x = unpack8<T>(v[i][h]);
+                if (unit != 1.f) x = mul(x, unit);
+                o[h] = codes8<T>(x, y, a * unit);
+            }
+        reinterpret_cast<uint4*>(p.codes)[(size_t)r * units + u] = make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
     }
     // a row with an infinity or a NaN has no codes: its scale, and all that is made with it, is NaN
     if (tid == 0) p.scales[r] = finite ? a / 127.f : __uint_as_float(0x7FC00000u);
@@ -105,12 +162,17 @@ cudaError_t run(const QuantArgs& p, cudaStream_t s) {
 }
 template <class T>
 cudaError_t run(const QuantArgs& p, cudaStream_t s) {
-    // threads of a row: 16 elements each, 32 and 64 where 1024 threads do not reach
+    // a thread's elements of a row: 32, fewer where the rows do not fill the GPU
     const int units = p.D / 16;
-    if (units <= 32) return run<T, 1, 32>(p, s);
-    if (units <= 64) return run<T, 1, 64>(p, s);
-    if (units <= 128) return run<T, 1, 128>(p, s);
-    if (units <= 256) return run<T, 1, 256>(p, s);
+    if ((long long)p.R * units < 32ll * 1024 * num_sms()) {
+        if (units <= 32) return run<T, 1, 32>(p, s);
+        if (units <= 64) return run<T, 1, 64>(p, s);
+        if (units <= 128) return run<T, 1, 128>(p, s);
+        if (units <= 256) return run<T, 1, 256>(p, s);
+    }
+    if (units <= 64) return run<T, 2, 32>(p, s);
+    if (units <= 128) return run<T, 2, 64>(p, s);
+    if (units <= 256) return run<T, 2, 128>(p, s);
     if (units <= 512) return run<T, 2, 256>(p, s);
     if (units <= 1024) return run<T, 2, 512>(p, s);
     return run<T, 4, 512>(p, s);
