@@ -34,6 +34,12 @@ constexpr float UNIT = 0x1p-80f;
 // keeps (c - d) r small there.
 __device__ __forceinline__ float variance(float c2, float d) { return fmaxf(c2 - d * d, 0x1p-22f * d * d); }
 
+// The sum of a chunk added to s.
+__device__ __forceinline__ void add(float2& s, const V8& x) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s = ffma2(x.p[k], f2(1.f), s);
+}
+
 // gamma and beta of a thread's columns in fp32, side by side for neighbouring threads.
 __device__ __forceinline__ V8 gamma_of(const Args& p, int c) { return p.gamma ? load8(p.ptype, p.gamma, c) : v8(1.f); }
 __device__ __forceinline__ V8 beta_of(const Args& p, int c) { return p.beta ? load8(p.ptype, p.beta, c) : v8(0.f); }

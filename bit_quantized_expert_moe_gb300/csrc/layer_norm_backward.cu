@@ -13,11 +13,10 @@ namespace {
 constexpr int BLOCK_THREADS = 512;  // most threads of a block: 128 registers each
 
 // A row group takes p.rows consecutive rows, the loads of the next SLOTS - 1
-// under way while it computes one (SLOTS = 1: none).  Two reductions a row: the
-// sum of x', then those of c = x' - m0, c^2, v and v c, from which all else follows
-// (layer_norm.cu says why the mean is taken in two steps).  The parameters'
-// gradients add up in registers, then over the block's groups, then over the blocks,
-// in a fixed order.
+// under way while it computes one (SLOTS = 1: none).  One reduction a row, of x', x'^2,
+// v and v x', and a second one around the mean where layer_norm.cu takes one.  The
+// parameters' gradients add up in registers, then over the block's groups, then over the
+// blocks, in a fixed order.
 template <class T, int VPT, int SLOTS>
 __global__ void __launch_bounds__(BLOCK_THREADS, 1) layer_norm_backward_kernel(const Args p) {
     extern __shared__ __align__(16) float smem[];
@@ -70,58 +69,66 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1) layer_norm_backward_kernel(c
             fetch();
             ring.wait();
         }
-        auto load_dh = [&](int i) { return unpack8<T>(SLOTS > 1 ? ring.get(VPT + i) : raw_at<T>(p.dh, off + i * next)); };
         V8 x[VPT];
-        float2 s = f2(0.f);
+        typename T::Raw dhs[VPT];
+        float2 q[4];
+        // the sums of x, x^2, v and v x
+        auto sums = [&](float (&t)[4]) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            x[i] = v8(0.f);
-            if (in[i]) x[i] = unpack8<T>(SLOTS > 1 ? ring.get(i) : raw_at<T>(p.x, off + i * next));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s = ffma2(x[i].p[k], f2(1.f), s);
-        }
-        // from the row's sum: the sums of c, c^2, v and v c
-        auto centre = [&](float sum, float (&t)[4]) {
-            const float2 m = f2(-sum * inv_d);
-            float2 q[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+            for (int k = 0; k < 4; ++k) q[k] = f2(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
                 if (in[i]) {
-                    x[i] = fma(x[i], 1.f, V8{{m, m, m, m}});
-                    const V8 v = mul(load_dh(i), table.get(0, i * p.threads + rg.tid));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        q[0] = ffma2(x[i].p[k], f2(1.f), q[0]);
-                        q[2] = ffma2(v.p[k], f2(1.f), q[2]);
-                    }
+                    const V8 v = mul(unpack8<T>(dhs[i]), table.get(0, i * p.threads + rg.tid));
+                    add(q[0], x[i]);
                     dot(q[1], x[i], x[i]);
+                    add(q[2], v);
                     dot(q[3], v, x[i]);
                 }
 #pragma unroll
             for (int k = 0; k < 4; ++k) t[k] = q[k].x + q[k].y;
             rg.sum4(t);
         };
-        float t[4] = {0.f, INFINITY, 0.f, 0.f}, eps = p.eps, unit = 1.f;
-        const float sum = rg.sum(s.x + s.y);
-        if (fabsf(sum) < 0x1p63f) centre(sum, t);
-        if (__builtin_expect(!(t[1] < INFINITY), 0)) {  // as in layer_norm.cu
-            unit = UNIT;
-            eps = fmaxf(eps * UNIT * UNIT, 0x1p-126f);
-            s = f2(0.f);
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                x[i] = mul(x[i], UNIT);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) s = ffma2(x[i].p[k], f2(in[i] ? 1.f : 0.f), s);
-            }
-            centre(rg.sum(s.x + s.y), t);
-        }
-        const float d = t[0] * inv_d, rs = rsqrtf(variance(t[1] * inv_d, d) + eps);
-        const float vm = t[2] * inv_d, vn = rs * (t[3] * inv_d - d * vm), r1 = rs * unit;
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (in[i]) {
-                const V8 nn = fma(x[i], rs, v8(-d * rs)), dh = load_dh(i);
+                x[i] = unpack8<T>(SLOTS > 1 ? ring.get(i) : raw_at<T>(p.x, off + i * next));
+                dhs[i] = SLOTS > 1 ? ring.get(VPT + i) : raw_at<T>(p.dh, off + i * next);
+            }
+        float t[4], eps = p.eps, unit = 1.f;
+        sums(t);
+        float shift = t[0] * inv_d, var = t[1] * inv_d - shift * shift;
+        if (__builtin_expect(!(shift * shift <= var && t[1] < INFINITY), 0)) {  // as in layer_norm.cu
+            auto centre = [&](float sum) {
+                const float2 m = f2(-sum * inv_d);
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (in[i]) x[i] = fma(x[i], 1.f, V8{{m, m, m, m}});
+                sums(t);
+            };
+            const bool ordinary = fabsf(t[0]) < 0x1p63f;
+            if (ordinary) centre(t[0]);
+            if (!(ordinary && t[1] < INFINITY)) {
+                unit = UNIT;
+                eps = fmaxf(eps * UNIT * UNIT, 0x1p-126f);
+                float2 s = f2(0.f);
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (in[i]) {
+                        x[i] = mul(x[i], UNIT);
+                        add(s, x[i]);
+                    }
+                centre(rg.sum(s.x + s.y));
+            }
+            shift = t[0] * inv_d;
+            var = variance(t[1] * inv_d, shift);
+        }
+        const float rs = rsqrtf(var + eps);
+        const float vm = t[2] * inv_d, vn = rs * (t[3] * inv_d - shift * vm), r1 = rs * unit;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (in[i]) {
+                const V8 nn = fma(x[i], rs, v8(-shift * rs)), dh = unpack8<T>(dhs[i]);
                 a_gamma[i] = fma(dh, nn, a_gamma[i]);
                 a_beta[i] = fma(dh, 1.f, a_beta[i]);
                 const V8 v = fma(dh, table.get(0, i * p.threads + rg.tid), fma(nn, -vn, v8(-vm)));
