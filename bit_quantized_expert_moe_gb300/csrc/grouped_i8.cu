@@ -4,18 +4,22 @@
 //
 // The integer rate of the tensor cores here is 1/11 of the 16-bit one (153 against
 // 1900 T), and an 8-bit code is a 16-bit float exactly: the products run in fp16,
-// with fp32 sums, which are exact up to 2^24.  The rows' codes are widened once, by a
-// kernel before (every block of 256 weight rows reads them again); the weights' stay
-// 8-bit in memory and in shared memory and are widened into tensor memory, from where
-// the MMA takes its A operand.
+// with fp32 sums, which are exact up to 2^24.  The weights stay 8-bit in memory and in
+// shared memory and are widened into tensor memory, from where the MMA takes its A
+// operand.  The rows' codes are widened once, in memory (every block of 256 weight rows
+// reads them again), by warps of the same kernel, ahead of the tiles that need them.
 //
 // Tiles of 256 weight rows x (at most) 192 rows r by CTA pairs (2-SM clusters,
 // cta_group::2), each CTA with its 128 weight rows and half of the rows r.  192 and
 // not 256: two accumulators and two stages of A share the 512 columns of tensor memory.
 //
-// Warp roles (512 threads a CTA): 0 TMA producer, 1 TMEM owner and (even CTA) MMA
+// Warp roles (576 threads a CTA): 0 TMA producer, 1 TMEM owner and (even CTA) MMA
 // issuer, 4-11 widen the weights (warp w: TMEM lanes 32 (w % 4) .. + 31, either half
-// of a stage's 128 k), 12-15 epilogue (the same lanes).
+// of a stage's 128 k), 12-15 epilogue (the same lanes), 2, 3, 16 and 17 widen rows.
+// Rows: units of 16 KB of a tile's rows, in the order of the tiles, taken from a counter by
+// CTAs that run already (a tile's copies wait for its units, and these for no CTA that
+// may not have started: another kernel may hold its SM).  A unit done is counted for
+// its tile; the counters are cleared by a kernel before.
 // Barriers: wfull[s] a CTA's own weights have landed; xfull[s] (even CTA) both CTAs'
 // rows have; afull[a] (even CTA) both CTAs' warps have widened a stage; empty[s],
 // aempty[a] and accfull[b] are signalled to both CTAs by the MMAs' completion, which
@@ -34,7 +38,8 @@ constexpr int BN = 192;      // most rows r of a tile
 constexpr int BL = 128;      // k of a stage: one 128-byte swizzle row of codes, two of fp16
 constexpr int W_BYTES = BM * BL;
 constexpr int OUT_BYTES = 32 * 80;  // an epilogue warp's block on its way out: 32 rows of 32 columns, 16 bytes apart
-constexpr int THREADS = 512;
+constexpr int THREADS = 576;
+constexpr int ROW_WARPS = 4;
 constexpr int WIDEN_WARP0 = 4, WIDEN_WARPS = 8, EP_WARP0 = 12, EP_WARPS = 4;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t A_COL = 2 * BN, A_COLS = BL / 2;  // two stages of A behind the accumulators
@@ -48,7 +53,7 @@ struct Ring {
     static constexpr int STAGE_BYTES = W_BYTES + 2 * X_BYTES, STAGES = COLS > 64 ? 5 : 8;
     static constexpr int BYTES = STAGES * STAGE_BYTES + EP_WARPS * OUT_BYTES;
     static constexpr int NBAR = 3 * STAGES + 8, OFF_SUMS = 8 * NBAR + 8;
-    static constexpr int BAR_BYTES = OFF_SUMS + 4 * (THREADS / 32);
+    static constexpr int BAR_BYTES = OFF_SUMS + 4 * (THREADS / 32) + 8;  // and the unit taken
     static size_t smem(int E) { return 1024 + (size_t)BYTES + BAR_BYTES + 4 * ((size_t)E + 1); }
 };
 
@@ -60,6 +65,10 @@ struct Params {
     bool bf16;
     int tile_cols;  // most rows r of a tile
     uint32_t* err;
+    const int8_t* x;
+    uint16_t* x16;
+    int* counts;    // units taken; units done of every row tile
+    int unit_rows;  // rows of a unit
 };
 
 __device__ __forceinline__ bool segment(const Params& p, int e, int& r0, int& cnt) {
@@ -77,6 +86,7 @@ struct Item {
 struct Work {
     int mb, items;
     const int* tile_pre;  // row tiles before each expert, [E + 1]
+    __device__ int tiles(const Params& p) const { return tile_pre[p.E]; }
     __device__ Item item(const Params& p, int i) const {
         Item t;
         const int tile = i / mb;
@@ -107,6 +117,27 @@ __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
     c ^= 0x80808080u;
     lo = hsub2_u32(__byte_perm(c, 0x64646464u, 0x4140), 0x64806480u);
     hi = hsub2_u32(__byte_perm(c, 0x64646464u, 0x4342), 0x64806480u);
+}
+
+// Rows that other CTAs have widened with ordinary stores, about to be copied by TMA.
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+__device__ __forceinline__ bool rows_ready(const int* count, int units, volatile int* abort_flag, uint32_t* err) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        int v;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+        if (v >= units) break;
+        if ((it & 63u) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > tc::WAIT_LIMIT_NS) {
+                *abort_flag = 1;
+                set_error(err, ERRBIT_TIMEOUT);
+                return false;
+            }
+        }
+    }
+    fence_proxy_async_global();
+    return true;
 }
 
 constexpr int BOXES = BN / 32;  // a CTA's half of a tile is 8 .. 96 rows; map i has boxes of 16 (i + 1) rows
@@ -153,7 +184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc::fence_mbar_init();
     }
     // the maps that the tiles may use (see launch)
-    if (warp == 2 && lane <= p.tile_cols / 32) tc::tma_prefetch_desc(lane ? &maps.x[lane - 1] : &maps.w);
+    if (warp == 3 && lane <= p.tile_cols / 32) tc::tma_prefetch_desc(lane ? &maps.x[lane - 1] : &maps.w);
     if (warp == 1) {
         tc::tmem_alloc_pair(smem_u32((const void*)tmem_slot), TMEM_COLS);
         tc::tmem_relinquish_pair();
@@ -217,6 +248,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             bool ok = true;
             for (int i = pair; ok && i < work.items; i += npairs) {
                 const Item t = work.item(p, i);
+                ok = rows_ready(p.counts + 1 + i / work.mb, ceil_div(t.ncols, p.unit_rows), abort_flag, p.err);
+                if (!ok) break;
                 const int half = mma_cols(t) >> 1, bi = (half + 15) / 16 - 1, xbytes = (bi + 1) * 16 * 128;
                 const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
                 for (int j = 0; j < blocks; ++j, ++g) {
@@ -325,6 +358,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
             }
         }
+    } else if (warp < WIDEN_WARP0 || warp >= EP_WARP0 + EP_WARPS) {
+        // ------------------------------------------------------- rows, in memory
+        volatile int* taken = reinterpret_cast<volatile int*>(warp_sums + THREADS / 32);
+        const int tid = 32 * (warp < WIDEN_WARP0 ? warp - 2 : warp - (EP_WARP0 + EP_WARPS) + 2) + lane;
+        const int per = ceil_div(p.tile_cols, p.unit_rows), units = work.items ? work.tiles(p) * per : 0;
+        // One thread takes units, the next while one is under way (and no more after a
+        // wait that gave up: the others may see the flag at another time).
+        int next = units;
+        if (tid == 0 && units) next = atomicAdd(p.counts, 1);
+        for (;;) {
+            if (tid == 0) *taken = next;
+            asm volatile("bar.sync 1, %0;" :: "n"(32 * ROW_WARPS) : "memory");
+            const int u = *taken;
+            if (u >= units) break;
+            if (tid == 0) next = *abort_flag ? units : atomicAdd(p.counts, 1);
+            const int tile = u / per;
+            const Item t = work.item(p, tile * work.mb);
+            const int r0 = (u - tile * per) * p.unit_rows, rows = min(p.unit_rows, t.ncols - r0);
+            if (rows > 0) {
+                constexpr int AHEAD = 8, STEP = 32 * ROW_WARPS;
+                const size_t first = (size_t)(t.c0 + r0) * p.K / 16;  // pieces of 16 codes
+                const uint4* src = reinterpret_cast<const uint4*>(p.x) + first;
+                uint4* dst = reinterpret_cast<uint4*>(p.x16) + 2 * first;
+                const int n = rows * (p.K / 16);
+                for (int i = tid; i < n; i += AHEAD * STEP) {
+                    uint4 w[AHEAD];
+#pragma unroll
+                    for (int k = 0; k < AHEAD; ++k)
+                        if (i + k * STEP < n) w[k] = __ldg(src + i + k * STEP);
+#pragma unroll
+                    for (int k = 0; k < AHEAD; ++k)
+                        if (i + k * STEP < n) {
+                            uint4 a, b;
+                            widen4(w[k].x, a.x, a.y);
+                            widen4(w[k].y, a.z, a.w);
+                            widen4(w[k].z, b.x, b.y);
+                            widen4(w[k].w, b.z, b.w);
+                            dst[2 * (i + k * STEP)] = a;
+                            dst[2 * (i + k * STEP) + 1] = b;
+                        }
+                }
+                fence_proxy_async_global();
+            }
+            // all of the unit is written, and `taken` read
+            asm volatile("bar.sync 1, %0;" :: "n"(32 * ROW_WARPS) : "memory");
+            if (tid == 0 && rows > 0)
+                asm volatile("red.release.gpu.global.add.s32 [%0], 1;" :: "l"(p.counts + 1 + tile) : "memory");
+        }
     } else if (warp >= EP_WARP0) {
         // ---------------------------------------------------------- epilogue
         const int q = warp & 3;
@@ -395,21 +476,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
 }
 
-// The rows' codes as fp16, 16 a thread and step.
-__global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t* __restrict__ x, uint16_t* __restrict__ out, size_t n16) {
+__global__ void __launch_bounds__(256) clear_counts_kernel(int* counts, int n) {
     grid_dependency_launch();
     grid_dependency_wait();
-    const size_t step = (size_t)gridDim.x * blockDim.x;
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16; i += step) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(x) + i);
-        uint4 a, b;
-        widen4(w.x, a.x, a.y);
-        widen4(w.y, a.z, a.w);
-        widen4(w.z, b.x, b.y);
-        widen4(w.w, b.z, b.w);
-        reinterpret_cast<uint4*>(out)[2 * i] = a;
-        reinterpret_cast<uint4*>(out)[2 * i + 1] = b;
-    }
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) counts[i] = 0;
 }
 
 int sm_pairs() { return std::max(1, num_sms() / 2); }
@@ -435,6 +505,10 @@ int tile_columns(const GroupedI8Shape& g, int pairs) {
     }
     return best;
 }
+
+// Most row tiles; the counters lie behind the widened rows.
+int row_tiles(const GroupedI8Shape& g, int cols) { return g.R / cols + std::min(g.R, g.E); }
+int* counts_of(const GroupedI8Shape& g) { return reinterpret_cast<int*>(g.x16 + (size_t)g.R * g.K); }
 
 template <int COLS>
 cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, int cols, cudaStream_t s) {
@@ -466,16 +540,14 @@ cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, int cols,
         return nc;
     });
     const Params p{g.R, g.E, g.N, g.K, g.offsets, d.x_scale, d.w_scale, static_cast<uint16_t*>(d.y),
-                   g.out == MOE_DT_BF16, cols, g.err};
+                   g.out == MOE_DT_BF16, cols, g.err, d.x, g.x16, counts_of(g), std::max(1, std::min(32, 16384 / g.K))};
     const int grid = 2 * std::max(1, std::min(max_pairs, tile_count(g, cols, false)));
     return launch_overlapped<grouped_i8_tc_kernel<COLS>>(dim3(grid), dim3(THREADS), Ring<COLS>::smem(g.E), s, maps, p);
 }
 cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s) {
-    const size_t n16 = (size_t)g.R * g.K / 16;
-    const int blocks = (int)std::min<size_t>((n16 + 255) / 256, (size_t)num_sms() * 8);
-    const cudaError_t e = launch_overlapped(widen_rows_kernel, blocks, 256, 0, s, d.x, g.x16, n16);
+    const int cols = tile_columns(g, sm_pairs()), n = 1 + row_tiles(g, cols);
+    const cudaError_t e = launch_overlapped(clear_counts_kernel, std::min(ceil_div(n, 256), 16), 256, 0, s, counts_of(g), n);
     if (e != cudaSuccess) return e;
-    const int cols = tile_columns(g, sm_pairs());
     return cols > 64 ? launch_tc<BN>(g, d, cols, s) : launch_tc<64>(g, d, cols, s);
 }
 
@@ -484,8 +556,8 @@ cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStrea
 static bool takes_few(int R, int E) { return R <= 32 || (R <= 128 && R <= E); }
 
 size_t grouped_i8_halves(int R, int E, int N, int K) {
-    (void)E, (void)N;
-    return R <= 32 ? 0 : (size_t)R * K;
+    (void)N;
+    return R <= 32 ? 0 : (size_t)R * K + 2 * (1 + (size_t)R / 64 + std::min(R, E));
 }
 cudaError_t launch_grouped_i8(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s) {
     return takes_few(g.R, g.E) ? launch_grouped_i8_few(g, d, s) : launch_tc(g, d, s);
