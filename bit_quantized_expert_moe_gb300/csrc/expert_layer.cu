@@ -55,19 +55,24 @@ struct Plan {
     // projection.  One token at 2048 x 768: eight slots hold the CTA's share of that.
     static constexpr int BLOCKS1 = 11, BLOCKS2 = 12;
     static constexpr int SLOT = 16 * BLOCKS1 * 128, NSLOT = NT == 1 ? 8 : 6;
-    static constexpr int UNITS1 = (2 * BLOCKS1 + GW - 1) / GW, UNITS2 = (2 * BLOCKS2 + GW - 1) / GW;  // of 32 inputs, a warp's most
+    static constexpr int UNITS1 = (2 * BLOCKS1 + GW - 1) / GW, UNITS2 = 2 * BLOCKS2;  // of 32 inputs: a warp's most; a chunk's
     // A row of h, 256 bytes for 64 inputs; 64 more, so that neighbours use other banks.
     // The rows of an expert with tokens beyond the 16th come in two batches.
     static constexpr int PITCH = BLOCKS2 * 256 + 64, NROW = NT == 1 ? 8 : 16, NBATCH = 8;
     static constexpr int HALVES = NT <= 2 ? 1 : 2;
+    // Phase 2's groups: up to 8 tokens, where a slot is one of eight's, pairs of warps, so
+    // that the latency of a chunk counts an eighth.  (One token 19.8, and 20.4 by two
+    // groups of eight.)  Barriers of a group's batches.
+    static constexpr int GW2 = NT == 1 ? 2 : GW, GROUPS2 = CW / GW2, TURNS = NT == 1 ? 1 : NBATCH;
+
     static constexpr int NBUF = 2, SUM_FLOATS = CW * 128;        // sums of 8 tokens: [CW][32][4]
     // phase 2: [CW][8 NT][17]
     static constexpr int SUMS = 4 * (NBUF * SUM_FLOATS > CW * 8 * NT * 17 ? NBUF * SUM_FLOATS : CW * 8 * NT * 17);
-    static constexpr int BARS = 16 * (NSLOT + GROUPS * NBATCH + NBUF) + 16;
+    static constexpr int BARS = 16 * (NSLOT + GROUPS2 * TURNS + NBUF) + 16;
     static constexpr int OFF_BARS = NSLOT * SLOT, OFF_ROWS = OFF_BARS + 512, OFF_SUMS = OFF_ROWS + NROW * PITCH;
     static constexpr int OFF_TAB = OFF_SUMS + SUMS;
     static_assert(NROW >= (NT < 2 ? 8 : 16) && BARS <= 512, "a batch's rows, the barriers");
-    static_assert(NSLOT % GROUPS == 0 && SLOT % 1024 == 0 && PITCH % 128 == 64, "layout");
+    static_assert(NSLOT % GROUPS == 0 && NSLOT % GROUPS2 == 0 && SLOT % 1024 == 0 && PITCH % 128 == 64, "layout");
 };
 
 struct Tab {
@@ -183,8 +188,8 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
     uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t ring = smem_u32(sm), rows_at = ring + L::OFF_ROWS;
     const uint32_t full = ring + L::OFF_BARS, empty = full + 8 * NSLOT;                  // slots
-    const uint32_t row_full = empty + 8 * NSLOT, row_empty = row_full + 8 * GROUPS * NBATCH;      // rows of a batch
-    const uint32_t sum_full = row_empty + 8 * GROUPS * NBATCH, sum_empty = sum_full + 8 * NBUF, h_ready = sum_empty + 8 * NBUF;
+    const uint32_t row_full = empty + 8 * NSLOT, row_empty = row_full + 8 * L::GROUPS2 * L::TURNS;      // rows of a batch
+    const uint32_t sum_full = row_empty + 8 * L::GROUPS2 * L::TURNS, sum_empty = sum_full + 8 * NBUF, h_ready = sum_empty + 8 * NBUF;
     float* sums = reinterpret_cast<float*>(sm + L::OFF_SUMS);
     Tab& tab = *reinterpret_cast<Tab*>(sm + L::OFF_TAB);
     volatile int* abort_flag = &tab.abort;
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             tc::mbar_init(full + 8 * i, 1);
             tc::mbar_init(empty + 8 * i, GW);
         }
-        for (int i = 0; i < GROUPS * NBATCH; ++i) {
+        for (int i = 0; i < L::GROUPS2 * L::TURNS; ++i) {
             tc::mbar_init(row_full + 8 * i, 1);
             tc::mbar_init(row_empty + 8 * i, GW);
         }
@@ -341,8 +346,8 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             q += ceil_div(nb1, cb1);
         }
         // Batches under way, at most NBATCH: lane i has batch i (mod NBATCH), its rows, its
-        // barrier and the parity of that.  A group has NBATCH barriers of its own.
-        int head = 0, tail = 0, used = 0, at = 0, mine = 0, turn0 = 0, turn1 = 0;
+        // barrier and the parity of that.  A group has TURNS barriers of its own.
+        int head = 0, tail = 0, used = 0, at = 0, mine = 0, turns[2] = {0, 0};
         bool ok = __all_sync(0xffffffffu, tc::mbar_wait(h_ready, 0, abort_flag, p.err));
         fence_proxy_async_global();  // h was written by ordinary stores
         for (int i = 0; ok && i < tiles2; ++i)
@@ -363,8 +368,11 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                             ++tail;
                         }
                         if (!ok) break;  // nothing is copied after a wait that gave up
-                        const int turn = q & 1 ? turn1++ : turn0++, slot = (q & 1) * NBATCH + turn % NBATCH;
-                        if (lane == head % NBATCH) mine = cnt | slot << 8 | (turn / NBATCH & 1) << 16;
+                        int turn;  // of the group's batches
+                        if (L::HALVES == 1) turn = head / L::GROUPS2;
+                        else turn = q & 1 ? turns[1]++ : turns[0]++;
+                        const int slot = q % L::GROUPS2 * L::TURNS + turn % L::TURNS;
+                        if (lane == head % NBATCH) mine = cnt | slot << 8 | (turn / L::TURNS & 1) << 16;
                         ++head;
                         used += cnt;
                         const uint32_t bar = row_full + 8 * slot;
@@ -519,69 +527,70 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             if (to.x != mid.x) add_up(mid.cnt);  // this one's, or a tile that was the other group's
             c = to;
         }
-        int q = c.q, turn = 0, at = 0;  // chunks, this group's batches, rows (mod NROW) before
+        const int q1 = c.q;  // chunks of phase 1
 
         // ---- phase 2
         tc::mbar_wait(h_ready, 0, abort_flag, p.err);
         grid_dependency_launch();  // the last phase: the next kernel may be scheduled
-        // accumulators: 8 tokens each, several so that few MMAs wait for the one before
-        constexpr int SETS = NT == 1 ? 4 : 2;
+        constexpr int SETS = 2;  // of accumulators: of h's values and of its rounding errors
         float out[SETS][NT][4];
+        const int group2 = warp / L::GW2, gw2 = warp % L::GW2, parts = ceil_div(nb2, cb2), chunks = n_uniq * parts;
+        const int rows_of_all = n_uniq ? tab.uoff[n_uniq - 1] + tab.ucnt[n_uniq - 1] : 0;
+        int turn = 0;  // this group's batches before
         for (int i = 0; i < tiles2; ++i) {
+            const int q = q1 + i * chunks;  // chunks before
+
             const Tile2 tl(rows, tiles2, i);
             const int ga = min(g, tl.n - 1), gb = min(g + 8, tl.n - 1);  // rows beyond the tile's: its last again
 #pragma unroll
             for (int s = 0; s < SETS; ++s)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) out[s][n][0] = out[s][n][1] = out[s][n][2] = out[s][n][3] = 0.f;
-            for (int u = 0; u < n_uniq; ++u) {
+            for (int j = (group2 - q) & (L::GROUPS2 - 1); j < chunks; j += L::GROUPS2) {
+                const int u = j / parts, part = j - u * parts, off = tab.uoff[u];
                 const uint32_t toks = tab.utok[u];
-                for (int b = 0; b < nb2; b += cb2, ++q) {
-                    const bool ours = (q & 1) == group;
-                    const int units = 2 * min(cb2, nb2 - b);
-                    const uint32_t slot = ring + (q % NSLOT) * L::SLOT;
+                const int units = 2 * min(cb2, nb2 - part * cb2);
+                const uint32_t slot = ring + ((q + j) % NSLOT) * L::SLOT;
+                // the rows before: those of earlier tiles, experts and parts
+                int at = parts * (i * rows_of_all + off) + part * __popc(toks);
+                wait(q + j);
 #pragma unroll
-                    for (int half = 0; half < L::HALVES; ++half) {
-                        constexpr int NB = NT <= 2 ? NT : 2;  // groups of 8 tokens of a batch
-                        const uint32_t few = L::HALVES == 1 ? toks : toks >> (16 * half) & 0xffffu;
-                        if (few == 0) continue;
-                        if (ours) {
-                            // this lane's column of every 8 tokens: its row, if it has one
-                            uint32_t has[NB], row[NB];
+                for (int half = 0; half < L::HALVES; ++half) {
+                    constexpr int NB = NT <= 2 ? NT : 2;  // groups of 8 tokens of a batch
+                    const uint32_t few = L::HALVES == 1 ? toks : toks >> (16 * half) & 0xffffu;
+                    if (L::HALVES > 1 && few == 0) continue;
+                    // this lane's column of every 8 tokens: its row, if it has one
+                    uint32_t has[NB], row[NB];
 #pragma unroll
-                            for (int n = 0; n < NB; ++n) {
-                                has[n] = few >> (8 * n + g) & 1u;
-                                const int r = at + (has[n] ? __popc(few & ((1u << (8 * n + g)) - 1u)) : 0);
-                                row[n] = rows_at + (r >= NROW ? r - NROW : r) * L::PITCH + 16 * t;
-                            }
-                            const int batch = group * NBATCH + turn % NBATCH;
-                            if (half == 0 || !(toks & 0xffffu)) wait(q);
-                            tc::mbar_wait(row_full + 8 * batch, (uint32_t)(turn / NBATCH) & 1u, abort_flag, p.err);
-#pragma unroll
-                            for (int i = 0; i < L::UNITS2; ++i) {
-                                const int unit = gw + GW * i, line = (unit >> 1) * tl.n;
-                                if (unit < units) {
-                                    const uint4 wa = weights_at(slot, line + ga, unit & 1, t), wb = weights_at(slot, line + gb, unit & 1, t);
-                                    const uint32_t from = 256 * (unit >> 1) + 64 * (unit & 1);
-#pragma unroll
-                                    for (int n = 0; n < NB; ++n)
-                                        if (NT == 1 || (few >> (8 * n) & 255u)) {
-                                            const uint4 hi = dec::lds128_if(row[n] + from, has[n]);
-                                            const uint4 lo = dec::lds128_if(row[n] + from + 128, has[n]);
-                                            mma<BF16>(out[NT == 1 ? 2 * (i & 1) : 0][2 * half + n], wa, wb, hi);
-                                            mma<BF16>(out[NT == 1 ? 2 * (i & 1) + 1 : 1][2 * half + n], wa, wb, lo);
-                                        }
-                                }
-                            }
-                            __syncwarp();
-                            if (lane == 0) tc::mbar_arrive(row_empty + 8 * batch);
-                            ++turn;
-                        }
-                        at += __popc(few);
-                        if (at >= NROW) at -= NROW;
+                    for (int n = 0; n < NB; ++n) {
+                        has[n] = few >> (8 * n + g) & 1u;
+                        const int r = at + (has[n] ? __popc(few & ((1u << (8 * n + g)) - 1u)) : 0);
+                        row[n] = rows_at + (r & (NROW - 1)) * L::PITCH + 16 * t;
                     }
-                    if (ours) release(q);
+                    const uint32_t batch = 8 * (group2 * L::TURNS + turn % L::TURNS);
+                    tc::mbar_wait(row_full + batch, (uint32_t)(turn / L::TURNS) & 1u, abort_flag, p.err);
+#pragma unroll 3
+                    for (int i = 0; i < L::UNITS2 / L::GW2; ++i) {
+                        const int unit = gw2 + L::GW2 * i, line = (unit >> 1) * tl.n;
+                        if (unit < units) {
+                            const uint4 wa = weights_at(slot, line + ga, unit & 1, t), wb = weights_at(slot, line + gb, unit & 1, t);
+                            const uint32_t from = 256 * (unit >> 1) + 64 * (unit & 1);
+#pragma unroll
+                            for (int n = 0; n < NB; ++n)
+                                if (NT == 1 || (few >> (8 * n) & 255u)) {
+                                    const uint4 hi = dec::lds128_if(row[n] + from, has[n]);
+                                    const uint4 lo = dec::lds128_if(row[n] + from + 128, has[n]);
+                                    mma<BF16>(out[0][2 * half + n], wa, wb, hi);
+                                    mma<BF16>(out[1][2 * half + n], wa, wb, lo);
+                                }
+                        }
+                    }
+                    __syncwarp();
+                    if (lane < GW / L::GW2) tc::mbar_arrive(row_empty + batch);
+                    ++turn;
+                    at += __popc(few);
                 }
+                if (lane < GW / L::GW2) tc::mbar_arrive(empty + 8 * ((q + j) % NSLOT));
             }
             // columns 2 t and 2 t + 1, rows g and g + 8
             float* mine = sums + warp * (8 * NT * 17);
@@ -589,9 +598,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    float v = out[0][n][c] + out[1][n][c];
-                    if (SETS == 4) v += out[SETS - 2][n][c] + out[SETS - 1][n][c];
-                    mine[(8 * n + 2 * t + (c & 1)) * 17 + g + 4 * (c & 2)] = v;
+                    mine[(8 * n + 2 * t + (c & 1)) * 17 + g + 4 * (c & 2)] = out[0][n][c] + out[1][n][c];
                 }
             dec::bar_sync(1, CONSUMERS);
             for (int j = threadIdx.x; j < p.T * 16; j += CONSUMERS) {

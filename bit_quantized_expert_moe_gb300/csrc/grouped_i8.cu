@@ -7,7 +7,8 @@
 // with fp32 sums, which are exact up to 2^24.  The weights stay 8-bit in memory and in
 // shared memory and are widened into tensor memory, from where the MMA takes its A
 // operand.  The rows' codes are widened once, in memory (every block of 256 weight rows
-// reads them again), by warps of the same kernel, ahead of the tiles that need them.
+// reads them again), by warps of the same kernel, ahead of the tiles that need them, or
+// where they are few by a kernel before.
 //
 // Tiles of 256 weight rows x (at most) 192 rows r by CTA pairs (2-SM clusters,
 // cta_group::2), each CTA with its 128 weight rows and half of the rows r.  192 and
@@ -67,7 +68,7 @@ struct Params {
     uint32_t* err;
     const int8_t* x;
     uint16_t* x16;
-    int* counts;    // units taken; units done of every row tile
+    int* counts;    // units taken; units done of every row tile; null: the rows are there
     int unit_rows;  // rows of a unit
 };
 
@@ -138,6 +139,16 @@ __device__ __forceinline__ bool rows_ready(const int* count, int units, volatile
     }
     fence_proxy_async_global();
     return true;
+}
+
+__device__ __forceinline__ void widen16(const uint4& w, uint4* out) {
+    uint4 a, b;
+    widen4(w.x, a.x, a.y);
+    widen4(w.y, a.z, a.w);
+    widen4(w.z, b.x, b.y);
+    widen4(w.w, b.z, b.w);
+    out[0] = a;
+    out[1] = b;
 }
 
 constexpr int BOXES = BN / 32;  // a CTA's half of a tile is 8 .. 96 rows; map i has boxes of 16 (i + 1) rows
@@ -248,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             bool ok = true;
             for (int i = pair; ok && i < work.items; i += npairs) {
                 const Item t = work.item(p, i);
-                ok = rows_ready(p.counts + 1 + i / work.mb, ceil_div(t.ncols, p.unit_rows), abort_flag, p.err);
+                ok = !p.counts || rows_ready(p.counts + 1 + i / work.mb, ceil_div(t.ncols, p.unit_rows), abort_flag, p.err);
                 if (!ok) break;
                 const int half = mma_cols(t) >> 1, bi = (half + 15) / 16 - 1, xbytes = (bi + 1) * 16 * 128;
                 const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
@@ -362,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------- rows, in memory
         volatile int* taken = reinterpret_cast<volatile int*>(warp_sums + THREADS / 32);
         const int tid = 32 * (warp < WIDEN_WARP0 ? warp - 2 : warp - (EP_WARP0 + EP_WARPS) + 2) + lane;
-        const int per = ceil_div(p.tile_cols, p.unit_rows), units = work.items ? work.tiles(p) * per : 0;
+        const int per = ceil_div(p.tile_cols, p.unit_rows), units = p.counts && work.items ? work.tiles(p) * per : 0;
         // One thread takes units, the next while one is under way (and no more after a
         // wait that gave up: the others may see the flag at another time).
         int next = units;
@@ -389,15 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         if (i + k * STEP < n) w[k] = __ldg(src + i + k * STEP);
 #pragma unroll
                     for (int k = 0; k < AHEAD; ++k)
-                        if (i + k * STEP < n) {
-                            uint4 a, b;
-                            widen4(w[k].x, a.x, a.y);
-                            widen4(w[k].y, a.z, a.w);
-                            widen4(w[k].z, b.x, b.y);
-                            widen4(w[k].w, b.z, b.w);
-                            dst[2 * (i + k * STEP)] = a;
-                            dst[2 * (i + k * STEP) + 1] = b;
-                        }
+                        if (i + k * STEP < n) widen16(w[k], dst + 2 * (i + k * STEP));
                 }
                 fence_proxy_async_global();
             }
@@ -476,6 +479,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
 }
 
+// The rows' codes as fp16, 16 a thread and step, before the product's kernel.
+__global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t* __restrict__ x, uint16_t* __restrict__ out, size_t n16) {
+    grid_dependency_launch();
+    grid_dependency_wait();
+    const size_t step = (size_t)gridDim.x * blockDim.x;
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16; i += step)
+        widen16(__ldg(reinterpret_cast<const uint4*>(x) + i), reinterpret_cast<uint4*>(out) + 2 * i);
+}
+
 __global__ void __launch_bounds__(256) clear_counts_kernel(int* counts, int n) {
     grid_dependency_launch();
     grid_dependency_wait();
@@ -511,7 +523,7 @@ int row_tiles(const GroupedI8Shape& g, int cols) { return g.R / cols + std::min(
 int* counts_of(const GroupedI8Shape& g) { return reinterpret_cast<int*>(g.x16 + (size_t)g.R * g.K); }
 
 template <int COLS>
-cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, int cols, cudaStream_t s) {
+cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, int cols, bool first, cudaStream_t s) {
     Maps maps;
     const uint64_t wd[3] = {(uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.E}, ws[2] = {(uint64_t)g.K, (uint64_t)g.N * g.K};
     const uint32_t wb[3] = {BL, BM, 1};
@@ -540,15 +552,21 @@ cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, int cols,
         return nc;
     });
     const Params p{g.R, g.E, g.N, g.K, g.offsets, d.x_scale, d.w_scale, static_cast<uint16_t*>(d.y),
-                   g.out == MOE_DT_BF16, cols, g.err, d.x, g.x16, counts_of(g), std::max(1, std::min(32, 16384 / g.K))};
+                   g.out == MOE_DT_BF16, cols, g.err, d.x, g.x16, first ? nullptr : counts_of(g), std::max(1, std::min(32, 16384 / g.K))};
     const int grid = 2 * std::max(1, std::min(max_pairs, tile_count(g, cols, false)));
     return launch_overlapped<grouped_i8_tc_kernel<COLS>>(dim3(grid), dim3(THREADS), Ring<COLS>::smem(g.E), s, maps, p);
 }
 cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s) {
     const int cols = tile_columns(g, sm_pairs()), n = 1 + row_tiles(g, cols);
-    const cudaError_t e = launch_overlapped(clear_counts_kernel, std::min(ceil_div(n, 256), 16), 256, 0, s, counts_of(g), n);
+    // Few rows are widened by a kernel before, which takes less than the first tiles'
+    // wait for their units: 1238 rows of K 272 7.1 us so, 9.0 by the same kernel; 4096 of
+    // 2048 86.8 and 83.3 (128 experts).
+    const size_t n16 = (size_t)g.R * g.K / 16;
+    const bool first = n16 <= (1 << 18);
+    const cudaError_t e = first ? launch_overlapped(widen_rows_kernel, std::max(1, ceil_div((int)n16, 256)), 256, 0, s, d.x, g.x16, n16)
+                                : launch_overlapped(clear_counts_kernel, std::min(ceil_div(n, 256), 16), 256, 0, s, counts_of(g), n);
     if (e != cudaSuccess) return e;
-    return cols > 64 ? launch_tc<BN>(g, d, cols, s) : launch_tc<64>(g, d, cols, s);
+    return cols > 64 ? launch_tc<BN>(g, d, cols, first, s) : launch_tc<64>(g, d, cols, first, s);
 }
 
 }  // namespace
