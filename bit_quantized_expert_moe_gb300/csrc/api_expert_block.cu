@@ -117,7 +117,7 @@ moe_status_t moe_grouped_mm_i8(moe_dtype_t out_dtype, const int8_t* x, const flo
 
 size_t moe_expert_layer_workspace_size(int32_t T, int32_t k, int32_t E, int32_t d_model, int32_t d_ff) {
     if (!layer_sizes_ok(T, k, E, d_model, d_ff) || !layer_supported(T, k, d_model, d_ff)) return 0;
-    return WS_HEADER + 2 * expert_layer_halves(T, k, d_ff);
+    return WS_HEADER + expert_layer_bytes(T, k, d_model, d_ff);
 }
 
 moe_status_t moe_expert_layer(moe_dtype_t dtype, const void* x, const float* logits, const void* w13, const void* w2,
@@ -131,7 +131,7 @@ moe_status_t moe_expert_layer(moe_dtype_t dtype, const void* x, const float* log
     if (T == 0) return MOE_OK;
     auto* ws = static_cast<unsigned char*>(workspace);
     return cuda_status(launch_expert_layer(ExpertLayer{dtype, x, logits, w13, w2, T, k, E, d_model, d_ff, out, topk_ids_out,
-                                                       reinterpret_cast<uint32_t*>(ws), reinterpret_cast<uint16_t*>(ws + WS_HEADER)},
+                                                       reinterpret_cast<uint32_t*>(ws), ws + WS_HEADER},
                                            stream));
 }
 

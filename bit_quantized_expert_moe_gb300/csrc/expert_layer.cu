@@ -56,8 +56,9 @@ struct Plan {
     static constexpr int BLOCKS1 = 11, BLOCKS2 = 12;
     static constexpr int SLOT = 16 * BLOCKS1 * 128, NSLOT = NT == 1 ? 8 : 6;
     static constexpr int UNITS1 = (2 * BLOCKS1 + GW - 1) / GW, UNITS2 = 2 * BLOCKS2;  // of 32 inputs: a warp's most; a chunk's
-    // A row of h, 256 bytes for 64 inputs; 64 more, so that neighbours use other banks.
-    // The rows of an expert with tokens beyond the 16th come in two batches.
+    // A row of h of a chunk, 256 bytes for 64 inputs; 64 more, so that neighbours use
+    // other banks.  A batch's rows are one bulk copy; more than 16 of an expert are two
+    // batches, of the tokens below 16 and of the others.
     static constexpr int PITCH = BLOCKS2 * 256 + 64, NROW = NT == 1 ? 8 : 16, NBATCH = 8;
     static constexpr int HALVES = NT <= 2 ? 1 : 2;
     // Phase 2's groups: up to 8 tokens, where a slot is one of eight's, pairs of warps, so
@@ -83,6 +84,7 @@ struct Tab {
     int uexp[MAX_R], uoff[MAX_R], ucnt[MAX_R];  // touched experts, ascending: id, first position, how many tokens
     uint32_t utok[MAX_R];                       // and which, one bit a token
     uint32_t warp_sums[CW];
+    int batches[2 * 8];                         // under way: rows, barrier, parity
     int n_uniq, abort;
 };
 
@@ -91,7 +93,10 @@ struct Params {
     const float* logits;
     uint16_t* out;
     int32_t* ids_out;
-    uint16_t* h;         // p h by sorted position, [R][f / 64][2][64]: 64 values, then their rounding errors
+    // p h: [chunks of an expert][R by sorted position][pitch bytes]: of 64 features their
+    // values, then the rounding errors of these; as a batch's rows lie in shared memory
+    uint8_t* h;
+    int pitch, nrow;     // and the rows of the ring of rows, a power of 2
     uint32_t* err;
     unsigned long long* bar_count;
     int T, k, E, d, f;
@@ -151,10 +156,10 @@ struct Tile2 {
     }
 };
 
-// A unit's 16 bytes of line `line` (128 bytes of 64 inputs) in a slot: 32 inputs
-// `half`, lane t; the 128-byte swizzle of the box.
-__device__ __forceinline__ uint4 weights_at(uint32_t slot, int line, int half, int t) {
-    return dec::lds128(slot + 128u * line + ((uint32_t)((4 * half + t) ^ (line & 7)) << 4));
+// Where a unit's 16 bytes of line `line` (128 bytes of 64 inputs) are in a slot: 32
+// inputs `half`, lane t; the 128-byte swizzle of the box.
+__device__ __forceinline__ uint32_t weights_at(uint32_t slot, int line, int half, int t) {
+    return slot + 128u * line + ((uint32_t)((4 * half + t) ^ (line & 7)) << 4);
 }
 
 // Where a group is in phase 1's list of chunks.
@@ -180,10 +185,11 @@ struct Place1 {
     }
 };
 
-template <bool BF16, int NT>
+// PAIR: up to 4 tokens, whose h and rounding errors are columns of one MMA.
+template <bool BF16, int NT, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_constant__ Maps maps, const Params p) {
     using L = Plan<NT>;
-    constexpr int NSLOT = L::NSLOT, NBATCH = L::NBATCH, NROW = L::NROW, NBUF = L::NBUF;
+    constexpr int NSLOT = L::NSLOT, NBATCH = L::NBATCH, NBUF = L::NBUF;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t ring = smem_u32(sm), rows_at = ring + L::OFF_ROWS;
@@ -340,53 +346,81 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
         __syncwarp();
     } else if (warp == ROWS_OF_H) {
         // ------------------- the tokens' rows of h of the chunks, a lane a bulk copy
-        int q = 0;  // chunks before
+        int q = 0;  // chunks of phase 1
         for (int x = x_lo; x < x_hi;) {
             x += Tile1(x, x_hi, f).n;
             q += ceil_div(nb1, cb1);
         }
-        // Batches under way, at most NBATCH: lane i has batch i (mod NBATCH), its rows, its
-        // barrier and the parity of that.  A group has TURNS barriers of its own.
-        int head = 0, tail = 0, used = 0, at = 0, mine = 0, turns[2] = {0, 0};
-        bool ok = __all_sync(0xffffffffu, tc::mbar_wait(h_ready, 0, abort_flag, p.err));
-        fence_proxy_async_global();  // h was written by ordinary stores
-        for (int i = 0; ok && i < tiles2; ++i)
-            for (int u = 0; ok && u < n_uniq; ++u) {
+        // A window of batches, a lane each: where their rows lie and go, which barrier of
+        // its group's TURNS ones a batch has.  Lanes copy as soon as there is room, in order:
+        // at most NBATCH batches and the ring's rows are under way.
+        constexpr int PER = 32 / L::HALVES;  // chunks of a window
+        const int parts = ceil_div(nb2, cb2), chunks = n_uniq * parts, all = tiles2 * chunks;
+        const int half = L::HALVES == 1 ? 0 : lane & 1;
+        const uint32_t below = (1u << lane) - 1u;
+        int head = 0, tail = 0, at = 0, given = 0, turns[2] = {0, 0};  // batches, given back; rows, given back
+        bool ok = true;
+        for (int base = 0; ok && base < all; base += PER) {
+            const int c = base + lane / L::HALVES;
+            int cnt = 0, from = 0;  // rows of the batch, the first
+            if (c < all) {
+                const int j = c % chunks, u = j / parts;
                 const uint32_t toks = tab.utok[u];
-                const uint16_t* src = p.h + (size_t)(tab.uoff[u] + lane) * (2 * f);
-                for (int b = 0; ok && b < nb2; b += cb2, ++q) {
-                    const uint32_t bytes = 256 * min(cb2, nb2 - b);
-#pragma unroll
-                    for (int half = 0; half < L::HALVES; ++half) {
-                        const uint32_t few = L::HALVES == 1 ? toks : toks >> (16 * half) & 0xffffu;
-                        const int cnt = __popc(few);
-                        if (cnt == 0) continue;
-                        while (ok && (head - tail >= NBATCH || used + cnt > NROW)) {
-                            const int o = __shfl_sync(0xffffffffu, mine, tail % NBATCH);
-                            ok = __all_sync(0xffffffffu, tc::mbar_wait(row_empty + 8 * (o >> 8 & 255), (uint32_t)o >> 16, abort_flag, p.err));
-                            used -= o & 255;
-                            ++tail;
-                        }
-                        if (!ok) break;  // nothing is copied after a wait that gave up
-                        int turn;  // of the group's batches
-                        if (L::HALVES == 1) turn = head / L::GROUPS2;
-                        else turn = q & 1 ? turns[1]++ : turns[0]++;
-                        const int slot = q % L::GROUPS2 * L::TURNS + turn % L::TURNS;
-                        if (lane == head % NBATCH) mine = cnt | slot << 8 | (turn / L::TURNS & 1) << 16;
-                        ++head;
-                        used += cnt;
-                        const uint32_t bar = row_full + 8 * slot;
-                        if (lane == 0) tc::mbar_arrive_expect_tx(bar, cnt * bytes);
-                        __syncwarp();
-                        const int r = at + lane;
-                        if (lane < cnt)
-                            tc::bulk_load(rows_at + (r >= NROW ? r - NROW : r) * L::PITCH,
-                                          src + (size_t)(half ? __popc(toks & 0xffffu) : 0) * (2 * f) + 128 * b, bytes, bar);
-                        at += cnt;
-                        if (at >= NROW) at -= NROW;
+                from = (j - u * parts) * R + tab.uoff[u];
+                cnt = __popc(toks);
+                if (L::HALVES > 1) {
+                    const int low = __popc(toks & 0xffffu);
+                    if (cnt > 16) {
+                        cnt = half ? cnt - low : low;
+                        from += half ? low : 0;
+                    } else if (half) {
+                        cnt = 0;
                     }
                 }
             }
+            const uint32_t any = __ballot_sync(0xffffffffu, cnt > 0), odd = __ballot_sync(0xffffffffu, (q + c) & 1);
+            const int index = head + __popc(any & below);
+            int place = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, place, o);
+                if (lane >= o) place += v;
+            }
+            const int total = __shfl_sync(0xffffffffu, place, 31);
+            place += at - cnt;
+            const uint32_t ours = (q + c) & 1 ? odd : ~odd;
+            const int turn = L::HALVES == 1 ? index / L::GROUPS2 : turns[(q + c) & 1] + __popc(any & ours & below);
+            const int slot = (q + c) % L::GROUPS2 * L::TURNS + turn % L::TURNS;
+            if (base == 0) {
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(h_ready, 0, abort_flag, p.err));
+                fence_proxy_async_global();  // h was written by ordinary stores
+            }
+            bool todo = cnt > 0;
+            while (ok && __any_sync(0xffffffffu, todo)) {
+                const bool go = todo && index - tail < NBATCH && place + cnt - given <= p.nrow;
+                if (go) {
+                    tab.batches[index % (2 * NBATCH)] = cnt | slot << 8 | (turn / L::TURNS & 1) << 16;
+                    const uint32_t bar = row_full + 8 * slot;
+                    const int to = place & (p.nrow - 1), front = min(cnt, p.nrow - to);
+                    const uint8_t* src = p.h + (size_t)from * p.pitch;
+                    tc::mbar_arrive_expect_tx(bar, cnt * p.pitch);
+                    tc::bulk_load(rows_at + to * p.pitch, src, front * p.pitch, bar);
+                    if (front < cnt) tc::bulk_load(rows_at, src + (size_t)front * p.pitch, (cnt - front) * p.pitch, bar);
+                    todo = false;
+                }
+                __syncwarp();
+                if (__any_sync(0xffffffffu, go)) continue;
+                const int o = tab.batches[tail % (2 * NBATCH)];
+                ok = tc::mbar_wait(row_empty + 8 * (o >> 8 & 255), (uint32_t)o >> 16, abort_flag, p.err);
+                ok = __all_sync(0xffffffffu, ok);  // (nothing is copied after a wait that gave up)
+                given += o & 255;
+                ++tail;
+            }
+            head += __popc(any);
+            at += total;
+            turns[0] += __popc(any & ~odd);
+            turns[1] += __popc(any & odd);
+        }
     } else if (warp == FINISHER) {
         // --------------------- phase 1's sums: h = SiLU(gate) up, two columns a lane
         const int g = lane >> 2, t = lane & 3;
@@ -417,8 +451,9 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                         const float h = tab.pw[off + col] * (a / (1.f + expf(-a)) * u);
                         const uint16_t hi = bits16<BF16>(h);
                         const float rest = h - value16<BF16>(hi);
-                        const int i = tl.i0 + g;
-                        uint16_t* to = p.h + ((size_t)(off + col) * nb2 + (i >> 6)) * 128 + (i & 63);
+                        const int i = tl.i0 + g, part = (i >> 6) / cb2;
+                        auto* to = reinterpret_cast<uint16_t*>(p.h + ((size_t)part * R + off + col) * p.pitch) +
+                                   ((i >> 6) - part * cb2) * 128 + (i & 63);
                         to[0] = hi;
                         to[64] = bits16<BF16>(isfinite(rest) ? rest : 0.f);
                     }
@@ -505,8 +540,12 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             mid.step(tab, x_hi, f, nb1, cb1);
             Place1 to = mid;
             to.step(tab, x_hi, f, nb1, cb1);
-            const int units = 2 * min(cb1, nb1 - c.b), gf = min(g, c.n - 1);  // rows beyond the tile's: its last again
-            const uint32_t slot = ring + (c.q % NSLOT) * L::SLOT;
+            const int units = 2 * min(cb1, nb1 - c.b);
+            // The lines of unit gw's gate and up rows (beyond the tile's rows: its last again);
+            // those of unit gw + GW are 8 n further, at the same place of the swizzle.
+            const uint32_t slot = ring + (c.q % NSLOT) * L::SLOT, further = 1024u * c.n;
+            const int line = (gw >> 1) * 2 * c.n + min(g, c.n - 1);
+            const uint32_t gate = weights_at(slot, line, gw & 1, t), up = weights_at(slot, line + c.n, gw & 1, t);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 if (8 * n < c.cnt) {
@@ -516,9 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                     if (n == 0) wait(c.q);
 #pragma unroll
                     for (int i = 0; i < L::UNITS1; ++i) {
-                        const int unit = gw + GW * i, line = (unit >> 1) * 2 * c.n + gf;
-                        if (unit < units)
-                            mma<BF16>(acc[n], weights_at(slot, line, unit & 1, t), weights_at(slot, line + c.n, unit & 1, t), v[i]);
+                        if (gw + GW * i < units) mma<BF16>(acc[n], dec::lds128(gate + i * further), dec::lds128(up + i * further), v[i]);
                         load(i, o);
                     }
                 }
@@ -532,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
         // ---- phase 2
         tc::mbar_wait(h_ready, 0, abort_flag, p.err);
         grid_dependency_launch();  // the last phase: the next kernel may be scheduled
-        constexpr int SETS = 2;  // of accumulators: of h's values and of its rounding errors
+        constexpr int SETS = 2;  // of accumulators: of h's values and of its rounding errors (PAIR: of every second unit)
         float out[SETS][NT][4];
         const int group2 = warp / L::GW2, gw2 = warp % L::GW2, parts = ceil_div(nb2, cb2), chunks = n_uniq * parts;
         const int rows_of_all = n_uniq ? tab.uoff[n_uniq - 1] + tab.ucnt[n_uniq - 1] : 0;
@@ -541,7 +578,10 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             const int q = q1 + i * chunks;  // chunks before
 
             const Tile2 tl(rows, tiles2, i);
-            const int ga = min(g, tl.n - 1), gb = min(g + 8, tl.n - 1);  // rows beyond the tile's: its last again
+            // lines of unit gw2 of rows g and g + 8 (beyond the tile's: its last again), and from
+            // there to unit gw2 + GW2
+            const int la = (gw2 >> 1) * tl.n + min(g, tl.n - 1), lb = (gw2 >> 1) * tl.n + min(g + 8, tl.n - 1);
+            const int step = L::GW2 / 2 * tl.n;
 #pragma unroll
             for (int s = 0; s < SETS; ++s)
 #pragma unroll
@@ -554,34 +594,36 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                 // the rows before: those of earlier tiles, experts and parts
                 int at = parts * (i * rows_of_all + off) + part * __popc(toks);
                 wait(q + j);
-#pragma unroll
-                for (int half = 0; half < L::HALVES; ++half) {
-                    constexpr int NB = NT <= 2 ? NT : 2;  // groups of 8 tokens of a batch
-                    const uint32_t few = L::HALVES == 1 ? toks : toks >> (16 * half) & 0xffffu;
-                    if (L::HALVES > 1 && few == 0) continue;
+                const bool two = L::HALVES > 1 && __popc(toks) > 16;
+                for (int half = 0; half <= (int)two; ++half) {
+                    const uint32_t few = !two ? toks : half ? toks & 0xffff0000u : toks & 0xffffu;
                     // this lane's column of every 8 tokens: its row, if it has one
-                    uint32_t has[NB], row[NB];
+                    uint32_t has[NT], row[NT];
 #pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        has[n] = few >> (8 * n + g) & 1u;
-                        const int r = at + (has[n] ? __popc(few & ((1u << (8 * n + g)) - 1u)) : 0);
-                        row[n] = rows_at + (r & (NROW - 1)) * L::PITCH + 16 * t;
+                    for (int n = 0; n < NT; ++n) {
+                        const int tok = PAIR ? g & 3 : 8 * n + g;
+                        has[n] = few >> tok & 1u;
+                        const int r = at + (has[n] ? __popc(few & ((1u << tok) - 1u)) : 0);
+                        row[n] = rows_at + (r & (p.nrow - 1)) * p.pitch + 16 * t + 64 * (gw2 & 1) + 256 * (gw2 >> 1) + (PAIR ? 128 * (g >> 2) : 0);
                     }
                     const uint32_t batch = 8 * (group2 * L::TURNS + turn % L::TURNS);
                     tc::mbar_wait(row_full + batch, (uint32_t)(turn / L::TURNS) & 1u, abort_flag, p.err);
-#pragma unroll 3
+#pragma unroll(PAIR ? 4 : 3)
                     for (int i = 0; i < L::UNITS2 / L::GW2; ++i) {
-                        const int unit = gw2 + L::GW2 * i, line = (unit >> 1) * tl.n;
-                        if (unit < units) {
-                            const uint4 wa = weights_at(slot, line + ga, unit & 1, t), wb = weights_at(slot, line + gb, unit & 1, t);
-                            const uint32_t from = 256 * (unit >> 1) + 64 * (unit & 1);
+                        if (gw2 + L::GW2 * i < units) {
+                            const int line = i * step;
+                            const uint4 wa = dec::lds128(weights_at(slot, la + line, gw2 & 1, t));
+                            const uint4 wb = dec::lds128(weights_at(slot, lb + line, gw2 & 1, t));
+                            const uint32_t from = i * (128 * L::GW2);
 #pragma unroll
-                            for (int n = 0; n < NB; ++n)
-                                if (NT == 1 || (few >> (8 * n) & 255u)) {
+                            for (int n = 0; n < NT; ++n)
+                                if (PAIR) {
+                                    mma<BF16>(out[i & 1][0], wa, wb, dec::lds128_if(row[0] + from, has[0]));
+                                } else if (NT == 1 || (few >> (8 * n) & 255u)) {
                                     const uint4 hi = dec::lds128_if(row[n] + from, has[n]);
                                     const uint4 lo = dec::lds128_if(row[n] + from + 128, has[n]);
-                                    mma<BF16>(out[0][2 * half + n], wa, wb, hi);
-                                    mma<BF16>(out[1][2 * half + n], wa, wb, lo);
+                                    mma<BF16>(out[0][n], wa, wb, hi);
+                                    mma<BF16>(out[1][n], wa, wb, lo);
                                 }
                         }
                     }
@@ -605,7 +647,10 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                 const int tok = j >> 4, r = j & 15;
                 float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < CW; ++w) v += sums[(w * 8 * NT + tok) * 17 + r];
+                for (int w = 0; w < CW; ++w) {
+                    v += sums[(w * 8 * NT + tok) * 17 + r];
+                    if (PAIR) v += sums[(w * 8 * NT + tok + 4) * 17 + r];
+                }
                 if (r < tl.n) p.out[(size_t)tok * d + r_lo + tl.r0 + r] = bits16<BF16>(v);
             }
             dec::bar_sync(1, CONSUMERS);
@@ -619,11 +664,14 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
     }
 }
 
-template <bool BF16, int NT>
-cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
+template <bool BF16, int NT, bool PAIR = false>
+cudaError_t launch(const Maps& maps, Params& p, cudaStream_t s) {
+    // narrow rows: more of them
+    p.nrow = Plan<NT>::NROW;
+    while (2 * p.nrow * p.pitch <= Plan<NT>::NROW * Plan<NT>::PITCH) p.nrow *= 2;
     constexpr size_t smem = 1024 + Plan<NT>::OFF_TAB + sizeof(Tab);
     static_assert(smem <= SMEM_MOST, "shared memory");
-    cudaError_t e = allow_smem<expert_layer_kernel<BF16, NT>>();
+    cudaError_t e = allow_smem<expert_layer_kernel<BF16, NT, PAIR>>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)num_sms());
@@ -639,15 +687,37 @@ cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, expert_layer_kernel<BF16, NT>, maps, p);
+    e = cudaLaunchKernelEx(&cfg, expert_layer_kernel<BF16, NT, PAIR>, maps, p);
     if (e == cudaSuccess) note_launch();
     return e;
 }
 
+// What the sizes alone settle: a CTA's output features, q or q + 1, come in tiles of at
+// most two sizes each; chunks of as many 64-input blocks each, as fit a slot.
+struct Cut {
+    int rows2[4], cb1, cb2, pitch;
+    Cut(int d, int f) {
+        const int q = d / num_sms();
+        int most = 1;
+        for (int i = 0; i < 4; ++i) {
+            const int rows = std::max(1, q + (i & 1)), tiles = ceil_div(rows, 16);
+            rows2[i] = i < 2 ? rows / tiles : ceil_div(rows, tiles);
+            most = std::max(most, rows2[i]);
+        }
+        using L = Plan<1>;  // (the others' are the same)
+        cb1 = ceil_div(d / 64, ceil_div(d / 64, L::BLOCKS1));
+        cb2 = ceil_div(f / 64, ceil_div(f / 64, std::min(L::BLOCKS2, 16 * L::BLOCKS1 / most)));
+        pitch = 256 * cb2 + 64;
+    }
+};
+
 }  // namespace
 
 bool expert_layer_supported(int T, int k) { return T <= MAX_T && T * k <= MAX_R && k <= 32; }
-size_t expert_layer_halves(int T, int k, int f) { return (size_t)2 * T * k * f; }
+size_t expert_layer_bytes(int T, int k, int d, int f) {
+    const Cut c(d, f);
+    return (size_t)T * k * ceil_div(f / 64, c.cb2) * c.pitch;
+}
 
 cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s) {
     const bool bf = l.dtype == MOE_DT_BF16;
@@ -665,18 +735,11 @@ cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s) {
     p.E = l.E;
     p.d = l.d;
     p.f = l.f;
-    // a CTA has q or q + 1 output features, in tiles of at most two sizes each
-    const int q = l.d / num_sms();
-    int rows2 = 1;
-    for (int i = 0; i < 4; ++i) {
-        const int rows = std::max(1, q + (i & 1)), tiles = ceil_div(rows, 16);
-        p.rows2[i] = i < 2 ? rows / tiles : ceil_div(rows, tiles);
-        rows2 = std::max(rows2, p.rows2[i]);
-    }
-    // chunks of as many 64-input blocks each, as fit a slot
-    using L = Plan<1>;  // (the others' are the same)
-    p.cb1 = ceil_div(l.d / 64, ceil_div(l.d / 64, L::BLOCKS1));
-    p.cb2 = ceil_div(l.f / 64, ceil_div(l.f / 64, std::min(L::BLOCKS2, 16 * L::BLOCKS1 / rows2)));
+    const Cut c(l.d, l.f);
+    std::copy(c.rows2, c.rows2 + 4, p.rows2);
+    p.cb1 = c.cb1;
+    p.cb2 = c.cb2;
+    p.pitch = c.pitch;
     Maps maps;
     bool ok = true;
     // gate_up as [expert][64-input block][gate, up][feature][64 inputs]
@@ -692,6 +755,7 @@ cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s) {
         ok = make_tensor_map_16(&maps.w2[i], bf, l.w2, 4, d2, s2, box);
     }
     if (!ok) return cudaErrorInvalidValue;
+    if (l.T <= 4) return bf ? launch<true, 1, true>(maps, p, s) : launch<false, 1, true>(maps, p, s);
     if (l.T <= 8) return bf ? launch<true, 1>(maps, p, s) : launch<false, 1>(maps, p, s);
     if (l.T <= 16) return bf ? launch<true, 2>(maps, p, s) : launch<false, 2>(maps, p, s);
     return bf ? launch<true, 4>(maps, p, s) : launch<false, 4>(maps, p, s);

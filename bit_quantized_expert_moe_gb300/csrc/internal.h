@@ -211,10 +211,10 @@ struct ExpertLayer {
     void* out;               // [T][d]
     int32_t* ids_out;        // [T][k] or null
     uint32_t* header;        // of the workspace
-    uint16_t* h;             // expert_layer_halves() behind it
+    uint8_t* h;              // expert_layer_bytes() behind it
 };
 bool expert_layer_supported(int T, int k);
-size_t expert_layer_halves(int T, int k, int f);
+size_t expert_layer_bytes(int T, int k, int d, int f);
 cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s);
 
 // 3D tensor map over 32-bit words: dims {d0, d1, d2} (d0 contiguous), byte

@@ -108,6 +108,10 @@ CASES = [
     (12, 4, 16, 1088, 1088),
     (24, 6, 30, 192, 2112),
     (14, 3, 7, 64, 192),
+    (4, 6, 24, 640, 1600),        # h in three chunks an expert; up to 4 tokens, and 5
+    (5, 6, 24, 640, 1600),
+    (32, 8, 20, 128, 832),        # more than 16 tokens of an expert
+    (32, 4, 8, 2496, 64),         # tiles of 17 output features
 ]
 
 
