@@ -122,12 +122,14 @@ __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
 
 // Rows that other CTAs have widened with ordinary stores, about to be copied by TMA.
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
-__device__ __forceinline__ bool rows_ready(const int* count, int units, volatile int* abort_flag, uint32_t* err) {
+__device__ __forceinline__ int units_done(const int* count) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+    return v;
+}
+__device__ __forceinline__ bool wait_units(const int* count, int units, volatile int* abort_flag, uint32_t* err) {
     const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        int v;
-        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
-        if (v >= units) break;
+    for (uint32_t it = 1; units_done(count) < units; ++it)
         if ((it & 63u) == 0) {
             if (*abort_flag) return false;
             if (globaltimer_ns() - t0 > tc::WAIT_LIMIT_NS) {
@@ -136,8 +138,6 @@ __device__ __forceinline__ bool rows_ready(const int* count, int units, volatile
                 return false;
             }
         }
-    }
-    fence_proxy_async_global();
     return true;
 }
 
@@ -257,10 +257,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             int s = 0, g = 0;  // stage, stages issued so far
             uint32_t phase = 1;
             bool ok = true;
-            for (int i = pair; ok && i < work.items; i += npairs) {
-                const Item t = work.item(p, i);
-                ok = !p.counts || rows_ready(p.counts + 1 + i / work.mb, ceil_div(t.ncols, p.unit_rows), abort_flag, p.err);
+            // The next tile is looked up while the ring is full, not between two tiles
+            // (offsets, a search and a look at its rows: 0.7 us of a tile's 6).
+            Item t{}, to{};
+            bool there = !p.counts;  // the tile's rows
+            if (pair < work.items) t = work.item(p, pair);
+            for (int i = pair; ok && i < work.items; i += npairs, t = to) {
+                if (!there) ok = wait_units(p.counts + 1 + i / work.mb, ceil_div(t.ncols, p.unit_rows), abort_flag, p.err);
                 if (!ok) break;
+                if (p.counts) fence_proxy_async_global();
+                there = !p.counts;
                 const int half = mma_cols(t) >> 1, bi = (half + 15) / 16 - 1, xbytes = (bi + 1) * 16 * 128;
                 const int m = t.m0 + (int)rank * BM, c = t.c0 + (int)rank * half;
                 for (int j = 0; j < blocks; ++j, ++g) {
@@ -273,6 +279,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     if (rank == 0) tc::mbar_arrive_expect_tx(bar_xfull + 8 * s, (two ? 4 : 2) * xbytes);
                     tc::tma_load_2d_pair(sx, &maps.x[bi], xfull_lead + 8 * s, BL * j, c);
                     if (two) tc::tma_load_2d_pair(sx + X_BYTES, &maps.x[bi], xfull_lead + 8 * s, BL * j + 64, c);
+                    if (j == min(STAGES, blocks) - 1 && i + npairs < work.items) {
+                        to = work.item(p, i + npairs);
+                        if (p.counts) there = units_done(p.counts + 1 + (i + npairs) / work.mb) >= ceil_div(to.ncols, p.unit_rows);
+                    }
                     if (++s == STAGES) {
                         s = 0;
                         phase ^= 1u;
@@ -289,9 +299,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             int s = 0, ic = 0, g = 0;
             uint32_t phase = 0;
             bool ok = true;
+            int cols = pair < work.items ? mma_cols(work.item(p, pair)) : 0;  // (the next tile's: as above)
             for (int i = pair; ok && i < work.items; i += npairs, ++ic) {
-                const Item t = work.item(p, i);
-                const uint32_t idesc = tc::idesc_16_f32(2 * BM, mma_cols(t), 0, false, false);
+                const uint32_t idesc = tc::idesc_16_f32(2 * BM, cols, 0, false, false);
                 const int b = ic & 1;
                 // both CTAs' epilogues have read the accumulator
                 ok = tc::mbar_wait_cluster(bar_accempty + 8 * b, ((uint32_t)(ic >> 1) & 1u) ^ 1u, abort_flag, p.err);
@@ -313,6 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     tc::mma_commit_pair(bar_empty + 8 * s);
                     tc::mma_commit_pair(bar_aempty + 8 * a);
                     if (j == blocks - 1) tc::mma_commit_pair(bar_accfull + 8 * b);
+                    if (j == 0 && i + npairs < work.items) cols = mma_cols(work.item(p, i + npairs));
                     if (++s == STAGES) {
                         s = 0;
                         phase ^= 1u;
