@@ -310,6 +310,50 @@ def test_grouped_mm_i8(M, counts, N, K, dtype):
     assert M.get_device_error(space) == M.MOE_OK
 
 
+MANY = [([1500, 0, 700, 9, 130], 264, 2048), ([40, 33, 0, 64, 65] * 13, 72, 2064), ([300, 1, 200], 520, 8448)]
+
+
+@pytest.mark.parametrize("counts,N,K", MANY)
+def test_grouped_mm_i8_many_rows(M, counts, N, K):
+    """Rows widened beside the product: tiles of many rows and of few, one row a unit; the same
+    outputs every time, on two streams at once and as a graph."""
+    x, xs, w, ws, off, ref, _ = product_case(counts, N, K)
+    args = dev(x, xs, w, ws, off)
+    spaces = [M.workspace(M.grouped_mm_i8_workspace_size(len(xs), len(counts), N, K)) for _ in range(2)]
+    got = M.grouped_mm_i8(*args, ws=spaces[0])
+    close(got, ref, ref.abs(), 4, "y")
+    streams = [torch.cuda.Stream() for _ in spaces]
+    torch.cuda.synchronize()
+    outs = [M.grouped_mm_i8(*args, ws=space, stream=s) for _ in range(15) for s, space in zip(streams, spaces)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, got) for o in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        y = M.grouped_mm_i8(*args, ws=spaces[0])
+    for seed in (1, 2):
+        args[0].copy_(codes(seed, *x.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, M.grouped_mm_i8(*args, ws=spaces[1]))
+        assert torch.equal(y, got) == (seed == 1)  # (those are the case's own codes)
+    assert all(M.get_device_error(space) == M.MOE_OK for space in spaces)
+
+
+def test_grouped_mm_i8_many_rows_outside_the_segments(M):
+    counts, N, K = [900, 0, 1300], 72, 2048
+    x, xs, w, ws, off, ref, _ = product_case(counts, N, K)
+    big, scale = torch.zeros(len(x) + 50, K, dtype=torch.int8), torch.ones(len(x) + 50)
+    big[20:20 + len(x)], scale[20:20 + len(x)] = x, xs
+    y = torch.full((len(x) + 50, N), 7.0, dtype=BF16, device="cuda")
+    space = M.workspace(M.grouped_mm_i8_workspace_size(len(big), 3, N, K))
+    M.grouped_mm_i8(*dev(big, scale, w, ws, off + 20), y=y, ws=space)
+    close(y[20:20 + len(x)], ref, ref.abs(), 4, "y")
+    assert (y[:20] == 7).all() and (y[20 + len(x):] == 7).all()
+    y.fill_(7)
+    M.grouped_mm_i8(*dev(big, scale, w, ws, torch.tensor([0, 900, 800, 2200], dtype=torch.int32)), y=y, ws=space)
+    assert M.get_device_error(space) == 6 and (y == 7).all()
+
+
 @pytest.mark.parametrize("counts", [[7, 1], [40, 90]])
 def test_grouped_mm_i8_largest_codes(M, counts):
     """All codes at -128, and sums beyond 2^24."""

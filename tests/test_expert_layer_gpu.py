@@ -246,3 +246,43 @@ def test_against_the_stages(M):
             h = (1.1 * a.abs() * u.abs() + 2 * (a * torch.sigmoid(a) * u).abs())
             big[t] += p[t, j].item() * (w2[e].double().abs() @ h)
     assert ((chain.cpu().double() - want).abs() <= 4 * 2.0 ** -8 * big + tol).all()
+
+
+def test_two_streams(M):
+    """Calls on two streams with a workspace each: every launch needs all SMs, and none waits
+    for one that has not started."""
+    E, d, f, k, T = 16, 512, 192, 4, 9
+    cases = []
+    for i in range(2):
+        x, lg, w13, w2 = (t.cuda() for t in case(20 * i, T, k, E, d, f, BF16))
+        ws = M.workspace(M.expert_layer_workspace_size(T, k, E, d, f))
+        cases.append((torch.cuda.Stream(), x, lg, w13, w2, ws, M.expert_layer(x, lg, w13, w2, k)))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(50):
+        for s, x, lg, w13, w2, ws, want in cases:
+            outs.append((M.expert_layer(x, lg, w13, w2, k, ws=ws, stream=s), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(got, want) for got, want in outs)
+    assert all(M.get_device_error(c[5]) == M.MOE_OK for c in cases)
+
+
+def test_a_barrier_wait_that_runs_out_reports_a_timeout(M):
+    """The CTAs' arrival counter one short of a multiple of the grid: the first CTA passes, the
+    others wait until the 2 s limit.  The call ends, reports it, and the next one is right."""
+    T, k, E, d, f = 2, 2, 8, 256, 192
+    x, lg, w13, w2 = case(30, T, k, E, d, f, BF16)
+    want, tol, _ = reference(x, lg, w13, w2, k)
+    args = x.cuda(), lg.cuda(), w13.cuda(), w2.cuda(), k
+    ws = M.workspace(M.expert_layer_workspace_size(T, k, E, d, f))
+    M.expert_layer(*args, ws=ws)
+    assert M.get_device_error(ws) == M.MOE_OK
+    n_sm = torch.cuda.get_device_properties(0).multi_processor_count
+    count = ws[64:72].view(torch.int64)
+    assert int(count.item()) == n_sm
+    count.fill_(2 * n_sm - 1)
+    M.expert_layer(*args, ws=ws)
+    assert M.get_device_error(ws) == 7  # MOE_ERR_TIMEOUT
+    assert int(ws[:256].count_nonzero()) == 0
+    check(M.expert_layer(*args, ws=ws), want, tol)
+    assert M.get_device_error(ws) == M.MOE_OK
