@@ -6,14 +6,14 @@
 //
 // What counts is reading the weights of the experts that have a token, once:
 // 6 d f bytes an expert.  One CTA an SM (cooperative); one producer thread streams
-// the CTA's share of both matrices through a ring of 24 KB slots (TMA), sixteen
+// the CTA's share of both matrices through a ring of 22 KB slots (TMA), sixteen
 // warps take them from there.  The share of the down projection does not depend on h, so
 // the ring fills with it while the CTAs meet between the two products: the stream
 // does not stop there.
-//   Phase 0  every CTA routes all tokens and sorts the assignments by expert.
+//   Phase 0  every CTA routes all tokens; the touched experts' list by one scan.
 //   Phase 1  the touched experts' features, one list of n_uniq f, are split evenly
 //            over the CTAs to a single feature (its gate and its up row): tiles of 8,
-//            4, 2 or 1 features, chunks of at most 768 inputs.  h goes to memory.
+//            4, 2 or 1 features, chunks of at most 704 inputs.  p h goes to memory.
 //   Phase 2  output features, split evenly over the CTAs; a CTA goes through all
 //            touched experts for its own, so the sum over experts is its own as well:
 //            no partial sums between CTAs, a fixed order, one rounding.
@@ -23,17 +23,25 @@
 // (zeros where the expert is not the token's) and h has the weight p already, so the
 // accumulators stay over all experts.  Both operands keep K in the order
 // in which a thread's 16-byte loads bring it, as in grouped_few.cu.
-// What bounds the consumers is latency, a chunk's 0.5 us at the full rate of the stream:
-// two groups of eight warps take every second chunk, its 32-input units dealt out to
-// the warps.  In phase 1 a warp has the tokens' values of its next chunk on their way in
-// registers (they stay in L1 from tile to tile); in phase 2, where every chunk brings
-// another expert's, a warp of its own has rows of h copied to a ring of rows in shared
-// memory, a bulk copy each.  (x that way too: 8 tokens at 7168 x 2048 x 256 experts 804
-// against 769 us, 32 at 2048 x 768 x 128 432 against 208; h in registers too: one
-// token's phase 2 5.4 against 4.5 us.)  Another warp adds the sixteen warps' sums up and
-// writes h, so that none of them waits for the others.
 // p h is kept as two 16-bit numbers, the second one the rounding error of the first, so
 // the output is rounded once as if h were fp32; twice the (few) MMAs of phase 2.
+//
+// What bounds the consumers is latency, a chunk's 0.5 us at the full rate of the stream:
+//   - two groups of eight warps take every second chunk of phase 1, its 32-input units
+//     dealt out to the warps, and pairs of warps every eighth one of phase 2 (up to 8
+//     tokens);
+//   - in phase 1 a warp has the tokens' values of its next chunk on their way in
+//     registers (they stay in L1 from tile to tile); in phase 2, where every chunk brings
+//     another expert's, a warp of its own has an expert's rows of h copied to a ring of
+//     rows in shared memory, a bulk copy for all of them (one for each row, issued one
+//     after the other, took 0.3 us a row);
+//   - another warp adds the sixteen warps' sums of phase 1 up and writes h, so that none
+//     of them waits for the others.
+// 2048 x 768, 8 of 128 experts a token: 1 token 18.4 us (4.1 TB/s, 60 % of the copy's
+// rate: routing 2.2 us, the meeting 1.0, from there to the end 2.9), 8 tokens 80 us (5.9
+// TB/s), 32 tokens 190 us (5.5); 7168 x 2048, 8 of 256: 8 tokens 757 to 778 us (6.5 to 6.7).
+// One group of eight warps that all wait for each other at a tile's end: 23.6, 109, 530
+// and 1084 us; x in the ring of rows as well: 8 tokens at 7168 804, 32 at 2048 432.
 #include "decode_ops.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"
@@ -61,9 +69,10 @@ struct Plan {
     // batches, of the tokens below 16 and of the others.
     static constexpr int PITCH = BLOCKS2 * 256 + 64, NROW = NT == 1 ? 8 : 16, NBATCH = 8;
     static constexpr int HALVES = NT <= 2 ? 1 : 2;
-    // Phase 2's groups: up to 8 tokens, where a slot is one of eight's, pairs of warps, so
-    // that the latency of a chunk counts an eighth.  (One token 19.8, and 20.4 by two
-    // groups of eight.)  Barriers of a group's batches.
+    // Phase 2's groups: up to 8 tokens pairs of warps, one for each slot, so that the
+    // latency of a chunk counts an eighth.  More tokens take two groups of eight (pairs,
+    // with eight slots of 16 KB: 32 tokens at 2048 x 768 243 us for 190).  Barriers of a
+    // group's batches.
     static constexpr int GW2 = NT == 1 ? 2 : GW, GROUPS2 = CW / GW2, TURNS = NT == 1 ? 1 : NBATCH;
 
     static constexpr int NBUF = 2, SUM_FLOATS = CW * 128;        // sums of 8 tokens: [CW][32][4]

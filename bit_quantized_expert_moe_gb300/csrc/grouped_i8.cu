@@ -14,6 +14,15 @@
 // cta_group::2), each CTA with its 128 weight rows and half of the rows r.  192 and
 // not 256: two accumulators and two stages of A share the 512 columns of tensor memory.
 //
+// What bounds it: with many rows an expert the MMAs (one expert, 7296 rows, 4096 x 4096
+// 130 us, 1888 TFLOP/s of the 1968 of a 16-bit library product); with few the weights'
+// stream and their widening, whose chain of loads, arithmetic and stores a stage is as
+// long as its copy (512 tokens over 256 experts of 7168 x 2048 640 us, 6.0 TB/s; 570 without
+// the widening).  4096 Zipf-skewed tokens, 128 experts of 1536 x 2048: 167 us, 197 with the
+// rows widened by a kernel before.  Tried: 16 widening warps 174 and 711 us (skewed,
+// large); two sets of four that take every second stage 196 and 679 for 192 and 671;
+// four stages of A for tiles of 128 columns: no change.
+//
 // Warp roles (576 threads a CTA): 0 TMA producer, 1 TMEM owner and (even CTA) MMA
 // issuer, 4-11 widen the weights (warp w: TMEM lanes 32 (w % 4) .. + 31, either half
 // of a stage's 128 k), 12-15 epilogue (the same lanes), 2, 3, 16 and 17 widen rows.

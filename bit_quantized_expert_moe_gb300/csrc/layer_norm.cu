@@ -13,8 +13,9 @@
 // those whose squares leave fp32, take a second reduction, of c = x' - m0 and c^2 around
 // m0, the mean as fp32 has it (off by some 2^-24 |m|):
 //   m = m0 + mean c,  variance = mean c^2 - (mean c)^2
-// without loss, since mean c is a rounding's size.  (Two reductions for every row: 4096 x
-// 2048 15.0 us, gradients 20.0.)
+// without loss, since mean c is a rounding's size.
+// 4096 x 7168 with the residual 41 us (5.7 TB/s, 84 % of the copy's rate), 4096 x 2048
+// 13.0 (5.2 TB/s); with two reductions for every row 15.0.
 #include "layer_norm.cuh"
 
 namespace moe {

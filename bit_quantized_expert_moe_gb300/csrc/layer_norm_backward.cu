@@ -3,7 +3,9 @@
 //   n  = (x' - m) r,  v = dh gamma
 //   dx = dx' + r (v - mean v - n mean(v n));  dgamma = sum dh n,  dbeta = sum dh
 // x' is the stored one, the value that every later reader sees.  Each tensor is
-// read and written once: bound by memory.
+// read and written once: bound by memory for many rows, by the latency of two launches
+// for few.  4096 x 2048 18.1 us (3.7 TB/s), of which a call of 100 rows takes 7.2; with two
+// reductions a row 20.0, with one chunk a thread (two row groups for four) 22.9.
 #include "layer_norm.cuh"
 
 namespace moe {
@@ -196,7 +198,8 @@ __global__ void __launch_bounds__(1024) layer_norm_reduce_kernel(const Args p) {
 }
 
 // One block an SM with as many row groups as its threads hold (15 named barriers),
-// fewer where the rows are few.
+// fewer where the rows are few.  640 threads: the same times; 768, which spill: 22.7 us
+// at 4096 x 2048 for 18.1.
 struct Plan {
     int vpt, threads, groups, rows, blocks;
 };

@@ -410,7 +410,7 @@ moe_status_t moe_grouped_mm_i8(moe_dtype_t out_dtype, const int8_t* x, const flo
  * moe_route_topk (logits may be -inf), then for token t with experts e_j and weights p_j
  *   out[t] = sum_j p_j Wd[e_j] (SiLU(Wg[e_j] x[t]) * (Wu[e_j] x[t]))
  * in bf16 or fp16 with fp32 accumulation and one rounding at the end (fp16: every
- * SiLU * up has to be below 65504).
+ * p * SiLU * up has to be below 65504).
  *   x       device [T][d_model]      logits  device fp32 [T][E]
  *   w13     device [E][2 d_ff][d_model], the gate's rows first
  *   w2      device [E][d_model][d_ff]
@@ -422,7 +422,8 @@ moe_status_t moe_grouped_mm_i8(moe_dtype_t out_dtype, const int8_t* x, const flo
  * (MOE_ERR_DEVICE_RANGE by moe_get_device_error).  One CTA on every SM (cooperative
  * launch), which meet once: calls that share a workspace must not overlap.
  * Workspace: >= moe_expert_layer_workspace_size(...) bytes, zeroed before its first use;
- * one for the most tokens also does for fewer.
+ * one for the most tokens also does for fewer (the size depends on the current device's
+ * SMs).  A CTA whose wait for the others runs out (2 s) gives MOE_ERR_TIMEOUT.
  */
 size_t moe_expert_layer_workspace_size(int32_t T, int32_t k, int32_t E, int32_t d_model, int32_t d_ff);
 moe_status_t moe_expert_layer(moe_dtype_t dtype, const void* x, const float* logits, const void* w13, const void* w2,
