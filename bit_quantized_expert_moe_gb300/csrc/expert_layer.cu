@@ -19,12 +19,15 @@
 //            no partial sums between CTAs, a fixed order, one rounding.
 // mma.sync m16n8k16 with the weight rows as M (phase 1: 8 features' gate rows and their
 // up rows, so that a thread has both) and an expert's tokens as N, 8 at a time: at a
-// few tokens an expert the tensor rate is no bound.  In phase 2 a column is a token
-// (zeros where the expert is not the token's) and h has the weight p already, so the
-// accumulators stay over all experts.  Both operands keep K in the order
+// few tokens an expert the tensor rate is no bound.  Both operands keep K in the order
 // in which a thread's 16-byte loads bring it, as in grouped_few.cu.
-// p h is kept as two 16-bit numbers, the second one the rounding error of the first, so
-// the output is rounded once as if h were fp32; twice the (few) MMAs of phase 2.
+// h has the weight p already and is kept as two 16-bit numbers, the second one the
+// rounding error of the first, so the output is rounded once as if h were fp32.  In phase
+// 2, up to 8 tokens, a column is a token (zeros where the expert is not the token's), so
+// the accumulators stay over all experts.  For more tokens, where most columns would be
+// empty (32 tokens: 190 us), the columns are an expert's tokens and a warp adds them to its
+// sums in shared memory.  Up to four tokens, or rows, h and its error are columns of one
+// MMA.
 //
 // What bounds the consumers is latency, a chunk's 0.5 us at the full rate of the stream:
 //   - two groups of eight warps take every second chunk of phase 1, its 32-input units
@@ -39,9 +42,11 @@
 //     of them waits for the others.
 // 2048 x 768, 8 of 128 experts a token: 1 token 18.4 us (4.1 TB/s, 60 % of the copy's
 // rate: routing 2.2 us, the meeting 1.0, from there to the end 2.9), 8 tokens 80 us (5.9
-// TB/s), 32 tokens 190 us (5.5); 7168 x 2048, 8 of 256: 8 tokens 757 to 778 us (6.5 to 6.7).
+// TB/s), 32 tokens 178 us (5.9); 7168 x 2048, 8 of 256: 8 tokens 757 to 778 us (6.5 to 6.7).
 // One group of eight warps that all wait for each other at a tile's end: 23.6, 109, 530
 // and 1084 us; x in the ring of rows as well: 8 tokens at 7168 804, 32 at 2048 432.
+#include <type_traits>
+
 #include "decode_ops.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"
@@ -578,8 +583,19 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
         // ---- phase 2
         tc::mbar_wait(h_ready, 0, abort_flag, p.err);
         grid_dependency_launch();  // the last phase: the next kernel may be scheduled
-        constexpr int SETS = 2;  // of accumulators: of h's values and of its rounding errors (PAIR: of every second unit)
-        float out[SETS][NT][4];
+        constexpr int SETS = 2;  // of accumulators: of h's values and of its errors, or (both in one) of every second unit
+        float out[SETS][NT == 1 ? 1 : 2][4];
+        auto clear_out = [&] {
+#pragma unroll
+            for (int s = 0; s < SETS; ++s)
+#pragma unroll
+                for (int n = 0; n < (NT == 1 ? 1 : 2); ++n) out[s][n][0] = out[s][n][1] = out[s][n][2] = out[s][n][3] = 0.f;
+        };
+        // a warp's sums: NT = 1: at the end of a tile; else all along
+        float* mine = sums + warp * (8 * NT * 17);
+        if (NT > 1)
+            for (int i = lane; i < 8 * NT * 17; i += 32) mine[i] = 0.f;
+        __syncwarp();
         const int group2 = warp / L::GW2, gw2 = warp % L::GW2, parts = ceil_div(nb2, cb2), chunks = n_uniq * parts;
         const int rows_of_all = n_uniq ? tab.uoff[n_uniq - 1] + tab.ucnt[n_uniq - 1] : 0;
         int turn = 0;  // this group's batches before
@@ -591,10 +607,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             // there to unit gw2 + GW2
             const int la = (gw2 >> 1) * tl.n + min(g, tl.n - 1), lb = (gw2 >> 1) * tl.n + min(g + 8, tl.n - 1);
             const int step = L::GW2 / 2 * tl.n;
-#pragma unroll
-            for (int s = 0; s < SETS; ++s)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) out[s][n][0] = out[s][n][1] = out[s][n][2] = out[s][n][3] = 0.f;
+            clear_out();
             for (int j = (group2 - q) & (L::GROUPS2 - 1); j < chunks; j += L::GROUPS2) {
                 const int u = j / parts, part = j - u * parts, off = tab.uoff[u];
                 const uint32_t toks = tab.utok[u];
@@ -606,59 +619,92 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                 const bool two = L::HALVES > 1 && __popc(toks) > 16;
                 for (int half = 0; half <= (int)two; ++half) {
                     const uint32_t few = !two ? toks : half ? toks & 0xffff0000u : toks & 0xffffu;
-                    // this lane's column of every 8 tokens: its row, if it has one
-                    uint32_t has[NT], row[NT];
+                    const int cnt = __popc(few);
+                    const bool pair = PAIR || (NT > 1 && cnt <= 4);
+                    // this lane's column of every 8: its row, if it has one
+                    constexpr int NB = NT == 1 ? 1 : 2;
+                    uint32_t has[NB], row[NB];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const int tok = PAIR ? g & 3 : 8 * n + g;
-                        has[n] = few >> tok & 1u;
-                        const int r = at + (has[n] ? __popc(few & ((1u << tok) - 1u)) : 0);
-                        row[n] = rows_at + (r & (p.nrow - 1)) * p.pitch + 16 * t + 64 * (gw2 & 1) + 256 * (gw2 >> 1) + (PAIR ? 128 * (g >> 2) : 0);
+                    for (int n = 0; n < NB; ++n) {
+                        const int col = pair ? g & 3 : 8 * n + g;
+                        has[n] = NT == 1 ? few >> col & 1u : col < cnt;
+                        const int r = at + (NT > 1 ? col : has[n] ? __popc(few & ((1u << col) - 1u)) : 0);
+                        row[n] = rows_at + (r & (p.nrow - 1)) * p.pitch + 16 * t + 64 * (gw2 & 1) + 256 * (gw2 >> 1) + (pair ? 128 * (g >> 2) : 0);
                     }
                     const uint32_t batch = 8 * (group2 * L::TURNS + turn % L::TURNS);
                     tc::mbar_wait(row_full + batch, (uint32_t)(turn / L::TURNS) & 1u, abort_flag, p.err);
-#pragma unroll(PAIR ? 4 : 3)
-                    for (int i = 0; i < L::UNITS2 / L::GW2; ++i) {
-                        if (gw2 + L::GW2 * i < units) {
-                            const int line = i * step;
-                            const uint4 wa = dec::lds128(weights_at(slot, la + line, gw2 & 1, t));
-                            const uint4 wb = dec::lds128(weights_at(slot, lb + line, gw2 & 1, t));
-                            const uint32_t from = i * (128 * L::GW2);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                if (PAIR) {
+                    auto units_of = [&](auto both, auto wide) {
+                        constexpr bool BOTH = decltype(both)::value, WIDE = decltype(wide)::value;
+#pragma unroll(BOTH ? 4 : 3)
+                        for (int i = 0; i < L::UNITS2 / L::GW2; ++i) {
+                            if (gw2 + L::GW2 * i < units) {
+                                const int line = i * step;
+                                const uint4 wa = dec::lds128(weights_at(slot, la + line, gw2 & 1, t));
+                                const uint4 wb = dec::lds128(weights_at(slot, lb + line, gw2 & 1, t));
+                                const uint32_t from = i * (128 * L::GW2);
+                                if (BOTH) {
                                     mma<BF16>(out[i & 1][0], wa, wb, dec::lds128_if(row[0] + from, has[0]));
-                                } else if (NT == 1 || (few >> (8 * n) & 255u)) {
-                                    const uint4 hi = dec::lds128_if(row[n] + from, has[n]);
-                                    const uint4 lo = dec::lds128_if(row[n] + from + 128, has[n]);
-                                    mma<BF16>(out[0][n], wa, wb, hi);
-                                    mma<BF16>(out[1][n], wa, wb, lo);
+                                } else {
+#pragma unroll
+                                    for (int n = 0; n < (WIDE ? NB : 1); ++n) {
+                                        const uint4 hi = dec::lds128_if(row[n] + from, has[n]);
+                                        const uint4 lo = dec::lds128_if(row[n] + from + 128, has[n]);
+                                        mma<BF16>(out[0][n], wa, wb, hi);
+                                        mma<BF16>(out[1][n], wa, wb, lo);
+                                    }
                                 }
+                            }
                         }
+                    };
+                    if constexpr (NT == 1) {
+                        units_of(std::integral_constant<bool, PAIR>{}, std::false_type{});
+                    } else {
+                        if (pair) units_of(std::true_type{}, std::false_type{});
+                        else if (cnt <= 8) units_of(std::false_type{}, std::false_type{});
+                        else units_of(std::false_type{}, std::true_type{});
+                        // columns 2 t and 2 t + 1, rows g and g + 8, into the tokens' sums
+                        const int first = off + (half ? __popc(toks & 0xffffu) : 0);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            float v[4];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                v[c] = out[0][n][c] + out[1][n][c];
+                                const float error = __shfl_xor_sync(0xffffffffu, v[c], 2);  // four columns further
+                                if (pair) v[c] += error;
+                            }
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const int col = 8 * n + 2 * t + c;
+                                if (col < cnt) {
+                                    float* o = mine + tab.tok[first + col] * 17 + g;
+                                    o[0] += v[c];
+                                    o[8] += v[2 + c];
+                                }
+                            }
+                        }
+                        clear_out();
                     }
                     __syncwarp();
                     if (lane < GW / L::GW2) tc::mbar_arrive(row_empty + batch);
                     ++turn;
-                    at += __popc(few);
+                    at += cnt;
                 }
                 if (lane < GW / L::GW2) tc::mbar_arrive(empty + 8 * ((q + j) % NSLOT));
             }
-            // columns 2 t and 2 t + 1, rows g and g + 8
-            float* mine = sums + warp * (8 * NT * 17);
+            if (NT == 1)  // columns 2 t and 2 t + 1, rows g and g + 8
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    mine[(8 * n + 2 * t + (c & 1)) * 17 + g + 4 * (c & 2)] = out[0][n][c] + out[1][n][c];
-                }
+                for (int c = 0; c < 4; ++c) mine[(2 * t + (c & 1)) * 17 + g + 4 * (c & 2)] = out[0][0][c] + out[1][0][c];
             dec::bar_sync(1, CONSUMERS);
             for (int j = threadIdx.x; j < p.T * 16; j += CONSUMERS) {
                 const int tok = j >> 4, r = j & 15;
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < CW; ++w) {
-                    v += sums[(w * 8 * NT + tok) * 17 + r];
-                    if (PAIR) v += sums[(w * 8 * NT + tok + 4) * 17 + r];
+                    float* o = sums + (w * 8 * NT + tok) * 17 + r;
+                    v += *o;
+                    if (PAIR) v += o[4 * 17];
+                    if (NT > 1) *o = 0.f;
                 }
                 if (r < tl.n) p.out[(size_t)tok * d + r_lo + tl.r0 + r] = bits16<BF16>(v);
             }
