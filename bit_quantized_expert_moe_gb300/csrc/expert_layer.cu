@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             for (int j = threadIdx.x; j < p.T * 16; j += CONSUMERS) {
                 const int tok = j >> 4, r = j & 15;
                 float v = 0.f;
-#pragma unroll
+#pragma unroll 4  // (run once or a few times: what counts is that little code is fetched)
                 for (int w = 0; w < CW; ++w) {
                     float* o = sums + (w * 8 * NT + tok) * 17 + r;
                     v += *o;
