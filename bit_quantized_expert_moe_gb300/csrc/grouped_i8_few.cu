@@ -15,7 +15,7 @@
 namespace moe {
 namespace {
 
-constexpr int ROWS = 16, COLS = 8, AHEAD = 4;
+constexpr int ROWS = 16, COLS = 8;
 
 __device__ __forceinline__ uint4 load_codes(const int8_t* p) {
     uint4 r;
@@ -30,7 +30,7 @@ __device__ __forceinline__ void mma16832(int (&c)[4], uint32_t a0, uint32_t a1, 
 }
 
 // This warp's part of K [k0, k1) of the products of weight rows wa and wb with RW rows.
-template <int RW>
+template <int RW, int AHEAD>
 __device__ __forceinline__ void dots(const int8_t* wa, const int8_t* wb, const int8_t* x, size_t ld, int k0, int k1, int t,
                                      int (&acc)[RW][2]) {
     for (int k = k0; k < k1; k += 64 * AHEAD) {
@@ -58,7 +58,8 @@ __device__ __forceinline__ void dots(const int8_t* wa, const int8_t* wb, const i
     }
 }
 
-template <int WARPS>
+// AHEAD: pairs of weight loads under way.
+template <int WARPS, int AHEAD>
 __global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const GroupedI8Shape g, const GroupedI8Data d) {
     __shared__ int seg[3];
     __shared__ int part[WARPS][COLS][ROWS + 1];
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const Groupe
     auto few = [&](auto n) {
         constexpr int RW = decltype(n)::value;
         int acc[RW][2] = {};
-        dots<RW>(wa, wb, x0, ld, k0, k1, t, acc);
+        dots<RW, AHEAD>(wa, wb, x0, ld, k0, k1, t, acc);
 #pragma unroll
         for (int j = 0; j < RW; ++j)
 #pragma unroll
@@ -138,11 +139,12 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const Groupe
         part[warp][2 * t + 1][gi + 8] = acc[3];
     }
     __syncthreads();
-    const int col = threadIdx.x / ROWS, n = threadIdx.x % ROWS;
-    if (col < rows && n0 + n < g.N) {  // (the first 128 threads)
+    for (int i = threadIdx.x; i < COLS * ROWS; i += 32 * WARPS) {
+        const int col = i / ROWS, n = i % ROWS;
+        if (col >= rows || n0 + n >= g.N) continue;
         int s = 0;
 #pragma unroll
-        for (int i = 0; i < WARPS; ++i) s += part[i][col][n];
+        for (int w = 0; w < WARPS; ++w) s += part[w][col][n];
         const float v = (float)s * __ldg(d.w_scale + (size_t)e * g.N + n0 + n) * __ldg(d.x_scale + r + col);
         static_cast<uint16_t*>(d.y)[(size_t)(r + col) * g.N + n0 + n] =
             g.out == MOE_DT_BF16 ? float_to_bf16_bits(v) : float_to_f16_bits(v);
@@ -151,13 +153,24 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const Groupe
 
 }  // namespace
 
-// Warps that share K: four, more where the blocks leave SMs without loads under way.
+// Warps that share K: four, more where the blocks leave SMs without loads under way (two:
+// 8 rows of 1536 x 2048 7.9 us for 6.4, 32 of 2048 x 768 9.8 for 9.4; eight 7.8 and 14.7).
+// Of the four, each asks for its part of K at once, or in as few and as even rounds as
+// 8 pairs of loads allow: with 4, 8 and 3 pairs 8 rows of 1536 x 2048 6.8, 6.4 us; 32 rows of
+// 2048 x 768 10.8, 11.7 and 9.4.
 cudaError_t launch_grouped_i8_few(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s) {
     const dim3 grid(ceil_div(g.N, ROWS), g.R);
     // blocks with work, at most
     const long long blocks = (long long)grid.x * std::min(g.R, g.E + g.R / COLS);
     const int warps = blocks > 4 * num_sms() ? 4 : blocks > 2 * num_sms() || g.K < 2048 ? 8 : 16;
-    auto* kernel = warps == 4 ? grouped_i8_few_kernel<4> : warps == 8 ? grouped_i8_few_kernel<8> : grouped_i8_few_kernel<16>;
+    const int units = ceil_div(g.K, 64 * 4), ahead = ceil_div(units, ceil_div(units, 8));
+    auto* kernel = warps == 16  ? grouped_i8_few_kernel<16, 4>
+                   : warps == 8 ? grouped_i8_few_kernel<8, 4>
+                   : ahead > 6  ? grouped_i8_few_kernel<4, 8>
+                   : ahead > 4  ? grouped_i8_few_kernel<4, 6>
+                   : ahead > 3  ? grouped_i8_few_kernel<4, 4>
+                   : ahead > 2  ? grouped_i8_few_kernel<4, 3>
+                                : grouped_i8_few_kernel<4, 2>;
     return launch_overlapped(kernel, grid, dim3(32 * warps), 0, s, g, d);
 }
 
