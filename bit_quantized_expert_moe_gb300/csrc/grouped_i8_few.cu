@@ -1,9 +1,9 @@
 // y = (x W_e^T) by the rows' and the output channels' scales, of 8-bit codes, for a
 // handful of rows in all or for about one an expert: decoding.
 //
-// As for 16-bit weights (grouped_few.cu) the weights' bytes are all that counts: a
-// block takes 16 weight rows of one expert and up to 8 of its rows, its warps share K
-// and add up in shared memory.  Integer sums, exact in any order; one rounding at the
+// As for 16-bit weights (grouped_few.cu) the weights' bytes are all that counts: KW
+// warps take 16 weight rows of one expert and up to 8 of its rows; they share K and add
+// up in shared memory.  Integer sums, exact in any order; one rounding at the
 // end.  Lane 4 g + t holds elements 16 t .. 16 t + 15 of every 64 for weight rows g and
 // g + 8.  Up to four rows by dp4a, a row at a time; more by mma.sync m16n8k32, which
 // runs at 1/11 of the 16-bit rate here and, at one row, costs more than the weights:
@@ -59,7 +59,7 @@ __device__ __forceinline__ void dots(const int8_t* wa, const int8_t* wb, const i
 }
 
 // AHEAD: pairs of weight loads under way.
-template <int WARPS, int AHEAD>
+template <int WARPS, int AHEAD, int KW = WARPS>
 __global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const GroupedI8Shape g, const GroupedI8Data d) {
     __shared__ int seg[3];
     __shared__ int part[WARPS][COLS][ROWS + 1];
@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const Groupe
     __syncthreads();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.y, n0 = blockIdx.x * ROWS;
+    constexpr int NW = WARPS / KW;  // times 16 weight rows
+    const int r = blockIdx.y, n0 = (blockIdx.x * NW + warp / KW) * ROWS;
     // the row's expert and its segment
     bool bad = false;
     for (int i = threadIdx.x; i < g.E; i += 32 * WARPS) {
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const Groupe
     const int rows = min(COLS, r1 - r);
 
     const int gi = lane >> 2, t = lane & 3;
-    const int kq = ceil_div(g.K, 64 * WARPS) * 64, k0 = warp * kq, k1 = min(g.K, k0 + kq);
+    const int kq = ceil_div(g.K, 64 * KW) * 64, k0 = warp % KW * kq, k1 = min(g.K, k0 + kq);
     const size_t ld = (size_t)g.K;
     const int8_t* wa = d.w + ((size_t)e * g.N + min(n0 + gi, g.N - 1)) * ld + 16 * t;
     const int8_t* wb = d.w + ((size_t)e * g.N + min(n0 + gi + 8, g.N - 1)) * ld + 16 * t;
@@ -139,14 +140,14 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const Groupe
         part[warp][2 * t + 1][gi + 8] = acc[3];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < COLS * ROWS; i += 32 * WARPS) {
-        const int col = i / ROWS, n = i % ROWS;
-        if (col >= rows || n0 + n >= g.N) continue;
+    for (int i = threadIdx.x; i < NW * COLS * ROWS; i += 32 * WARPS) {
+        const int nw = i / (COLS * ROWS), col = i / ROWS % COLS, n = (blockIdx.x * NW + nw) * ROWS + i % ROWS;
+        if (col >= rows || n >= g.N) continue;
         int s = 0;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) s += part[w][col][n];
-        const float v = (float)s * __ldg(d.w_scale + (size_t)e * g.N + n0 + n) * __ldg(d.x_scale + r + col);
-        static_cast<uint16_t*>(d.y)[(size_t)(r + col) * g.N + n0 + n] =
+        for (int w = 0; w < KW; ++w) s += part[nw * KW + w][col][i % ROWS];
+        const float v = (float)s * __ldg(d.w_scale + (size_t)e * g.N + n) * __ldg(d.x_scale + r + col);
+        static_cast<uint16_t*>(d.y)[(size_t)(r + col) * g.N + n] =
             g.out == MOE_DT_BF16 ? float_to_bf16_bits(v) : float_to_f16_bits(v);
     }
 }
@@ -157,20 +158,25 @@ __global__ void __launch_bounds__(32 * WARPS) grouped_i8_few_kernel(const Groupe
 // 8 rows of 1536 x 2048 7.9 us for 6.4, 32 of 2048 x 768 9.8 for 9.4; eight 7.8 and 14.7).
 // Of the four, each asks for its part of K at once, or in as few and as even rounds as
 // 8 pairs of loads allow: with 4, 8 and 3 pairs 8 rows of 1536 x 2048 6.8, 6.4 us; 32 rows of
-// 2048 x 768 10.8, 11.7 and 9.4.
+// 2048 x 768 10.8, 11.7 and 9.4.  Where K is short, two of them or each one has weight rows
+// of its own: a block's set-up takes longer than its part of K
+// (105 rows, 176 experts of 2704 x 176 21.8 -> 10.3 us, 75 rows, 249 of 3272 x 128 8.1 -> 5.0,
+// 16 rows, 128 of 2048 x 512 7.8 -> 7.0).
 cudaError_t launch_grouped_i8_few(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s) {
-    const dim3 grid(ceil_div(g.N, ROWS), g.R);
-    // blocks with work, at most
-    const long long blocks = (long long)grid.x * std::min(g.R, g.E + g.R / COLS);
+    // blocks with work, at most, if all warps share K
+    const long long blocks = (long long)ceil_div(g.N, ROWS) * std::min(g.R, g.E + g.R / COLS);
     const int warps = blocks > 4 * num_sms() ? 4 : blocks > 2 * num_sms() || g.K < 2048 ? 8 : 16;
-    const int units = ceil_div(g.K, 64 * 4), ahead = ceil_div(units, ceil_div(units, 8));
+    const int share = warps > 4 || g.K > 512 ? warps : g.K > 256 ? 2 : 1;
+    const int units = ceil_div(g.K, 64 * share), ahead = ceil_div(units, ceil_div(units, 8));
     auto* kernel = warps == 16  ? grouped_i8_few_kernel<16, 4>
                    : warps == 8 ? grouped_i8_few_kernel<8, 4>
+                   : share == 1 ? grouped_i8_few_kernel<4, 4, 1>
+                   : share == 2 ? grouped_i8_few_kernel<4, 4, 2>
                    : ahead > 6  ? grouped_i8_few_kernel<4, 8>
                    : ahead > 4  ? grouped_i8_few_kernel<4, 6>
                    : ahead > 3  ? grouped_i8_few_kernel<4, 4>
-                   : ahead > 2  ? grouped_i8_few_kernel<4, 3>
-                                : grouped_i8_few_kernel<4, 2>;
+                                : grouped_i8_few_kernel<4, 3>;
+    const dim3 grid(ceil_div(g.N, ROWS * (warps / share)), g.R);
     return launch_overlapped(kernel, grid, dim3(32 * warps), 0, s, g, d);
 }
 

@@ -310,6 +310,18 @@ def test_grouped_mm_i8(M, counts, N, K, dtype):
     assert M.get_device_error(space) == M.MOE_OK
 
 
+SHORT = [([1, 0, 3, 1, 0, 9] * 2, 1000, 176), ([2, 1, 0, 1] * 25, 328, 16), ([1, 0, 2, 17, 0, 12], 1048, 336),
+         ([1, 1, 0, 1] * 30, 200, 512)]
+
+
+@pytest.mark.parametrize("counts,N,K", SHORT)
+def test_grouped_mm_i8_few_rows_short_k(M, counts, N, K):
+    """Many experts of few rows each and a short K: warps with weight rows of their own, some
+    of them behind N."""
+    x, xs, w, ws, off, ref, _ = product_case(counts, N, K)
+    close(M.grouped_mm_i8(*dev(x, xs, w, ws, off)), ref, ref.abs(), 4, "y")
+
+
 MANY = [([1500, 0, 700, 9, 130], 264, 2048), ([40, 33, 0, 64, 65] * 13, 72, 2064), ([300, 1, 200], 520, 8448)]
 
 
