@@ -16,7 +16,7 @@ and, for 16-bit experts and training (expert16.py):
     block_norm_backward_workspace_size
 and, for expert blocks in 8 and 16 bits (expert16.py too):
     layer_norm, layer_norm_backward, layer_norm_backward_workspace_size,
-    quantize_rows, grouped_mm_i8, grouped_mm_i8_workspace_size,
+    quantize_rows, quantize_rows_workspace_size, grouped_mm_i8, grouped_mm_i8_workspace_size,
     expert_layer, expert_layer_workspace_size
 """
 from __future__ import annotations
@@ -88,7 +88,8 @@ def lib() -> ctypes.CDLL:
             "moe_layer_norm": (I32, [I32] * 4 + [F] + [V] * 7),
             "moe_layer_norm_backward_workspace_size": (SZ, [I32] * 2),
             "moe_layer_norm_backward": (I32, [I32] * 4 + [F] + [V] * 8 + [SZ, V]),
-            "moe_quantize_rows": (I32, [I32, V, V] + [I32] * 4 + [V] * 3),
+            "moe_quantize_rows": (I32, [I32, V, V] + [I32] * 4 + [V, V, V, SZ, V]),
+            "moe_quantize_rows_workspace_size": (SZ, [I32] * 3),
             "moe_grouped_mm_i8_workspace_size": (SZ, [I32] * 4),
             "moe_grouped_mm_i8": (I32, [I32] + [V] * 5 + [I32] * 4 + [V, V, SZ, V]),
             "moe_expert_layer_workspace_size": (SZ, [I32] * 5),
@@ -342,7 +343,8 @@ def get_device_error(ws: torch.Tensor, stream=None) -> int:
 
 from . import expert16 as _expert16_loader  # noqa: E402
 from .expert16 import (block_norm_backward_workspace_size, expert_layer_workspace_size,  # noqa: E402, F401
-                       grouped_mm_i8_workspace_size, grouped_mm_workspace_size, layer_norm_backward_workspace_size)
+                       grouped_mm_i8_workspace_size, grouped_mm_workspace_size, layer_norm_backward_workspace_size,
+                       quantize_rows_workspace_size)
 
 
 def __getattr__(name: str):

@@ -84,14 +84,21 @@ moe_status_t moe_layer_norm_backward(moe_dtype_t dtype, moe_dtype_t param_dtype,
     return cuda_status(launch_layer_norm_backward(n, LayerNormGrads{x_out, dh, dx_out, dx, dgamma, dbeta}, part, stream));
 }
 
+size_t moe_quantize_rows_workspace_size(int32_t T, int32_t R, int32_t D) {
+    if (T < 1 || R < 0 || T > MAX_ROWS || R > MAX_ROWS || !width_supported(D, 16, MAX_WIDTH)) return 0;
+    return quantize_rows_bytes(T, R, D);
+}
+
 moe_status_t moe_quantize_rows(moe_dtype_t dtype, const void* x, const int32_t* row_map, int32_t k, int32_t T, int32_t R,
-                               int32_t D, int8_t* codes, float* scales, cudaStream_t stream) {
+                               int32_t D, int8_t* codes, float* scales, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream) {
     if (T < 0 || R < 0 || D < 1 || k < 1 || (!row_map && R != T && R > 0)) return MOE_ERR_INVALID_ARG;
     if (!row_type(dtype) || T > MAX_ROWS || R > MAX_ROWS || !width_supported(D, 16, MAX_WIDTH)) return MOE_ERR_UNSUPPORTED;
     if (R == 0) return MOE_OK;
     if ((T > 0 && !x) || !codes || !scales) return MOE_ERR_INVALID_ARG;
-    if (!all_aligned({x, row_map, codes, scales})) return MOE_ERR_MISALIGNED;
-    return cuda_status(launch_quantize_rows(dtype, x, row_map, k, T, R, D, codes, scales, stream));
+    if (!all_aligned({x, row_map, codes, scales, workspace})) return MOE_ERR_MISALIGNED;
+    if (workspace && workspace_bytes < moe_quantize_rows_workspace_size(T, R, D)) return MOE_ERR_WORKSPACE;
+    return cuda_status(launch_quantize_rows(dtype, x, row_map, k, T, R, D, codes, scales, workspace, stream));
 }
 
 size_t moe_grouped_mm_i8_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K) {

@@ -496,9 +496,9 @@ PyObject* py_layer_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n,
 // ------------------------------------------------------------- 8-bit experts
 PyObject* py_quantize_rows(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     return guarded([&] {
-        static const auto names = intern<6>({"x", "row_map", "k", "codes", "scales", "stream"});
-        const Args<6> a("quantize_rows", names, 1, args, n, kw);
-        const Tensor x = a.needed_tensor(0), map = a.tensor(1), codes0 = a.tensor(3), scales0 = a.tensor(4);
+        static const auto names = intern<7>({"x", "row_map", "k", "codes", "scales", "ws", "stream"});
+        const Args<7> a("quantize_rows", names, 1, args, n, kw);
+        const Tensor x = a.needed_tensor(0), map = a.tensor(1), codes0 = a.tensor(3), scales0 = a.tensor(4), ws0 = a.tensor(5);
         dims("x", x, 2);
         const moe_dtype_t dt = moe_type(x.scalar_type());
         if (map.defined()) {
@@ -506,11 +506,15 @@ PyObject* py_quantize_rows(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
             want("row_map", map, {map.size(0)}, at::kInt);
         }
         const int64_t T = x.size(0), D = x.size(1), R = map.defined() ? map.size(0) : T, k = a.integer(2, 1);
-        on_one_device({x, map, codes0, scales0});
-        const OnStream on(a, 5, x);
+        on_one_device({x, map, codes0, scales0, ws0});
+        const OnStream on(a, 6, x);
         const Tensor codes = output(codes0, "codes", x, {R, D}, at::kChar), scales = output(scales0, "scales", x, {R}, at::kFloat);
+        // (without a map R = T, and none is needed)
+        const size_t need = moe_quantize_rows_workspace_size(size32(T), size32(R), size32(D));
+        const Tensor ws = need && !ws0.defined() ? workspace(ws0, need, x) : ws0;
         check(moe_quantize_rows(dt, ptr(x), ptr_as<int32_t>(map), size32(k), size32(T), size32(R), size32(D),
-                                ptr_as<int8_t>(codes), ptr_as<float>(scales), on.s), "moe_quantize_rows");
+                                ptr_as<int8_t>(codes), ptr_as<float>(scales), ptr(ws), ws.defined() ? (size_t)ws.numel() : 0, on.s),
+              "moe_quantize_rows");
         return wrap_all({codes, scales});
     });
 }
@@ -615,7 +619,7 @@ PyMethodDef methods[] = {
      "Gradients of layer_norm at the stored x_out (x, where there is no y); dx is that of x and of y.  None for the\n"
      "gradient of what was not there."},
     {"quantize_rows", FAST(py_quantize_rows),
-     "quantize_rows(x, row_map=None, k=1, codes=None, scales=None, stream=None) -> (codes, scales)\n\n"
+     "quantize_rows(x, row_map=None, k=1, codes=None, scales=None, ws=None, stream=None) -> (codes, scales)\n\n"
      "For v = x[row_map[r] // k] (x[r] without a map): scales[r] = max|v| / 127 and codes[r] = 127 v / max|v|, rounded\n"
      "to nearest even.  row_map is `sorted` of permute(), k its choices a token.  A row that is not finite has scale NaN."},
     {"grouped_mm_i8", FAST(py_grouped_mm_i8),

@@ -181,8 +181,9 @@ cudaError_t launch_layer_norm(const LayerNormShape& n, const void* x, const void
 cudaError_t launch_layer_norm_backward(const LayerNormShape& n, const LayerNormGrads& g, float* part, cudaStream_t s);
 
 // Rows x[row_map[r] / k] (x[r] without a map) as 8-bit codes and scales.
+size_t quantize_rows_bytes(int T, int R, int D);
 cudaError_t launch_quantize_rows(moe_dtype_t dt, const void* x, const int32_t* row_map, int k, int T, int R, int D,
-                                 int8_t* codes, float* scales, cudaStream_t s);
+                                 int8_t* codes, float* scales, void* ws, cudaStream_t s);
 
 struct GroupedI8Shape {
     moe_dtype_t out;         // bf16 or fp16

@@ -3,14 +3,15 @@
 // for x = row (row_map[r] / k), so that the rows of a permutation go to their places
 // without a 16-bit copy in between.
 //
-// The rows' gather makes k rows of one: what bounds it is not the memory but the
-// instructions of an element, and packed ones keep them at about five: the maximum of
-// pairs of 16-bit patterns, products and sums of pairs in fp32, and rounding by adding
-// 1.5 2^23, whose low byte is the code.  A thread holds its part of the row in registers
-// between the maximum and the codes.
-// 4096 rows of 2048 bf16 gathered to 32768: 33 us, 134 MB through L2 and 67 MB written at
-// 6.1 TB/s; with each code's border looked at by itself 59 us, and 77 us where bf16's
-// frequent ties took a branch.
+// What bounds it is not the memory but the instructions of an element, and packed ones
+// keep them at about five: the maximum of pairs of 16-bit patterns, products and sums of
+// pairs in fp32, and rounding by adding 1.5 2^23, whose low byte is the code.  A thread
+// holds its part of the row in registers between the maximum and the codes.  Where the
+// gather makes several rows of one, as top-k routing does, the rows of x are quantised
+// once into the workspace and their codes copied.
+// 4096 rows of 2048 bf16 gathered to 32768: 17 us, 67 MB written; each of the 32768
+// quantised by itself 32 us, with each code's border looked at alone 59 us, and 77 us
+// where bf16's frequent ties took a branch.
 //
 // The codes are those of the formula exactly.  With y = 1 / a, t0 = (127 x) y and the
 // residual 127 x - t0 a, which an fma has exactly, t = t0 + residual y is the quotient
@@ -158,6 +159,40 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) quantize_rows_k
     if (tid == 0) p.scales[r] = finite ? a / 127.f : __uint_as_float(0x7FC00000u);
 }
 
+// codes[r] = made[row_map[r] / k], and the scales: G lanes a row, four loads under way.
+struct CopyArgs {
+    const int32_t* row_map;
+    int k, T, R, units;
+    const uint4* made;
+    const float* made_scales;
+    uint4* codes;
+    float* scales;
+};
+template <int G>
+__global__ void __launch_bounds__(256) gather_codes_kernel(const CopyArgs p) {
+    constexpr int ROWS = 256 / G, AHEAD = 4;
+    grid_dependency_launch();
+    grid_dependency_wait();
+    const int r = blockIdx.x * ROWS + threadIdx.x / G, t = threadIdx.x % G;
+    if (r >= p.R) return;
+    const int a = __ldg(p.row_map + r), src = a < 0 ? -1 : a / p.k;
+    const bool there = src >= 0 && src < p.T;
+    const uint4* from = p.made + (size_t)(there ? src : 0) * p.units;
+    uint4* to = p.codes + (size_t)r * p.units;
+    for (int u = t; u < p.units; u += AHEAD * G) {
+        uint4 v[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (there && u + i * G < p.units) v[i] = __ldg(from + u + i * G);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (u + i * G < p.units) to[u + i * G] = v[i];
+    }
+    if (t == 0) p.scales[r] = there ? __ldg(p.made_scales + src) : 0.f;
+}
+
 template <class T, int VPT, int THREADS>
 cudaError_t run(const QuantArgs& p, cudaStream_t s) {
     constexpr int rows = THREADS >= 256 ? 1 : 256 / THREADS;
@@ -181,12 +216,35 @@ cudaError_t run(const QuantArgs& p, cudaStream_t s) {
     return run<T, 4, 512>(p, s);
 }
 
+constexpr long long MADE_ONCE = 16 << 20;
+size_t made_scales_bytes(int T) { return ((size_t)T * 4 + 255) / 256 * 256; }
+
 }  // namespace
 
+// A second launch pays where rows of x are taken at least twice on average and there is
+// more to save than its latency.  By themselves and once: 4096 rows of 2048 bf16 taken
+// 8 times 31.6, 17.5 us, 512 of 7168 12.2, 9.8; 4096 of 2048 taken twice 8.8, 8.9; 512 of
+// 2048 taken 8 times 5.1, 5.9.
+size_t quantize_rows_bytes(int T, int R, int D) {
+    if (R / 2 < T || (long long)R * D < MADE_ONCE) return 0;
+    return made_scales_bytes(T) + (size_t)T * D;
+}
 cudaError_t launch_quantize_rows(moe_dtype_t dt, const void* x, const int32_t* row_map, int k, int T, int R, int D,
-                                 int8_t* codes, float* scales, cudaStream_t s) {
-    const QuantArgs p{x, row_map, k, T, R, D, codes, scales};
-    return dt == MOE_DT_BF16 ? run<Bf16>(p, s) : dt == MOE_DT_F16 ? run<F16>(p, s) : run<F32>(p, s);
+                                 int8_t* codes, float* scales, void* ws, cudaStream_t s) {
+    auto rows = [&](const QuantArgs& p) {
+        return dt == MOE_DT_BF16 ? run<Bf16>(p, s) : dt == MOE_DT_F16 ? run<F16>(p, s) : run<F32>(p, s);
+    };
+    if (!ws || !row_map || T == 0 || quantize_rows_bytes(T, R, D) == 0)
+        return rows(QuantArgs{x, row_map, k, T, R, D, codes, scales});
+    auto* made_scales = static_cast<float*>(ws);
+    auto* made = static_cast<int8_t*>(ws) + made_scales_bytes(T);
+    const cudaError_t err = rows(QuantArgs{x, nullptr, 1, T, T, D, made, made_scales});
+    if (err != cudaSuccess) return err;
+    const int units = D / 16, lanes = units < 32 ? 8 : 32;
+    const CopyArgs p{row_map, k, T, R, units, reinterpret_cast<const uint4*>(made), made_scales,
+                     reinterpret_cast<uint4*>(codes), scales};
+    return launch_overlapped(lanes == 8 ? gather_codes_kernel<8> : gather_codes_kernel<32>, ceil_div(R, 256 / lanes), 256,
+                             0, s, p);
 }
 
 }  // namespace moe

@@ -15,7 +15,7 @@ whole layer of 16-bit experts for a few tokens.
                         eps=1e-6, ws=None, stream=None)
     layer_norm(x, y=None, gamma=None, beta=None, eps=1e-5, x_out=None, h=None, stream=None)
     layer_norm_backward(x_out, dh, dx_out=None, gamma=None, beta=None, eps=1e-5, ws=None, stream=None)
-    quantize_rows(x, row_map=None, k=1, codes=None, scales=None, stream=None)
+    quantize_rows(x, row_map=None, k=1, codes=None, scales=None, ws=None, stream=None)
     grouped_mm_i8(x, x_scale, w, w_scale, offsets, y=None, dtype=torch.bfloat16, ws=None, stream=None)
     expert_layer(x, logits, w13, w2, k, out=None, ids=None, ws=None, stream=None)
 
@@ -71,6 +71,10 @@ def block_norm_backward_workspace_size(T: int, D: int, G: int = 1) -> int:
 
 def layer_norm_backward_workspace_size(T: int, D: int) -> int:
     return lib().moe_layer_norm_backward_workspace_size(T, D)
+
+
+def quantize_rows_workspace_size(T: int, R: int, D: int) -> int:
+    return lib().moe_quantize_rows_workspace_size(T, R, D)
 
 
 def grouped_mm_i8_workspace_size(R: int, E: int, N: int, K: int) -> int:

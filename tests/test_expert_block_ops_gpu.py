@@ -250,6 +250,41 @@ def test_quantize_rows_map(M):
     assert none.shape == (0, D) and s.shape == (0,)
 
 
+@pytest.mark.parametrize("T,R,D,dtype", [(301, 9000, 2048, BF16), (700, 81000, 208, F16), (64, 1500, 12304, F32),
+                                         (1, 600, 32768, BF16)])
+def test_quantize_rows_taken_several_times(M, T, R, D, dtype):
+    """Rows quantised once and copied: any map, entries out of range, given spaces and none,
+    and the same codes as of each row by itself."""
+    k = 3
+    x = randn(1, dtype, T, D)
+    if T > 9:
+        x[9, 7] = float("inf")
+    m = torch.randint(-k, (T + 1) * k, (R,), generator=torch.Generator().manual_seed(2), dtype=torch.int32)
+    need = M.quantize_rows_workspace_size(T, R, D)
+    assert need > T * D
+    src = torch.div(m, k, rounding_mode="floor").long()
+    there = (src >= 0) & (src < T)
+    want, want_s = codes_reference(torch.where(torch.isfinite(x), x, torch.zeros_like(x)))
+    if T > 9:
+        want[9], want_s[9] = 0, float("nan")
+    src = src.clamp(0, T - 1)
+    want, want_s = want[src] * there[:, None], torch.where(there, want_s[src], torch.zeros(()))
+    space = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    for ws in (None, space[256:256 + need]):
+        codes, scales = M.quantize_rows(x.cuda(), m.cuda(), k, ws=ws)
+        assert torch.equal(codes.cpu(), want)
+        assert torch.equal(scales.cpu().nan_to_num(-1), want_s.nan_to_num(-1))
+    assert (space[:256] == 0x5A).all() and (space[256 + need:] == 0x5A).all()
+    xd, md, codes, scales = *dev(x, m), torch.empty_like(codes), torch.empty_like(scales)
+    torch.cuda.synchronize()
+    assert M.lib().moe_quantize_rows({BF16: 0, F16: 1, F32: 2}[dtype], xd.data_ptr(), md.data_ptr(), k, T, R, D,
+                                     codes.data_ptr(), scales.data_ptr(), None, 0, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(codes.cpu(), want)
+    with pytest.raises(RuntimeError):
+        M.quantize_rows(x.cuda(), m.cuda(), k, ws=space[:need - 256])
+
+
 # ------------------------------------------------------------- 8-bit products
 def codes(seed, *shape, lo=-127, hi=128):
     return torch.randint(lo, hi, shape, generator=torch.Generator().manual_seed(seed), dtype=torch.int8)

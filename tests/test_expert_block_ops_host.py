@@ -70,8 +70,8 @@ def test_layer_norm_backward_rejects_bad_arguments(M):
 
 
 def test_quantize_rows_rejects_bad_arguments(M):
-    def call(dt=BF16, x=P, m=P, k=2, T=8, R=16, D=64, codes=P, scales=P):
-        return M.lib().moe_quantize_rows(dt, x, m, k, T, R, D, codes, scales, None)
+    def call(dt=BF16, x=P, m=P, k=2, T=8, R=16, D=64, codes=P, scales=P, ws=P, wsb=BIG):
+        return M.lib().moe_quantize_rows(dt, x, m, k, T, R, D, codes, scales, ws, wsb, None)
 
     assert call(T=-1) == INVALID
     assert call(R=-1) == INVALID
@@ -85,8 +85,13 @@ def test_quantize_rows_rejects_bad_arguments(M):
     assert call(T=ROWS) == UNSUPPORTED
     for hole in ("x", "codes", "scales"):
         assert call(**{hole: None}) == INVALID, hole
-    for hole in ("x", "m", "codes", "scales"):
+    for hole in ("x", "m", "codes", "scales", "ws"):
         assert call(**{hole: P + 8}) == MISALIGNED, hole
+    need = M.quantize_rows_workspace_size(1000, 9000, 2048)
+    assert need >= 1000 * (2048 + 4)
+    assert call(T=1000, R=9000, D=2048, k=9, wsb=need - 1) == WORKSPACE
+    for sizes in ((8000, 8000, 2048), (500, 4000, 2048), (1000, 8000, 2056), (0, 8, 64), (8, -1, 64), (8, ROWS, 64), (2, 4, 64)):
+        assert M.quantize_rows_workspace_size(*sizes) == 0
     assert call(R=0) == OK
     assert call(R=0, x=None, codes=None, scales=None) == OK
 
