@@ -24,7 +24,7 @@
 // h has the weight p already and is kept as two 16-bit numbers, the second one the
 // rounding error of the first, so the output is rounded once as if h were fp32.  In phase
 // 2, up to 8 tokens, a column is a token (zeros where the expert is not the token's), so
-// the accumulators stay over all experts.  For more tokens, where most columns would be
+// a thread's sums stay its own over all experts.  For more tokens, where most columns would be
 // empty (32 tokens: 190 us), the columns are an expert's tokens and a warp adds them to its
 // sums in shared memory.  Up to four tokens, or rows, h and its error are columns of one
 // MMA.
@@ -597,6 +597,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             for (int i = lane; i < 8 * NT * 17; i += 32) mine[i] = 0.f;
         __syncwarp();
         const int group2 = warp / L::GW2, gw2 = warp % L::GW2, parts = ceil_div(nb2, cb2), chunks = n_uniq * parts;
+        float total[4];  // NT = 1: over the experts
         const int rows_of_all = n_uniq ? tab.uoff[n_uniq - 1] + tab.ucnt[n_uniq - 1] : 0;
         int turn = 0;  // this group's batches before
         for (int i = 0; i < tiles2; ++i) {
@@ -608,6 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             const int la = (gw2 >> 1) * tl.n + min(g, tl.n - 1), lb = (gw2 >> 1) * tl.n + min(g + 8, tl.n - 1);
             const int step = L::GW2 / 2 * tl.n;
             clear_out();
+            total[0] = total[1] = total[2] = total[3] = 0.f;
             for (int j = (group2 - q) & (L::GROUPS2 - 1); j < chunks; j += L::GROUPS2) {
                 const int u = j / parts, part = j - u * parts, off = tab.uoff[u];
                 const uint32_t toks = tab.utok[u];
@@ -658,6 +660,14 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                     };
                     if constexpr (NT == 1) {
                         units_of(std::integral_constant<bool, PAIR>{}, std::false_type{});
+                        // a token without this expert has zeros for h, but weights that are no
+                        // numbers do not give zeros
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int col = PAIR ? (2 * t + (c & 1)) & 3 : 2 * t + (c & 1);
+                            total[c] += few >> col & 1u ? out[0][0][c] + out[1][0][c] : 0.f;
+                        }
+                        clear_out();
                     } else {
                         if (pair) units_of(std::true_type{}, std::false_type{});
                         else if (cnt <= 8) units_of(std::false_type{}, std::false_type{});
@@ -694,7 +704,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             }
             if (NT == 1)  // columns 2 t and 2 t + 1, rows g and g + 8
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mine[(2 * t + (c & 1)) * 17 + g + 4 * (c & 2)] = out[0][0][c] + out[1][0][c];
+                for (int c = 0; c < 4; ++c) mine[(2 * t + (c & 1)) * 17 + g + 4 * (c & 2)] = total[c];
             dec::bar_sync(1, CONSUMERS);
             for (int j = threadIdx.x; j < p.T * 16; j += CONSUMERS) {
                 const int tok = j >> 4, r = j & 15;

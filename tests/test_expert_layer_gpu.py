@@ -161,6 +161,24 @@ def test_an_expert_that_is_not_finite_spoils_its_own_tokens_alone(M):
     assert torch.isnan(got[has]).all() and torch.equal(got[~has], clean[~has])
 
 
+@pytest.mark.parametrize("T", [2, 4, 8, 20])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_down_weights_that_are_not_finite(M, T, value):
+    """The tokens of other experts are as they were."""
+    k, E, d, f = 2, 8, 192, 128
+    x, lg, w13, w2 = case(5, T, k, E, d, f, BF16)
+    lg[0, 3], lg[1, 3] = 9.0, -9.0
+    _, _, ids = reference(x, lg, w13, w2, k)
+    clean = M.expert_layer(x.cuda(), lg.cuda(), w13.cuda(), w2.cuda(), k)
+    w2[3, ::5] = value
+    got = M.expert_layer(x.cuda(), lg.cuda(), w13.cuda(), w2.cuda(), k)
+    has = torch.from_numpy((ids == 3).any(1))
+    assert has[0] and not has[1]
+    assert not torch.isfinite(got[has][:, ::5]).any() and torch.equal(got[~has], clean[~has])
+    other = torch.arange(d) % 5 > 0
+    assert torch.equal(got[:, other], clean[:, other])
+
+
 def test_logits_that_are_no_numbers(M):
     """No read out of range, and other tokens are as they were."""
     T, k, E, d, f = 3, 2, 8, 128, 64
