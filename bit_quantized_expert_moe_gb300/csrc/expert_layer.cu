@@ -25,7 +25,7 @@
 // rounding error of the first, so the output is rounded once as if h were fp32.  In phase
 // 2, up to 8 tokens, a column is a token (zeros where the expert is not the token's), so
 // a thread's sums stay its own over all experts.  For more tokens, where most columns would be
-// empty (32 tokens: 190 us), the columns are an expert's tokens and a warp adds them to its
+// empty, the columns are an expert's tokens and a warp adds them to its
 // sums in shared memory.  Up to four tokens, or rows, h and its error are columns of one
 // MMA.
 //
@@ -37,12 +37,15 @@
 //     registers (they stay in L1 from tile to tile); in phase 2, where every chunk brings
 //     another expert's, a warp of its own has an expert's rows of h copied to a ring of
 //     rows in shared memory, a bulk copy for all of them (one for each row, issued one
-//     after the other, took 0.3 us a row);
-//   - another warp adds the sixteen warps' sums of phase 1 up and writes h, so that none
-//     of them waits for the others.
-// 2048 x 768, 8 of 128 experts a token: 1 token 18.4 us (4.1 TB/s, 60 % of the copy's
-// rate: routing 2.2 us, the meeting 1.0, from there to the end 2.9), 8 tokens 80 us (5.9
-// TB/s), 32 tokens 178 us (5.9); 7168 x 2048, 8 of 256: 8 tokens 757 to 778 us (6.5 to 6.7).
+//     after the other, took 0.3 us a row); it takes back what has been read of all batches
+//     under way at once (one by one: 28 tokens, 151 experts of 768 x 256, 88 us for 79);
+//   - two warps in turn add the sixteen warps' sums of phase 1 up and write h, so that none
+//     of them waits for the others (one, and divisions to find each tile: 12 tokens, 128
+//     experts of 512 x 1024, 119 us for 89);
+//   - small chunks of phase 2 share a slot, so that more of them are under way.
+// 2048 x 768, 8 of 128 experts a token: 1 token 18.3 us (4.1 TB/s, 61 % of the copy's
+// rate: routing 2.2 us, the meeting 1.0, from there to the end 2.9), 8 tokens 80 us (6.0
+// TB/s), 32 tokens 164 us (6.4); 7168 x 2048, 8 of 256: 8 tokens 748 us (6.7).
 // One group of eight warps that all wait for each other at a tile's end: 23.6, 109, 530
 // and 1084 us; x in the ring of rows as well: 8 tokens at 7168 804, 32 at 2048 432.
 #include <type_traits>
@@ -56,8 +59,8 @@ namespace {
 
 constexpr int MAX_T = 32, MAX_R = 256;
 constexpr int GROUPS = 2, GW = 8, CW = GROUPS * GW;  // consumer warps
-constexpr int CONSUMERS = 32 * CW, THREADS = CONSUMERS + 96;
-constexpr int PRODUCER = CW, ROWS_OF_H = CW + 1, FINISHER = CW + 2;  // warps
+constexpr int CONSUMERS = 32 * CW, FINISHERS = 2, THREADS = CONSUMERS + 64 + 32 * FINISHERS;
+constexpr int PRODUCER = CW, ROWS_OF_H = CW + 1, FINISHER = CW + 2;  // warps, the first of FINISHERS
 // By NT, the most groups of 8 tokens of an expert.  The ring's slots are a multiple of
 // the groups, so that each is always one group's: a wait names a round of its barrier by
 // the round's parity, and a group that took every second round of a slot would take the
@@ -72,21 +75,23 @@ struct Plan {
     // A row of h of a chunk, 256 bytes for 64 inputs; 64 more, so that neighbours use
     // other banks.  A batch's rows are one bulk copy; more than 16 of an expert are two
     // batches, of the tokens below 16 and of the others.
-    static constexpr int PITCH = BLOCKS2 * 256 + 64, NROW = NT == 1 ? 8 : 16, NBATCH = 8;
+    static constexpr int PITCH = BLOCKS2 * 256 + 64, NROW = NT == 1 ? 8 : 16, NBATCH = 16;
     static constexpr int HALVES = NT <= 2 ? 1 : 2;
     // Phase 2's groups: up to 8 tokens pairs of warps, one for each slot, so that the
     // latency of a chunk counts an eighth.  More tokens take two groups of eight (pairs,
     // with eight slots of 16 KB: 32 tokens at 2048 x 768 243 us for 190).  Barriers of a
     // group's batches.
-    static constexpr int GW2 = NT == 1 ? 2 : GW, GROUPS2 = CW / GW2, TURNS = NT == 1 ? 1 : NBATCH;
+    static constexpr int GW2 = NT == 1 ? 2 : GW, GROUPS2 = CW / GW2, TURNS = NT == 1 ? NBATCH / GROUPS2 : NBATCH;
 
     static constexpr int NBUF = 2, SUM_FLOATS = CW * 128;        // sums of 8 tokens: [CW][32][4]
     // phase 2: [CW][8 NT][17]
     static constexpr int SUMS = 4 * (NBUF * SUM_FLOATS > CW * 8 * NT * 17 ? NBUF * SUM_FLOATS : CW * 8 * NT * 17);
-    static constexpr int BARS = 16 * (NSLOT + GROUPS2 * TURNS + NBUF) + 16;
-    static constexpr int OFF_BARS = NSLOT * SLOT, OFF_ROWS = OFF_BARS + 512, OFF_SUMS = OFF_ROWS + NROW * PITCH;
+    // Phase 2 cuts a slot in up to MOST_PARTS parts, where its chunks are that small.
+    static constexpr int MOST_PARTS = 4;
+    static constexpr int BARS = 16 * ((1 + MOST_PARTS) * NSLOT + GROUPS2 * TURNS + NBUF) + 16;
+    static constexpr int OFF_BARS = NSLOT * SLOT, OFF_ROWS = OFF_BARS + 1280, OFF_SUMS = OFF_ROWS + NROW * PITCH;
     static constexpr int OFF_TAB = OFF_SUMS + SUMS;
-    static_assert(NROW >= (NT < 2 ? 8 : 16) && BARS <= 512, "a batch's rows, the barriers");
+    static_assert(NROW >= (NT < 2 ? 8 : 16) && BARS <= 1280, "a batch's rows, the barriers");
     static_assert(NSLOT % GROUPS == 0 && NSLOT % GROUPS2 == 0 && SLOT % 1024 == 0 && PITCH % 128 == 64, "layout");
 };
 
@@ -98,7 +103,7 @@ struct Tab {
     int uexp[MAX_R], uoff[MAX_R], ucnt[MAX_R];  // touched experts, ascending: id, first position, how many tokens
     uint32_t utok[MAX_R];                       // and which, one bit a token
     uint32_t warp_sums[CW];
-    int batches[2 * 8];                         // under way: rows, barrier, parity
+    int batches[2 * 16];                        // under way: rows, barrier, parity
     int n_uniq, abort;
 };
 
@@ -115,6 +120,7 @@ struct Params {
     unsigned long long* bar_count;
     int T, k, E, d, f;
     int cb1, cb2;        // 64-input blocks of a chunk of either phase
+    int cut;             // phase 2 cuts a slot in 1 << cut parts
     int rows2[4];        // rows of the maps of the down projection
 };
 struct Maps {
@@ -152,9 +158,21 @@ __device__ __forceinline__ int share(int n, int c, int parts) { return (int)((ui
 // features i0 .. i0 + n - 1, box of map m (n = 8 >> m).
 struct Tile1 {
     int u, i0, n, m;
+    __device__ Tile1() : u(0), i0(0), n(0), m(0) {}
     __device__ Tile1(int x, int end, int f) {
         u = x / f;
         i0 = x - u * f;
+        size(x, end, f);
+    }
+    // the tile behind, at x
+    __device__ void next(int x, int end, int f) {
+        if ((i0 += n) == f) {
+            i0 = 0;
+            ++u;
+        }
+        size(x, end, f);
+    }
+    __device__ void size(int x, int end, int f) {
         const int most = min(min(8, f - i0), end - x);
         m = 3 - (31 - __clz(most));
         n = 8 >> m;
@@ -179,13 +197,15 @@ __device__ __forceinline__ uint32_t weights_at(uint32_t slot, int line, int half
 // Where a group is in phase 1's list of chunks.
 struct Place1 {
     int x, b, q;         // tile's first feature, chunk's first block; chunks before
-    int i0, n, cnt, off; // of the tile
-    __device__ Place1(const Tab& tab, int x_, int end, int f) : x(x_), b(0), q(0), i0(0), n(0), cnt(0), off(0) { tile(tab, end, f); }
-    __device__ void tile(const Tab& tab, int end, int f) {
-        if (x >= end) return;
-        const Tile1 t(x, end, f);
-        i0 = t.i0;
-        n = t.n;
+    int cnt, off;        // of the tile
+    Tile1 t;
+    __device__ Place1(const Tab& tab, int x_, int end, int f) : x(x_), b(0), q(0), cnt(0), off(0) {
+        if (x < end) {
+            t = Tile1(x, end, f);
+            rows(tab);
+        }
+    }
+    __device__ void rows(const Tab& tab) {
         cnt = tab.ucnt[t.u];
         off = tab.uoff[t.u];
     }
@@ -194,8 +214,10 @@ struct Place1 {
         ++q;
         if ((b += cb) < nb) return;
         b = 0;
-        x += n;
-        tile(tab, end, f);
+        x += t.n;
+        if (x >= end) return;
+        t.next(x, end, f);
+        rows(tab);
     }
 };
 
@@ -208,7 +230,8 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
     uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t ring = smem_u32(sm), rows_at = ring + L::OFF_ROWS;
     const uint32_t full = ring + L::OFF_BARS, empty = full + 8 * NSLOT;                  // slots
-    const uint32_t row_full = empty + 8 * NSLOT, row_empty = row_full + 8 * L::GROUPS2 * L::TURNS;      // rows of a batch
+    const uint32_t full2 = empty + 8 * NSLOT, empty2 = full2 + 8 * NSLOT * L::MOST_PARTS;     // their parts, phase 2
+    const uint32_t row_full = empty2 + 8 * NSLOT * L::MOST_PARTS, row_empty = row_full + 8 * L::GROUPS2 * L::TURNS;      // rows of a batch
     const uint32_t sum_full = row_empty + 8 * L::GROUPS2 * L::TURNS, sum_empty = sum_full + 8 * NBUF, h_ready = sum_empty + 8 * NBUF;
     float* sums = reinterpret_cast<float*>(sm + L::OFF_SUMS);
     Tab& tab = *reinterpret_cast<Tab*>(sm + L::OFF_TAB);
@@ -223,6 +246,10 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
         for (int i = 0; i < NSLOT; ++i) {
             tc::mbar_init(full + 8 * i, 1);
             tc::mbar_init(empty + 8 * i, GW);
+        }
+        for (int i = 0; i < NSLOT * L::MOST_PARTS; ++i) {
+            tc::mbar_init(full2 + 8 * i, 1);
+            tc::mbar_init(empty2 + 8 * i, GW);
         }
         for (int i = 0; i < L::GROUPS2 * L::TURNS; ++i) {
             tc::mbar_init(row_full + 8 * i, 1);
@@ -317,6 +344,13 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
     const int n_uniq = tab.n_uniq;
     const int x_lo = share(n_uniq * f, cta, G), x_hi = share(n_uniq * f, cta + 1, G);
     const int r_lo = share(d, cta, G), rows = share(d, cta + 1, G) - r_lo, tiles2 = ceil_div(rows, 16);
+    // Part i of the slots in phase 2, which begins at slot s0: the slots become free in
+    // that order.
+    auto part_at = [&](int i, int s0) {
+        const int slot = s0 + (i >> p.cut);
+        return ring + (slot < NSLOT ? slot : slot - NSLOT) * L::SLOT + (i & ((1 << p.cut) - 1)) * ((L::SLOT >> p.cut) & ~1023);
+    };
+    const int slots2 = NSLOT << p.cut;
     // A wait that gave up goes on with what is there: no arrival and no barrier is left
     // out, and every address stays where it was.
 
@@ -337,8 +371,8 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                     phase ^= 1u;
                 }
             };
+            Tile1 t(x_lo, x_hi, f);
             for (int x = x_lo; ok && x < x_hi;) {
-                const Tile1 t(x, x_hi, f);
                 const int e = tab.uexp[t.u];
                 for (int b = 0; b < nb1 && next(cb1 * 2 * t.n * 128); b += cb1, advance())
                     asm volatile(
@@ -346,25 +380,40 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                         " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];"
                         :: "r"(ring + s * L::SLOT), "l"(&maps.w13[t.m]), "r"(full + 8 * s), "r"(0), "r"(t.i0), "r"(b), "r"(e) : "memory");
                 x += t.n;
+                if (x < x_hi) t.next(x, x_hi, f);
             }
+            // the first round of the parts waits for the slots of phase 1
+            const int s0 = s;
+            int at = 0;
+            uint32_t round = 0;
+            auto next2 = [&](uint32_t bytes) {
+                if (round) {
+                    ok = ok && tc::mbar_wait(empty2 + 8 * at, (round - 1) & 1u, abort_flag, p.err);
+                } else if ((at & ((1 << p.cut) - 1)) == 0) {
+                    ok = ok && tc::mbar_wait(empty + 8 * s, phase, abort_flag, p.err);
+                    advance();
+                }
+                if (ok) tc::mbar_arrive_expect_tx(full2 + 8 * at, bytes);
+                return ok;
+            };
             for (int i = 0; ok && i < tiles2; ++i) {
                 const Tile2 t(rows, tiles2, i);
                 const int m = t.n == p.rows2[0] ? 0 : t.n == p.rows2[1] ? 1 : t.n == p.rows2[2] ? 2 : 3;
                 for (int u = 0; ok && u < n_uniq; ++u) {
                     const int e = tab.uexp[u];
-                    for (int b = 0; b < nb2 && next(cb2 * t.n * 128); b += cb2, advance())
-                        tc::tma_load_4d(ring + s * L::SLOT, &maps.w2[m], full + 8 * s, 0, r_lo + t.r0, b, e);
+                    for (int b = 0; b < nb2 && next2(cb2 * t.n * 128); b += cb2) {
+                        tc::tma_load_4d(part_at(at, s0), &maps.w2[m], full2 + 8 * at, 0, r_lo + t.r0, b, e);
+                        if (++at == slots2) {
+                            at = 0;
+                            ++round;
+                        }
+                    }
                 }
             }
         }
         __syncwarp();
     } else if (warp == ROWS_OF_H) {
         // ------------------- the tokens' rows of h of the chunks, a lane a bulk copy
-        int q = 0;  // chunks of phase 1
-        for (int x = x_lo; x < x_hi;) {
-            x += Tile1(x, x_hi, f).n;
-            q += ceil_div(nb1, cb1);
-        }
         // A window of batches, a lane each: where their rows lie and go, which barrier of
         // its group's TURNS ones a batch has.  Lanes copy as soon as there is room, in order:
         // at most NBATCH batches and the ring's rows are under way.
@@ -392,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                     }
                 }
             }
-            const uint32_t any = __ballot_sync(0xffffffffu, cnt > 0), odd = __ballot_sync(0xffffffffu, (q + c) & 1);
+            const uint32_t any = __ballot_sync(0xffffffffu, cnt > 0), odd = __ballot_sync(0xffffffffu, c & 1);
             const int index = head + __popc(any & below);
             int place = cnt;
 #pragma unroll
@@ -402,9 +451,9 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             }
             const int total = __shfl_sync(0xffffffffu, place, 31);
             place += at - cnt;
-            const uint32_t ours = (q + c) & 1 ? odd : ~odd;
-            const int turn = L::HALVES == 1 ? index / L::GROUPS2 : turns[(q + c) & 1] + __popc(any & ours & below);
-            const int slot = (q + c) % L::GROUPS2 * L::TURNS + turn % L::TURNS;
+            const uint32_t ours = c & 1 ? odd : ~odd;
+            const int turn = L::HALVES == 1 ? index / L::GROUPS2 : turns[c & 1] + __popc(any & ours & below);
+            const int slot = c % L::GROUPS2 * L::TURNS + turn % L::TURNS;
             if (base == 0) {
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(h_ready, 0, abort_flag, p.err));
                 fence_proxy_async_global();  // h was written by ordinary stores
@@ -424,26 +473,34 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                 }
                 __syncwarp();
                 if (__any_sync(0xffffffffu, go)) continue;
-                const int o = tab.batches[tail % (2 * NBATCH)];
-                ok = tc::mbar_wait(row_empty + 8 * (o >> 8 & 255), (uint32_t)o >> 16, abort_flag, p.err);
+                // the oldest batch's wait, and how many behind it have been given back too
+                const int copied = head + __popc(any & ~__ballot_sync(0xffffffffu, todo));
+                const int o = tab.batches[(tail + lane) % (2 * NBATCH)];
+                const uint32_t bar = row_empty + 8 * (o >> 8 & 255);
+                if (lane == 0) ok = tc::mbar_wait(bar, (uint32_t)o >> 16, abort_flag, p.err);
+                const bool back = lane == 0 || (tail + lane < copied && tc::mbar_test_cluster(bar, (uint32_t)o >> 16));
                 ok = __all_sync(0xffffffffu, ok);  // (nothing is copied after a wait that gave up)
-                given += o & 255;
-                ++tail;
+                const int n = __ffs(~__ballot_sync(0xffffffffu, back)) - 1;
+                given += __reduce_add_sync(0xffffffffu, lane < n ? o & 255 : 0);
+                tail += n;
             }
             head += __popc(any);
             at += total;
             turns[0] += __popc(any & ~odd);
             turns[1] += __popc(any & odd);
         }
-    } else if (warp == FINISHER) {
+    } else if (warp >= FINISHER) {
         // --------------------- phase 1's sums: h = SiLU(gate) up, two columns a lane
         const int g = lane >> 2, t = lane & 3;
+        const int which = warp - FINISHER;
+        const uint32_t by_cb2 = (1u << 20) / (uint32_t)cb2 + 1;  // for blocks below 2^9, chunks of at most 12
         int k = 0;
+        Tile1 tl(x_lo, x_hi, f);
         for (int x = x_lo; x < x_hi;) {
-            const Tile1 tl(x, x_hi, f);
             const int cnt = tab.ucnt[tl.u], off = tab.uoff[tl.u];
             for (int n = 0; 8 * n < cnt; ++n, ++k) {
                 const int buf = k % NBUF;
+                if (k % FINISHERS != which) continue;
                 tc::mbar_wait(sum_full + 8 * buf, (uint32_t)(k / NBUF) & 1u, abort_flag, p.err);
                 __syncwarp();
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -465,7 +522,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                         const float h = tab.pw[off + col] * (a / (1.f + expf(-a)) * u);
                         const uint16_t hi = bits16<BF16>(h);
                         const float rest = h - value16<BF16>(hi);
-                        const int i = tl.i0 + g, part = (i >> 6) / cb2;
+                        const int i = tl.i0 + g, part = (uint32_t)(i >> 6) * by_cb2 >> 20;
                         auto* to = reinterpret_cast<uint16_t*>(p.h + ((size_t)part * R + off + col) * p.pitch) +
                                    ((i >> 6) - part * cb2) * 128 + (i & 63);
                         to[0] = hi;
@@ -474,13 +531,14 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                 }
             }
             x += tl.n;
+            if (x < x_hi) tl.next(x, x_hi, f);
         }
         // Every CTA's h is written before anyone reads it.  The arrival count only
         // grows, G a launch, so a CTA's own arrival tells it the count at which this
         // launch's barrier opens.
         fence_proxy_async_global();  // it is read by bulk copies
-        __syncwarp();
-        if (lane == 0) {
+        dec::bar_sync(2, 32 * FINISHERS);
+        if (which == 0 && lane == 0) {
             const uint64_t old = dec::atom_add_release_gpu(p.bar_count, 1ull);
             const uint64_t target = (old / (uint64_t)G + 1) * (uint64_t)G;
             const uint64_t t0 = globaltimer_ns();
@@ -557,9 +615,9 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             const int units = 2 * min(cb1, nb1 - c.b);
             // The lines of unit gw's gate and up rows (beyond the tile's rows: its last again);
             // those of unit gw + GW are 8 n further, at the same place of the swizzle.
-            const uint32_t slot = ring + (c.q % NSLOT) * L::SLOT, further = 1024u * c.n;
-            const int line = (gw >> 1) * 2 * c.n + min(g, c.n - 1);
-            const uint32_t gate = weights_at(slot, line, gw & 1, t), up = weights_at(slot, line + c.n, gw & 1, t);
+            const uint32_t slot = ring + (c.q % NSLOT) * L::SLOT, further = 1024u * c.t.n;
+            const int line = (gw >> 1) * 2 * c.t.n + min(g, c.t.n - 1);
+            const uint32_t gate = weights_at(slot, line, gw & 1, t), up = weights_at(slot, line + c.t.n, gw & 1, t);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 if (8 * n < c.cnt) {
@@ -578,7 +636,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             if (to.x != mid.x) add_up(mid.cnt);  // this one's, or a tile that was the other group's
             c = to;
         }
-        const int q1 = c.q;  // chunks of phase 1
+        const int s0 = c.q % NSLOT;  // behind the last chunk of phase 1
 
         // ---- phase 2
         tc::mbar_wait(h_ready, 0, abort_flag, p.err);
@@ -599,10 +657,12 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
         const int group2 = warp / L::GW2, gw2 = warp % L::GW2, parts = ceil_div(nb2, cb2), chunks = n_uniq * parts;
         float total[4];  // NT = 1: over the experts
         const int rows_of_all = n_uniq ? tab.uoff[n_uniq - 1] + tab.ucnt[n_uniq - 1] : 0;
+        const int u_step = L::GROUPS2 / parts, part_step = L::GROUPS2 - u_step * parts;
         int turn = 0;  // this group's batches before
+        int at_part = group2;  // of the slots, of this group's next chunk
+        uint32_t parity = 0;
         for (int i = 0; i < tiles2; ++i) {
-            const int q = q1 + i * chunks;  // chunks before
-
+            const int q = i * chunks;  // chunks before
             const Tile2 tl(rows, tiles2, i);
             // lines of unit gw2 of rows g and g + 8 (beyond the tile's: its last again), and from
             // there to unit gw2 + GW2
@@ -610,14 +670,15 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
             const int step = L::GW2 / 2 * tl.n;
             clear_out();
             total[0] = total[1] = total[2] = total[3] = 0.f;
-            for (int j = (group2 - q) & (L::GROUPS2 - 1); j < chunks; j += L::GROUPS2) {
-                const int u = j / parts, part = j - u * parts, off = tab.uoff[u];
+            int j = (group2 - q) & (L::GROUPS2 - 1), u = j / parts, part = j - u * parts;
+            for (; j < chunks; j += L::GROUPS2) {
+                const int off = tab.uoff[u];
                 const uint32_t toks = tab.utok[u];
                 const int units = 2 * min(cb2, nb2 - part * cb2);
-                const uint32_t slot = ring + ((q + j) % NSLOT) * L::SLOT;
+                const uint32_t slot = part_at(at_part, s0);
                 // the rows before: those of earlier tiles, experts and parts
                 int at = parts * (i * rows_of_all + off) + part * __popc(toks);
-                wait(q + j);
+                tc::mbar_wait(full2 + 8 * at_part, parity, abort_flag, p.err);
                 const bool two = L::HALVES > 1 && __popc(toks) > 16;
                 for (int half = 0; half <= (int)two; ++half) {
                     const uint32_t few = !two ? toks : half ? toks & 0xffff0000u : toks & 0xffffu;
@@ -700,7 +761,16 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                     ++turn;
                     at += cnt;
                 }
-                if (lane < GW / L::GW2) tc::mbar_arrive(empty + 8 * ((q + j) % NSLOT));
+                if (lane < GW / L::GW2) tc::mbar_arrive(empty2 + 8 * at_part);
+                if ((at_part += L::GROUPS2) >= slots2) {
+                    at_part -= slots2;
+                    parity ^= 1u;
+                }
+                u += u_step;
+                if ((part += part_step) >= parts) {
+                    part -= parts;
+                    ++u;
+                }
             }
             if (NT == 1)  // columns 2 t and 2 t + 1, rows g and g + 8
 #pragma unroll
@@ -760,7 +830,7 @@ cudaError_t launch(const Maps& maps, Params& p, cudaStream_t s) {
 // What the sizes alone settle: a CTA's output features, q or q + 1, come in tiles of at
 // most two sizes each; chunks of as many 64-input blocks each, as fit a slot.
 struct Cut {
-    int rows2[4], cb1, cb2, pitch;
+    int rows2[4], cb1, cb2, pitch, cut;
     Cut(int d, int f) {
         const int q = d / num_sms();
         int most = 1;
@@ -773,6 +843,8 @@ struct Cut {
         cb1 = ceil_div(d / 64, ceil_div(d / 64, L::BLOCKS1));
         cb2 = ceil_div(f / 64, ceil_div(f / 64, std::min(L::BLOCKS2, 16 * L::BLOCKS1 / most)));
         pitch = 256 * cb2 + 64;
+        cut = 0;
+        while (1 << cut < L::MOST_PARTS && most * cb2 * 128 <= (L::SLOT >> (cut + 1) & ~1023)) ++cut;
     }
 };
 
@@ -805,6 +877,7 @@ cudaError_t launch_expert_layer(const ExpertLayer& l, cudaStream_t s) {
     p.cb1 = c.cb1;
     p.cb2 = c.cb2;
     p.pitch = c.pitch;
+    p.cut = c.cut;
     Maps maps;
     bool ok = true;
     // gate_up as [expert][64-input block][gate, up][feature][64 inputs]

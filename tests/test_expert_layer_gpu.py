@@ -112,6 +112,9 @@ CASES = [
     (5, 6, 24, 640, 1600),
     (32, 8, 20, 128, 832),        # more than 16 tokens of an expert
     (32, 4, 8, 2496, 64),         # tiles of 17 output features
+    (28, 6, 101, 384, 256),       # many experts of few tokens: several rounds of parts of slots
+    (8, 8, 60, 256, 1600),
+    (13, 5, 90, 1280, 192),
 ]
 
 
