@@ -45,7 +45,8 @@
 //   - small chunks of phase 2 share a slot, so that more of them are under way.
 // 2048 x 768, 8 of 128 experts a token: 1 token 18.3 us (4.1 TB/s, 61 % of the copy's
 // rate: routing 2.2 us, the meeting 1.0, from there to the end 2.9), 8 tokens 80 us (6.0
-// TB/s), 32 tokens 164 us (6.4); 7168 x 2048, 8 of 256: 8 tokens 748 us (6.7).
+// TB/s), 32 tokens 164 us (6.4); 7168 x 2048, 8 of 256: 8 tokens 748 to
+// 767 us (6.6 to 6.8).
 // One group of eight warps that all wait for each other at a tile's end: 23.6, 109, 530
 // and 1084 us; x in the ring of rows as well: 8 tokens at 7168 804, 32 at 2048 432.
 #include <type_traits>
