@@ -86,7 +86,8 @@ moe_status_t moe_layer_norm_backward(moe_dtype_t dtype, moe_dtype_t param_dtype,
 
 size_t moe_quantize_rows_workspace_size(int32_t T, int32_t R, int32_t D) {
     if (T < 1 || R < 0 || T > MAX_ROWS || R > MAX_ROWS || !width_supported(D, 16, MAX_WIDTH)) return 0;
-    return quantize_rows_bytes(T, R, D);
+    const size_t bytes = quantize_rows_bytes(T, R, D);
+    return bytes ? WS_HEADER + bytes : 0;
 }
 
 moe_status_t moe_quantize_rows(moe_dtype_t dtype, const void* x, const int32_t* row_map, int32_t k, int32_t T, int32_t R,
@@ -98,7 +99,9 @@ moe_status_t moe_quantize_rows(moe_dtype_t dtype, const void* x, const int32_t* 
     if ((T > 0 && !x) || !codes || !scales) return MOE_ERR_INVALID_ARG;
     if (!all_aligned({x, row_map, codes, scales, workspace})) return MOE_ERR_MISALIGNED;
     if (workspace && workspace_bytes < moe_quantize_rows_workspace_size(T, R, D)) return MOE_ERR_WORKSPACE;
-    return cuda_status(launch_quantize_rows(dtype, x, row_map, k, T, R, D, codes, scales, workspace, stream));
+    // the header stays as it is: a workspace that other calls use has its error word and counters there
+    void* const space = workspace ? static_cast<unsigned char*>(workspace) + WS_HEADER : nullptr;
+    return cuda_status(launch_quantize_rows(dtype, x, row_map, k, T, R, D, codes, scales, space, stream));
 }
 
 size_t moe_grouped_mm_i8_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K) {

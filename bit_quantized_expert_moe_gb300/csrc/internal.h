@@ -180,7 +180,8 @@ size_t layer_norm_partial_floats(int T, int D);  // scratch of the backward pass
 cudaError_t launch_layer_norm(const LayerNormShape& n, const void* x, const void* y, void* x_out, void* h, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(const LayerNormShape& n, const LayerNormGrads& g, float* part, cudaStream_t s);
 
-// Rows x[row_map[r] / k] (x[r] without a map) as 8-bit codes and scales.
+// Rows x[row_map[r] / k] (x[r] without a map) as 8-bit codes and scales.  `ws`: as many bytes
+// as quantize_rows_bytes(), behind the workspace's header, or null.
 size_t quantize_rows_bytes(int T, int R, int D);
 cudaError_t launch_quantize_rows(moe_dtype_t dt, const void* x, const int32_t* row_map, int k, int T, int R, int D,
                                  int8_t* codes, float* scales, void* ws, cudaStream_t s);

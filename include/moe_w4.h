@@ -384,8 +384,9 @@ moe_status_t moe_layer_norm_backward(moe_dtype_t dtype, moe_dtype_t param_dtype,
  * A row that holds an infinity or a NaN gets the scale NaN and codes 0, so that all
  * that is made of it is NaN.
  * Workspace: moe_quantize_rows_workspace_size(T, R, D) bytes, in which rows that are
- * taken several times get their codes once; NULL (each taken row is quantised by itself,
- * with the same results) or a size of 0 needs none.  Nothing in it is kept for a later call.
+ * taken several times get their codes once, behind the header (which is neither read nor
+ * written); NULL (each taken row is quantised by itself, with the same results) or a size
+ * of 0 needs none.  Nothing in it is kept for a later call.
  */
 size_t moe_quantize_rows_workspace_size(int32_t T, int32_t R, int32_t D);
 moe_status_t moe_quantize_rows(moe_dtype_t dtype, const void* x, const int32_t* row_map, int32_t k, int32_t T,
