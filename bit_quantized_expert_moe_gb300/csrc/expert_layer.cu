@@ -22,7 +22,9 @@
 // few tokens an expert the tensor rate is no bound.  Both operands keep K in the order
 // in which a thread's 16-byte loads bring it, as in grouped_few.cu.
 // h has the weight p already and is kept as two 16-bit numbers, the second one the
-// rounding error of the first, so the output is rounded once as if h were fp32.  In phase
+// rounding error of the first (in fp16 times 2^11, so that it does not get lost among the
+// subnormals where h is small): off by 2^-17 |p h| in bf16, by 2^-23 |p h| or 2^-36
+// in fp16, far below the output's rounding unless its sum cancels.  In phase
 // 2, up to 8 tokens, a column is a token (zeros where the expert is not the token's), so
 // a thread's sums stay its own over all experts.  For more tokens, where most columns would be
 // empty, the columns are an expert's tokens and a warp adds them to its
@@ -114,7 +116,8 @@ struct Params {
     uint16_t* out;
     int32_t* ids_out;
     // p h: [chunks of an expert][R by sorted position][pitch bytes]: of 64 features their
-    // values, then the rounding errors of these; as a batch's rows lie in shared memory
+    // values, then the rounding errors of these in their unit; as a batch's rows lie in shared
+    // memory
     uint8_t* h;
     int pitch, nrow;     // and the rows of the ring of rows, a power of 2
     uint32_t* err;
@@ -148,6 +151,11 @@ template <bool BF16>
 __device__ __forceinline__ float value16(uint16_t b) {
     return BF16 ? __uint_as_float((uint32_t)b << 16) : half_bits_to_float(b);
 }
+
+// The rounding error of an fp16 number is at most 16 below its end, 65520, and an fp16 number
+// itself times 2^11.
+template <bool BF16>
+constexpr float ERROR_UNIT = BF16 ? 1.f : 0x1p-11f;
 
 // Between ordinary accesses to global memory and bulk copies of it.
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
@@ -527,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                         auto* to = reinterpret_cast<uint16_t*>(p.h + ((size_t)part * R + off + col) * p.pitch) +
                                    ((i >> 6) - part * cb2) * 128 + (i & 63);
                         to[0] = hi;
-                        to[64] = bits16<BF16>(isfinite(rest) ? rest : 0.f);
+                        to[64] = bits16<BF16>(isfinite(rest) ? rest * (1.f / ERROR_UNIT<BF16>) : 0.f);
                     }
                 }
             }
@@ -727,7 +735,8 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const int col = PAIR ? (2 * t + (c & 1)) & 3 : 2 * t + (c & 1);
-                            total[c] += few >> col & 1u ? out[0][0][c] + out[1][0][c] : 0.f;
+                            // (both sets have values, in columns up to 3, or the second one has errors)
+                            total[c] += few >> col & 1u ? fmaf(out[1][0][c], PAIR ? 1.f : ERROR_UNIT<BF16>, out[0][0][c]) : 0.f;
                         }
                         clear_out();
                     } else {
@@ -741,9 +750,9 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                             float v[4];
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
-                                v[c] = out[0][n][c] + out[1][n][c];
+                                v[c] = fmaf(out[1][n][c], pair ? 1.f : ERROR_UNIT<BF16>, out[0][n][c]);
                                 const float error = __shfl_xor_sync(0xffffffffu, v[c], 2);  // four columns further
-                                if (pair) v[c] += error;
+                                if (pair) v[c] = fmaf(error, ERROR_UNIT<BF16>, v[c]);
                             }
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
@@ -784,7 +793,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                 for (int w = 0; w < CW; ++w) {
                     float* o = sums + (w * 8 * NT + tok) * 17 + r;
                     v += *o;
-                    if (PAIR) v += o[4 * 17];
+                    if (PAIR) v = fmaf(o[4 * 17], ERROR_UNIT<BF16>, v);
                     if (NT > 1) *o = 0.f;
                 }
                 if (r < tl.n) p.out[(size_t)tok * d + r_lo + tl.r0 + r] = bits16<BF16>(v);

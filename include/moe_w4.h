@@ -415,8 +415,9 @@ moe_status_t moe_grouped_mm_i8(moe_dtype_t out_dtype, const int8_t* x, const flo
  * The whole layer of 16-bit experts for a few tokens, in one kernel: routing as
  * moe_route_topk (logits may be -inf), then for token t with experts e_j and weights p_j
  *   out[t] = sum_j p_j Wd[e_j] (SiLU(Wg[e_j] x[t]) * (Wu[e_j] x[t]))
- * in bf16 or fp16 with fp32 accumulation and one rounding at the end (fp16: every
- * p * SiLU * up has to be below 65504).
+ * in bf16 or fp16 with fp32 accumulation and one rounding at the end.  Between the two
+ * products p * SiLU * up is held to 2^-17 of itself in bf16 and to 2^-23 in fp16, there to
+ * 2^-36 at best, and has to be below 65504.
  *   x       device [T][d_model]      logits  device fp32 [T][E]
  *   w13     device [E][2 d_ff][d_model], the gate's rows first
  *   w2      device [E][d_model][d_ff]
