@@ -19,7 +19,7 @@ namespace moe {
 // ---------------------------------------------------------------------------
 constexpr uint32_t ERRBIT_RANGE = 1u;    // an expert id outside [0, E)
 constexpr uint32_t ERRBIT_TIMEOUT = 2u;  // a bounded pipeline wait gave up
-constexpr uint32_t ERRBIT_F16_RANGE = 4u;  // a value outside the fp16 range of the tensor-core regime
+constexpr uint32_t ERRBIT_F16_RANGE = 4u;  // a finite value outside the range of fp16, in which a product takes it
 constexpr size_t WS_HEADER = 256;
 
 struct WsHeader {

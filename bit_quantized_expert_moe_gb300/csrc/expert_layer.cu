@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_layer_kernel(const __grid_c
                         const float h = tab.pw[off + col] * (a / (1.f + expf(-a)) * u);
                         const uint16_t hi = bits16<BF16>(h);
                         const float rest = h - value16<BF16>(hi);
+                        if (!BF16 && isfinite(h) && !isfinite(rest)) set_error(p.err, ERRBIT_F16_RANGE);
                         const int i = tl.i0 + g, part = (uint32_t)(i >> 6) * by_cb2 >> 20;
                         auto* to = reinterpret_cast<uint16_t*>(p.h + ((size_t)part * R + off + col) * p.pitch) +
                                    ((i >> 6) - part * cb2) * 128 + (i & 63);

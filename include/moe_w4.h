@@ -62,7 +62,7 @@ typedef enum {
     MOE_ERR_CUDA = 5,          /* a CUDA launch or runtime call failed */
     MOE_ERR_DEVICE_RANGE = 6,  /* device side: an expert id was outside [0, E) */
     MOE_ERR_TIMEOUT = 7,       /* device side: a bounded pipeline wait gave up */
-    MOE_ERR_F16_RANGE = 8,     /* device side: a value left fp16's range in the tensor-core regime */
+    MOE_ERR_F16_RANGE = 8,     /* device side: a value left fp16's range where a product takes it in fp16 */
     MOE_ERR_SCRATCH_LIMIT = 9, /* moe_permute_noalloc: T*k larger than its fixed scratch allows */
     MOE_ERR_CAPTURE = 10       /* moe_permute_noalloc: first call on a device made while its stream captures */
 } moe_status_t;
@@ -416,8 +416,9 @@ moe_status_t moe_grouped_mm_i8(moe_dtype_t out_dtype, const int8_t* x, const flo
  * moe_route_topk (logits may be -inf), then for token t with experts e_j and weights p_j
  *   out[t] = sum_j p_j Wd[e_j] (SiLU(Wg[e_j] x[t]) * (Wu[e_j] x[t]))
  * in bf16 or fp16 with fp32 accumulation and one rounding at the end.  Between the two
- * products p * SiLU * up is held to 2^-17 of itself in bf16 and to 2^-23 in fp16, there to
- * 2^-36 at best, and has to be below 65504.
+ * products p * SiLU * up is held to 2^-17 of itself in bf16 and to 2^-23 in fp16, or to
+ * 2^-36 there; in fp16 one of 65520 or more becomes an infinity and gives
+ * MOE_ERR_F16_RANGE (moe_get_device_error).
  *   x       device [T][d_model]      logits  device fp32 [T][E]
  *   w13     device [E][2 d_ff][d_model], the gate's rows first
  *   w2      device [E][d_model][d_ff]
