@@ -64,15 +64,17 @@ moe_dtype_t moe_type(at::ScalarType t) {
 
 // The tensors of a call that are there: dense, and on the device of the first, on
 // which the call runs.  Where autograd records, it learns nothing of the call: said
-// once for each place of a program (as the warnings' filters have it).
-void on_one_device(std::initializer_list<std::reference_wrapper<const Tensor>> ts) {
+// once for each place of a program (as the warnings' filters have it), with what
+// computes the gradients of `fn` (null: nothing does).
+void on_one_device(const char* fn, const char* gradients, std::initializer_list<std::reference_wrapper<const Tensor>> ts) {
     const Tensor& first = *ts.begin();
     for (const Tensor& t : ts)
         if (t.defined() && t.requires_grad() && at::GradMode::is_enabled()) {
+            const std::string from = gradients ? std::string(" and take the gradients from ") + gradients
+                                               : std::string("; there is nothing that gives the gradients of ") + fn;
             if (PyErr_WarnEx(PyExc_UserWarning,
-                             "an operand requires gradients, but the 16-bit expert operators record no graph: their outputs "
-                             "do not require gradients; call them under torch.no_grad() and take the gradients from "
-                             "grouped_mm_dx, grouped_mm_dw, swiglu_backward and block_norm_backward", 1) < 0)
+                             ("an operand requires gradients, but the expert operators record no graph: the outputs of " +
+                              std::string(fn) + " do not require gradients; call it under torch.no_grad()" + from).c_str(), 1) < 0)
                 throw Raised{};
             break;
         }
@@ -275,7 +277,7 @@ PyObject* py_grouped_mm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject
         const int64_t R = x.size(0), K = x.size(1), E = w.size(0), N = w.size(1);
         want("w", w, {E, N, K}, x.scalar_type());
         const Tensor given = a.tensor(3), ws = a.tensor(4);
-        on_one_device({x, w, off, given, ws});
+        on_one_device("grouped_mm", "grouped_mm_dx and grouped_mm_dw", {x, w, off, given, ws});
         const OnStream on(a, 5, x);
         const Tensor y = output(given, "y", x, {R, N}, x.scalar_type());
         return grouped(moe_grouped_mm, "moe_grouped_mm", x, w, off, R, E, N, K, y, ws, on.s);
@@ -291,7 +293,7 @@ PyObject* py_grouped_mm_dx(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
         const int64_t R = dy.size(0), N = dy.size(1), E = w.size(0), K = w.size(2);
         want("w", w, {E, N, K}, dy.scalar_type());
         const Tensor given = a.tensor(3), ws = a.tensor(4);
-        on_one_device({dy, w, off, given, ws});
+        on_one_device("grouped_mm_dx", nullptr, {dy, w, off, given, ws});
         const OnStream on(a, 5, dy);
         const Tensor dx = output(given, "dx", dy, {R, K}, dy.scalar_type());
         return grouped(moe_grouped_mm_dx, "moe_grouped_mm_dx", dy, w, off, R, E, N, K, dx, ws, on.s);
@@ -307,7 +309,7 @@ PyObject* py_grouped_mm_dw(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
         const int64_t R = dy.size(0), N = dy.size(1), K = x.size(1), E = off.numel() - 1;
         want("x", x, {R, K}, dy.scalar_type());
         const Tensor given = a.tensor(3), ws = a.tensor(4);
-        on_one_device({dy, x, off, given, ws});
+        on_one_device("grouped_mm_dw", nullptr, {dy, x, off, given, ws});
         const OnStream on(a, 5, dy);
         const Tensor dw = output(given, "dw", dy, {E, N, K}, dy.scalar_type());
         return grouped(moe_grouped_mm_dw, "moe_grouped_mm_dw", dy, x, off, R, E, N, K, dw, ws, on.s);
@@ -331,7 +333,7 @@ PyObject* py_swiglu(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw
         const int64_t F = gated_width(gu, row_w, row_map), R = gu.size(0);
         const moe_dtype_t dt = moe_type(gu.scalar_type());
         const Tensor given = a.tensor(3);
-        on_one_device({gu, row_w, row_map, given});
+        on_one_device("swiglu", "swiglu_backward", {gu, row_w, row_map, given});
         const OnStream on(a, 4, gu);
         const Tensor h = output(given, "h", gu, {R, F}, gu.scalar_type());
         check(moe_swiglu(dt, ptr(gu), ptr_as<float>(row_w), ptr_as<int32_t>(row_map), size32(R), size32(F), ptr(h),
@@ -350,7 +352,7 @@ PyObject* py_swiglu_backward(PyObject*, PyObject* const* args, Py_ssize_t n, PyO
         want("dh", dh, {R, F}, t);
         const Tensor given = a.tensor(4);
         Tensor dw = a.tensor(5);
-        on_one_device({gu, dh, row_w, row_map, given, dw});
+        on_one_device("swiglu_backward", nullptr, {gu, dh, row_w, row_map, given, dw});
         const OnStream on(a, 6, gu);
         const Tensor dgu = output(given, "dgu", gu, {R, 2 * F}, t);
         if (dw.defined() || row_w.defined()) dw = output(dw, "drow_w", gu, {R}, at::kFloat);
@@ -395,7 +397,7 @@ PyObject* py_block_norm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject
         const Norm m(x, post, gate, pre);
         m.row("y", y);
         Tensor xo = a.tensor(7), h = a.tensor(8);
-        on_one_device({x, y, post, gate, pre, xo, h});
+        on_one_device("block_norm", "block_norm_backward", {x, y, post, gate, pre, xo, h});
         const OnStream on(a, 9, x);
         if (xo.defined() || y.defined()) xo = output(xo, "x_out", x, {m.T, m.D}, m.type);
         if (h.defined() || pre.defined()) h = output(h, "h", x, {m.T, m.D}, m.type);
@@ -416,7 +418,7 @@ PyObject* py_block_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n,
         m.row("dx_out", dxo);
         m.row("dh", dh);
         const int32_t T = size32(m.T), D = size32(m.D), G = size32(m.G);
-        on_one_device({x, y, dxo, dh, post, gate, pre, given_ws});
+        on_one_device("block_norm_backward", nullptr, {x, y, dxo, dh, post, gate, pre, given_ws});
         const OnStream on(a, 10, x);
         const Tensor none;
         const Tensor dx = output(none, "dx", x, {m.T, m.D}, m.type);
@@ -462,7 +464,7 @@ PyObject* py_layer_norm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject
         const LayerNorm m("x", x, gamma, beta);
         m.row("y", y);
         Tensor xo = a.tensor(5), h = a.tensor(6);
-        on_one_device({x, y, gamma, beta, xo, h});
+        on_one_device("layer_norm", "layer_norm_backward", {x, y, gamma, beta, xo, h});
         const OnStream on(a, 7, x);
         if (xo.defined() || y.defined()) xo = output(xo, "x_out", x, {m.T, m.D}, m.type);
         h = output(h, "h", x, {m.T, m.D}, m.type);
@@ -481,7 +483,7 @@ PyObject* py_layer_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n,
         m.row("dx_out", dxo);
         const int32_t T = size32(m.T), D = size32(m.D);
         const Tensor given_ws = a.tensor(6), none;
-        on_one_device({x, dh, dxo, gamma, beta, given_ws});
+        on_one_device("layer_norm_backward", nullptr, {x, dh, dxo, gamma, beta, given_ws});
         const OnStream on(a, 7, x);
         const Tensor dx = output(none, "dx", x, {m.T, m.D}, m.type);
         const Tensor dgamma = gamma.defined() ? output(none, "dgamma", x, {m.D}, m.ptype) : none;
@@ -506,7 +508,7 @@ PyObject* py_quantize_rows(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
             want("row_map", map, {map.size(0)}, at::kInt);
         }
         const int64_t T = x.size(0), D = x.size(1), R = map.defined() ? map.size(0) : T, k = a.integer(2, 1);
-        on_one_device({x, map, codes0, scales0, ws0});
+        on_one_device("quantize_rows", nullptr, {x, map, codes0, scales0, ws0});
         const OnStream on(a, 6, x);
         const Tensor codes = output(codes0, "codes", x, {R, D}, at::kChar), scales = output(scales0, "scales", x, {R}, at::kFloat);
         // (without a map R = T, and none is needed)
@@ -535,7 +537,7 @@ PyObject* py_grouped_mm_i8(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
         const at::ScalarType type = a.dtype(6, y0.defined() ? y0.scalar_type() : at::kBFloat16);
         const moe_dtype_t dt = moe_type(type);
         const int32_t r = size32(R), e = size32(E), nn = size32(N), k = size32(K);
-        on_one_device({x, xs, w, ws_, off, y0, ws0});
+        on_one_device("grouped_mm_i8", nullptr, {x, xs, w, ws_, off, y0, ws0});
         const OnStream on(a, 8, x);
         const Tensor y = output(y0, "y", x, {R, N}, type);
         const Tensor ws = workspace(ws0, ws0.defined() ? 0 : moe_grouped_mm_i8_workspace_size(r, e, nn, k), off);
@@ -563,7 +565,7 @@ PyObject* py_expert_layer(PyObject*, PyObject* const* args, Py_ssize_t n, PyObje
         want("w13", w13, {E, 2 * f, d}, type);
         if (ids.defined()) want("ids", ids, {T, k}, at::kInt);
         const int32_t t = size32(T), kk = size32(k), e = size32(E), dd = size32(d), ff = size32(f);
-        on_one_device({x, logits, w13, w2, out0, ids, ws0});
+        on_one_device("expert_layer", nullptr, {x, logits, w13, w2, out0, ids, ws0});
         const OnStream on(a, 8, x);
         const Tensor out = output(out0, "out", x, {T, d}, type);
         // a new one is zeroed: the CTAs' count has to start somewhere
