@@ -4,7 +4,7 @@
 //
 // The integer rate of the tensor cores here is 1/11 of the 16-bit one (153 against
 // 1900 T), and an 8-bit code is a 16-bit float exactly: the products run in fp16,
-// with fp32 sums, which are exact up to 2^24.  The weights stay 8-bit in memory and in
+// with fp32 sums, which are exact while they are within 2^24.  The weights stay 8-bit in memory and in
 // shared memory and are widened into tensor memory, from where the MMA takes its A
 // operand.  The rows' codes are widened once, in memory (every block of 256 weight rows
 // reads them again), by warps of the same kernel, ahead of the tiles that need them, or
@@ -578,9 +578,14 @@ cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, int cols,
 }
 cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStream_t s) {
     const int cols = tile_columns(g, sm_pairs()), n = 1 + row_tiles(g, cols);
-    // Few rows are widened by a kernel before, which takes less than the first tiles'
-    // wait for their units: 1238 rows of K 272 7.1 us so, 9.0 by the same kernel; 4096 of
-    // 2048 86.8 and 83.3 (128 experts).
+    // Few rows are widened by a kernel before, which takes less than the first tiles' wait
+    // for their units; many by the same kernel.  Either way (us), by pieces of 16 codes:
+    // 2^14.4 1238 rows, 8 experts of 520 x 272 6.9, 8.5; 2^15 512 rows, 16 of 2048 x 1024 12.3,
+    // 14.0; 2^16 512 rows, 128 of 1536 x 2048 76.6, 75.6; 2^17.6 12000 rows, 8 of 520 x 272 19.0,
+    // 19.5; 2^17.8 512 rows, 256 of 2048 x 7168 527, 516; 2^18 4096 rows, 16 of 2048 x 1024 24.6,
+    // 25.0, 2048 rows, 128 of 1536 x 2048 83.0, 80.4; 2^19 4096 of these 85.9, 83.1, 8192 rows,
+    // 16 of 2048 x 1024 43.0, 41.9.  From 2^16 to 2^18 many experts lose up to 3 % by it, few
+    // gain as much.
     const size_t n16 = (size_t)g.R * g.K / 16;
     const bool first = n16 <= (1 << 18);
     const cudaError_t e = first ? launch_overlapped(widen_rows_kernel, std::max(1, ceil_div((int)n16, 256)), 256, 0, s, d.x, g.x16, n16)
@@ -591,6 +596,9 @@ cudaError_t launch_tc(const GroupedI8Shape& g, const GroupedI8Data& d, cudaStrea
 
 }  // namespace
 
+// Up to 32 rows, or 128 where they are no more than the experts, go to the kernel for few
+// rows.  Spread by chance over 128 experts of 1536 x 2048, 128 rows take 41.8 us there and 129
+// by this kernel 52.9; all at one expert 14.6 and 11.5, which the sizes do not tell.
 static bool takes_few(int R, int E) { return R <= 32 || (R <= 128 && R <= E); }
 
 size_t grouped_i8_halves(int R, int E, int N, int K) {

@@ -3,9 +3,10 @@
 //   n  = (x' - m) r,  v = dh gamma
 //   dx = dx' + r (v - mean v - n mean(v n));  dgamma = sum dh n,  dbeta = sum dh
 // x' is the stored one, the value that every later reader sees.  Each tensor is
-// read and written once: bound by memory for many rows, by the latency of two launches
-// for few.  4096 x 2048 18.1 us (3.7 TB/s), of which a call of 100 rows takes 7.2; with two
-// reductions a row 20.0, with one chunk a thread (two row groups for four) 22.9.
+// read and written once.  Few rows are bound by the latency of two launches, one behind the
+// other (100 rows 7.2 us); many by that and by the row groups' barriers rather than by memory:
+// 4096 x 2048 17.1 to 18.1 us (3.7 to 3.9 TB/s), 4096 x 7168 48.9 (4.8), fp32 102.  4096 x 2048
+// with two reductions a row 20.0, with one chunk a thread (two row groups for four) 22.9.
 #include "layer_norm.cuh"
 
 namespace moe {

@@ -25,9 +25,10 @@ get_device_error(ws) reads; without one nobody learns of them.  Outputs and
 workspaces that are not given belong to the call's stream; operands that belong to
 another have to outlast the call there (record_stream).  No call records an
 autograd graph (operands that require gradients draw a warning where autograd
-records): the gradients are the calls above.  The functions are compiled
-(csrc/expert16_binding.cpp, argument marshalling only); this module loads them at
-their first use.
+records): gradients come from grouped_mm_dx, grouped_mm_dw and the calls named
+_backward; quantize_rows, grouped_mm_i8 and expert_layer have none.  The functions
+are compiled (csrc/expert16_binding.cpp, argument marshalling only); this module
+loads them at their first use.
 """
 from __future__ import annotations
 

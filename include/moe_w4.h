@@ -400,8 +400,9 @@ moe_status_t moe_quantize_rows(moe_dtype_t dtype, const void* x, const int32_t* 
  *   x  device int8 [R][K]     x_scale  device fp32 [R]
  *   w  device int8 [E][N][K]  w_scale  device fp32 [E][N]     (codes -128 .. 127)
  *   y  device [R][N], bf16 or fp16 (`out_dtype`), rounded once
- * K is a multiple of 16, N of 8, both at most 32768.  The sum is exact up to 2^24 and
- * held in fp32 beyond that (in 32-bit integers for few rows).  Offsets, rows outside
+ * K is a multiple of 16, N of 8, both at most 32768.  The sum is exact as long as its
+ * partial sums are within 2^24 and held in fp32 beyond that, or in 32-bit integers for few
+ * rows (exact; a row's result can depend on R there).  Offsets, rows outside
  * the segments and the error word as for moe_grouped_mm.
  * Workspace: >= moe_grouped_mm_i8_workspace_size(R, E, N, K) bytes; one for the most
  * rows also does for fewer.
